@@ -493,4 +493,8 @@ hc_status hc_trace_collect(hc_trace_entry* out, int max_entries, int* n_entries)
 }
 #endif
 
+/* Channels-last sequence-mixer operators: group norm with an activation, a
+ * short causal convolution and a selective state-space scan. */
+#include "hc_mixer.h"
+
 #endif /* HC_H */

@@ -6,7 +6,7 @@
 // news/18980 section 2.2).  Here the shards' partials sit side by side in one
 // buffer and are summed in shard order, so the result does not depend on
 // timing and repeats bit for bit.
-#include "common.cuh"
+#include "rows.cuh"
 
 namespace hc {
 namespace {
@@ -122,7 +122,35 @@ __global__ void column_group_kernel(const float* __restrict__ in, float* __restr
     }
 }
 
+// Column totals (launch_column_totals): a block takes 32 columns; warp w adds
+// rows w, w + 32, ..., then the warps' sums are added in order.
+__global__ void __launch_bounds__(1024) column_totals_kernel(const float* __restrict__ in, long long rows,
+                                                             float* __restrict__ a, int na, float* __restrict__ b,
+                                                             int nb, float* __restrict__ c, int nc) {
+    __shared__ float sm[32][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int k = blockIdx.x * 32 + lane, count = na + nb + nc;
+    float t = 0.0f;
+    if (k < count) {
+#pragma unroll 4
+        for (long long r = w; r < rows; r += 32) t += __ldg(in + r * count + k);
+    }
+    sm[w][lane] = t;
+    __syncthreads();
+    if (w == 0 && k < count) {
+        for (int j = 1; j < 32; j++) t += sm[j][lane];
+        float* o = k < na ? a : k < na + nb ? b : c;
+        if (o) o[k < na ? k : k < na + nb ? k - na : k - na - nb] = t;
+    }
+}
+
 }  // namespace
+
+hc_status launch_column_totals(const float* in, long long rows, float* a, int na, float* b, int nb, float* c, int nc,
+                               cudaStream_t st) {
+    column_totals_kernel<<<cdiv((long long)na + nb + nc, 32), 1024, 0, st>>>(in, rows, a, na, b, nb, c, nc);
+    return launched("column_totals_kernel", st);
+}
 
 size_t column_sum_tmp_floats(int rows, int count) {
     return (size_t)((rows + kColumnGroup - 1) / kColumnGroup) * count;

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libhc.so")
@@ -133,6 +134,9 @@ EXPORTS = [
     "hc_conv2d_fwd_act", "hc_conv2d_bwd_act", "hc_conv2d_bwd_residual", "hc_trace_enable", "hc_trace_collect",
     "hc_halo_pad", "hc_halo_pack", "hc_halo_unpack", "hc_conv2d_fwd_rank", "hc_conv2d_bwd_rank",
     "hc_conv2d_workspace_size_rank", "hc_sum_partials", "hc_set_sm_count",
+    "hc_groupnorm_workspace_size", "hc_groupnorm_fwd", "hc_groupnorm_bwd", "hc_causal_conv_fwd",
+    "hc_causal_conv_workspace_size", "hc_causal_conv_bwd", "hc_causal_conv_step", "hc_selective_scan_workspace_size",
+    "hc_selective_scan_saved_size", "hc_selective_scan_fwd", "hc_selective_scan_bwd", "hc_selective_scan_step",
 ]
 
 
@@ -389,6 +393,192 @@ def hc_trace_collect(max_entries: int = 256):
     n = C.c_int(0)
     st = _lib.hc_trace_collect(arr, max_entries, C.byref(n))
     return st, {arr[i].name.decode(): (int(arr[i].launches), float(arr[i].total_ms)) for i in range(n.value)}
+
+
+# ---- channels-last sequence-mixer operators (include/hc_mixer.h) ------------
+HC_DTYPE_F32, HC_DTYPE_BF16, HC_DTYPE_F16 = range(3)
+HC_PW_NONE, HC_PW_SILU, HC_PW_GELU = range(3)
+_DTYPES = {"torch.float32": HC_DTYPE_F32, "torch.bfloat16": HC_DTYPE_BF16, "torch.float16": HC_DTYPE_F16}
+
+
+class hc_groupnorm_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("N", "P", "C", "groups")] + [("eps", C.c_float), ("act", C.c_int),
+                                                                    ("dtype", C.c_int)]
+
+
+class hc_causal_conv_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "L", "D", "K", "act", "dtype")]
+
+
+class hc_selective_scan_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "L", "D", "groups", "d_state", "softplus", "dtype")]
+
+
+def _dtype(t) -> int:
+    """An hc_dtype from a torch dtype (or an hc_dtype); -1, which the library refuses, for another type."""
+    if isinstance(t, int):
+        return t
+    v = _DTYPES.get(t)
+    if v is None:
+        v = _DTYPES[t] = _DTYPES.get(str(t), -1)
+    return v
+
+
+def groupnorm_desc(N, P, C, groups, dtype, eps=1e-5, act=HC_PW_NONE) -> hc_groupnorm_desc:
+    return hc_groupnorm_desc(N, P, C, groups, eps, act, _dtype(dtype))
+
+
+def causal_conv_desc(B, L, D, K, dtype, act=HC_PW_NONE) -> hc_causal_conv_desc:
+    return hc_causal_conv_desc(B, L, D, K, act, _dtype(dtype))
+
+
+def selective_scan_desc(B, L, D, d_state, dtype, groups=1, softplus=1) -> hc_selective_scan_desc:
+    return hc_selective_scan_desc(B, L, D, groups, d_state, softplus, _dtype(dtype))
+
+
+_ABSENT = (0, 0, 0, 0)
+_pack_rows = struct.Struct("@Pqqq").pack
+_pack_scan_in = struct.Struct("@" + "Pqqq" * 5 + "PPP").pack
+_pack_scan_grad = struct.Struct("@" + "Pqqq" * 5 + "PPPP").pack
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t if isinstance(t, int) else t.data_ptr()
+
+
+def _view(t, *shape):
+    """The fields of an hc_rows for a torch tensor (batch, row, channel) or (batch, channel) with adjacent channels."""
+    if t is None:
+        return _ABSENT
+    if t.shape != shape:
+        raise HcError(HC_ERR_INVALID_ARG, f"a tensor of shape {tuple(t.shape)} where {shape} is wanted")
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] > 1:
+        raise HcError(HC_ERR_INVALID_ARG, "a channels-last tensor needs adjacent channels")
+    dt = _DTYPES.get(t.dtype)
+    return t.data_ptr(), s[0], s[1] if len(s) == 3 else 0, _dtype(t.dtype) if dt is None else dt
+
+
+def _rows(t, *shape) -> bytes:
+    return _pack_rows(*_view(t, *shape))
+
+
+_R, _Z = C.c_char_p, C.c_size_t  # a packed hc_rows (or hc_scan_in, hc_scan_grad)
+for _n, _a in (("hc_groupnorm_workspace_size", [_P, _I, C.POINTER(_Z)]),
+               ("hc_groupnorm_fwd", [_P, _R, _P, _P, _R, _P, _P, _P, _Z, _P]),
+               ("hc_groupnorm_bwd", [_P, _R, _P, _P, _P, _P, _R, _R, _P, _P, _P, _Z, _P]),
+               ("hc_causal_conv_fwd", [_P, _R, _P, _P, _R, _P, _P, _P, _P]),
+               ("hc_causal_conv_workspace_size", [_P, C.POINTER(_Z)]),
+               ("hc_causal_conv_bwd", [_P, _R, _P, _P, _R, _R, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+               ("hc_causal_conv_step", [_P, _R, _P, _P, _P, _R, _P]),
+               ("hc_selective_scan_workspace_size", [_P, _I, C.POINTER(_Z)]),
+               ("hc_selective_scan_saved_size", [_P, C.POINTER(_Z)]),
+               ("hc_selective_scan_fwd", [_P, _R, _P, _P, _R, _P, _P, _P, _Z, _P]),
+               ("hc_selective_scan_bwd", [_P, _R, _P, _P, _P, _R, _P, _R, _P, _Z, _P]),
+               ("hc_selective_scan_step", [_P, _R, _P, _R, _P])):
+    getattr(_lib, _n).argtypes = _a
+    getattr(_lib, _n).restype = C.c_int
+
+
+def hc_groupnorm_workspace_size(d: hc_groupnorm_desc, pass_: int):
+    """Returns (status, bytes): pass 0 for the forward pass, 1 for both."""
+    b = C.c_size_t(0)
+    st = _lib.hc_groupnorm_workspace_size(C.byref(d), int(pass_), C.byref(b))
+    return st, b.value
+
+
+def hc_groupnorm_fwd(d, x, gamma, beta, y, mean=None, rstd=None, ws=None, ws_bytes=0, stream=None) -> int:
+    """y = act(group norm of x); x and y are (N, P, C) tensors with adjacent channels."""
+    s = d.N, d.P, d.C
+    return _lib.hc_groupnorm_fwd(C.byref(d), _rows(x, *s), _addr(gamma), _addr(beta), _rows(y, *s), _addr(mean),
+                                 _addr(rstd), _addr(ws), ws_bytes, _stream(stream))
+
+
+def hc_groupnorm_bwd(d, x, gamma, beta, mean, rstd, gy, gx, ggamma=None, gbeta=None, ws=None, ws_bytes=0,
+                     stream=None) -> int:
+    s = d.N, d.P, d.C
+    return _lib.hc_groupnorm_bwd(C.byref(d), _rows(x, *s), _addr(gamma), _addr(beta), _addr(mean), _addr(rstd),
+                                 _rows(gy, *s), _rows(gx, *s), _addr(ggamma), _addr(gbeta), _addr(ws), ws_bytes,
+                                 _stream(stream))
+
+
+def hc_causal_conv_fwd(d, x, w, bias, y, state_in=None, state_out=None, lens=None, stream=None) -> int:
+    """x and y are (B, L, D) tensors with adjacent channels; states (B, K - 1, D) contiguous; lens int32 (B,)."""
+    s = d.B, d.L, d.D
+    return _lib.hc_causal_conv_fwd(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _rows(y, *s), _addr(state_in),
+                                   _addr(state_out), _addr(lens), _stream(stream))
+
+
+def hc_causal_conv_workspace_size(d: hc_causal_conv_desc):
+    """Returns (status, bytes) of the backward pass."""
+    b = C.c_size_t(0)
+    st = _lib.hc_causal_conv_workspace_size(C.byref(d), C.byref(b))
+    return st, b.value
+
+
+def hc_causal_conv_bwd(d, x, w, bias, gy, gx, gw, gb, state_in=None, gstate_out=None, gstate_in=None, lens=None,
+                       ws=None, ws_bytes=0, stream=None) -> int:
+    s = d.B, d.L, d.D
+    return _lib.hc_causal_conv_bwd(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _rows(gy, *s),
+                                   None if gx is None else _rows(gx, *s), _addr(gw), _addr(gb), _addr(state_in),
+                                   _addr(gstate_out), _addr(gstate_in), _addr(lens), _addr(ws), ws_bytes,
+                                   _stream(stream))
+
+
+def hc_causal_conv_step(d, x, w, bias, state, y, stream=None) -> int:
+    """One token: x and y are (B, D) tensors; state is moved on in place."""
+    s = d.B, d.D
+    return _lib.hc_causal_conv_step(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _addr(state), _rows(y, *s),
+                                    _stream(stream))
+
+
+def hc_selective_scan_workspace_size(d: hc_selective_scan_desc, pass_: int):
+    """Returns (status, bytes): pass 0 for the forward pass, 1 for both."""
+    b = C.c_size_t(0)
+    st = _lib.hc_selective_scan_workspace_size(C.byref(d), int(pass_), C.byref(b))
+    return st, b.value
+
+
+def hc_selective_scan_saved_size(d: hc_selective_scan_desc):
+    """Returns (status, bytes) of the states kept for the backward pass."""
+    b = C.c_size_t(0)
+    st = _lib.hc_selective_scan_saved_size(C.byref(d), C.byref(b))
+    return st, b.value
+
+
+def _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias) -> bytes:
+    s, m = lead + (d.D,), lead + (d.groups * d.d_state,)
+    return _pack_scan_in(*_view(u, *s), *_view(dt, *s), *_view(Bm, *m), *_view(Cm, *m), *_view(z, *s), _addr(A),
+                         _addr(D), _addr(dt_bias))
+
+
+def hc_selective_scan_fwd(d, u, dt, A, Bm, Cm, y, D=None, z=None, dt_bias=None, h0=None, hT=None, lens=None,
+                          saved=None, ws=None, ws_bytes=0, stream=None) -> int:
+    """u, dt, z, y are (B, L, D) and Bm, Cm (B, L, groups * d_state) tensors with adjacent channels; lens int32 (B,)."""
+    lead = (d.B, d.L)
+    return _lib.hc_selective_scan_fwd(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(h0),
+                                      _addr(lens), _rows(y, *lead, d.D), _addr(hT), _addr(saved), _addr(ws), ws_bytes,
+                                      _stream(stream))
+
+
+def hc_selective_scan_bwd(d, u, dt, A, Bm, Cm, gy, saved, gu, gdt, gA, gB, gC, D=None, z=None, dt_bias=None, h0=None,
+                          lens=None, ghT=None, gD=None, gz=None, gdt_bias=None, gh0=None, ws=None, ws_bytes=0,
+                          stream=None) -> int:
+    """The gradients of hc_selective_scan_fwd on the same inputs, from the states it saved."""
+    lead = (d.B, d.L)
+    s, m = lead + (d.D,), lead + (d.groups * d.d_state,)
+    grads = _pack_scan_grad(*_view(gu, *s), *_view(gdt, *s), *_view(gB, *m), *_view(gC, *m), *_view(gz, *s), _addr(gA),
+                            _addr(gD), _addr(gdt_bias), _addr(gh0))
+    return _lib.hc_selective_scan_bwd(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(h0),
+                                      _addr(lens), _addr(saved), _rows(gy, *s), _addr(ghT), grads, _addr(ws), ws_bytes,
+                                      _stream(stream))
+
+
+def hc_selective_scan_step(d, u, dt, A, Bm, Cm, state, y, D=None, z=None, dt_bias=None, stream=None) -> int:
+    """One token: u, dt, z, y are (B, D) and Bm, Cm (B, groups * d_state) tensors; state is updated in place."""
+    lead = (d.B,)
+    return _lib.hc_selective_scan_step(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(state),
+                                       _rows(y, d.B, d.D), _stream(stream))
 
 
 def check(status: int, what: str = "hc call") -> None:
