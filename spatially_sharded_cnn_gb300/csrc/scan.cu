@@ -8,6 +8,13 @@
 // several channels of a thread, a step size serves four states, and both sums
 // the scan needs -- y over states, the gradients of B and C over channels --
 // are partly in-thread and take few shuffles.
+//
+// The recurrence is sequential in the rows.  Where sequences and channels alone
+// do not fill the GPU, a sequence is cut into segments of whole tiles: one pass
+// takes every segment from a zero state, the segments' results are joined
+// (h_out = exp(A * sum of steps) * h_in + h_local), and the full pass then runs
+// every segment from its own first state.  The extra pass costs its
+// exponentials again and buys a factor of `segs` in parallelism.
 #include "rows.cuh"
 
 namespace hc {
@@ -23,12 +30,15 @@ struct ScanArgs {
     const float *A, *D, *bias, *h0, *ghT;
     const int* lens;
     float *hT, *saved, *gh0;
-    float* part;  // backward: [B][D * N | D | D] sums of gA, gD, gdt_bias
+    float* part;  // backward: [B][segs][D * N | D | D] sums of gA, gD, gdt_bias
     float* gbc;   // backward, several channel tiles a group: [tile][B][L][G][2][N]
     int B, L, Dm, G, Dg, N;
     int dtype, softplus, vec;
     int ctiles;  // channel tiles per group
     int tiles;   // row tiles per sequence
+    int segs, seg_tiles;  // segments a sequence is cut into, row tiles in each
+    float* carry;         // [B][segs][D][NP]: a segment's state from a zero state, then the state it starts from
+    float* dsum;          // [B][segs][D]: its sum of step sizes
 };
 
 __device__ __forceinline__ float ld1(const void* p, long long i, int dt) {
@@ -140,7 +150,7 @@ template <int NL> struct FwdTile {
     static constexpr size_t SMEM = sizeof(float) * SC_T * (3 * CT + 2 * NP);
 };
 
-// One block: CT channels of one group of one sequence, all its rows.
+// One block: CT channels of one group of one segment.
 template <int NL>
 __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
     using S = FwdTile<NL>;
@@ -151,7 +161,8 @@ __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __
     float* Bs = ys + SC_T * S::CT;              // [T][NP]
     float* Cs = Bs + SC_T * S::NP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ct = blockIdx.x % (a.G * a.ctiles), b = blockIdx.x / (a.G * a.ctiles);
+    const int ct = blockIdx.x % (a.G * a.ctiles), bs = blockIdx.x / (a.G * a.ctiles);
+    const int b = bs / a.segs, seg = bs % a.segs;
     const int g = ct / a.ctiles, c0 = (ct % a.ctiles) * S::CT;  // first channel inside the group
     const int cn = min(S::CT, a.Dg - c0);                       // channels of this block
     const int d0 = g * a.Dg + c0;
@@ -164,12 +175,16 @@ __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __
         for (int j = 0; j < 4; j++) A2[i][j] = h[i][j] = 0.0f;
         if (tc + i < cn) {
             ld_states(a.A + (long long)(d0 + tc + i) * a.N, 4 * n, a.N, A2[i]);
-            if (a.h0) ld_states(a.h0 + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, h[i]);
+            if (a.segs > 1)
+                load_pack<float, 4>(a.carry + ((long long)bs * a.Dm + d0 + tc + i) * S::NP + 4 * n, h[i]);
+            else if (a.h0)
+                ld_states(a.h0 + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, h[i]);
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) A2[i][j] *= kLog2e;
     }
-    for (int tile = 0; tile < a.tiles; tile++) {
+    const int tile1 = min((seg + 1) * a.seg_tiles, a.tiles);
+    for (int tile = seg * a.seg_tiles; tile < tile1; tile++) {
         const int t0 = tile * SC_T, rows = min(SC_T, a.L - t0);
         if (t0 < len) {
             for (int q = tid; q < SC_T * (S::CT / 4); q += S::THREADS) {
@@ -251,10 +266,141 @@ __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __
         }
         __syncthreads();
     }
-    if (a.hT) {
+    if (a.hT && seg == a.segs - 1) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
             if (tc + i < cn) st_states(a.hT + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, h[i]);
+    }
+}
+
+// A segment's state from a zero state.  REV false: the state itself, over
+// x = step * u and B, rows upwards.  REV true: the state's gradient, over
+// q = gy * silu(z) and C, rows downwards: G_{t-1} = exp(step_t A) (G_t + q_t C_t).
+template <int NL, bool REV>
+__global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_carry_kernel(const __grid_constant__ ScanArgs a) {
+    using S = FwdTile<NL>;
+    extern __shared__ float4 sm4[];
+    float* dl = reinterpret_cast<float*>(sm4);  // [T][CT] step sizes
+    float* xs = dl + SC_T * S::CT;              // [T][CT] step * u, or q
+    float* Bs = xs + SC_T * S::CT;              // [T][NP]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ct = blockIdx.x % (a.G * a.ctiles), bs = blockIdx.x / (a.G * a.ctiles);
+    const int b = bs / a.segs, seg = bs % a.segs;
+    const int g = ct / a.ctiles, c0 = (ct % a.ctiles) * S::CT;
+    const int cn = min(S::CT, a.Dg - c0);
+    const int d0 = g * a.Dg + c0;
+    const int n = lane % NL, tc = warp * S::WC + (lane / NL) * 4;
+    const int len = scan_len(a, b);
+    float A2[4][4], h[4][4], sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        sum[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) A2[i][j] = h[i][j] = 0.0f;
+        if (tc + i < cn) ld_states(a.A + (long long)(d0 + tc + i) * a.N, 4 * n, a.N, A2[i]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) A2[i][j] *= kLog2e;
+    }
+    const int tile0 = seg * a.seg_tiles, tile1 = min(tile0 + a.seg_tiles, a.tiles);
+    for (int k = tile0; k < tile1; k++) {
+        const int t0 = (REV ? tile1 - 1 - (k - tile0) : k) * SC_T;
+        if (t0 >= len) continue;
+        for (int q = tid; q < SC_T * (S::CT / 4); q += S::THREADS) {
+            const int t = q / (S::CT / 4), c = (q % (S::CT / 4)) * 4;
+            float x[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
+            if (t0 + t < len && c < cn) {
+                const hc_rows& in = REV ? a.gy : a.u;
+                ld4(in.p, b * in.batch + (t0 + t) * in.row + d0, a.dtype, c, cn, a.vec, x);
+                ld4(a.dt.p, b * a.dt.batch + (t0 + t) * a.dt.row + d0, a.dtype, c, cn, a.vec, s);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (a.bias && c + i < cn) s[i] += a.bias[d0 + c + i];
+                    if (a.softplus) s[i] = softplus_f(s[i]);
+                    if (!REV) x[i] *= s[i];
+                }
+                if (REV && a.z.p) {
+                    float zz[4];
+                    ld4(a.z.p, b * a.z.batch + (t0 + t) * a.z.row + d0, a.dtype, c, cn, a.vec, zz);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) x[i] *= silu_f(zz[i]);
+                }
+            }
+            store_pack<float, 4>(dl + t * S::CT + c, s);
+            store_pack<float, 4>(xs + t * S::CT + c, x);
+        }
+        for (int q = tid; q < SC_T * S::NP; q += S::THREADS) {
+            const int t = q / S::NP, j = q % S::NP;
+            const hc_rows& in = REV ? a.Cm : a.Bm;
+            Bs[q] = t0 + t < len && j < a.N ? ld1(in.p, b * in.batch + (t0 + t) * in.row + g * a.N + j, a.dtype) : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int v = 0; v < SC_T; v++) {
+            const int t = REV ? SC_T - 1 - v : v;
+            float s[4], x[4], B[4];
+            load_pack<float, 4>(dl + t * S::CT + tc, s);
+            load_pack<float, 4>(xs + t * S::CT + tc, x);
+            load_pack<float, 4>(Bs + t * S::NP + 4 * n, B);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                sum[i] += s[i];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float e = ex2f(s[i] * A2[i][j]);
+                    h[i][j] = REV ? e * fmaf(x[i], B[j], h[i][j]) : fmaf(e, h[i][j], x[i] * B[j]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (tc + i >= cn) continue;
+        const long long d = (long long)bs * a.Dm + d0 + tc + i;
+        store_pack<float, 4>(a.carry + d * S::NP + 4 * n, h[i]);
+        if (n == 0) a.dsum[d] = sum[i];
+    }
+}
+
+// Replaces every segment's local result by the state it starts from.  A block
+// takes SJ_STATES adjacent states of a sequence, its 32 rows of threads equal
+// runs of segments: each run is joined, the runs' results are joined in order
+// through shared memory, and each run is gone through again.
+constexpr int SJ_STATES = 32;
+template <bool REV>
+__global__ void __launch_bounds__(1024) scan_join_kernel(const __grid_constant__ ScanArgs a, int NP) {
+    __shared__ float hs[32][SJ_STATES + 1], as[32][SJ_STATES + 1];
+    const int col = threadIdx.x % SJ_STATES, r = threadIdx.x / SJ_STATES;
+    const int b = blockIdx.y;
+    const long long q = (long long)blockIdx.x * SJ_STATES + col;
+    const bool on = q < (long long)a.Dm * NP;
+    const int d = on ? (int)(q / NP) : 0, n = on ? (int)(q % NP) : 0;
+    const float A2 = on && n < a.N ? a.A[(long long)d * a.N + n] * kLog2e : 0.0f;
+    const int per = (a.segs + 31) / 32, s0 = r * per, s1 = min(s0 + per, a.segs);
+    float* cp = a.carry + (long long)b * a.segs * a.Dm * NP + (on ? q : 0);
+    const float* dp = a.dsum + (long long)b * a.segs * a.Dm + d;
+    const long long hstep = (long long)a.Dm * NP;
+    float h = 0.0f, total = 0.0f;
+#pragma unroll 4
+    for (int k = s0; k < s1; k++) {
+        const int s = REV ? a.segs - 1 - k : k;
+        const float w = dp[(long long)s * a.Dm];
+        h = fmaf(ex2f(w * A2), h, cp[s * hstep]);
+        total += w;
+    }
+    hs[r][col] = h;
+    as[r][col] = total;
+    __syncthreads();
+    const float* first = REV ? a.ghT : a.h0;
+    h = first && on && n < a.N ? first[((long long)b * a.Dm + d) * a.N + n] : 0.0f;
+    for (int k = 0; k < r; k++) h = fmaf(ex2f(as[k][col] * A2), h, hs[k][col]);
+    if (!on) return;
+#pragma unroll 4
+    for (int k = s0; k < s1; k++) {
+        const int s = REV ? a.segs - 1 - k : k;
+        const float v = cp[s * hstep], w = dp[(long long)s * a.Dm];
+        cp[s * hstep] = h;
+        h = fmaf(ex2f(w * A2), h, v);
     }
 }
 
@@ -270,7 +416,7 @@ template <int NL> struct BwdTile {
     static constexpr size_t SMEM = sizeof(float) * SC_T * (6 * CT + 2 * NP + 2 * NP * W);
 };
 
-// One block: CT channels of one group of one sequence, its tiles from the last
+// One block: CT channels of one group of one segment, its tiles from the last
 // to the first.  A tile's states are recomputed from its saved first state and
 // kept in registers, then the state's gradient runs back through them.
 template <int NL>
@@ -287,7 +433,8 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
     float* Cs = Bs + SC_T * S::NP;
     float* red = Cs + SC_T * S::NP;  // [W][T][2][NP]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ct = blockIdx.x % (a.G * a.ctiles), b = blockIdx.x / (a.G * a.ctiles);
+    const int ct = blockIdx.x % (a.G * a.ctiles), bs = blockIdx.x / (a.G * a.ctiles);
+    const int b = bs / a.segs, seg = bs % a.segs;
     const int g = ct / a.ctiles, c0 = (ct % a.ctiles) * S::CT;
     const int cn = min(S::CT, a.Dg - c0);
     const int d0 = g * a.Dg + c0;
@@ -300,7 +447,10 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
         for (int j = 0; j < 4; j++) A2[i][j] = G[i][j] = gA[i][j] = 0.0f;
         if (tc + i < cn) {
             ld_states(a.A + (long long)(d0 + tc + i) * a.N, 4 * n, a.N, A2[i]);
-            if (a.ghT) ld_states(a.ghT + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, G[i]);
+            if (a.segs > 1)
+                load_pack<float, 4>(a.carry + ((long long)bs * a.Dm + d0 + tc + i) * S::NP + 4 * n, G[i]);
+            else if (a.ghT)
+                ld_states(a.ghT + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, G[i]);
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) A2[i][j] *= kLog2e;
@@ -314,7 +464,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
         bv[k] = a.bias && ec + k < cn ? a.bias[d0 + ec + k] : 0.0f;
         sD[k] = sb[k] = 0.0f;
     }
-    for (int tile = a.tiles - 1; tile >= 0; tile--) {
+    for (int tile = min((seg + 1) * a.seg_tiles, a.tiles) - 1; tile >= seg * a.seg_tiles; tile--) {
         const int t0 = tile * SC_T, rows = min(SC_T, a.L - t0);
         const bool live = t0 < len;
         if (live) {
@@ -382,6 +532,8 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
                     }
                 }
             }
+            // gA summed tile by tile: a running sum over all rows would lose an ulp a row
+            float ga_tile[2][4] = {};
 #pragma unroll
             for (int t = SC_T - 1; t >= 0; t--) {
                 float B[4], C[4], bc[8], gb[2] = {0, 0}, ea[2] = {0, 0};
@@ -404,7 +556,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
                         const float ga = gg * ex2f(sv[i] * A2[i][j]);
                         const float E = ga * H[t][i][j];
                         ea[i] = fmaf(E, A2[i][j], ea[i]);
-                        gA[i][j] = fmaf(E, sv[i], gA[i][j]);
+                        ga_tile[i][j] = fmaf(E, sv[i], ga_tile[i][j]);
                         G[i][j] = ga;
                     }
                 }
@@ -445,6 +597,10 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
                     for (int i = 0; i < KEEP; i++) r[i] = bc[i];
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) gA[i][j] += ga_tile[i][j];
             __syncthreads();
         }
         for (int t = er; t < rows; t += S::RROWS) {
@@ -497,7 +653,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
         }
         __syncthreads();
     }
-    float* pb = a.part + (long long)b * (a.N + 2) * a.Dm;
+    float* pb = a.part + (long long)bs * (a.N + 2) * a.Dm;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         if (tc + i < cn) {
@@ -505,7 +661,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __
 #pragma unroll
             for (int j = 0; j < 4; j++)
                 if (4 * n + j < a.N) pb[d * a.N + 4 * n + j] = gA[i][j];
-            if (a.gh0) st_states(a.gh0 + ((long long)b * a.Dm + d) * a.N, 4 * n, a.N, G[i]);
+            if (a.gh0 && seg == 0) st_states(a.gh0 + ((long long)b * a.Dm + d) * a.N, 4 * n, a.N, G[i]);
         }
     }
     // gD and gdt_bias over the epilogue's row lanes, in order
@@ -579,9 +735,10 @@ bool scan_desc_ok(const hc_selective_scan_desc* d) {
     return d && d->B > 0 && d->L >= 0 && d->D > 0 && d->groups > 0 && d->D % d->groups == 0 && d->d_state > 0 &&
            (d->softplus == 0 || d->softplus == 1) && dtype_ok(d->dtype);
 }
-// Launch limits: (sequence, channel tile) on grid x.
+// Launch limits: (sequence, segment, channel tile) on grid x, sequences on grid y.
 bool scan_size_ok(const hc_selective_scan_desc* d) {
-    return d->d_state <= 64 && d->D <= (1 << 20) && (long long)d->B * d->D < (1LL << 31) && d->L <= 0x7fffffff - 64;
+    return d->d_state <= 64 && d->D <= (1 << 20) && d->B <= 65535 && (long long)d->B * d->D < (1LL << 31) &&
+           d->L <= 0x7fffffff - 64;
 }
 int scan_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
@@ -595,14 +752,45 @@ template <typename F> hc_status scan_dispatch(int N, F&& f) {
     return f.template operator()<16>();
 }
 
-// Channel tiles a group in the backward kernel.
-int bwd_ctiles(const hc_selective_scan_desc* d) {
-    const int ct = 8 * 32 / scan_lanes(d->d_state);
-    return (int)cdiv(d->D / d->groups, ct);
+// Channel tiles a group in a kernel whose warps take `per_lane` channels a lane group.
+int scan_ctiles(const hc_selective_scan_desc* d, int warps, int per_lane) {
+    return (int)cdiv(d->D / d->groups, warps * per_lane * 32 / scan_lanes(d->d_state));
 }
+int fwd_ctiles(const hc_selective_scan_desc* d) { return scan_ctiles(d, scan_lanes(d->d_state) == 1 ? 2 : 4, 4); }
+int bwd_ctiles(const hc_selective_scan_desc* d) { return scan_ctiles(d, 4, 2); }
+
+// Segments: none where (sequence, channel tile) blocks give every SM `want` of
+// them, else as many as make up for it, of two tiles at least.
+struct Segs {
+    int n, tiles;
+};
+Segs scan_segs(const hc_selective_scan_desc* d, int ctiles, int want) {
+    const int tiles = (int)cdiv(d->L, SC_T);
+    const long long blocks = (long long)d->B * d->groups * ctiles, full = (long long)want * device_sm_count();
+    if (blocks * 2 > full || tiles < 4) return {1, tiles > 0 ? tiles : 1};
+    long long n = full / blocks;
+    if (n > tiles / 2) n = tiles / 2;
+    const int per = (int)cdiv(tiles, n);
+    return {(int)cdiv(tiles, per), per};
+}
+Segs fwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, fwd_ctiles(d), 6); }
+Segs bwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, bwd_ctiles(d), 2); }
+
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+size_t carry_floats(const hc_selective_scan_desc* d, int segs) {
+    return segs > 1 ? (size_t)d->B * segs * d->D * 4 * scan_lanes(d->d_state) : 0;
+}
+size_t carry_bytes(const hc_selective_scan_desc* d, int segs) {
+    return up256(4 * carry_floats(d, segs)) + up256(segs > 1 ? 4 * (size_t)d->B * segs * d->D : 0);
+}
 size_t part_bytes(const hc_selective_scan_desc* d) {
-    return up256(sizeof(float) * d->B * (size_t)(d->d_state + 2) * d->D);
+    return up256(sizeof(float) * d->B * bwd_segs(d).n * (size_t)(d->d_state + 2) * d->D);
+}
+void set_segs(ScanArgs& a, const hc_selective_scan_desc* d, Segs s, void* ws) {
+    a.segs = s.n;
+    a.seg_tiles = s.tiles;
+    a.carry = (float*)ws;
+    a.dsum = (float*)((char*)ws + up256(4 * carry_floats(d, s.n)));
 }
 
 ScanArgs scan_args(const hc_selective_scan_desc* d, const hc_scan_in* in) {
@@ -634,6 +822,22 @@ bool scan_in_ok(const hc_selective_scan_desc* d, const hc_scan_in* in, long long
            f32_opt_ok(in->dt_bias);
 }
 
+// The first states of the segments (REV: of the gradient, from the last row up).
+template <int NL, bool REV> hc_status launch_scan_carry(ScanArgs a, cudaStream_t st) {
+    using S = FwdTile<NL>;
+    static std::atomic<unsigned long long> attr{0};
+    once_per_device(attr, [] {
+        return cudaFuncSetAttribute(scan_carry_kernel<NL, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)S::SMEM) == cudaSuccess;
+    });
+    a.ctiles = (int)cdiv(a.Dg, S::CT);
+    scan_carry_kernel<NL, REV><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
+    hc_status e = launched("scan_carry_kernel", st);
+    if (e) return e;
+    scan_join_kernel<REV><<<dim3(cdiv((long long)a.Dm * S::NP, SJ_STATES), a.B), 1024, 0, st>>>(a, S::NP);
+    return launched("scan_join_kernel", st);
+}
+
 struct ScanFwd {
     ScanArgs a;
     cudaStream_t st;
@@ -644,8 +848,12 @@ struct ScanFwd {
             return cudaFuncSetAttribute(scan_fwd_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)S::SMEM) == cudaSuccess;
         });
+        if (a.segs > 1) {
+            const hc_status e = launch_scan_carry<NL, false>(a, st);
+            if (e) return e;
+        }
         a.ctiles = (int)cdiv(a.Dg, S::CT);
-        scan_fwd_kernel<NL><<<(unsigned)a.B * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
+        scan_fwd_kernel<NL><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
         return launched("scan_fwd_kernel", st);
     }
 };
@@ -661,7 +869,11 @@ struct ScanBwd {
             return cudaFuncSetAttribute(scan_bwd_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)S::SMEM) == cudaSuccess;
         });
-        scan_bwd_kernel<NL><<<(unsigned)a.B * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
+        if (a.segs > 1) {
+            const hc_status e = launch_scan_carry<NL, true>(a, st);
+            if (e) return e;
+        }
+        scan_bwd_kernel<NL><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
         hc_status e = launched("scan_bwd_kernel", st);
         if (e) return e;
         const long long bc = (long long)a.B * a.L * a.G * 2 * a.N;
@@ -670,7 +882,7 @@ struct ScanBwd {
             scan_bc_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(a);
             if ((e = launched("scan_bc_kernel", st))) return e;
         }
-        return launch_column_totals(a.part, a.B, g->gA, a.Dm * a.N, g->gD, a.Dm, g->gdt_bias, a.Dm, st);
+        return launch_column_totals(a.part, (long long)a.B * a.segs, g->gA, a.Dm * a.N, g->gD, a.Dm, g->gdt_bias, a.Dm, st);
     }
 };
 
@@ -697,16 +909,18 @@ using namespace hc;
 
 extern "C" {
 
-// Workspace of the backward pass: [gA, gD, gdt_bias sums][gB, gC sums of each
-// channel tile, where a group has several].
+// Workspace: forward [segment states][segment step sums]; backward the same two,
+// [gA, gD, gdt_bias sums][gB, gC sums of each channel tile, where a group has
+// several].
 hc_status hc_selective_scan_workspace_size(const hc_selective_scan_desc* d, int pass, size_t* bytes) {
     if (!scan_desc_ok(d) || pass < 0 || pass > 1 || !bytes) return HC_ERR_INVALID_ARG;
     if (!scan_size_ok(d)) return HC_ERR_UNSUPPORTED;
-    *bytes = 0;
+    *bytes = carry_bytes(d, fwd_segs(d).n);
     if (pass == 1) {
         const int tiles = bwd_ctiles(d);
-        *bytes = part_bytes(d);
-        if (tiles > 1) *bytes += sizeof(float) * tiles * (size_t)d->B * d->L * d->groups * 2 * d->d_state;
+        size_t b = carry_bytes(d, bwd_segs(d).n) + part_bytes(d);
+        if (tiles > 1) b += sizeof(float) * tiles * (size_t)d->B * d->L * d->groups * 2 * d->d_state;
+        if (b > *bytes) *bytes = b;
     }
     return HC_OK;
 }
@@ -738,6 +952,7 @@ hc_status hc_selective_scan_fwd(const hc_selective_scan_desc* d, const hc_scan_i
     f.a.lens = lens;
     f.a.saved = (float*)saved;
     f.a.vec = vec4(f.a);
+    set_segs(f.a, d, fwd_segs(d), ws);
     return scan_dispatch(d->d_state, f);
 }
 
@@ -773,9 +988,11 @@ hc_status hc_selective_scan_bwd(const hc_selective_scan_desc* d, const hc_scan_i
     f.a.gh0 = g->gh0;
     f.a.lens = lens;
     f.a.saved = (float*)saved;
-    f.a.part = (float*)ws;
+    set_segs(f.a, d, bwd_segs(d), ws);
+    const size_t carried = carry_bytes(d, f.a.segs);
+    f.a.part = (float*)((char*)ws + carried);
     f.a.ctiles = bwd_ctiles(d);
-    f.a.gbc = f.a.ctiles > 1 ? (float*)((char*)ws + part_bytes(d)) : nullptr;
+    f.a.gbc = f.a.ctiles > 1 ? (float*)((char*)ws + carried + part_bytes(d)) : nullptr;
     f.a.vec = vec4(f.a);
     return scan_dispatch(d->d_state, f);
 }
