@@ -38,12 +38,45 @@ template <typename T, int V> __device__ __forceinline__ void store_pack(T* p, co
     *reinterpret_cast<Pack<T, V>*>(p) = q;
 }
 
-// SiLU x * s and its slope s * (1 + x * (1 - s)), s = 1 / (1 + exp(-x)).
-__device__ __forceinline__ float sigmoid_f(float x) { return 1.0f / (1.0f + expf(-x)); }
-__device__ __forceinline__ float silu_f(float x) { return x / (1.0f + expf(-x)); }
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// 2^x and 1/x on the special function unit (2 and 1 ulp; results below the
+// normal range are zero).
+__device__ __forceinline__ float ex2f(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcpf(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// SiLU x * s and its slope s * (1 + x * (1 - s)), s = 1 / (1 + exp(-x)): a few
+// ulps from two special-function results, which the elementwise kernels would
+// otherwise spend most of their instructions on.
+__device__ __forceinline__ float sigmoid_f(float x) { return rcpf(1.0f + ex2f(-kLog2e * x)); }
+__device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }
 __device__ __forceinline__ float silu_d(float x) {
     const float s = sigmoid_f(x);
-    return s * (1.0f + x * (1.0f - s));
+    return s * fmaf(x, 1.0f - s, 1.0f);
+}
+// log(1 + exp(x)) = max(x, 0) + log(1 + e), e = exp(-|x|), with log(1 + e) =
+// 2 atanh(v), v = e / (2 + e) <= 1/3, by the series of atanh up to v^13 (the
+// next term is below 2^-25 of the sum): relative accuracy also where e is small,
+// which a logarithm of the rounded 1 + e would not give.
+__device__ __forceinline__ float softplus_f(float x) {
+    const float e = ex2f(-kLog2e * fabsf(x));
+    const float v = e * rcpf(2.0f + e), w = v * v;
+    float p = fmaf(w, 1.0f / 13, 1.0f / 11);
+    p = fmaf(w, p, 1.0f / 9);
+    p = fmaf(w, p, 1.0f / 7);
+    p = fmaf(w, p, 1.0f / 5);
+    p = fmaf(w, p, 1.0f / 3);
+    p = fmaf(w, p, 1.0f);
+    return fmaf(2.0f * v, p, fmaxf(x, 0.0f));
 }
 
 template <int ACT> __device__ __forceinline__ float act_f(float x) {

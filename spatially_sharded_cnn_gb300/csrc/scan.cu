@@ -20,9 +20,7 @@
 namespace hc {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int SC_T = 16;  // rows a tile; the backward pass keeps a tile's states in registers
+constexpr int SC_T = 8;  // rows a tile; the backward pass keeps a tile's states in registers
 
 struct ScanArgs {
     hc_rows u, dt, Bm, Cm, z, y;         // forward
@@ -54,21 +52,8 @@ __device__ __forceinline__ void st1(void* p, long long i, int dt, float v) {
     else
         static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
-// Channels c .. c + 3 of a row, those at or past n as zeros; vec: aligned to
+// Channels c .. c + 3 of a row, those at or past n left alone; vec: aligned to
 // four elements, and then n is a multiple of 4.
-__device__ __forceinline__ void ld4(const void* p, long long i, int dt, int c, int n, bool vec, float (&f)[4]) {
-    if (vec && c < n) {
-        if (dt == HC_DTYPE_F32)
-            load_pack<float, 4>(static_cast<const float*>(p) + i + c, f);
-        else if (dt == HC_DTYPE_BF16)
-            load_pack<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16*>(p) + i + c, f);
-        else
-            load_pack<__half, 4>(static_cast<const __half*>(p) + i + c, f);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; k++) f[k] = c + k < n ? ld1(p, i + c + k, dt) : 0.0f;
-}
 __device__ __forceinline__ void st4(void* p, long long i, int dt, int c, int n, bool vec, const float (&f)[4]) {
     if (vec && c < n) {
         if (dt == HC_DTYPE_F32)
@@ -103,14 +88,6 @@ __device__ __forceinline__ void st_states(float* p, int n0, int N, const float (
         if (n0 + k < N) p[n0 + k] = f[k];
 }
 
-__device__ __forceinline__ float ex2f(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-// log(1 + exp(x)); above 20 it is x to fp32 precision.
-__device__ __forceinline__ float softplus_f(float x) { return x > 20.0f ? x : log1pf(expf(x)); }
-
 __device__ __forceinline__ int scan_len(const ScanArgs& a, int b) {
     return a.lens ? min(max(a.lens[b], 0), a.L) : a.L;
 }
@@ -141,224 +118,491 @@ __device__ __forceinline__ int lanes_sum(float (&v)[M], int n) {
     return first;
 }
 
-template <int NL> struct FwdTile {
+// Two fp32 values in one 64-bit register pair: one instruction for two
+// multiply-adds.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pk2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpk2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 ex2x2(f32x2 v) {
+    float a, b;
+    unpk2(v, a, b);
+    return pk2(ex2f(a), ex2f(b));
+}
+
+__device__ __forceinline__ void cp_async(unsigned dst, const void* src, int bytes, bool on) {
+    const int n = on ? bytes : 0;  // the rest of the destination is zeroed
+    if (bytes == 16)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// The layout the three kernels share.  A thread holds states 4n .. 4n + 3 of
+// four channels as two channel pairs; a block's CT channels times a tile's rows
+// are also walked elementwise, every thread at four fixed channels.
+template <int NL> struct Tile {
     static constexpr int NP = 4 * NL, CG = 32 / NL;
-    static constexpr int W = NL == 1 ? 2 : 4;  // warps
-    static constexpr int WC = 4 * CG;          // channels a warp
-    static constexpr int CT = W * WC;          // channels a block
+    static constexpr int W = NL == 1 ? 1 : NL == 2 ? 2 : 4;  // warps
+    static constexpr int WC = 4 * CG;                        // channels a warp
+    static constexpr int CT = W * WC;                        // channels a block
     static constexpr int THREADS = W * 32;
-    static constexpr size_t SMEM = sizeof(float) * SC_T * (3 * CT + 2 * NP);
+    static constexpr int ROWS = THREADS / (CT / 4) < SC_T ? THREADS / (CT / 4) : SC_T;  // rows walked at once
+    static constexpr int PLANE = SC_T * CT;                                             // values of a tile
+    static constexpr int BC = 2 * SC_T * NP / THREADS;  // values of B and C a thread fetches
 };
 
-// One block: CT channels of one group of one segment.
+// Where a block works: CT channels of one group of one segment.
+struct Where {
+    int b, seg, bs, g, c0, cn, d0, len, tile0, tile1;
+    __device__ __forceinline__ Where(const ScanArgs& a, int CT) {
+        const int ct = blockIdx.x % (a.G * a.ctiles);
+        bs = blockIdx.x / (a.G * a.ctiles);
+        b = bs / a.segs;
+        seg = bs % a.segs;
+        g = ct / a.ctiles;
+        c0 = (ct % a.ctiles) * CT;  // first channel inside the group
+        cn = min(CT, a.Dg - c0);
+        d0 = g * a.Dg + c0;
+        len = scan_len(a, b);
+        tile0 = seg * a.seg_tiles;
+        tile1 = min(tile0 + a.seg_tiles, a.tiles);
+    }
+    // one past the last tile with a row of the sequence
+    __device__ __forceinline__ int live1() const { return max(tile0, min(tile1, (len + SC_T - 1) / SC_T)); }
+};
+
+// A thread's place in the elementwise walk.  Read anew for every tile, so that
+// the addresses made from it are not kept in registers across the recurrence.
+template <int NL> struct Walk {
+    int ec, er;  // four channels from ec, rows er, er + ROWS, ...
+    __device__ __forceinline__ Walk() {
+        int tid = threadIdx.x;
+        asm volatile("" : "+r"(tid));
+        ec = tid % (Tile<NL>::CT / 4) * 4;
+        er = tid / (Tile<NL>::CT / 4);
+    }
+};
+
+// Starts the copy of a tile's rows of one tensor to plane k of the raw buffer.
 template <int NL>
-__global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
-    using S = FwdTile<NL>;
-    extern __shared__ float4 sm4[];
-    float* dl = reinterpret_cast<float*>(sm4);  // [T][CT] step sizes
-    float* du = dl + SC_T * S::CT;              // [T][CT] step * u
-    float* ys = du + SC_T * S::CT;              // [T][CT] C . h
-    float* Bs = ys + SC_T * S::CT;              // [T][NP]
-    float* Cs = Bs + SC_T * S::NP;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ct = blockIdx.x % (a.G * a.ctiles), bs = blockIdx.x / (a.G * a.ctiles);
-    const int b = bs / a.segs, seg = bs % a.segs;
-    const int g = ct / a.ctiles, c0 = (ct % a.ctiles) * S::CT;  // first channel inside the group
-    const int cn = min(S::CT, a.Dg - c0);                       // channels of this block
-    const int d0 = g * a.Dg + c0;
-    const int n = lane % NL, tc = warp * S::WC + (lane / NL) * 4;  // this thread's states and channels
-    const int len = scan_len(a, b);
-    float A2[4][4], h[4][4];
+__device__ __forceinline__ void fetch(const ScanArgs& a, const hc_rows& r, const Where& w, const Walk<NL>& at, int t0,
+                                      int k, char* raw) {
+    using S = Tile<NL>;
+    const int sh = a.dtype == HC_DTYPE_F32 ? 2 : 1;
+    const char* p = static_cast<const char*>(r.p) + ((w.b * r.batch + w.d0 + at.ec) << sh);
+    for (int t = at.er; t < SC_T; t += S::ROWS) {  // none for er >= ROWS = SC_T
+        const bool on = t0 + t < w.len && at.ec < w.cn;
+        char* dst = raw + ((k * S::PLANE + t * S::CT + at.ec) << sh);
+        const char* q = on ? p + (((t0 + t) * r.row) << sh) : p;
+        if (a.vec) {
+            cp_async((unsigned)__cvta_generic_to_shared(dst), q, 4 << sh, on);
+            continue;
+        }
+        for (int i = 0; i < 4; i++) {
+            const bool in = on && at.ec + i < w.cn;
+            if (sh == 2)
+                reinterpret_cast<unsigned*>(dst)[i] = in ? reinterpret_cast<const unsigned*>(q)[i] : 0u;
+            else
+                reinterpret_cast<unsigned short*>(dst)[i] =
+                    in ? reinterpret_cast<const unsigned short*>(q)[i] : (unsigned short)0;
+        }
+    }
+}
+// Four channels of row t of plane k.
+template <int NL>
+__device__ __forceinline__ void get(const ScanArgs& a, const char* raw, int k, int t, int ec, float (&f)[4]) {
+    const int at = k * Tile<NL>::PLANE + t * Tile<NL>::CT + ec;
+    if (a.dtype == HC_DTYPE_F32)
+        load_pack<float, 4>(reinterpret_cast<const float*>(raw) + at, f);
+    else if (a.dtype == HC_DTYPE_BF16)
+        load_pack<__nv_bfloat16, 4>(reinterpret_cast<const __nv_bfloat16*>(raw) + at, f);
+    else
+        load_pack<__half, 4>(reinterpret_cast<const __half*>(raw) + at, f);
+}
+// A tile's B and C, a few values a thread, held as loaded until put_bc.
+template <int NL>
+__device__ __forceinline__ void fetch_bc(const ScanArgs& a, const Where& w, int t0, unsigned (&bc)[Tile<NL>::BC]) {
+    using S = Tile<NL>;
+    const int sh = a.dtype == HC_DTYPE_F32 ? 2 : 1;
+#pragma unroll
+    for (int i = 0; i < S::BC; i++) {
+        const int q = threadIdx.x + i * S::THREADS;
+        const int t = q / S::NP % SC_T, n = q % S::NP;
+        const hc_rows& r = q / (SC_T * S::NP) ? a.Cm : a.Bm;
+        bc[i] = 0;
+        if (t0 + t < w.len && n < a.N) {
+            const char* p = static_cast<const char*>(r.p) + ((w.b * r.batch + (t0 + t) * r.row + w.g * a.N + n) << sh);
+            bc[i] = sh == 2 ? *reinterpret_cast<const unsigned*>(p) : *reinterpret_cast<const unsigned short*>(p);
+        }
+    }
+}
+// To bc2[2][T][NP], each value twice (a pair for the packed multiply-adds).
+template <int NL>
+__device__ __forceinline__ void put_bc(const ScanArgs& a, const unsigned (&bc)[Tile<NL>::BC], f32x2* bc2) {
+#pragma unroll
+    for (int i = 0; i < Tile<NL>::BC; i++) {
+        const float v = a.dtype == HC_DTYPE_F32    ? __uint_as_float(bc[i])
+                        : a.dtype == HC_DTYPE_BF16 ? __uint_as_float(bc[i] << 16)
+                                                   : __half2float(__ushort_as_half((unsigned short)bc[i]));
+        bc2[threadIdx.x + i * Tile<NL>::THREADS] = pk2(v, v);
+    }
+}
+
+__device__ __forceinline__ void ld_pairs(const float* p, f32x2 (&v)[2]) {
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(p);
+    v[0] = q.x;
+    v[1] = q.y;
+}
+__device__ __forceinline__ void ld_dup(const f32x2* p, f32x2 (&v)[4]) {
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(p), r = *reinterpret_cast<const ulonglong2*>(p + 2);
+    v[0] = q.x;
+    v[1] = q.y;
+    v[2] = r.x;
+    v[3] = r.y;
+}
+// The four channels' four states each as channel pairs, from rows of fp32
+// states (`padded`: rows of NP with every state there, else rows of N).
+template <int NL>
+__device__ __forceinline__ void ld_tile(const float* p, long long step, int n, int N, bool padded, int tc, int cn,
+                                        f32x2 (&v)[2][4]) {
+    float f[4][4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) A2[i][j] = h[i][j] = 0.0f;
-        if (tc + i < cn) {
-            ld_states(a.A + (long long)(d0 + tc + i) * a.N, 4 * n, a.N, A2[i]);
-            if (a.segs > 1)
-                load_pack<float, 4>(a.carry + ((long long)bs * a.Dm + d0 + tc + i) * S::NP + 4 * n, h[i]);
-            else if (a.h0)
-                ld_states(a.h0 + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, h[i]);
+        for (int j = 0; j < 4; j++) f[i][j] = 0.0f;
+        if (p && tc + i < cn) {
+            if (padded)
+                load_pack<float, 4>(p + i * step + 4 * n, f[i]);
+            else
+                ld_states(p + i * step, 4 * n, N, f[i]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; j++) A2[i][j] *= kLog2e;
     }
-    const int tile1 = min((seg + 1) * a.seg_tiles, a.tiles);
-    for (int tile = seg * a.seg_tiles; tile < tile1; tile++) {
-        const int t0 = tile * SC_T, rows = min(SC_T, a.L - t0);
-        if (t0 < len) {
-            for (int q = tid; q < SC_T * (S::CT / 4); q += S::THREADS) {
-                const int t = q / (S::CT / 4), c = (q % (S::CT / 4)) * 4;
-                float x[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
-                if (t0 + t < len && c < cn) {
-                    ld4(a.u.p, b * a.u.batch + (t0 + t) * a.u.row + d0, a.dtype, c, cn, a.vec, x);
-                    ld4(a.dt.p, b * a.dt.batch + (t0 + t) * a.dt.row + d0, a.dtype, c, cn, a.vec, s);
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        if (a.bias && c + k < cn) s[k] += a.bias[d0 + c + k];
-                        if (a.softplus) s[k] = softplus_f(s[k]);
-                        x[k] *= s[k];
-                    }
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[i][j] = pk2(f[2 * i][j], f[2 * i + 1][j]);
+}
+template <int NL>
+__device__ __forceinline__ void st_tile(float* p, long long step, int n, int N, bool padded, int tc, int cn,
+                                        const f32x2 (&v)[2][4]) {
+    float f[4][4];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) unpk2(v[i][j], f[2 * i][j], f[2 * i + 1][j]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (tc + i >= cn) continue;
+        if (padded)
+            store_pack<float, 4>(p + i * step + 4 * n, f[i]);
+        else
+            st_states(p + i * step, 4 * n, N, f[i]);
+    }
+}
+template <int NL>
+__device__ __forceinline__ void ld_rates(const ScanArgs& a, int d, int n, int tc, int cn, f32x2 (&A2)[2][4]) {
+    ld_tile<NL>(a.A + (long long)d * a.N, a.N, n, a.N, false, tc, cn, A2);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) A2[i][j] = mul2(A2[i][j], pk2(kLog2e, kLog2e));
+}
+
+// Sums y over a channel group's NL lanes and writes the channels' totals to row[0 .. 4).
+template <int NL> __device__ __forceinline__ void put_lanes_sum(f32x2 a, f32x2 b, int n, float* row) {
+    float y[4];
+    unpk2(a, y[0], y[1]);
+    unpk2(b, y[2], y[3]);
+    const int first = lanes_sum<4, NL>(y, n);
+    constexpr int KEEP = NL >= 4 ? 1 : 4 / NL;
+    if (NL <= 4 || n < 4) {
+#pragma unroll
+        for (int i = 0; i < KEEP; i++) row[first + i] = y[i];
+    }
+}
+// Sums v over a warp's channel groups (lanes n, n + NL, ...) and writes the four states' totals to out[0 .. 4).
+template <int NL> __device__ __forceinline__ void put_groups_sum(const f32x2 (&v)[4], int lane, float* out) {
+    constexpr int CG = 32 / NL;
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        float lo, hi;
+        unpk2(v[j], lo, hi);
+        f[j] = lo + hi;
+    }
+    int at = 0, left = 4;
+#pragma unroll
+    for (int o = NL; o < 32; o <<= 1) {
+        if (left > 1) {
+            const int half = left / 2;
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                if (i < half) {
+                    const float send = up ? f[i] : f[i + half], keep = up ? f[i + half] : f[i];
+                    f[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
                 }
-                store_pack<float, 4>(dl + t * S::CT + c, s);
-                store_pack<float, 4>(du + t * S::CT + c, x);
             }
-            for (int q = tid; q < SC_T * S::NP; q += S::THREADS) {
-                const int t = q / S::NP, k = q % S::NP;
-                const bool on = t0 + t < len && k < a.N;
-                Bs[q] = on ? ld1(a.Bm.p, b * a.Bm.batch + (t0 + t) * a.Bm.row + g * a.N + k, a.dtype) : 0.0f;
-                Cs[q] = on ? ld1(a.Cm.p, b * a.Cm.batch + (t0 + t) * a.Cm.row + g * a.N + k, a.dtype) : 0.0f;
-            }
-            if (a.saved) {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (tc + i < cn)
-                        store_pack<float, 4>(a.saved + (((long long)b * a.tiles + tile) * a.Dm + d0 + tc + i) * S::NP +
-                                                 4 * n,
-                                             h[i]);
-            }
-            __syncthreads();
-#pragma unroll 2
-            for (int t = 0; t < SC_T; t++) {
-                float s[4], x[4], B[4], C[4], y[4];
-                load_pack<float, 4>(dl + t * S::CT + tc, s);
-                load_pack<float, 4>(du + t * S::CT + tc, x);
-                load_pack<float, 4>(Bs + t * S::NP + 4 * n, B);
-                load_pack<float, 4>(Cs + t * S::NP + 4 * n, C);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    y[i] = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        h[i][j] = fmaf(ex2f(s[i] * A2[i][j]), h[i][j], x[i] * B[j]);
-                        y[i] = fmaf(C[j], h[i][j], y[i]);
-                    }
-                }
-                const int first = lanes_sum<4, NL>(y, n);
-                constexpr int KEEP = NL >= 4 ? 1 : 4 / NL;
-                if (NL <= 4 || n < 4) {
-#pragma unroll
-                    for (int i = 0; i < KEEP; i++) ys[t * S::CT + tc + first + i] = y[i];
-                }
-            }
-            __syncthreads();
+            at += up ? half : 0;
+            left = half;
+        } else {
+            f[0] += __shfl_xor_sync(0xffffffffu, f[0], o);
         }
-        for (int q = tid; q < rows * (S::CT / 4); q += S::THREADS) {
-            const int t = q / (S::CT / 4), c = (q % (S::CT / 4)) * 4;
-            if (c >= cn) continue;
-            float o[4] = {0, 0, 0, 0};
-            if (t0 + t < len) {
-                float x[4], zz[4];
-                load_pack<float, 4>(ys + t * S::CT + c, o);
-                if (a.D) {
-                    ld4(a.u.p, b * a.u.batch + (t0 + t) * a.u.row + d0, a.dtype, c, cn, a.vec, x);
+    }
+    constexpr int KEEP = CG >= 4 ? 1 : 4 / CG;
+    if (CG <= 4 || lane / NL < 4) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        if (c + k < cn) o[k] = fmaf(a.D[d0 + c + k], x[k], o[k]);
-                }
-                if (a.z.p) {
-                    ld4(a.z.p, b * a.z.batch + (t0 + t) * a.z.row + d0, a.dtype, c, cn, a.vec, zz);
+        for (int i = 0; i < KEEP; i++) out[at + i] = f[i];
+    }
+}
+
+// dt_bias and D of a block's channels to shared memory: bD[2][CT].
+template <int NL> __device__ __forceinline__ void put_params(const ScanArgs& a, const Where& w, float* bD) {
+    for (int c = threadIdx.x; c < Tile<NL>::CT; c += Tile<NL>::THREADS) {
+        bD[c] = a.bias && c < w.cn ? a.bias[w.d0 + c] : 0.0f;
+        bD[Tile<NL>::CT + c] = a.D && c < w.cn ? a.D[w.d0 + c] : 0.0f;
+    }
+}
+// The step sizes of four channels, from dt + dt_bias.
+__device__ __forceinline__ void steps(const ScanArgs& a, bool on, float (&s)[4]) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++) o[k] *= silu_f(zz[k]);
+    for (int k = 0; k < 4; k++) s[k] = on ? (a.softplus ? softplus_f(s[k]) : s[k]) : 0.0f;
+}
+__device__ __forceinline__ void add4(float (&a)[4], const float* p) {
+    float b[4];
+    load_pack<float, 4>(p, b);
+#pragma unroll
+    for (int k = 0; k < 4; k++) a[k] += b[k];
+}
+
+template <int NL> constexpr size_t fwd_smem() {
+    using S = Tile<NL>;
+    return sizeof(float) * (5 * S::PLANE + 2 * S::CT + 4 * SC_T * S::NP + 3 * S::PLANE);
+}
+template <int NL> __global__ void __launch_bounds__(Tile<NL>::THREADS) scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
+    using S = Tile<NL>;
+    extern __shared__ float4 sm4[];
+    float* dl = reinterpret_cast<float*>(sm4);  // step sizes
+    float* xs = dl + S::PLANE;                  // step * u
+    float* us = xs + S::PLANE;                  // D * u
+    float* gs = us + S::PLANE;                  // silu(z)
+    float* ys = gs + S::PLANE;                  // C . h
+    float* bD = ys + S::PLANE;                             // dt_bias, D
+    f32x2* bc2 = reinterpret_cast<f32x2*>(bD + 2 * S::CT);  // [B, C][T][NP], twice each
+    char* raw = reinterpret_cast<char*>(bc2 + 2 * SC_T * S::NP);
+    const int lane = threadIdx.x & 31, n = lane % NL, tc = (threadIdx.x >> 5) * S::WC + lane / NL * 4;
+    const Where w(a, S::CT);
+    const bool gate = a.z.p != nullptr;
+    f32x2 A2[2][4], h[2][4];
+    ld_rates<NL>(a, w.d0 + tc, n, tc, w.cn, A2);
+    if (a.segs > 1)
+        ld_tile<NL>(a.carry + ((long long)w.bs * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc, w.cn, h);
+    else
+        ld_tile<NL>(a.h0 ? a.h0 + ((long long)w.b * a.Dm + w.d0 + tc) * a.N : nullptr, a.N, n, a.N, false, tc, w.cn, h);
+    put_params<NL>(a, w, bD);
+    unsigned bc[S::BC];
+    const auto start = [&](int t0) {
+        const Walk<NL> at;
+        fetch<NL>(a, a.dt, w, at, t0, 0, raw);
+        fetch<NL>(a, a.u, w, at, t0, 1, raw);
+        if (gate) fetch<NL>(a, a.z, w, at, t0, 2, raw);
+        fetch_bc<NL>(a, w, t0, bc);
+    };
+    const int live1 = w.live1();
+    if (w.tile0 < live1) start(w.tile0 * SC_T);
+    for (int tile = w.tile0; tile < live1; tile++) {
+        const int t0 = tile * SC_T;
+        cp_async_wait();
+        __syncthreads();
+        for (Walk<NL> at; at.er < SC_T; at.er += S::ROWS) {
+            const int t = at.er, q = t * S::CT + at.ec;
+            float s[4], x[4], D[4];
+            get<NL>(a, raw, 0, t, at.ec, s);
+            get<NL>(a, raw, 1, t, at.ec, x);
+            load_pack<float, 4>(bD + S::CT + at.ec, D);
+            add4(s, bD + at.ec);
+            steps(a, t0 + t < w.len, s);
+            store_pack<float, 4>(dl + q, s);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                D[k] *= x[k];
+                x[k] *= s[k];
+            }
+            store_pack<float, 4>(xs + q, x);
+            store_pack<float, 4>(us + q, D);
+            if (gate) {
+                get<NL>(a, raw, 2, t, at.ec, s);
+#pragma unroll
+                for (int k = 0; k < 4; k++) s[k] = silu_f(s[k]);
+                store_pack<float, 4>(gs + q, s);
+            }
+        }
+        put_bc<NL>(a, bc, bc2);
+        __syncthreads();
+        if (tile + 1 < live1) start(t0 + SC_T);
+        if (a.saved)
+            st_tile<NL>(a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc,
+                        w.cn, h);
+#pragma unroll 4
+        for (int t = 0; t < SC_T; t++) {
+            f32x2 s[2], x[2], B[4], C[4], y[2];
+            ld_pairs(dl + t * S::CT + tc, s);
+            ld_pairs(xs + t * S::CT + tc, x);
+            ld_dup(bc2 + t * S::NP + 4 * n, B);
+            ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    h[i][j] = fma2(ex2x2(mul2(s[i], A2[i][j])), h[i][j], mul2(x[i], B[j]));
+                    y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
                 }
             }
-            st4(a.y.p, b * a.y.batch + (t0 + t) * a.y.row + d0, a.dtype, c, cn, a.vec, o);
+            put_lanes_sum<NL>(y[0], y[1], n, ys + t * S::CT + tc);
         }
         __syncthreads();
-    }
-    if (a.hT && seg == a.segs - 1) {
+        const int rows = min(SC_T, a.L - t0);
+        for (Walk<NL> at; at.er < rows; at.er += S::ROWS) {
+            const int t = at.er, q = t * S::CT + at.ec;
+            float o[4], z[4];
+            load_pack<float, 4>(ys + q, o);
+            add4(o, us + q);
+            if (gate) {
+                load_pack<float, 4>(gs + q, z);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (tc + i < cn) st_states(a.hT + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, h[i]);
+                for (int k = 0; k < 4; k++) o[k] *= z[k];
+            }
+            if (t0 + t >= w.len) o[0] = o[1] = o[2] = o[3] = 0.0f;
+            st4(a.y.p, w.b * a.y.batch + (t0 + t) * a.y.row + w.d0, a.dtype, at.ec, w.cn, a.vec, o);
+        }
     }
+    // rows past the sequence's last tile
+    const int end = min(w.tile1 * SC_T, a.L);
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const Walk<NL> at;
+    for (int t = live1 * SC_T + at.er; t < end && at.er < S::ROWS; t += S::ROWS)
+        st4(a.y.p, w.b * a.y.batch + t * a.y.row + w.d0, a.dtype, at.ec, w.cn, a.vec, zero);
+    if (a.hT && w.seg == a.segs - 1)
+        st_tile<NL>(a.hT + ((long long)w.b * a.Dm + w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, h);
 }
 
 // A segment's state from a zero state.  REV false: the state itself, over
 // x = step * u and B, rows upwards.  REV true: the state's gradient, over
 // q = gy * silu(z) and C, rows downwards: G_{t-1} = exp(step_t A) (G_t + q_t C_t).
+template <int NL> constexpr size_t carry_smem() {
+    using S = Tile<NL>;
+    return sizeof(float) * (2 * S::PLANE + 2 * S::CT + 4 * SC_T * S::NP + 3 * S::PLANE);
+}
 template <int NL, bool REV>
-__global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_carry_kernel(const __grid_constant__ ScanArgs a) {
-    using S = FwdTile<NL>;
+__global__ void __launch_bounds__(Tile<NL>::THREADS) scan_carry_kernel(const __grid_constant__ ScanArgs a) {
+    using S = Tile<NL>;
     extern __shared__ float4 sm4[];
-    float* dl = reinterpret_cast<float*>(sm4);  // [T][CT] step sizes
-    float* xs = dl + SC_T * S::CT;              // [T][CT] step * u, or q
-    float* Bs = xs + SC_T * S::CT;              // [T][NP]
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ct = blockIdx.x % (a.G * a.ctiles), bs = blockIdx.x / (a.G * a.ctiles);
-    const int b = bs / a.segs, seg = bs % a.segs;
-    const int g = ct / a.ctiles, c0 = (ct % a.ctiles) * S::CT;
-    const int cn = min(S::CT, a.Dg - c0);
-    const int d0 = g * a.Dg + c0;
-    const int n = lane % NL, tc = warp * S::WC + (lane / NL) * 4;
-    const int len = scan_len(a, b);
-    float A2[4][4], h[4][4], sum[4];
+    float* dl = reinterpret_cast<float*>(sm4);
+    float* xs = dl + S::PLANE;
+    float* bD = xs + S::PLANE;
+    f32x2* bc2 = reinterpret_cast<f32x2*>(bD + 2 * S::CT);
+    char* raw = reinterpret_cast<char*>(bc2 + 2 * SC_T * S::NP);
+    const int lane = threadIdx.x & 31, n = lane % NL, tc = (threadIdx.x >> 5) * S::WC + lane / NL * 4;
+    const Where w(a, S::CT);
+    f32x2 A2[2][4], h[2][4], sum[2];
+    ld_rates<NL>(a, w.d0 + tc, n, tc, w.cn, A2);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        sum[i] = 0.0f;
+    for (int i = 0; i < 2; i++) {
+        sum[i] = pk2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < 4; j++) A2[i][j] = h[i][j] = 0.0f;
-        if (tc + i < cn) ld_states(a.A + (long long)(d0 + tc + i) * a.N, 4 * n, a.N, A2[i]);
-#pragma unroll
-        for (int j = 0; j < 4; j++) A2[i][j] *= kLog2e;
+        for (int j = 0; j < 4; j++) h[i][j] = sum[i];
     }
-    const int tile0 = seg * a.seg_tiles, tile1 = min(tile0 + a.seg_tiles, a.tiles);
-    for (int k = tile0; k < tile1; k++) {
-        const int t0 = (REV ? tile1 - 1 - (k - tile0) : k) * SC_T;
-        if (t0 >= len) continue;
-        for (int q = tid; q < SC_T * (S::CT / 4); q += S::THREADS) {
-            const int t = q / (S::CT / 4), c = (q % (S::CT / 4)) * 4;
-            float x[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
-            if (t0 + t < len && c < cn) {
-                const hc_rows& in = REV ? a.gy : a.u;
-                ld4(in.p, b * in.batch + (t0 + t) * in.row + d0, a.dtype, c, cn, a.vec, x);
-                ld4(a.dt.p, b * a.dt.batch + (t0 + t) * a.dt.row + d0, a.dtype, c, cn, a.vec, s);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (a.bias && c + i < cn) s[i] += a.bias[d0 + c + i];
-                    if (a.softplus) s[i] = softplus_f(s[i]);
-                    if (!REV) x[i] *= s[i];
-                }
-                if (REV && a.z.p) {
-                    float zz[4];
-                    ld4(a.z.p, b * a.z.batch + (t0 + t) * a.z.row + d0, a.dtype, c, cn, a.vec, zz);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) x[i] *= silu_f(zz[i]);
-                }
-            }
-            store_pack<float, 4>(dl + t * S::CT + c, s);
-            store_pack<float, 4>(xs + t * S::CT + c, x);
-        }
-        for (int q = tid; q < SC_T * S::NP; q += S::THREADS) {
-            const int t = q / S::NP, j = q % S::NP;
-            const hc_rows& in = REV ? a.Cm : a.Bm;
-            Bs[q] = t0 + t < len && j < a.N ? ld1(in.p, b * in.batch + (t0 + t) * in.row + g * a.N + j, a.dtype) : 0.0f;
-        }
+    put_params<NL>(a, w, bD);
+    unsigned bc[S::BC];
+    const bool gate = REV && a.z.p;
+    const auto start = [&](int t0) {
+        const Walk<NL> at;
+        fetch<NL>(a, a.dt, w, at, t0, 0, raw);
+        fetch<NL>(a, REV ? a.gy : a.u, w, at, t0, 1, raw);
+        if (gate) fetch<NL>(a, a.z, w, at, t0, 2, raw);
+        fetch_bc<NL>(a, w, t0, bc);
+    };
+    const int tiles = w.live1() - w.tile0;
+    const int first = REV ? w.tile0 + tiles - 1 : w.tile0, dir = REV ? -1 : 1;
+    if (tiles > 0) start(first * SC_T);
+    for (int k = 0; k < tiles; k++) {
+        const int t0 = (first + dir * k) * SC_T;
+        cp_async_wait();
         __syncthreads();
+        for (Walk<NL> at; at.er < SC_T; at.er += S::ROWS) {
+            const int t = at.er, q = t * S::CT + at.ec;
+            float s[4], x[4], z[4];
+            get<NL>(a, raw, 0, t, at.ec, s);
+            get<NL>(a, raw, 1, t, at.ec, x);
+            add4(s, bD + at.ec);
+            steps(a, t0 + t < w.len, s);
+            if (!REV) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) x[i] *= s[i];
+            } else if (gate) {
+                get<NL>(a, raw, 2, t, at.ec, z);
+#pragma unroll
+                for (int i = 0; i < 4; i++) x[i] *= silu_f(z[i]);
+            }
+            store_pack<float, 4>(dl + q, s);
+            store_pack<float, 4>(xs + q, x);
+        }
+        put_bc<NL>(a, bc, bc2);
+        __syncthreads();
+        if (k + 1 < tiles) start(t0 + dir * SC_T);
 #pragma unroll 4
         for (int v = 0; v < SC_T; v++) {
             const int t = REV ? SC_T - 1 - v : v;
-            float s[4], x[4], B[4];
-            load_pack<float, 4>(dl + t * S::CT + tc, s);
-            load_pack<float, 4>(xs + t * S::CT + tc, x);
-            load_pack<float, 4>(Bs + t * S::NP + 4 * n, B);
+            f32x2 s[2], x[2], B[4];
+            ld_pairs(dl + t * S::CT + tc, s);
+            ld_pairs(xs + t * S::CT + tc, x);
+            ld_dup(bc2 + ((REV ? SC_T : 0) + t) * S::NP + 4 * n, B);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                sum[i] += s[i];
+            for (int i = 0; i < 2; i++) {
+                sum[i] = add2(sum[i], s[i]);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const float e = ex2f(s[i] * A2[i][j]);
-                    h[i][j] = REV ? e * fmaf(x[i], B[j], h[i][j]) : fmaf(e, h[i][j], x[i] * B[j]);
+                    const f32x2 e = ex2x2(mul2(s[i], A2[i][j]));
+                    h[i][j] = REV ? mul2(e, fma2(x[i], B[j], h[i][j])) : fma2(e, h[i][j], mul2(x[i], B[j]));
                 }
             }
         }
         __syncthreads();
     }
+    const long long d = (long long)w.bs * a.Dm + w.d0 + tc;
+    st_tile<NL>(a.carry + d * S::NP, S::NP, n, a.N, true, tc, w.cn, h);
+    if (n == 0) {
+        float t[4];
+        unpk2(sum[0], t[0], t[1]);
+        unpk2(sum[1], t[2], t[3]);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        if (tc + i >= cn) continue;
-        const long long d = (long long)bs * a.Dm + d0 + tc + i;
-        store_pack<float, 4>(a.carry + d * S::NP + 4 * n, h[i]);
-        if (n == 0) a.dsum[d] = sum[i];
+        for (int i = 0; i < 4; i++)
+            if (tc + i < w.cn) a.dsum[d + i] = t[i];
     }
 }
 
@@ -404,280 +648,226 @@ __global__ void __launch_bounds__(1024) scan_join_kernel(const __grid_constant__
     }
 }
 
-template <int NL> struct BwdTile {
-    static constexpr int NP = 4 * NL, CG = 32 / NL;
-    static constexpr int W = 4;
-    static constexpr int WC = 2 * CG;  // channels a warp, two a thread
-    static constexpr int CT = W * WC;
-    static constexpr int THREADS = W * 32;
-    // tile rows the elementwise parts cover at once
-    static constexpr int RROWS = THREADS / (CT / 4) < SC_T ? THREADS / (CT / 4) : SC_T;
-    // step, u, q, C . h, G . B, E . A; B, C; the warps' gB and gC
-    static constexpr size_t SMEM = sizeof(float) * SC_T * (6 * CT + 2 * NP + 2 * NP * W);
-};
-
-// One block: CT channels of one group of one segment, its tiles from the last
-// to the first.  A tile's states are recomputed from its saved first state and
-// kept in registers, then the state's gradient runs back through them.
+// A block's tiles from the last to the first.  A tile's states are recomputed
+// from its saved first state and kept in registers (H), with y and gC on the
+// way, then the state's gradient runs back through them.
+template <int NL> constexpr size_t bwd_smem() {
+    using S = Tile<NL>;
+    return sizeof(float) * (9 * S::PLANE + 2 * S::CT + 2 * S::ROWS * S::CT + 4 * SC_T * S::NP + S::W * SC_T * 2 * S::NP +
+                            4 * S::PLANE);
+}
 template <int NL>
-__global__ void __launch_bounds__(BwdTile<NL>::THREADS) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
-    using S = BwdTile<NL>;
+__global__ void __launch_bounds__(Tile<NL>::THREADS) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
+    using S = Tile<NL>;
     extern __shared__ float4 sm4[];
-    float* dl = reinterpret_cast<float*>(sm4);
-    float* us = dl + SC_T * S::CT;
-    float* qs = us + SC_T * S::CT;
-    float* ys = qs + SC_T * S::CT;
-    float* GBs = ys + SC_T * S::CT;
-    float* EAs = GBs + SC_T * S::CT;
-    float* Bs = EAs + SC_T * S::CT;
-    float* Cs = Bs + SC_T * S::NP;
-    float* red = Cs + SC_T * S::NP;  // [W][T][2][NP]
+    float* dl = reinterpret_cast<float*>(sm4);  // step sizes
+    float* us = dl + S::PLANE;                  // u
+    float* xs = us + S::PLANE;                  // step * u
+    float* qs = xs + S::PLANE;                  // gy * silu(z)
+    float* ps = qs + S::PLANE;                  // slope of the step size
+    float* ws = ps + S::PLANE;                  // gy * silu'(z)
+    float* ys = ws + S::PLANE;                  // C . h
+    float* GB = ys + S::PLANE;                  // G . B
+    float* EA = GB + S::PLANE;                  // E . A / ln 2
+    float* bD = EA + S::PLANE;                  // dt_bias, D
+    float* sums = bD + 2 * S::CT;               // [ROWS][2][CT], each thread's gD and gdt_bias
+    f32x2* bc2 = reinterpret_cast<f32x2*>(sums + 2 * S::ROWS * S::CT);
+    float* red = reinterpret_cast<float*>(bc2 + 2 * SC_T * S::NP);  // [W][T][2][NP], the warps' gB and gC
+    char* raw = reinterpret_cast<char*>(red + S::W * SC_T * 2 * S::NP);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ct = blockIdx.x % (a.G * a.ctiles), bs = blockIdx.x / (a.G * a.ctiles);
-    const int b = bs / a.segs, seg = bs % a.segs;
-    const int g = ct / a.ctiles, c0 = (ct % a.ctiles) * S::CT;
-    const int cn = min(S::CT, a.Dg - c0);
-    const int d0 = g * a.Dg + c0;
-    const int n = lane % NL, cg = lane / NL, tc = warp * S::WC + cg * 2;
-    const int len = scan_len(a, b);
-    float A2[2][4], G[2][4], gA[2][4];
+    const int n = lane % NL, tc = warp * S::WC + lane / NL * 4;
+    const Where w(a, S::CT);
+    const bool gate = a.z.p != nullptr;
+    f32x2 A2[2][4], G[2][4], gA[2][4];
+    ld_rates<NL>(a, w.d0 + tc, n, tc, w.cn, A2);
+    if (a.segs > 1)
+        ld_tile<NL>(a.carry + ((long long)w.bs * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc, w.cn, G);
+    else
+        ld_tile<NL>(a.ghT ? a.ghT + ((long long)w.b * a.Dm + w.d0 + tc) * a.N : nullptr, a.N, n, a.N, false, tc, w.cn,
+                    G);
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) A2[i][j] = G[i][j] = gA[i][j] = 0.0f;
-        if (tc + i < cn) {
-            ld_states(a.A + (long long)(d0 + tc + i) * a.N, 4 * n, a.N, A2[i]);
-            if (a.segs > 1)
-                load_pack<float, 4>(a.carry + ((long long)bs * a.Dm + d0 + tc + i) * S::NP + 4 * n, G[i]);
-            else if (a.ghT)
-                ld_states(a.ghT + ((long long)b * a.Dm + d0 + tc + i) * a.N, 4 * n, a.N, G[i]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; j++) A2[i][j] *= kLog2e;
-    }
-    // the elementwise parts: four fixed channels a thread
-    const int ec = (tid % (S::CT / 4)) * 4, er = tid / (S::CT / 4);
-    float Dv[4], bv[4], sD[4], sb[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        Dv[k] = a.D && ec + k < cn ? a.D[d0 + ec + k] : 0.0f;
-        bv[k] = a.bias && ec + k < cn ? a.bias[d0 + ec + k] : 0.0f;
-        sD[k] = sb[k] = 0.0f;
-    }
-    for (int tile = min((seg + 1) * a.seg_tiles, a.tiles) - 1; tile >= seg * a.seg_tiles; tile--) {
+        for (int j = 0; j < 4; j++) gA[i][j] = pk2(0.0f, 0.0f);
+    put_params<NL>(a, w, bD);
+    for (int q = tid; q < 2 * S::ROWS * S::CT; q += S::THREADS) sums[q] = 0.0f;
+    unsigned bc[S::BC];
+    const auto start = [&](int t0) {
+        const Walk<NL> at;
+        fetch<NL>(a, a.dt, w, at, t0, 0, raw);
+        fetch<NL>(a, a.u, w, at, t0, 1, raw);
+        fetch<NL>(a, a.gy, w, at, t0, 2, raw);
+        if (gate) fetch<NL>(a, a.z, w, at, t0, 3, raw);
+        fetch_bc<NL>(a, w, t0, bc);
+    };
+    const int live1 = w.live1();
+    __syncthreads();
+    if (w.tile0 < live1) start((live1 - 1) * SC_T);
+    for (int tile = w.tile1 - 1; tile >= w.tile0; tile--) {
         const int t0 = tile * SC_T, rows = min(SC_T, a.L - t0);
-        const bool live = t0 < len;
+        const bool live = tile < live1;
         if (live) {
-            for (int t = er; t < SC_T; t += S::RROWS) {  // none for er >= RROWS = SC_T
-                float x[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
-                if (t0 + t < len && ec < cn) {
-                    ld4(a.u.p, b * a.u.batch + (t0 + t) * a.u.row + d0, a.dtype, ec, cn, a.vec, x);
-                    ld4(a.dt.p, b * a.dt.batch + (t0 + t) * a.dt.row + d0, a.dtype, ec, cn, a.vec, s);
-                    ld4(a.gy.p, b * a.gy.batch + (t0 + t) * a.gy.row + d0, a.dtype, ec, cn, a.vec, q);
+            cp_async_wait();
+            __syncthreads();
+            for (Walk<NL> at; at.er < SC_T; at.er += S::ROWS) {
+                const int t = at.er, c = t * S::CT + at.ec;
+                float s[4], u[4], q[4], p[4];
+                get<NL>(a, raw, 0, t, at.ec, s);
+                get<NL>(a, raw, 1, t, at.ec, u);
+                get<NL>(a, raw, 2, t, at.ec, q);
+                add4(s, bD + at.ec);
+#pragma unroll
+                for (int k = 0; k < 4; k++) p[k] = a.softplus ? sigmoid_f(s[k]) : 1.0f;
+                steps(a, t0 + t < w.len, s);
+                store_pack<float, 4>(dl + c, s);
+                store_pack<float, 4>(us + c, u);
+                store_pack<float, 4>(ps + c, p);
+#pragma unroll
+                for (int k = 0; k < 4; k++) u[k] *= s[k];
+                store_pack<float, 4>(xs + c, u);
+                if (gate) {
+                    get<NL>(a, raw, 3, t, at.ec, u);
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        s[k] += bv[k];
-                        if (a.softplus) s[k] = softplus_f(s[k]);
+                        const float r = sigmoid_f(u[k]);
+                        p[k] = q[k] * r * fmaf(u[k], 1.0f - r, 1.0f);
+                        q[k] *= u[k] * r;
                     }
-                    if (a.z.p) {
-                        float zz[4];
-                        ld4(a.z.p, b * a.z.batch + (t0 + t) * a.z.row + d0, a.dtype, ec, cn, a.vec, zz);
-#pragma unroll
-                        for (int k = 0; k < 4; k++) q[k] *= silu_f(zz[k]);
-                    }
+                    store_pack<float, 4>(ws + c, p);
                 }
-                store_pack<float, 4>(dl + t * S::CT + ec, s);
-                store_pack<float, 4>(us + t * S::CT + ec, x);
-                store_pack<float, 4>(qs + t * S::CT + ec, q);
+                store_pack<float, 4>(qs + c, q);
             }
-            for (int q = tid; q < SC_T * S::NP; q += S::THREADS) {
-                const int t = q / S::NP, k = q % S::NP;
-                const bool on = t0 + t < len && k < a.N;
-                Bs[q] = on ? ld1(a.Bm.p, b * a.Bm.batch + (t0 + t) * a.Bm.row + g * a.N + k, a.dtype) : 0.0f;
-                Cs[q] = on ? ld1(a.Cm.p, b * a.Cm.batch + (t0 + t) * a.Cm.row + g * a.N + k, a.dtype) : 0.0f;
-            }
-            // H[t] is the state before the tile's row t
-            float H[SC_T + 1][2][4];
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-#pragma unroll
-                for (int j = 0; j < 4; j++) H[0][i][j] = 0.0f;
-                if (tc + i < cn)
-                    load_pack<float, 4>(
-                        a.saved + (((long long)b * a.tiles + tile) * a.Dm + d0 + tc + i) * S::NP + 4 * n, H[0][i]);
-            }
+            put_bc<NL>(a, bc, bc2);
             __syncthreads();
+            if (tile > w.tile0) start(t0 - SC_T);
+            const float* first =
+                a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP;
+            // H[t] is the state before row t (H[0] is read again where it is needed again)
+            f32x2 H[SC_T][2][4], h[2][4];
+            ld_tile<NL>(first, S::NP, n, a.N, true, tc, w.cn, h);
 #pragma unroll
             for (int t = 0; t < SC_T; t++) {
-                float B[4], C[4], y[2];
-                const float2 s = *reinterpret_cast<const float2*>(dl + t * S::CT + tc);
-                const float2 x = *reinterpret_cast<const float2*>(us + t * S::CT + tc);
-                const float sv[2] = {s.x, s.y}, xv[2] = {s.x * x.x, s.y * x.y};
-                load_pack<float, 4>(Bs + t * S::NP + 4 * n, B);
-                load_pack<float, 4>(Cs + t * S::NP + 4 * n, C);
+                f32x2 s[2], x[2], q[2], B[4], C[4], y[2], gc[4];
+                ld_pairs(dl + t * S::CT + tc, s);
+                ld_pairs(xs + t * S::CT + tc, x);
+                ld_pairs(qs + t * S::CT + tc, q);
+                ld_dup(bc2 + t * S::NP + 4 * n, B);
+                ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    y[i] = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        H[t + 1][i][j] = fmaf(ex2f(sv[i] * A2[i][j]), H[t][i][j], xv[i] * B[j]);
-                        y[i] = fmaf(C[j], H[t + 1][i][j], y[i]);
+                        if (t) H[t][i][j] = h[i][j];
+                        h[i][j] = fma2(ex2x2(mul2(s[i], A2[i][j])), h[i][j], mul2(x[i], B[j]));
+                        y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
+                        gc[j] = i ? fma2(q[i], h[i][j], gc[j]) : mul2(q[i], h[i][j]);
                     }
                 }
-                if (a.z.p) {
-                    const int first = lanes_sum<2, NL>(y, n);
-                    if (NL <= 2 || n < 2) {
-                        ys[t * S::CT + tc + first] = y[0];
-                        if (NL == 1) ys[t * S::CT + tc + 1] = y[1];
-                    }
-                }
+                if (gate) put_lanes_sum<NL>(y[0], y[1], n, ys + t * S::CT + tc);
+                put_groups_sum<NL>(gc, lane, red + ((warp * SC_T + t) * 2 + 1) * S::NP + 4 * n);
             }
-            // gA summed tile by tile: a running sum over all rows would lose an ulp a row
-            float ga_tile[2][4] = {};
+            // nothing of the way up is kept for the way down but H: the exponentials are taken again
+            asm volatile("" ::: "memory");
+            // gA summed tile by tile: one running sum over all rows would lose more
+            f32x2 ga[2][4];
 #pragma unroll
             for (int t = SC_T - 1; t >= 0; t--) {
-                float B[4], C[4], bc[8], gb[2] = {0, 0}, ea[2] = {0, 0};
-                const float2 s = *reinterpret_cast<const float2*>(dl + t * S::CT + tc);
-                const float2 x = *reinterpret_cast<const float2*>(us + t * S::CT + tc);
-                const float2 q = *reinterpret_cast<const float2*>(qs + t * S::CT + tc);
-                const float sv[2] = {s.x, s.y}, xv[2] = {s.x * x.x, s.y * x.y}, qv[2] = {q.x, q.y};
-                load_pack<float, 4>(Bs + t * S::NP + 4 * n, B);
-                load_pack<float, 4>(Cs + t * S::NP + 4 * n, C);
-#pragma unroll
-                for (int j = 0; j < 8; j++) bc[j] = 0.0f;
+                f32x2 s[2], x[2], q[2], B[4], C[4], gb[2], ea[2], gB[4];
+                ld_pairs(dl + t * S::CT + tc, s);
+                ld_pairs(xs + t * S::CT + tc, x);
+                ld_pairs(qs + t * S::CT + tc, q);
+                ld_dup(bc2 + t * S::NP + 4 * n, B);
+                ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
+                if (t == 0) ld_tile<NL>(first, S::NP, n, a.N, true, tc, w.cn, H[0]);
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const float gg = fmaf(qv[i], C[j], G[i][j]);
-                        bc[j] = fmaf(gg, xv[i], bc[j]);
-                        bc[4 + j] = fmaf(qv[i], H[t + 1][i][j], bc[4 + j]);
-                        gb[i] = fmaf(gg, B[j], gb[i]);
-                        const float ga = gg * ex2f(sv[i] * A2[i][j]);
-                        const float E = ga * H[t][i][j];
-                        ea[i] = fmaf(E, A2[i][j], ea[i]);
-                        ga_tile[i][j] = fmaf(E, sv[i], ga_tile[i][j]);
-                        G[i][j] = ga;
+                        const f32x2 g = fma2(q[i], C[j], G[i][j]);
+                        gB[j] = i ? fma2(g, x[i], gB[j]) : mul2(g, x[i]);
+                        gb[i] = j ? fma2(g, B[j], gb[i]) : mul2(g, B[j]);
+                        G[i][j] = mul2(g, ex2x2(mul2(s[i], A2[i][j])));
+                        const f32x2 E = mul2(G[i][j], H[t][i][j]);
+                        ea[i] = j ? fma2(E, A2[i][j], ea[i]) : mul2(E, A2[i][j]);
+                        ga[i][j] = t == SC_T - 1 ? mul2(E, s[i]) : fma2(E, s[i], ga[i][j]);
                     }
                 }
-                const int first = lanes_sum<2, NL>(gb, n);
-                lanes_sum<2, NL>(ea, n);
-                if (NL <= 2 || n < 2) {
-                    GBs[t * S::CT + tc + first] = gb[0];
-                    EAs[t * S::CT + tc + first] = ea[0] * kLn2;
-                    if (NL == 1) {
-                        GBs[t * S::CT + tc + 1] = gb[1];
-                        EAs[t * S::CT + tc + 1] = ea[1] * kLn2;
-                    }
-                }
-                // over the channels: lanes n, n + NL, ... of the warp
-                int at = 0, left = 8;
-#pragma unroll
-                for (int o = NL; o < 32; o <<= 1) {
-                    if (left > 1) {
-                        const int half = left / 2;
-                        const bool up = (lane & o) != 0;
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            if (i < half) {
-                                const float send = up ? bc[i] : bc[i + half], keep = up ? bc[i + half] : bc[i];
-                                bc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                            }
-                        }
-                        at += up ? half : 0;
-                        left = half;
-                    } else {
-                        bc[0] += __shfl_xor_sync(0xffffffffu, bc[0], o);
-                    }
-                }
-                constexpr int KEEP = S::CG >= 8 ? 1 : 8 / S::CG;
-                if (S::CG <= 8 || cg < 8) {
-                    float* r = red + (warp * SC_T + t) * 2 * S::NP + (at / 4) * S::NP + 4 * n + at % 4;
-#pragma unroll
-                    for (int i = 0; i < KEEP; i++) r[i] = bc[i];
-                }
+                put_lanes_sum<NL>(gb[0], gb[1], n, GB + t * S::CT + tc);
+                put_lanes_sum<NL>(ea[0], ea[1], n, EA + t * S::CT + tc);
+                put_groups_sum<NL>(gB, lane, red + (warp * SC_T + t) * 2 * S::NP + 4 * n);
             }
 #pragma unroll
             for (int i = 0; i < 2; i++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) gA[i][j] += ga_tile[i][j];
+                for (int j = 0; j < 4; j++) gA[i][j] = add2(gA[i][j], ga[i][j]);
             __syncthreads();
         }
-        for (int t = er; t < rows; t += S::RROWS) {
-            if (ec >= cn) continue;
+        for (Walk<NL> at; at.er < rows; at.er += S::ROWS) {
+            const int t = at.er, c = t * S::CT + at.ec;
             float gu[4] = {0, 0, 0, 0}, gd[4] = {0, 0, 0, 0}, gz[4] = {0, 0, 0, 0};
-            if (t0 + t < len) {
-                float GB[4], EA[4], x[4], s[4], q[4];
-                load_pack<float, 4>(GBs + t * S::CT + ec, GB);
-                load_pack<float, 4>(EAs + t * S::CT + ec, EA);
-                load_pack<float, 4>(us + t * S::CT + ec, x);
-                load_pack<float, 4>(dl + t * S::CT + ec, s);
-                load_pack<float, 4>(qs + t * S::CT + ec, q);
-                float raw[4];
-                ld4(a.dt.p, b * a.dt.batch + (t0 + t) * a.dt.row + d0, a.dtype, ec, cn, a.vec, raw);
+            if (t0 + t < w.len) {
+                float b[4], e[4], u[4], q[4], D[4], v[4];
+                float* sum = sums + (t % S::ROWS) * 2 * S::CT + at.ec;
+                load_pack<float, 4>(GB + c, b);
+                load_pack<float, 4>(us + c, u);
+                load_pack<float, 4>(qs + c, q);
+                load_pack<float, 4>(bD + S::CT + at.ec, D);
+                load_pack<float, 4>(dl + c, v);
+#pragma unroll
+                for (int k = 0; k < 4; k++) gu[k] = fmaf(b[k], v[k], D[k] * q[k]);
+                load_pack<float, 4>(EA + c, e);
+                load_pack<float, 4>(ps + c, v);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    gu[k] = fmaf(GB[k], s[k], Dv[k] * q[k]);
-                    gd[k] = fmaf(GB[k], x[k], EA[k]);
-                    if (a.softplus) gd[k] *= sigmoid_f(raw[k] + bv[k]);
-                    sb[k] += gd[k];
-                    sD[k] = fmaf(q[k], x[k], sD[k]);
+                    gd[k] = fmaf(b[k], u[k], e[k] * kLn2) * v[k];
+                    b[k] = gd[k];
+                    q[k] *= u[k];
                 }
-                if (a.gz.p) {
-                    float zz[4], w[4], y[4];
-                    ld4(a.z.p, b * a.z.batch + (t0 + t) * a.z.row + d0, a.dtype, ec, cn, a.vec, zz);
-                    ld4(a.gy.p, b * a.gy.batch + (t0 + t) * a.gy.row + d0, a.dtype, ec, cn, a.vec, w);
-                    load_pack<float, 4>(ys + t * S::CT + ec, y);
+                add4(q, sum);
+                store_pack<float, 4>(sum, q);
+                add4(b, sum + S::CT);
+                store_pack<float, 4>(sum + S::CT, b);
+                if (gate) {
+                    load_pack<float, 4>(ys + c, e);
+                    load_pack<float, 4>(ws + c, v);
 #pragma unroll
-                    for (int k = 0; k < 4; k++) gz[k] = w[k] * fmaf(Dv[k], x[k], y[k]) * silu_d(zz[k]);
+                    for (int k = 0; k < 4; k++) gz[k] = v[k] * fmaf(D[k], u[k], e[k]);
                 }
             }
-            st4(a.gu.p, b * a.gu.batch + (t0 + t) * a.gu.row + d0, a.dtype, ec, cn, a.vec, gu);
-            st4(a.gdt.p, b * a.gdt.batch + (t0 + t) * a.gdt.row + d0, a.dtype, ec, cn, a.vec, gd);
-            if (a.gz.p) st4(a.gz.p, b * a.gz.batch + (t0 + t) * a.gz.row + d0, a.dtype, ec, cn, a.vec, gz);
+            st4(a.gu.p, w.b * a.gu.batch + (t0 + t) * a.gu.row + w.d0, a.dtype, at.ec, w.cn, a.vec, gu);
+            st4(a.gdt.p, w.b * a.gdt.batch + (t0 + t) * a.gdt.row + w.d0, a.dtype, at.ec, w.cn, a.vec, gd);
+            if (gate) st4(a.gz.p, w.b * a.gz.batch + (t0 + t) * a.gz.row + w.d0, a.dtype, at.ec, w.cn, a.vec, gz);
         }
         for (int q = tid; q < rows * 2 * S::NP; q += S::THREADS) {
-            const int t = q / (2 * S::NP), w = (q / S::NP) & 1, k = q % S::NP;
+            const int t = q / (2 * S::NP), c = (q / S::NP) & 1, k = q % S::NP;
             if (k >= a.N) continue;
             float v = 0.0f;
-            if (t0 + t < len) {
+            if (t0 + t < w.len) {
 #pragma unroll
-                for (int m = 0; m < S::W; m++) v += red[(m * SC_T + t) * 2 * S::NP + w * S::NP + k];
+                for (int m = 0; m < S::W; m++) v += red[(m * SC_T + t) * 2 * S::NP + c * S::NP + k];
             }
             if (a.gbc) {
-                a.gbc[((((long long)(ct % a.ctiles) * a.B + b) * a.L + t0 + t) * a.G + g) * 2 * a.N + w * a.N + k] = v;
+                a.gbc[((((long long)(w.c0 / S::CT) * a.B + w.b) * a.L + t0 + t) * a.G + w.g) * 2 * a.N + c * a.N + k] = v;
             } else {
-                const hc_rows& o = w ? a.gC : a.gB;
-                st1(o.p, b * o.batch + (t0 + t) * o.row + g * a.N + k, a.dtype, v);
+                const hc_rows& o = c ? a.gC : a.gB;
+                st1(o.p, w.b * o.batch + (t0 + t) * o.row + w.g * a.N + k, a.dtype, v);
             }
         }
-        __syncthreads();
     }
-    float* pb = a.part + (long long)bs * (a.N + 2) * a.Dm;
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        if (tc + i < cn) {
-            const long long d = d0 + tc + i;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (4 * n + j < a.N) pb[d * a.N + 4 * n + j] = gA[i][j];
-            if (a.gh0 && seg == 0) st_states(a.gh0 + ((long long)b * a.Dm + d) * a.N, 4 * n, a.N, G[i]);
-        }
-    }
-    // gD and gdt_bias over the epilogue's row lanes, in order
-    if (er < S::RROWS) {
-        store_pack<float, 4>(dl + er * S::CT + ec, sD);
-        store_pack<float, 4>(us + er * S::CT + ec, sb);
-    }
+    float* pb = a.part + (long long)w.bs * (a.N + 2) * a.Dm;
+    st_tile<NL>(pb + (long long)(w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, gA);
+    if (a.gh0 && w.seg == 0)
+        st_tile<NL>(a.gh0 + ((long long)w.b * a.Dm + w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, G);
+    // gD and gdt_bias over the rows of threads, in order
     __syncthreads();
-    for (int c = tid; c < cn; c += S::THREADS) {
+    for (int c = tid; c < w.cn; c += S::THREADS) {
         float x = 0.0f, y = 0.0f;
-        for (int r = 0; r < S::RROWS; r++) {
-            x += dl[r * S::CT + c];
-            y += us[r * S::CT + c];
+        for (int r = 0; r < S::ROWS; r++) {
+            x += sums[r * 2 * S::CT + c];
+            y += sums[(r * 2 + 1) * S::CT + c];
         }
-        pb[(long long)a.N * a.Dm + d0 + c] = x;
-        pb[(long long)(a.N + 1) * a.Dm + d0 + c] = y;
+        pb[(long long)a.N * a.Dm + w.d0 + c] = x;
+        pb[(long long)(a.N + 1) * a.Dm + w.d0 + c] = y;
     }
 }
 
@@ -752,29 +942,28 @@ template <typename F> hc_status scan_dispatch(int N, F&& f) {
     return f.template operator()<16>();
 }
 
-// Channel tiles a group in a kernel whose warps take `per_lane` channels a lane group.
-int scan_ctiles(const hc_selective_scan_desc* d, int warps, int per_lane) {
-    return (int)cdiv(d->D / d->groups, warps * per_lane * 32 / scan_lanes(d->d_state));
+// Channel tiles a group (Tile<NL>::CT channels each).
+int scan_ctiles(const hc_selective_scan_desc* d) {
+    const int nl = scan_lanes(d->d_state);
+    return (int)cdiv(d->D / d->groups, nl <= 4 ? 128 : 512 / nl);
 }
-int fwd_ctiles(const hc_selective_scan_desc* d) { return scan_ctiles(d, scan_lanes(d->d_state) == 1 ? 2 : 4, 4); }
-int bwd_ctiles(const hc_selective_scan_desc* d) { return scan_ctiles(d, 4, 2); }
 
 // Segments: none where (sequence, channel tile) blocks give every SM `want` of
 // them, else as many as make up for it, of two tiles at least.
 struct Segs {
     int n, tiles;
 };
-Segs scan_segs(const hc_selective_scan_desc* d, int ctiles, int want) {
+Segs scan_segs(const hc_selective_scan_desc* d, int want) {
     const int tiles = (int)cdiv(d->L, SC_T);
-    const long long blocks = (long long)d->B * d->groups * ctiles, full = (long long)want * device_sm_count();
+    const long long blocks = (long long)d->B * d->groups * scan_ctiles(d), full = (long long)want * device_sm_count();
     if (blocks * 2 > full || tiles < 4) return {1, tiles > 0 ? tiles : 1};
     long long n = full / blocks;
     if (n > tiles / 2) n = tiles / 2;
     const int per = (int)cdiv(tiles, n);
     return {(int)cdiv(tiles, per), per};
 }
-Segs fwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, fwd_ctiles(d), 6); }
-Segs bwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, bwd_ctiles(d), 2); }
+Segs fwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, 4); }
+Segs bwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, 2); }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 size_t carry_floats(const hc_selective_scan_desc* d, int segs) {
@@ -812,6 +1001,7 @@ ScanArgs scan_args(const hc_selective_scan_desc* d, const hc_scan_in* in) {
     a.dtype = d->dtype;
     a.softplus = d->softplus;
     a.tiles = (int)cdiv(d->L, SC_T);
+    a.ctiles = scan_ctiles(d);
     return a;
 }
 
@@ -824,14 +1014,13 @@ bool scan_in_ok(const hc_selective_scan_desc* d, const hc_scan_in* in, long long
 
 // The first states of the segments (REV: of the gradient, from the last row up).
 template <int NL, bool REV> hc_status launch_scan_carry(ScanArgs a, cudaStream_t st) {
-    using S = FwdTile<NL>;
+    using S = Tile<NL>;
     static std::atomic<unsigned long long> attr{0};
     once_per_device(attr, [] {
         return cudaFuncSetAttribute(scan_carry_kernel<NL, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)S::SMEM) == cudaSuccess;
+                                    (int)carry_smem<NL>()) == cudaSuccess;
     });
-    a.ctiles = (int)cdiv(a.Dg, S::CT);
-    scan_carry_kernel<NL, REV><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
+    scan_carry_kernel<NL, REV><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, carry_smem<NL>(), st>>>(a);
     hc_status e = launched("scan_carry_kernel", st);
     if (e) return e;
     scan_join_kernel<REV><<<dim3(cdiv((long long)a.Dm * S::NP, SJ_STATES), a.B), 1024, 0, st>>>(a, S::NP);
@@ -842,18 +1031,17 @@ struct ScanFwd {
     ScanArgs a;
     cudaStream_t st;
     template <int NL> hc_status operator()() {
-        using S = FwdTile<NL>;
+        using S = Tile<NL>;
         static std::atomic<unsigned long long> attr{0};
         once_per_device(attr, [] {
             return cudaFuncSetAttribute(scan_fwd_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)S::SMEM) == cudaSuccess;
+                                        (int)fwd_smem<NL>()) == cudaSuccess;
         });
         if (a.segs > 1) {
             const hc_status e = launch_scan_carry<NL, false>(a, st);
             if (e) return e;
         }
-        a.ctiles = (int)cdiv(a.Dg, S::CT);
-        scan_fwd_kernel<NL><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
+        scan_fwd_kernel<NL><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, fwd_smem<NL>(), st>>>(a);
         return launched("scan_fwd_kernel", st);
     }
 };
@@ -863,17 +1051,17 @@ struct ScanBwd {
     const hc_scan_grad* g;
     cudaStream_t st;
     template <int NL> hc_status operator()() {
-        using S = BwdTile<NL>;
+        using S = Tile<NL>;
         static std::atomic<unsigned long long> attr{0};
         once_per_device(attr, [] {
             return cudaFuncSetAttribute(scan_bwd_kernel<NL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)S::SMEM) == cudaSuccess;
+                                        (int)bwd_smem<NL>()) == cudaSuccess;
         });
         if (a.segs > 1) {
             const hc_status e = launch_scan_carry<NL, true>(a, st);
             if (e) return e;
         }
-        scan_bwd_kernel<NL><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, S::SMEM, st>>>(a);
+        scan_bwd_kernel<NL><<<(unsigned)a.B * a.segs * a.G * a.ctiles, S::THREADS, bwd_smem<NL>(), st>>>(a);
         hc_status e = launched("scan_bwd_kernel", st);
         if (e) return e;
         const long long bc = (long long)a.B * a.L * a.G * 2 * a.N;
@@ -917,7 +1105,7 @@ hc_status hc_selective_scan_workspace_size(const hc_selective_scan_desc* d, int 
     if (!scan_size_ok(d)) return HC_ERR_UNSUPPORTED;
     *bytes = carry_bytes(d, fwd_segs(d).n);
     if (pass == 1) {
-        const int tiles = bwd_ctiles(d);
+        const int tiles = scan_ctiles(d);
         size_t b = carry_bytes(d, bwd_segs(d).n) + part_bytes(d);
         if (tiles > 1) b += sizeof(float) * tiles * (size_t)d->B * d->L * d->groups * 2 * d->d_state;
         if (b > *bytes) *bytes = b;
@@ -991,7 +1179,6 @@ hc_status hc_selective_scan_bwd(const hc_selective_scan_desc* d, const hc_scan_i
     set_segs(f.a, d, bwd_segs(d), ws);
     const size_t carried = carry_bytes(d, f.a.segs);
     f.a.part = (float*)((char*)ws + carried);
-    f.a.ctiles = bwd_ctiles(d);
     f.a.gbc = f.a.ctiles > 1 ? (float*)((char*)ws + carried + part_bytes(d)) : nullptr;
     f.a.vec = vec4(f.a);
     return scan_dispatch(d->d_state, f);
