@@ -1,0 +1,144 @@
+// scan_fwd.cu -- the forward pass of the selective scan (scan.cu).
+#include "scan.cuh"
+
+namespace hc {
+namespace {
+
+template <int NL> constexpr size_t fwd_smem() {
+    using S = FwdTile<NL>;
+    return sizeof(float) * (5 * S::PLANE + 2 * S::CT + 4 * SC_T * S::NP + 3 * S::PLANE);
+}
+template <int NL, int DT> __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
+    using S = FwdTile<NL>;
+    extern __shared__ float4 sm4[];
+    float* dl = reinterpret_cast<float*>(sm4);  // step sizes * log2 e
+    float* xs = dl + S::PLANE;                  // step * u
+    float* us = xs + S::PLANE;                  // D * u
+    float* gs = us + S::PLANE;                  // silu(z)
+    float* ys = gs + S::PLANE;                  // C . h
+    float* bD = ys + S::PLANE;                             // dt_bias, D
+    f32x2* bc2 = reinterpret_cast<f32x2*>(bD + 2 * S::CT);  // [B, C][T][NP], twice each
+    char* raw = reinterpret_cast<char*>(bc2 + 2 * SC_T * S::NP);
+    const int lane = threadIdx.x & 31, n = lane % NL, tc = (threadIdx.x >> 5) * S::WC + lane / NL * 4;
+    const Where w(a, S::CT);
+    const bool gate = a.z.p != nullptr;
+    f32x2 A[2][4], h[2][4];
+    ld_rates(a, w.d0 + tc, n, tc, w.cn, A);
+    if (a.segs > 1)
+        ld_tile(a.carry + ((long long)w.bs * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc, w.cn, h);
+    else
+        ld_tile(a.h0 ? a.h0 + ((long long)w.b * a.Dm + w.d0 + tc) * a.N : nullptr, a.N, n, a.N, false, tc, w.cn, h);
+    put_params<S>(a, w, bD);
+    typename EltOf<DT>::type bc[S::BC];
+    const auto start = [&](int t0) {
+        const Walk<S> at;
+        fetch<S, DT>(a, a.dt, w, at, t0, 0, raw);
+        fetch<S, DT>(a, a.u, w, at, t0, 1, raw);
+        if (gate) fetch<S, DT>(a, a.z, w, at, t0, 2, raw);
+        fetch_bc<S, DT>(a, w, t0, bc);
+    };
+    const int live1 = w.live1();
+    if (w.tile0 < live1) start(w.tile0 * SC_T);
+    for (int tile = w.tile0; tile < live1; tile++) {
+        const int t0 = tile * SC_T;
+        cp_async_wait();
+        __syncthreads();
+        const Walk<S> at;
+#pragma unroll
+        for (int i = 0; i < S::STEPS && at.on; i++) {
+            const int t = at.er + i * S::ROWS, q = t * S::CT + at.ec;
+            float s[4], x[4], D[4];
+            get<S, DT>(raw, 0, t, at.ec, s);
+            get<S, DT>(raw, 1, t, at.ec, x);
+            load_pack<float, 4>(bD + S::CT + at.ec, D);
+            add4(s, bD + at.ec);
+            steps(a, t0 + t < w.len, s, dl + q);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                D[k] *= x[k];
+                x[k] *= s[k];
+            }
+            store_pack<float, 4>(xs + q, x);
+            store_pack<float, 4>(us + q, D);
+            if (gate) {
+                get<S, DT>(raw, 2, t, at.ec, s);
+#pragma unroll
+                for (int k = 0; k < 4; k++) s[k] = silu_f(s[k]);
+                store_pack<float, 4>(gs + q, s);
+            }
+        }
+        put_bc<S, DT>(bc, bc2);
+        __syncthreads();
+        if (tile + 1 < live1) start(t0 + SC_T);
+        if (a.saved)
+            st_tile(a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc,
+                        w.cn, h);
+#pragma unroll 4
+        for (int t = 0; t < SC_T; t++) {
+            f32x2 s[2], x[2], B[4], C[4], y[2];
+            ld_pairs(dl + t * S::CT + tc, s);
+            ld_pairs(xs + t * S::CT + tc, x);
+            ld_dup(bc2 + t * S::NP + 4 * n, B);
+            ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    h[i][j] = fma2(decay2(s[i], A[i][j]), h[i][j], mul2(x[i], B[j]));
+                    y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
+                }
+            }
+            put_lanes_sum<NL>(y, n, ys + t * S::CT + tc);
+        }
+        __syncthreads();
+        const int rows = min(SC_T, a.L - t0);
+        const Walk<S> to;
+#pragma unroll
+        for (int i = 0; i < S::STEPS; i++) {
+            const int t = to.er + i * S::ROWS, q = t * S::CT + to.ec;
+            if (!to.on || t >= rows) break;
+            float o[4], z[4];
+            load_pack<float, 4>(ys + q, o);
+            add4(o, us + q);
+            if (gate) {
+                load_pack<float, 4>(gs + q, z);
+#pragma unroll
+                for (int k = 0; k < 4; k++) o[k] *= z[k];
+            }
+            if (t0 + t >= w.len) o[0] = o[1] = o[2] = o[3] = 0.0f;
+            put<DT>(out_row<DT>(a.y, w, t0, t), to.ec, w.cn, a.vec, o);
+        }
+    }
+    // rows past the sequence's last tile
+    const int end = min(w.tile1 * SC_T, a.L);
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const Walk<S> at;
+    for (int t = live1 * SC_T + at.er; t < end && at.on; t += S::ROWS)
+        put<DT>(out_row<DT>(a.y, w, t, 0), at.ec, w.cn, a.vec, zero);
+    if (a.hT && w.seg == a.segs - 1)
+        st_tile(a.hT + ((long long)w.b * a.Dm + w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, h);
+}
+
+struct Launch {
+    const ScanArgs& a;
+    cudaStream_t st;
+    template <int NL, int DT> hc_status run() {
+        static std::atomic<unsigned long long> attr{0};
+        once_per_device(attr, [] {
+            return cudaFuncSetAttribute(scan_fwd_kernel<NL, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)fwd_smem<NL>()) == cudaSuccess;
+        });
+        scan_fwd_kernel<NL, DT>
+            <<<(unsigned)a.B * a.segs * a.G * a.ctiles, FwdTile<NL>::THREADS, fwd_smem<NL>(), st>>>(a);
+        return launched("scan_fwd_kernel", st);
+    }
+};
+
+}  // namespace
+
+hc_status launch_scan_fwd(const ScanArgs& a, cudaStream_t st) {
+    Launch f{a, st};
+    return scan_dispatch(a.N, a.dtype, f);
+}
+
+}  // namespace hc
