@@ -6,7 +6,7 @@
 
 namespace hc {
 
-constexpr int SC_T = 8;  // rows a tile; the backward pass keeps a tile's states in registers
+constexpr int SC_T = 8;  // rows a tile; the forward pass saves the state before each tile for the backward pass
 
 struct ScanArgs {
     hc_rows u, dt, Bm, Cm, z, y;         // forward
@@ -151,7 +151,7 @@ template <int NL_, int P_> struct Tile {
 };
 
 template <int NL> using FwdTile = Tile<NL, 2>;
-template <int NL> using BwdTile = Tile<NL, 1>;
+template <int NL> using BwdTile = Tile<NL, 2>;
 
 // Where a block works: CT channels of one group of one segment.
 struct Where {

@@ -4,14 +4,18 @@
 namespace hc {
 namespace {
 
-// A block's tiles from the last to the first.  A tile's states are recomputed
-// from its saved first state and kept in registers (H), with y and gC on the
-// way, then the state's gradient runs back through them.
+// A block's tiles from the last to the first, each in two halves, the later one
+// first.  A half's states are recomputed from its first state and kept in
+// registers (H), with y and gC on the way, then the state's gradient runs back
+// through them.  A tile's first state was saved; that of its later half is
+// recomputed from it.  Half tiles keep a thread at 168 registers, three blocks an
+// SM; whole tiles take 255 and two.
 template <int NL> constexpr size_t bwd_smem() {
     using S = BwdTile<NL>;
     return sizeof(float) * (9 * S::PLANE + 2 * S::CT + 2 * S::ROWS * S::CT + 4 * SC_T * S::NP + S::W * SC_T * 2 * S::NP +
-                            4 * S::PLANE);
+                            4 * S::PLANE + 8 * S::P * S::THREADS);
 }
+constexpr int HALF = SC_T / 2;
 template <int NL, int DT>
 __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREADS) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
     using S = BwdTile<NL>;
@@ -30,12 +34,13 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
     float* sums = bD + 2 * S::CT;               // [ROWS][2][CT], each thread's gD and gdt_bias
     f32x2* bc2 = reinterpret_cast<f32x2*>(sums + 2 * S::ROWS * S::CT);
     float* red = reinterpret_cast<float*>(bc2 + 2 * SC_T * S::NP);  // [W][T][2][NP], the warps' gB and gC
-    char* raw = reinterpret_cast<char*>(red + S::W * SC_T * 2 * S::NP);
+    f32x2* gA = reinterpret_cast<f32x2*>(red + S::W * SC_T * 2 * S::NP);  // [P][4][threads], each thread's sums
+    char* raw = reinterpret_cast<char*>(gA + 4 * S::P * S::THREADS);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = lane % NL, tc = warp * S::WC + lane / NL * 2 * S::P;
     const Where w(a, S::CT);
     const bool gate = a.z.p != nullptr;
-    f32x2 A[S::P][4], G[S::P][4], gA[S::P][4];
+    f32x2 A[S::P][4], G[S::P][4];
     ld_rates(a, w.d0 + tc, n, tc, w.cn, A);
     if (a.segs > 1)
         ld_tile(a.carry + ((long long)w.bs * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc, w.cn, G);
@@ -45,7 +50,7 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
 #pragma unroll
     for (int i = 0; i < S::P; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) gA[i][j] = pk2(0.0f, 0.0f);
+        for (int j = 0; j < 4; j++) gA[(4 * i + j) * S::THREADS + tid] = pk2(0.0f, 0.0f);
     put_params<S>(a, w, bD);
     for (int q = tid; q < 2 * S::ROWS * S::CT; q += S::THREADS) sums[q] = 0.0f;
     typename EltOf<DT>::type bc[S::BC];
@@ -100,64 +105,87 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
             if (tile > w.tile0) start(t0 - SC_T);
             const float* first =
                 a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP;
-            // H[t] is the state before row t (H[0] is read again where it is needed again)
-            f32x2 H[SC_T][S::P][4], h[S::P][4];
+            f32x2 h[S::P][4];
             ld_tile(first, S::NP, n, a.N, true, tc, w.cn, h);
 #pragma unroll
-            for (int t = 0; t < SC_T; t++) {
-                f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4], y[S::P], gc[4];
+            for (int t = 0; t < HALF; t++) {
+                f32x2 s[S::P], x[S::P], B[4];
                 ld_pairs(dl + t * S::CT + tc, s);
                 ld_pairs(xs + t * S::CT + tc, x);
-                ld_pairs(qs + t * S::CT + tc, q);
                 ld_dup(bc2 + t * S::NP + 4 * n, B);
-                ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
 #pragma unroll
-                for (int i = 0; i < S::P; i++) {
+                for (int i = 0; i < S::P; i++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        if (t) H[t][i][j] = h[i][j];
-                        h[i][j] = fma2(decay2(s[i], A[i][j]), h[i][j], mul2(x[i], B[j]));
-                        y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
-                        gc[j] = i ? fma2(q[i], h[i][j], gc[j]) : mul2(q[i], h[i][j]);
-                    }
-                }
-                if (gate) put_lanes_sum<NL>(y, n, ys + t * S::CT + tc);
-                put_groups_sum<NL>(gc, lane, red + ((warp * SC_T + t) * 2 + 1) * S::NP + 4 * n);
+                    for (int j = 0; j < 4; j++) h[i][j] = fma2(decay2(s[i], A[i][j]), h[i][j], mul2(x[i], B[j]));
             }
-            // nothing of the way up is kept for the way down but H: the exponentials are taken again
-            asm volatile("" ::: "memory");
             // gA summed tile by tile: one running sum over all rows would lose more
             f32x2 ga[S::P][4];
 #pragma unroll
-            for (int t = SC_T - 1; t >= 0; t--) {
-                f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4], gb[S::P], ea[S::P], gB[4];
-                ld_pairs(dl + t * S::CT + tc, s);
-                ld_pairs(xs + t * S::CT + tc, x);
-                ld_pairs(qs + t * S::CT + tc, q);
-                ld_dup(bc2 + t * S::NP + 4 * n, B);
-                ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
-                if (t == 0) ld_tile(first, S::NP, n, a.N, true, tc, w.cn, H[0]);
+            for (int i = 0; i < S::P; i++)
 #pragma unroll
-                for (int i = 0; i < S::P; i++) {
+                for (int j = 0; j < 4; j++) ga[i][j] = pk2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int t1 = HALF; t1 >= 0; t1 -= HALF) {
+                if (t1 == 0) ld_tile(first, S::NP, n, a.N, true, tc, w.cn, h);
+                f32x2 H[HALF][S::P][4];  // the state before row t1 + t
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const f32x2 g = fma2(q[i], C[j], G[i][j]);
-                        gB[j] = i ? fma2(g, x[i], gB[j]) : mul2(g, x[i]);
-                        gb[i] = j ? fma2(g, B[j], gb[i]) : mul2(g, B[j]);
-                        G[i][j] = mul2(g, decay2(s[i], A[i][j]));
-                        const f32x2 E = mul2(G[i][j], H[t][i][j]);
-                        ea[i] = j ? fma2(E, A[i][j], ea[i]) : mul2(E, A[i][j]);
-                        ga[i][j] = t == SC_T - 1 ? mul2(E, s[i]) : fma2(E, s[i], ga[i][j]);
+                for (int t = 0; t < HALF; t++) {
+                    const int r = t1 + t;
+                    f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4], y[S::P], gc[4];
+                    ld_pairs(dl + r * S::CT + tc, s);
+                    ld_pairs(xs + r * S::CT + tc, x);
+                    ld_pairs(qs + r * S::CT + tc, q);
+                    ld_dup(bc2 + r * S::NP + 4 * n, B);
+                    ld_dup(bc2 + (SC_T + r) * S::NP + 4 * n, C);
+#pragma unroll
+                    for (int i = 0; i < S::P; i++) {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            H[t][i][j] = h[i][j];
+                            h[i][j] = fma2(decay2(s[i], A[i][j]), h[i][j], mul2(x[i], B[j]));
+                            y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
+                            gc[j] = i ? fma2(q[i], h[i][j], gc[j]) : mul2(q[i], h[i][j]);
+                        }
                     }
+                    if (gate) put_lanes_sum<NL>(y, n, ys + r * S::CT + tc);
+                    put_groups_sum<NL>(gc, lane, red + ((warp * SC_T + r) * 2 + 1) * S::NP + 4 * n);
                 }
-                put_lanes_sum<NL>(gb, n, GB + t * S::CT + tc);
-                put_lanes_sum<NL>(ea, n, EA + t * S::CT + tc);
-                put_groups_sum<NL>(gB, lane, red + (warp * SC_T + t) * 2 * S::NP + 4 * n);
+                // nothing of the way up is kept for the way down but H: the exponentials are taken again
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int t = HALF - 1; t >= 0; t--) {
+                    const int r = t1 + t;
+                    f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4], gb[S::P], ea[S::P], gB[4];
+                    ld_pairs(dl + r * S::CT + tc, s);
+                    ld_pairs(xs + r * S::CT + tc, x);
+                    ld_pairs(qs + r * S::CT + tc, q);
+                    ld_dup(bc2 + r * S::NP + 4 * n, B);
+                    ld_dup(bc2 + (SC_T + r) * S::NP + 4 * n, C);
+#pragma unroll
+                    for (int i = 0; i < S::P; i++) {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const f32x2 g = fma2(q[i], C[j], G[i][j]);
+                            gB[j] = i ? fma2(g, x[i], gB[j]) : mul2(g, x[i]);
+                            gb[i] = j ? fma2(g, B[j], gb[i]) : mul2(g, B[j]);
+                            G[i][j] = mul2(g, decay2(s[i], A[i][j]));
+                            const f32x2 E = mul2(G[i][j], H[t][i][j]);
+                            ea[i] = j ? fma2(E, A[i][j], ea[i]) : mul2(E, A[i][j]);
+                            ga[i][j] = fma2(E, s[i], ga[i][j]);
+                        }
+                    }
+                    put_lanes_sum<NL>(gb, n, GB + r * S::CT + tc);
+                    put_lanes_sum<NL>(ea, n, EA + r * S::CT + tc);
+                    put_groups_sum<NL>(gB, lane, red + (warp * SC_T + r) * 2 * S::NP + 4 * n);
+                }
             }
 #pragma unroll
             for (int i = 0; i < S::P; i++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) gA[i][j] = fma2(ga[i][j], pk2(kLn2, kLn2), gA[i][j]);
+                for (int j = 0; j < 4; j++) {
+                    f32x2* sum = gA + (4 * i + j) * S::THREADS + tid;
+                    *sum = add2(ga[i][j], *sum);
+                }
             __syncthreads();
         }
         const Walk<S> to;
@@ -216,7 +244,12 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
         }
     }
     float* pb = a.part + (long long)w.bs * (a.N + 2) * a.Dm;
-    st_tile(pb + (long long)(w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, gA);
+    f32x2 ga[S::P][4];
+#pragma unroll
+    for (int i = 0; i < S::P; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) ga[i][j] = mul2(gA[(4 * i + j) * S::THREADS + tid], pk2(kLn2, kLn2));
+    st_tile(pb + (long long)(w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, ga);
     if (a.gh0 && w.seg == 0)
         st_tile(a.gh0 + ((long long)w.b * a.Dm + w.d0 + tc) * a.N, a.N, n, a.N, false, tc, w.cn, G);
     // gD and gdt_bias over the rows of threads, in order

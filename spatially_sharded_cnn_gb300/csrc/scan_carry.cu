@@ -102,45 +102,55 @@ __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_carry_kernel(const 
 }
 
 // Replaces every segment's local result by the state it starts from.  A block
-// takes SJ_STATES adjacent states of a sequence, its 32 rows of threads equal
-// runs of segments: each run is joined, the runs' results are joined in order
-// through shared memory, and each run is gone through again.
-constexpr int SJ_STATES = 32;
-template <bool REV>
-__global__ void __launch_bounds__(1024) scan_join_kernel(const __grid_constant__ ScanArgs a, int NP) {
-    __shared__ float hs[32][SJ_STATES + 1], as[32][SJ_STATES + 1];
-    const int col = threadIdx.x % SJ_STATES, r = threadIdx.x / SJ_STATES;
+// takes SJ_THREADS / R adjacent states of a sequence and R rows of threads, each
+// with an equal run of segments: each run is joined, the runs' results are
+// joined in order through shared memory, and each run is gone through again.
+// Few segments take one row (no second walk's worth of work is saved), many as
+// many rows as keep the walks short.
+constexpr int SJ_THREADS = 256;
+template <bool REV, int R>
+__global__ void __launch_bounds__(SJ_THREADS) scan_join_kernel(const __grid_constant__ ScanArgs a, int NP) {
+    constexpr int S = SJ_THREADS / R;
+    __shared__ float hs[R][S + 1], as[R][S + 1];
+    const int col = threadIdx.x % S, r = threadIdx.x / S;
     const int b = blockIdx.y;
-    const long long q = (long long)blockIdx.x * SJ_STATES + col;
+    const long long q = (long long)blockIdx.x * S + col;
     const bool on = q < (long long)a.Dm * NP;
     const int d = on ? (int)(q / NP) : 0, n = on ? (int)(q % NP) : 0;
     const float A = on && n < a.N ? a.A[(long long)d * a.N + n] : 0.0f;
-    const int per = (a.segs + 31) / 32, s0 = r * per, s1 = min(s0 + per, a.segs);
-    float* cp = a.carry + (long long)b * a.segs * a.Dm * NP + (on ? q : 0);
-    const float* dp = a.dsum + (long long)b * a.segs * a.Dm + d;
-    const long long hstep = (long long)a.Dm * NP;
-    float h = 0.0f, total = 0.0f;
+    const int per = (a.segs + R - 1) / R, s0 = min(r * per, a.segs), s1 = min(s0 + per, a.segs);
+    const long long hstep = REV ? -(long long)a.Dm * NP : (long long)a.Dm * NP, wstep = REV ? -a.Dm : a.Dm;
+    const long long at = (long long)b * a.segs + (REV ? a.segs - 1 - s0 : s0);
+    float* cp = a.carry + at * a.Dm * NP + (on ? q : 0);
+    const float* dp = a.dsum + at * a.Dm + d;
+    float h = 0.0f;
+    if (R > 1) {
+        float total = 0.0f;
 #pragma unroll 4
-    for (int k = s0; k < s1; k++) {
-        const int s = REV ? a.segs - 1 - k : k;
-        const float w = dp[(long long)s * a.Dm];
-        h = fmaf(ex2f(w * A), h, cp[s * hstep]);
-        total += w;
+        for (int k = 0; k < s1 - s0; k++) {
+            const float w = dp[k * wstep];
+            h = fmaf(ex2f(w * A), h, cp[k * hstep]);
+            total += w;
+        }
+        hs[r][col] = h;
+        as[r][col] = total;
+        __syncthreads();
     }
-    hs[r][col] = h;
-    as[r][col] = total;
-    __syncthreads();
     const float* first = REV ? a.ghT : a.h0;
     h = first && on && n < a.N ? first[((long long)b * a.Dm + d) * a.N + n] : 0.0f;
-    for (int k = 0; k < r; k++) h = fmaf(ex2f(as[k][col] * A), h, hs[k][col]);
+    if (R > 1)
+        for (int k = 0; k < r; k++) h = fmaf(ex2f(as[k][col] * A), h, hs[k][col]);
     if (!on) return;
 #pragma unroll 4
-    for (int k = s0; k < s1; k++) {
-        const int s = REV ? a.segs - 1 - k : k;
-        const float v = cp[s * hstep], w = dp[(long long)s * a.Dm];
-        cp[s * hstep] = h;
+    for (int k = 0; k < s1 - s0; k++) {
+        const float v = cp[k * hstep], w = dp[k * wstep];
+        cp[k * hstep] = h;
         h = fmaf(ex2f(w * A), h, v);
     }
+}
+template <bool REV, int R> void join(const ScanArgs& a, int NP, cudaStream_t st) {
+    scan_join_kernel<REV, R>
+        <<<dim3(cdiv((long long)a.Dm * NP, SJ_THREADS / R), a.B), SJ_THREADS, 0, st>>>(a, NP);
 }
 
 template <bool REV> struct Launch {
@@ -157,7 +167,10 @@ template <bool REV> struct Launch {
         const hc_status e = launched("scan_carry_kernel", st);
         if (e) return e;
         constexpr int NP = FwdTile<NL>::NP;
-        scan_join_kernel<REV><<<dim3(cdiv((long long)a.Dm * NP, SJ_STATES), a.B), 1024, 0, st>>>(a, NP);
+        if (a.segs <= 8)
+            join<REV, 1>(a, NP, st);
+        else
+            join<REV, 8>(a, NP, st);
         return launched("scan_join_kernel", st);
     }
 };
