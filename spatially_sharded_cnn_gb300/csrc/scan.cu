@@ -149,13 +149,13 @@ struct Segs {
 Segs scan_segs(const hc_selective_scan_desc* d, int ctiles, int want) {
     const int tiles = (int)cdiv(d->L, SC_T);
     const long long blocks = (long long)d->B * d->groups * ctiles, full = (long long)want * device_sm_count();
-    if (blocks * 2 > full || tiles < 16) return {1, tiles > 0 ? tiles : 1};
+    if (blocks * 3 > full || tiles < 16) return {1, tiles > 0 ? tiles : 1};
     long long n = full / blocks;
     if (n > tiles / 2) n = tiles / 2;
     const int per = (int)cdiv(tiles, n);
     return {(int)cdiv(tiles, per), per};
 }
-Segs fwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, fwd_ctiles(d), 4); }
+Segs fwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, fwd_ctiles(d), 6); }
 Segs bwd_segs(const hc_selective_scan_desc* d) { return scan_segs(d, bwd_ctiles(d), 3); }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }

@@ -73,7 +73,7 @@ template <int NL, int DT> __global__ void __launch_bounds__(FwdTile<NL>::THREADS
         if (a.saved)
             st_tile(a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc,
                         w.cn, h);
-#pragma unroll 4
+#pragma unroll
         for (int t = 0; t < SC_T; t++) {
             f32x2 s[2], x[2], B[4], C[4], y[2];
             ld_pairs(dl + t * S::CT + tc, s);
