@@ -54,6 +54,41 @@ __device__ __forceinline__ float rcpf(float x) {
     return r;
 }
 
+// The same for data that is not read again soon: evicted first.
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw(const T* p) {
+    return *reinterpret_cast<const Pack<T, V>*>(p);
+}
+template <int BYTES> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<4> { using type = unsigned; };
+template <> struct Word<2> { using type = unsigned short; };
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw_last(const T* p) {
+    using W = typename Word<sizeof(T) * V>::type;
+    union U {
+        W w;
+        Pack<T, V> q;
+        __device__ U() {}
+    } u;
+    u.w = __ldcs(reinterpret_cast<const W*>(p));
+    return u.q;
+}
+template <typename T, int V> __device__ __forceinline__ void store_pack_last(T* p, const float (&f)[V]) {
+    using W = typename Word<sizeof(T) * V>::type;
+    union U {
+        W w;
+        Pack<T, V> q;
+        __device__ U() {}
+    } u;
+#pragma unroll
+    for (int i = 0; i < V; i++) u.q.v[i] = from_f<T>(f[i]);
+    __stcs(reinterpret_cast<W*>(p), u.w);
+}
+template <typename T, int V> __device__ __forceinline__ void unpack(const Pack<T, V>& q, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i++) f[i] = to_f(q.v[i]);
+}
+
 // SiLU x * s and its slope s * (1 + x * (1 - s)), s = 1 / (1 + exp(-x)): a few
 // ulps from two special-function results, which the elementwise kernels would
 // otherwise spend most of their instructions on.
@@ -79,11 +114,30 @@ __device__ __forceinline__ float softplus_f(float x) {
     return fmaf(2.0f * v, p, fmaxf(x, 0.0f));
 }
 
+// Phi(x) and e = exp(-x^2 / 2) by Abramowitz and Stegun 7.1.26: erfc(z) =
+// (a1 t + ... + a5 t^5) exp(-z^2), t = 1 / (1 + 0.3275911 z), z = |x| / sqrt 2, within
+// 1.5e-7; no branch, and the exponential serves the slope Phi(x) + x phi(x).
+__device__ __forceinline__ float normal_cdf(float x, float& e) {
+    const float t = rcpf(fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
+    e = ex2f(-0.5f * kLog2e * x * x);
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    const float half = 0.5f * t * p * e;  // Phi(-|x|)
+    return x >= 0.0f ? 1.0f - half : half;
+}
+
 template <int ACT> __device__ __forceinline__ float act_f(float x) {
-    return ACT == HC_PW_SILU ? silu_f(x) : ACT == HC_PW_GELU ? gelu_f(x) : x;
+    float e;
+    return ACT == HC_PW_SILU ? silu_f(x) : ACT == HC_PW_GELU ? x * normal_cdf(x, e) : x;
 }
 template <int ACT> __device__ __forceinline__ float act_d(float x) {
-    return ACT == HC_PW_SILU ? silu_d(x) : ACT == HC_PW_GELU ? gelu_d(x) : 1.0f;
+    if (ACT == HC_PW_SILU) return silu_d(x);
+    if (ACT != HC_PW_GELU) return 1.0f;
+    float e;
+    const float c = normal_cdf(x, e);
+    return fmaf(x * 0.39894228040143268f, e, c);
 }
 
 // Column sums of in[rows][na + nb + nc] in a fixed order: the first na columns
