@@ -4,15 +4,22 @@
 // the left halo of a sequence cut into blocks.
 //
 // Bound by memory: a thread takes V adjacent channels and a run of rows, slides
-// a K-row window in registers and reads each row once; only the K - 1 rows
-// where two runs meet are read twice (from L1 or L2).
+// a K-row window in registers (two channels a register pair, packed
+// multiply-adds) and reads each row once; only the K - 1 rows where two runs meet
+// are read twice (from L1 or L2).  The next few rows are loaded while the last
+// ones are worked on, which is what keeps enough bytes in flight.
 #include "rows.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int CC_THREADS = 256;
-constexpr int CC_RUN = 32;  // rows a thread takes at most
+constexpr int CC_THREADS = 128;
+constexpr int CC_RUN = 64;  // rows a thread takes at most
+// Channels a thread where the rows allow it, and rows loaded ahead.  Forward on 8 x
+// 4096 x 1024 bf16: 4 channels and 8 rows 35 us, 4 and 4 40, 8 and 4 39; backward
+// on 56 x 1023 x 264 fp32: 4 rows 63 us, 8 rows 84 (two windows and two tensors fill
+// its registers).
+constexpr int CC_V = 4, CC_FWD_U = 8, CC_BWD_U = 4;
 
 // Thread (col, r) of a block: channel vector blockIdx.y * ncol + col, run
 // (blockIdx.x % blocks) * R + r of sequence blockIdx.x / blocks.
@@ -31,6 +38,67 @@ __device__ __forceinline__ void load_or_zero(const T* p, bool on, float (&f)[V])
 #pragma unroll
         for (int i = 0; i < V; i++) f[i] = 0.0f;
     }
+}
+// V channels as pairs (the second of a lone channel's is zero).
+template <int V> struct Pairs {
+    static constexpr int N = (V + 1) / 2;
+    f32x2 v[N];
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = pk2(f[2 * i], 2 * i + 1 < V ? f[2 * i + 1 < V ? 2 * i + 1 : 0] : 0.0f);
+    }
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            float lo, hi;
+            unpk2(v[i], lo, hi);
+            f[2 * i] = lo;
+            if (2 * i + 1 < V) f[2 * i + 1 < V ? 2 * i + 1 : 0] = hi;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = 0;
+    }
+};
+// The weights and bias of a thread's channels: V * K adjacent floats, by 16 bytes
+// (single loads at a stride of K floats cost more than a run's rows).
+template <int V, int K>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, int c0, Pairs<V> (&wk)[K], Pairs<V>& b) {
+    float t[V * K], f[V];
+    constexpr int Q = V % 4 == 0 ? 4 : 1;
+#pragma unroll
+    for (int q = 0; q < V * K; q += Q) {
+        float v[Q];
+        load_pack<float, Q>(w + (long long)c0 * K + q, v);
+#pragma unroll
+        for (int i = 0; i < Q; i++) t[q + i] = v[i];
+    }
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+#pragma unroll
+        for (int i = 0; i < V; i++) f[i] = t[i * K + k];
+        wk[k].set(f);
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) f[i] = 0.0f;
+    if (bias) {
+#pragma unroll
+        for (int q = 0; q < V; q += Q) {
+            float v[Q];
+            load_pack<float, Q>(bias + c0 + q, v);
+#pragma unroll
+            for (int i = 0; i < Q; i++) f[q + i] = v[i];
+        }
+    }
+    b.set(f);
+}
+// Rows t .. t + U - 1 of those below end, as stored.
+template <typename T, int V, int U>
+__device__ __forceinline__ void load_rows(const T* p, long long row, int t, int end, Pack<T, V> (&q)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; u++)
+        if (t + u < end) q[u] = load_raw<T, V>(p + (t + u) * row);
 }
 
 __device__ __forceinline__ int seq_len(const int* lens, int b, int L) {
@@ -74,35 +142,41 @@ __global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, Vie
     const int t0 = (int)t0l, t1 = min(t0 + s.run, s.L), live = min(t1, len);
     T* yb = y.p + b * y.batch + c0;
     if (t0 < live) {
-        float wk[K][V], bb[V], win[K][V];
+        Pack<T, V> now[CC_FWD_U], next[CC_FWD_U];
+        load_rows<T, V>(xb, x.row, t0, live, now);
+        Pairs<V> wk[K], bb, win[K];
+        load_taps<V, K>(w, bias, c0, wk, bb);
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            bb[i] = bias ? bias[c0 + i] : 0.0f;
-#pragma unroll
-            for (int k = 0; k < K; k++) wk[k][i] = w[(long long)(c0 + i) * K + k];
+        for (int k = 0; k < K - 1; k++) {
+            float f[V];
+            load_row<T, V, K>(xb, x.row, si, s.D, t0 - (K - 1) + k, true, f);
+            win[k].set(f);
         }
+        for (int t = t0; t < live; t += CC_FWD_U) {
+            load_rows<T, V>(xb, x.row, t + CC_FWD_U, live, next);
 #pragma unroll
-        for (int k = 0; k < K - 1; k++) load_row<T, V, K>(xb, x.row, si, s.D, t0 - (K - 1) + k, true, win[k]);
-        constexpr int U = 4;  // rows in flight
-        for (int t = t0; t < live; t += U) {
-            float in[U][V];
+            for (int u = 0; u < CC_FWD_U; u++) {
+                if (t + u < live) {
+                    float f[V];
+                    unpack(now[u], f);
+                    win[K - 1].set(f);
+                    Pairs<V> o;
 #pragma unroll
-            for (int u = 0; u < U; u++) load_or_zero<T, V>(xb + (t + u) * x.row, t + u < live, in[u]);
+                    for (int i = 0; i < Pairs<V>::N; i++) {
+                        o.v[i] = bb.v[i];
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                float o[V];
+                        for (int k = 0; k < K; k++) o.v[i] = fma2(wk[k].v[i], win[k].v[i], o.v[i]);
+                    }
+                    o.get(f);
 #pragma unroll
-                for (int i = 0; i < V; i++) {
-                    win[K - 1][i] = in[u][i];
-                    float a = bb[i];
-#pragma unroll
-                    for (int k = 0; k < K; k++) a = fmaf(wk[k][i], win[k][i], a);
-                    o[i] = act_f<ACT>(a);
-#pragma unroll
-                    for (int k = 0; k < K - 1; k++) win[k][i] = win[k + 1][i];
+                    for (int i = 0; i < V; i++) f[i] = act_f<ACT>(f[i]);
+                    store_pack<T, V>(yb + (t + u) * y.row, f);
                 }
-                if (t + u < live) store_pack<T, V>(yb + (t + u) * y.row, o);
+#pragma unroll
+                for (int k = 0; k < K - 1; k++) win[k] = win[k + 1];
             }
+#pragma unroll
+            for (int u = 0; u < CC_FWD_U; u++) now[u] = next[u];
         }
     }
     float zero[V];
@@ -129,13 +203,10 @@ __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, Vie
     const int len = seq_len(lens, b, s.L);
     const long long t0l = ((long long)blk * s.R + r) * s.run;
     const int c0 = cvec * V;
-    float gw[K][V], gb[V];
+    Pairs<V> gw[K], gb;
+    gb.zero();
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        gb[i] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; k++) gw[k][i] = 0.0f;
-    }
+    for (int k = 0; k < K; k++) gw[k].zero();
     if (on && (t0l < s.L || t0l == 0)) {
         const int t0 = (int)t0l, t1 = min(t0 + s.run, s.L);
         const T* xb = x.p + b * x.batch + c0;
@@ -143,65 +214,91 @@ __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, Vie
         T* gxb = gx.p ? gx.p + b * gx.batch + c0 : nullptr;
         const long long cs = (long long)b * (K - 1) * s.D + c0;
         const T* si = state_in ? state_in + cs : nullptr;
-        float wk[K][V], bb[V], win[K][V], gwin[K][V];
+        const int end = t1 + K - 1;  // one past the last row whose g this run needs
+        const int live = min(end, len);
+        Pack<T, V> xn[CC_BWD_U], gn[CC_BWD_U], xq[CC_BWD_U], gq[CC_BWD_U];
+        load_rows<T, V>(xb, x.row, t0, live, xn);
+        load_rows<T, V>(gyb, gy.row, t0, live, gn);
+        Pairs<V> wk[K], bb, win[K], gwin[K];
+        load_taps<V, K>(w, bias, c0, wk, bb);
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            bb[i] = bias ? bias[c0 + i] : 0.0f;
+        for (int k = 0; k < K; k++) gwin[k].zero();
 #pragma unroll
-            for (int k = 0; k < K; k++) {
-                wk[k][i] = w[(long long)(c0 + i) * K + k];
-                gwin[k][i] = 0.0f;
-            }
+        for (int k = 0; k < K - 1; k++) {
+            float f[V];
+            load_row<T, V, K>(xb, x.row, si, s.D, t0 - (K - 1) + k, t0 <= len, f);
+            win[k].set(f);
         }
-#pragma unroll
-        for (int k = 0; k < K - 1; k++)
-            load_row<T, V, K>(xb, x.row, si, s.D, t0 - (K - 1) + k, t0 <= len, win[k]);
         // gwin[K - 1] = g_t; the row finished at t is t - (K - 1)
-        for (int t = t0; t < t1 + K - 1; t++) {
-            float in[V], g[V];
-            const bool there = t < len;
-            load_or_zero<T, V>(xb + t * x.row, there, in);
-            load_or_zero<T, V>(gyb + t * gy.row, there, g);
-            const bool mine = t < t1;
-            float o[V];
+        for (int t = t0; t < end; t += CC_BWD_U) {
+            load_rows<T, V>(xb, x.row, t + CC_BWD_U, live, xq);
+            load_rows<T, V>(gyb, gy.row, t + CC_BWD_U, live, gq);
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                win[K - 1][i] = in[i];
-                float a = bb[i];
+            for (int u = 0; u < CC_BWD_U; u++) {
+                const int tt = t + u;
+                float f[V], g[V];
+                if (tt < live) {
+                    unpack(xn[u], f);
+                    win[K - 1].set(f);
+                    Pairs<V> o;
 #pragma unroll
-                for (int k = 0; k < K; k++) a = fmaf(wk[k][i], win[k][i], a);
-                const float gt = there ? g[i] * act_d<ACT>(a) : 0.0f;
-                gwin[K - 1][i] = gt;
-                const float gm = mine ? gt : 0.0f;
-                gb[i] += gm;
+                    for (int i = 0; i < Pairs<V>::N; i++) {
+                        o.v[i] = bb.v[i];
 #pragma unroll
-                for (int k = 0; k < K; k++) gw[k][i] = fmaf(gm, win[k][i], gw[k][i]);
-                float q = 0.0f;
+                        for (int k = 0; k < K; k++) o.v[i] = fma2(wk[k].v[i], win[k].v[i], o.v[i]);
+                    }
+                    o.get(f);
+                    unpack(gn[u], g);
 #pragma unroll
-                for (int k = 0; k < K; k++) q = fmaf(wk[k][i], gwin[K - 1 - k][i], q);
-                o[i] = q;
+                    for (int i = 0; i < V; i++) f[i] = g[i] * act_d<ACT>(f[i]);
+                    gwin[K - 1].set(f);
+                    if (tt < t1) {  // its own row
+#pragma unroll
+                        for (int i = 0; i < Pairs<V>::N; i++) {
+                            gb.v[i] = add2(gb.v[i], gwin[K - 1].v[i]);
+#pragma unroll
+                            for (int k = 0; k < K; k++)
+                                gw[k].v[i] = fma2(gwin[K - 1].v[i], win[k].v[i], gw[k].v[i]);
+                        }
+                    }
+                } else {
+                    win[K - 1].zero();
+                    gwin[K - 1].zero();
+                }
+                const int row = tt - (K - 1);
+                if (tt < end && (row >= t0 ? gxb != nullptr : t0 == 0 && gstate_in != nullptr)) {
+                    Pairs<V> o;
+#pragma unroll
+                    for (int i = 0; i < Pairs<V>::N; i++) {
+                        o.v[i] = mul2(wk[0].v[i], gwin[K - 1].v[i]);
+#pragma unroll
+                        for (int k = 1; k < K; k++) o.v[i] = fma2(wk[k].v[i], gwin[K - 1 - k].v[i], o.v[i]);
+                    }
+                    o.get(f);
+                    const int j = row - (len - (K - 1));  // its row of state_out, if any
+                    if (row >= len) {
+#pragma unroll
+                        for (int i = 0; i < V; i++) f[i] = 0.0f;
+                    } else if (gstate_out && j >= 0) {
+                        load_pack<T, V>(gstate_out + cs + (long long)j * s.D, g);
+#pragma unroll
+                        for (int i = 0; i < V; i++) f[i] += g[i];
+                    }
+                    if (row >= t0)
+                        store_pack<T, V>(gxb + row * gx.row, f);
+                    else
+                        store_pack<T, V>(gstate_in + cs + (long long)(row + K - 1) * s.D, f);
+                }
 #pragma unroll
                 for (int k = 0; k < K - 1; k++) {
-                    win[k][i] = win[k + 1][i];
-                    gwin[k][i] = gwin[k + 1][i];
+                    win[k] = win[k + 1];
+                    gwin[k] = gwin[k + 1];
                 }
             }
-            const int row = t - (K - 1);
-            if (row >= t0 ? gxb != nullptr : t0 == 0 && gstate_in != nullptr) {
-                const int j = row - (len - (K - 1));  // its row of state_out, if any
-                if (row >= len) {
 #pragma unroll
-                    for (int i = 0; i < V; i++) o[i] = 0.0f;
-                } else if (gstate_out && j >= 0) {
-                    float q[V];
-                    load_pack<T, V>(gstate_out + cs + (long long)j * s.D, q);
-#pragma unroll
-                    for (int i = 0; i < V; i++) o[i] += q[i];
-                }
-                if (row >= t0)
-                    store_pack<T, V>(gxb + row * gx.row, o);
-                else
-                    store_pack<T, V>(gstate_in + cs + (long long)(row + K - 1) * s.D, o);
+            for (int u = 0; u < CC_BWD_U; u++) {
+                xn[u] = xq[u];
+                gn[u] = gq[u];
             }
         }
     }
@@ -212,8 +309,10 @@ __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, Vie
 #pragma unroll
     for (int k = 0; k <= K; k++) {
         if (on) {
+            float f[V];
+            (k < K ? gw[k < K ? k : 0] : gb).get(f);
 #pragma unroll
-            for (int i = 0; i < V; i++) sm[r * wd + col * V + i] = k < K ? gw[k < K ? k : 0][i] : gb[i];
+            for (int i = 0; i < V; i++) sm[r * wd + col * V + i] = f[i];
         }
         __syncthreads();
         for (int q = threadIdx.x; q < wd; q += CC_THREADS) {
@@ -261,10 +360,11 @@ CcShape cc_shape(const hc_causal_conv_desc* d, int V) {
     s.cv = d->D / V;
     s.ncol = s.cv < CC_THREADS ? s.cv : CC_THREADS;
     s.R = CC_THREADS / s.ncol;
-    // runs of CC_RUN rows, shorter where that leaves the GPU without two blocks an SM
+    // runs of CC_RUN rows, shorter where that leaves the GPU without eight blocks an SM (backward as above: runs of 16,
+    // 32, 64 rows 82, 66, 61 us)
     const long long cols = cdiv(s.cv, s.ncol);
     long long runs = cdiv(s.L, CC_RUN);
-    const long long want = cdiv(2LL * device_sm_count() * s.R, (long long)s.B * cols);
+    const long long want = cdiv(8LL * device_sm_count() * s.R, (long long)s.B * cols);
     if (runs < want) runs = want;
     const long long most = cdiv(s.L, 4);
     if (runs > most) runs = most;
@@ -275,12 +375,9 @@ CcShape cc_shape(const hc_causal_conv_desc* d, int V) {
     return s;
 }
 
-// Wide vectors: 16 bytes where the window fits the registers, 8 for long kernels.
-int cc_width(int dtype, int K) { return dtype == HC_DTYPE_F32 || K > 4 ? 4 : 8; }
-
 size_t cc_part_bytes(const hc_causal_conv_desc* d) {
     size_t rows = 0;
-    for (int v : {1, 4, 8}) {
+    for (int v : {1, CC_V}) {
         if (d->D % v) continue;
         const CcShape s = cc_shape(d, v);
         const size_t n = (size_t)s.B * s.blocks;
@@ -303,8 +400,7 @@ template <typename T, int V, int K, typename F> hc_status cc_act(int act, F&& f)
                              : f.template operator()<T, V, K, HC_PW_NONE>();
 }
 template <typename T, int K, typename F> hc_status cc_vec(bool vec, int act, F&& f) {
-    constexpr int V = sizeof(T) == 4 || K > 4 ? 4 : 8;
-    return vec ? cc_act<T, V, K>(act, f) : cc_act<T, 1, K>(act, f);
+    return vec ? cc_act<T, CC_V, K>(act, f) : cc_act<T, 1, K>(act, f);
 }
 template <typename T, typename F> hc_status cc_k(int K, bool vec, int act, F&& f) {
     switch (K) {
@@ -394,7 +490,7 @@ hc_status hc_causal_conv_fwd(const hc_causal_conv_desc* d, const hc_rows* x, con
         !ptr_al(lens, 4))
         return HC_ERR_INVALID_ARG;
     traced_begin((cudaStream_t)stream);
-    const int v = cc_width(d->dtype, d->K);
+    const int v = CC_V;
     const bool vec = d->D % v == 0 && rows_vec(x, v) && rows_vec(y, v);
     return cc_dispatch(d, vec, CcFwd{d, x, y, w, bias, state_in, state_out, lens, (cudaStream_t)stream});
 }
@@ -422,7 +518,7 @@ hc_status hc_causal_conv_bwd(const hc_causal_conv_desc* d, const hc_rows* x, con
     const bool params = gw || gb;
     if (params && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
     traced_begin((cudaStream_t)stream);
-    const int v = cc_width(d->dtype, d->K);
+    const int v = CC_V;
     const bool vec = d->D % v == 0 && rows_vec(x, v) && rows_vec(gy, v) && (!gx || rows_vec(gx, v));
     return cc_dispatch(d, vec, CcBwd{d, x, gy, gx, w, bias, gw, gb, state_in, gstate_out, gstate_in, lens,
                                      params ? (float*)ws : nullptr, (cudaStream_t)stream});
@@ -436,7 +532,7 @@ hc_status hc_causal_conv_step(const hc_causal_conv_desc* d, const hc_rows* x, co
         !f32_opt_ok(bias) || !f32_ok(state))
         return HC_ERR_INVALID_ARG;
     traced_begin((cudaStream_t)stream);
-    const int v = cc_width(d->dtype, d->K);
+    const int v = CC_V;
     // a row stride that one token does not use does not decide the width
     const hc_rows x1{x->p, x->batch, 0, x->dtype}, y1{y->p, y->batch, 0, y->dtype};
     const bool vec = d->D % v == 0 && rows_vec(&x1, v) && rows_vec(&y1, v);

@@ -145,6 +145,32 @@ template <int ACT> __device__ __forceinline__ float act_d(float x) {
 hc_status launch_column_totals(const float* in, long long rows, float* a, int na, float* b, int nb, float* c, int nc,
                                cudaStream_t st);
 
+// Two fp32 values in one 64-bit register pair: one instruction for two
+// multiply-adds.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pk2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpk2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 inline size_t dtype_size(int dt) { return dt == HC_DTYPE_F32 ? 4 : 2; }
 inline bool dtype_ok(int dt) { return dt == HC_DTYPE_F32 || dt == HC_DTYPE_BF16 || dt == HC_DTYPE_F16; }
 inline bool ptr_al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
