@@ -446,17 +446,23 @@ def _addr(t) -> int:
     return 0 if t is None else t if isinstance(t, int) else t.data_ptr()
 
 
+def _refuse(t, shape):
+    if t.shape != shape:
+        raise HcError(HC_ERR_INVALID_ARG, f"a tensor of shape {tuple(t.shape)} where {shape} is wanted")
+    raise HcError(HC_ERR_INVALID_ARG, "a channels-last tensor needs adjacent channels")
+
+
 def _view(t, *shape):
     """The fields of an hc_rows for a torch tensor (batch, row, channel) or (batch, channel) with adjacent channels."""
     if t is None:
         return _ABSENT
-    if t.shape != shape:
-        raise HcError(HC_ERR_INVALID_ARG, f"a tensor of shape {tuple(t.shape)} where {shape} is wanted")
     s = t.stride()
-    if s[-1] != 1 and shape[-1] > 1:
-        raise HcError(HC_ERR_INVALID_ARG, "a channels-last tensor needs adjacent channels")
+    if t.shape != shape or (s[-1] != 1 and shape[-1] > 1):
+        _refuse(t, shape)
     dt = _DTYPES.get(t.dtype)
-    return t.data_ptr(), s[0], s[1] if len(s) == 3 else 0, _dtype(t.dtype) if dt is None else dt
+    if dt is None:
+        dt = _dtype(t.dtype)
+    return t.data_ptr(), s[0], s[1] if len(s) == 3 else 0, dt
 
 
 def _rows(t, *shape) -> bytes:
