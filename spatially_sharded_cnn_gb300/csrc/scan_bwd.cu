@@ -103,8 +103,13 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
             put_bc<S, DT>(bc, bc2);
             __syncthreads();
             if (tile > w.tile0) start(t0 - SC_T);
-            const float* first =
-                a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP;
+            const float* first = a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP;
+            if (tile > w.tile0) {  // the next tile's states on their way to L2
+#pragma unroll
+                for (int i = 0; i < 2 * S::P; i++)
+                    if (tc + i < w.cn)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(first - ((long long)a.Dm - i) * S::NP + 4 * n));
+            }
             f32x2 h[S::P][4];
             ld_tile(first, S::NP, n, a.N, true, tc, w.cn, h);
 #pragma unroll
@@ -128,10 +133,13 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
             for (int t1 = HALF; t1 >= 0; t1 -= HALF) {
                 if (t1 == 0) ld_tile(first, S::NP, n, a.N, true, tc, w.cn, h);
                 f32x2 H[HALF][S::P][4];  // the state before row t1 + t
+                // a row's sums follow the next row's multiply-adds: their shuffles wait while there is other work,
+                // and their stores do not hold up its loads
+                f32x2 y[S::P], gc[4], y0[S::P], gc0[4];
 #pragma unroll
                 for (int t = 0; t < HALF; t++) {
                     const int r = t1 + t;
-                    f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4], y[S::P], gc[4];
+                    f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4];
                     ld_pairs(dl + r * S::CT + tc, s);
                     ld_pairs(xs + r * S::CT + tc, x);
                     ld_pairs(qs + r * S::CT + tc, q);
@@ -139,23 +147,30 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
                     ld_dup(bc2 + (SC_T + r) * S::NP + 4 * n, C);
 #pragma unroll
                     for (int i = 0; i < S::P; i++) {
+                        y0[i] = y[i];
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
+                            if (!i) gc0[j] = gc[j];
                             H[t][i][j] = h[i][j];
                             h[i][j] = fma2(decay2(s[i], A[i][j]), h[i][j], mul2(x[i], B[j]));
                             y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
                             gc[j] = i ? fma2(q[i], h[i][j], gc[j]) : mul2(q[i], h[i][j]);
                         }
                     }
-                    if (gate) put_lanes_sum<NL>(y, n, ys + r * S::CT + tc);
-                    put_groups_sum<NL>(gc, lane, red + ((warp * SC_T + r) * 2 + 1) * S::NP + 4 * n);
+                    if (t) {
+                        put_lanes_sum<NL>(y0, n, ys + (r - 1) * S::CT + tc);
+                        put_groups_sum<NL>(gc0, lane, red + ((warp * SC_T + r - 1) * 2 + 1) * S::NP + 4 * n);
+                    }
                 }
+                put_lanes_sum<NL>(y, n, ys + (t1 + HALF - 1) * S::CT + tc);
+                put_groups_sum<NL>(gc, lane, red + ((warp * SC_T + t1 + HALF - 1) * 2 + 1) * S::NP + 4 * n);
                 // nothing of the way up is kept for the way down but H: the exponentials are taken again
                 asm volatile("" ::: "memory");
+                f32x2 gb[S::P], ea[S::P], gB[4], gb0[S::P], ea0[S::P], gB0[4];
 #pragma unroll
                 for (int t = HALF - 1; t >= 0; t--) {
                     const int r = t1 + t;
-                    f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4], gb[S::P], ea[S::P], gB[4];
+                    f32x2 s[S::P], x[S::P], q[S::P], B[4], C[4];
                     ld_pairs(dl + r * S::CT + tc, s);
                     ld_pairs(xs + r * S::CT + tc, x);
                     ld_pairs(qs + r * S::CT + tc, q);
@@ -163,8 +178,11 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
                     ld_dup(bc2 + (SC_T + r) * S::NP + 4 * n, C);
 #pragma unroll
                     for (int i = 0; i < S::P; i++) {
+                        gb0[i] = gb[i];
+                        ea0[i] = ea[i];
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
+                            if (!i) gB0[j] = gB[j];
                             const f32x2 g = fma2(q[i], C[j], G[i][j]);
                             gB[j] = i ? fma2(g, x[i], gB[j]) : mul2(g, x[i]);
                             gb[i] = j ? fma2(g, B[j], gb[i]) : mul2(g, B[j]);
@@ -174,10 +192,15 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
                             ga[i][j] = fma2(E, s[i], ga[i][j]);
                         }
                     }
-                    put_lanes_sum<NL>(gb, n, GB + r * S::CT + tc);
-                    put_lanes_sum<NL>(ea, n, EA + r * S::CT + tc);
-                    put_groups_sum<NL>(gB, lane, red + (warp * SC_T + r) * 2 * S::NP + 4 * n);
+                    if (t < HALF - 1) {
+                        put_lanes_sum<NL>(gb0, n, GB + (r + 1) * S::CT + tc);
+                        put_lanes_sum<NL>(ea0, n, EA + (r + 1) * S::CT + tc);
+                        put_groups_sum<NL>(gB0, lane, red + (warp * SC_T + r + 1) * 2 * S::NP + 4 * n);
+                    }
                 }
+                put_lanes_sum<NL>(gb, n, GB + t1 * S::CT + tc);
+                put_lanes_sum<NL>(ea, n, EA + t1 * S::CT + tc);
+                put_groups_sum<NL>(gB, lane, red + (warp * SC_T + t1) * 2 * S::NP + 4 * n);
             }
 #pragma unroll
             for (int i = 0; i < S::P; i++)

@@ -73,23 +73,28 @@ template <int NL, int DT> __global__ void __launch_bounds__(FwdTile<NL>::THREADS
         if (a.saved)
             st_tile(a.saved + (((long long)w.b * a.tiles + tile) * a.Dm + w.d0 + tc) * S::NP, S::NP, n, a.N, true, tc,
                         w.cn, h);
+        // a row's sum over states follows the next row's multiply-adds: its shuffles
+        // wait while there is other work, and its store does not hold up their loads
+        f32x2 y[2], before[2];
 #pragma unroll
         for (int t = 0; t < SC_T; t++) {
-            f32x2 s[2], x[2], B[4], C[4], y[2];
+            f32x2 s[2], x[2], B[4], C[4];
             ld_pairs(dl + t * S::CT + tc, s);
             ld_pairs(xs + t * S::CT + tc, x);
             ld_dup(bc2 + t * S::NP + 4 * n, B);
             ld_dup(bc2 + (SC_T + t) * S::NP + 4 * n, C);
 #pragma unroll
             for (int i = 0; i < 2; i++) {
+                before[i] = y[i];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     h[i][j] = fma2(decay2(s[i], A[i][j]), h[i][j], mul2(x[i], B[j]));
                     y[i] = j ? fma2(C[j], h[i][j], y[i]) : mul2(C[j], h[i][j]);
                 }
             }
-            put_lanes_sum<NL>(y, n, ys + t * S::CT + tc);
+            if (t) put_lanes_sum<NL>(before, n, ys + (t - 1) * S::CT + tc);
         }
+        put_lanes_sum<NL>(y, n, ys + (SC_T - 1) * S::CT + tc);
         __syncthreads();
         const int rows = min(SC_T, a.L - t0);
         const Walk<S> to;
