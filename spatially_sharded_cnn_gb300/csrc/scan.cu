@@ -31,22 +31,39 @@ template <int DT> __device__ __forceinline__ void st(void* p, long long i, float
     static_cast<T*>(p)[i] = from_f<T>(v);
 }
 
-// gB and gC: the channel tiles' sums in tile order, a warp a row.
-template <int DT> __global__ void __launch_bounds__(256) scan_bc_kernel(const __grid_constant__ ScanArgs a) {
-    const int lane = threadIdx.x & 31, width = a.G * 2 * a.N;
-    const long long rows = (long long)a.B * a.L, per = rows * width;
-    for (long long r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8LL) {
-        const int b = (int)(r / a.L), t = (int)(r - (long long)b * a.L);
-        for (int j = lane; j < width; j += 32) {
-            const float* p = a.gbc + r * width + j;
-            float v = 0.0f;
+// gB and gC: the channel tiles' sums in tile order, Q states a thread.
+template <int DT, int Q> __global__ void __launch_bounds__(256) scan_bc_kernel(const __grid_constant__ ScanArgs a) {
+    const unsigned width = (unsigned)(a.G * 2 * a.N) / Q;
+    const long long rows = (long long)a.B * a.L, per = rows * width * Q;
+    for (long long q = blockIdx.x * 256LL + threadIdx.x; q < rows * width; q += gridDim.x * 256LL) {
+        const long long r = q < 0x7fffffffLL ? (unsigned)q / width : q / width;
+        const unsigned j = (unsigned)(q - r * width) * Q;
+        const long long b = r < 0x7fffffffLL ? (unsigned)r / (unsigned)a.L : r / a.L;
+        const int t = (int)(r - b * a.L);
+        float v[Q], e[Q];
+        load_pack<float, Q>(a.gbc + q * Q, v);
 #pragma unroll 4
-            for (int m = 0; m < a.ctiles; m++) v += p[m * per];
-            const int g = j / (2 * a.N), k = j - g * 2 * a.N, c = k >= a.N;
-            const hc_rows& o = c ? a.gC : a.gB;
-            st<DT>(o.p, b * o.batch + t * o.row + g * a.N + k - c * a.N, v);
+        for (int m = 1; m < a.ctiles; m++) {
+            load_pack<float, Q>(a.gbc + m * per + q * Q, e);
+#pragma unroll
+            for (int i = 0; i < Q; i++) v[i] += e[i];
         }
+        const unsigned g = j / (2 * a.N), k = j - g * 2 * a.N, c = k >= (unsigned)a.N;
+        const hc_rows& o = c ? a.gC : a.gB;
+        const long long at = b * o.batch + t * o.row + g * a.N + k - c * a.N;
+#pragma unroll
+        for (int i = 0; i < Q; i++) st<DT>(o.p, at + i, v[i]);
     }
+}
+template <int DT> void sum_bc(const ScanArgs& a, cudaStream_t st) {
+    const bool four = a.N % 4 == 0;
+    const long long n = (long long)a.B * a.L * a.G * 2 * a.N / (four ? 4 : 1);
+    const long long blocks = (n + 255) / 256, most = 64LL * device_sm_count();
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    if (four)
+        scan_bc_kernel<DT, 4><<<grid, 256, 0, st>>>(a);
+    else
+        scan_bc_kernel<DT, 1><<<grid, 256, 0, st>>>(a);
 }
 
 // One token: NL lanes a channel, 32 / NL channels a warp.
@@ -97,16 +114,13 @@ struct Step {
 };
 
 hc_status launch_scan_bc(const ScanArgs& a, cudaStream_t st) {
-    const long long rows = (long long)a.B * a.L;
-    if (!a.gbc || rows == 0) return HC_OK;
-    const long long blocks = (rows + 7) / 8, most = 8LL * device_sm_count();
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    if (!a.gbc || a.L == 0) return HC_OK;
     if (a.dtype == HC_DTYPE_F32)
-        scan_bc_kernel<HC_DTYPE_F32><<<grid, 256, 0, st>>>(a);
+        sum_bc<HC_DTYPE_F32>(a, st);
     else if (a.dtype == HC_DTYPE_BF16)
-        scan_bc_kernel<HC_DTYPE_BF16><<<grid, 256, 0, st>>>(a);
+        sum_bc<HC_DTYPE_BF16>(a, st);
     else
-        scan_bc_kernel<HC_DTYPE_F16><<<grid, 256, 0, st>>>(a);
+        sum_bc<HC_DTYPE_F16>(a, st);
     return launched("scan_bc_kernel", st);
 }
 

@@ -340,12 +340,13 @@ template <typename S> __device__ __forceinline__ void put_params(const ScanArgs&
         bD[S::CT + c] = a.D && c < w.cn ? a.D[w.d0 + c] : 0.0f;
     }
 }
-// The step sizes of four channels, from dt + dt_bias; and to `dl` those times
+// The step sizes of four channels, from dt and dt_bias; and to `dl` those times
 // log2 e, so that exp(step * A) is 2^(dl * A).
-__device__ __forceinline__ void steps(const ScanArgs& a, bool on, float (&s)[4], float* dl) {
+__device__ __forceinline__ void steps(const ScanArgs& a, bool on, float (&s)[4], const float (&bias)[4], float* dl) {
     float t[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
+        s[k] += bias[k];
         if (a.softplus) s[k] = softplus_f(s[k]);
         if (!on) s[k] = 0.0f;
         t[k] = s[k] * kLog2e;

@@ -72,33 +72,41 @@ __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREA
             cp_async_wait();
             __syncthreads();
             const Walk<S> at;
+            if (at.on) {
+                // every row's loads before the first row's stores
+                float s[S::STEPS][4], u[S::STEPS][4], q[S::STEPS][4], z[S::STEPS][4], bias[4];
+                load_pack<float, 4>(bD + at.ec, bias);
 #pragma unroll
-            for (int i = 0; i < S::STEPS && at.on; i++) {
-                const int t = at.er + i * S::ROWS, c = t * S::CT + at.ec;
-                float s[4], u[4], q[4], p[4];
-                get<S, DT>(raw, 0, t, at.ec, s);
-                get<S, DT>(raw, 1, t, at.ec, u);
-                get<S, DT>(raw, 2, t, at.ec, q);
-                add4(s, bD + at.ec);
-#pragma unroll
-                for (int k = 0; k < 4; k++) p[k] = a.softplus ? sigmoid_f(s[k]) : 1.0f;
-                steps(a, t0 + t < w.len, s, dl + c);
-                store_pack<float, 4>(us + c, u);
-                store_pack<float, 4>(ps + c, p);
-#pragma unroll
-                for (int k = 0; k < 4; k++) u[k] *= s[k];
-                store_pack<float, 4>(xs + c, u);
-                if (gate) {
-                    get<S, DT>(raw, 3, t, at.ec, u);
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const float r = sigmoid_f(u[k]);
-                        p[k] = q[k] * r * fmaf(u[k], 1.0f - r, 1.0f);
-                        q[k] *= u[k] * r;
-                    }
-                    store_pack<float, 4>(ws + c, p);
+                for (int i = 0; i < S::STEPS; i++) {
+                    const int t = at.er + i * S::ROWS;
+                    get<S, DT>(raw, 0, t, at.ec, s[i]);
+                    get<S, DT>(raw, 1, t, at.ec, u[i]);
+                    get<S, DT>(raw, 2, t, at.ec, q[i]);
+                    if (gate) get<S, DT>(raw, 3, t, at.ec, z[i]);
                 }
-                store_pack<float, 4>(qs + c, q);
+#pragma unroll
+                for (int i = 0; i < S::STEPS; i++) {
+                    const int t = at.er + i * S::ROWS, c = t * S::CT + at.ec;
+                    float p[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) p[k] = a.softplus ? sigmoid_f(s[i][k] + bias[k]) : 1.0f;
+                    store_pack<float, 4>(ps + c, p);
+                    steps(a, t0 + t < w.len, s[i], bias, dl + c);
+                    store_pack<float, 4>(us + c, u[i]);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) u[i][k] *= s[i][k];
+                    store_pack<float, 4>(xs + c, u[i]);
+                    if (gate) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float v = z[i][k], r = sigmoid_f(v);
+                            p[k] = q[i][k] * r * fmaf(v, 1.0f - r, 1.0f);
+                            q[i][k] *= v * r;
+                        }
+                        store_pack<float, 4>(ws + c, p);
+                    }
+                    store_pack<float, 4>(qs + c, q[i]);
+                }
             }
             put_bc<S, DT>(bc, bc2);
             __syncthreads();

@@ -49,23 +49,26 @@ __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_carry_kernel(const 
         cp_async_wait();
         __syncthreads();
         const Walk<S> at;
+        if (at.on) {
+            float s[S::STEPS][4], x[S::STEPS][4], z[S::STEPS][4], bias[4];
+            load_pack<float, 4>(bD + at.ec, bias);
 #pragma unroll
-        for (int i = 0; i < S::STEPS && at.on; i++) {
-            const int t = at.er + i * S::ROWS, q = t * S::CT + at.ec;
-            float s[4], x[4], z[4];
-            get<S, DT>(raw, 0, t, at.ec, s);
-            get<S, DT>(raw, 1, t, at.ec, x);
-            add4(s, bD + at.ec);
-            steps(a, t0 + t < w.len, s, dl + q);
-            if (!REV) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) x[i] *= s[i];
-            } else if (gate) {
-                get<S, DT>(raw, 2, t, at.ec, z);
-#pragma unroll
-                for (int i = 0; i < 4; i++) x[i] *= silu_f(z[i]);
+            for (int i = 0; i < S::STEPS; i++) {
+                get<S, DT>(raw, 0, at.er + i * S::ROWS, at.ec, s[i]);
+                get<S, DT>(raw, 1, at.er + i * S::ROWS, at.ec, x[i]);
+                if (gate) get<S, DT>(raw, 2, at.er + i * S::ROWS, at.ec, z[i]);
             }
-            store_pack<float, 4>(xs + q, x);
+#pragma unroll
+            for (int i = 0; i < S::STEPS; i++) {
+                const int t = at.er + i * S::ROWS, q = t * S::CT + at.ec;
+                steps(a, t0 + t < w.len, s[i], bias, dl + q);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    if (!REV) x[i][k] *= s[i][k];
+                    if (gate) x[i][k] *= silu_f(z[i][k]);
+                }
+                store_pack<float, 4>(xs + q, x[i]);
+            }
         }
         put_bc<S, DT>(bc, bc2);
         __syncthreads();

@@ -44,27 +44,34 @@ template <int NL, int DT> __global__ void __launch_bounds__(FwdTile<NL>::THREADS
         cp_async_wait();
         __syncthreads();
         const Walk<S> at;
-#pragma unroll
-        for (int i = 0; i < S::STEPS && at.on; i++) {
-            const int t = at.er + i * S::ROWS, q = t * S::CT + at.ec;
-            float s[4], x[4], D[4];
-            get<S, DT>(raw, 0, t, at.ec, s);
-            get<S, DT>(raw, 1, t, at.ec, x);
+        if (at.on) {
+            // every row's loads before the first row's stores
+            float s[S::STEPS][4], x[S::STEPS][4], z[S::STEPS][4], D[4], bias[4];
+            load_pack<float, 4>(bD + at.ec, bias);
             load_pack<float, 4>(bD + S::CT + at.ec, D);
-            add4(s, bD + at.ec);
-            steps(a, t0 + t < w.len, s, dl + q);
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                D[k] *= x[k];
-                x[k] *= s[k];
+            for (int i = 0; i < S::STEPS; i++) {
+                get<S, DT>(raw, 0, at.er + i * S::ROWS, at.ec, s[i]);
+                get<S, DT>(raw, 1, at.er + i * S::ROWS, at.ec, x[i]);
+                if (gate) get<S, DT>(raw, 2, at.er + i * S::ROWS, at.ec, z[i]);
             }
-            store_pack<float, 4>(xs + q, x);
-            store_pack<float, 4>(us + q, D);
-            if (gate) {
-                get<S, DT>(raw, 2, t, at.ec, s);
 #pragma unroll
-                for (int k = 0; k < 4; k++) s[k] = silu_f(s[k]);
-                store_pack<float, 4>(gs + q, s);
+            for (int i = 0; i < S::STEPS; i++) {
+                const int t = at.er + i * S::ROWS, q = t * S::CT + at.ec;
+                steps(a, t0 + t < w.len, s[i], bias, dl + q);
+                float o[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    o[k] = D[k] * x[i][k];
+                    x[i][k] *= s[i][k];
+                }
+                store_pack<float, 4>(xs + q, x[i]);
+                store_pack<float, 4>(us + q, o);
+                if (gate) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) z[i][k] = silu_f(z[i][k]);
+                    store_pack<float, 4>(gs + q, z[i]);
+                }
             }
         }
         put_bc<S, DT>(bc, bc2);
@@ -98,20 +105,27 @@ template <int NL, int DT> __global__ void __launch_bounds__(FwdTile<NL>::THREADS
         __syncthreads();
         const int rows = min(SC_T, a.L - t0);
         const Walk<S> to;
+        float o[S::STEPS][4], skip[S::STEPS][4], open[S::STEPS][4];
+        if (to.on) {
 #pragma unroll
-        for (int i = 0; i < S::STEPS; i++) {
-            const int t = to.er + i * S::ROWS, q = t * S::CT + to.ec;
-            if (!to.on || t >= rows) break;
-            float o[4], z[4];
-            load_pack<float, 4>(ys + q, o);
-            add4(o, us + q);
-            if (gate) {
-                load_pack<float, 4>(gs + q, z);
-#pragma unroll
-                for (int k = 0; k < 4; k++) o[k] *= z[k];
+            for (int i = 0; i < S::STEPS; i++) {
+                const int q = (to.er + i * S::ROWS) * S::CT + to.ec;
+                load_pack<float, 4>(ys + q, o[i]);
+                load_pack<float, 4>(us + q, skip[i]);
+                if (gate) load_pack<float, 4>(gs + q, open[i]);
             }
-            if (t0 + t >= w.len) o[0] = o[1] = o[2] = o[3] = 0.0f;
-            put<DT>(out_row<DT>(a.y, w, t0, t), to.ec, w.cn, a.vec, o);
+#pragma unroll
+            for (int i = 0; i < S::STEPS; i++) {
+                const int t = to.er + i * S::ROWS;
+                const bool on = t0 + t < w.len;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    o[i][k] += skip[i][k];
+                    if (gate) o[i][k] *= open[i][k];
+                    if (!on) o[i][k] = 0.0f;
+                }
+                if (t < rows) put<DT>(out_row<DT>(a.y, w, t0, t), to.ec, w.cn, a.vec, o[i]);
+            }
         }
     }
     // rows past the sequence's last tile
