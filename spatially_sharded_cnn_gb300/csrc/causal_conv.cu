@@ -352,13 +352,31 @@ __global__ void __launch_bounds__(128) cc_step_kernel(View<const T> x, View<T> y
     for (int k = 0; k < K - 1; k++) store_pack<T, V>(sb + (long long)k * D, win[k + 1]);
 }
 
+// Channel vectors a block: the split of a row into equal parts (of 128 bytes or
+// more, and whole 32-byte sectors) that leaves the fewest threads without one.
+// (264 fp32 channels: 66 of 128 threads busy with one part, 126 with five.)
+int cc_columns(int cv) {
+    int best = cv < CC_THREADS ? cv : CC_THREADS;
+    double most = 0.0;
+    for (int parts = 1; parts <= 16; parts++) {
+        const int n = (int)cdiv(cv, parts);
+        if (n > CC_THREADS || (parts > 1 && (n % 2 || n < 8))) continue;
+        const double busy = (double)cv * (CC_THREADS / n) / cdiv(cv, n);
+        if (busy > 1.05 * most) {
+            most = busy;
+            best = n;
+        }
+    }
+    return best;
+}
+
 CcShape cc_shape(const hc_causal_conv_desc* d, int V) {
     CcShape s;
     s.B = d->B;
     s.L = d->L;
     s.D = d->D;
     s.cv = d->D / V;
-    s.ncol = s.cv < CC_THREADS ? s.cv : CC_THREADS;
+    s.ncol = cc_columns(s.cv);
     s.R = CC_THREADS / s.ncol;
     // runs of CC_RUN rows, shorter where that leaves the GPU without eight blocks an SM (backward as above: runs of 16,
     // 32, 64 rows 82, 66, 61 us)

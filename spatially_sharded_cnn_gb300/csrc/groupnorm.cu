@@ -423,7 +423,7 @@ template <typename F> __device__ __forceinline__ void gn_join(float2* sm, int gr
         const int n = min(groups - g0, GN_THREADS), g = g0 + tid % n, q = tid / n;
         float2 t = make_float2(0.0f, 0.0f);
         if (q < parts) {
-#pragma unroll 4
+#pragma unroll 8
             for (int k = q; k < chunks; k += parts) {
                 const float2 e = f(k, g);
                 t.x += e.x;
@@ -522,16 +522,16 @@ __global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x,
     // the squared deviations from them
     const float2* p = part + (long long)n * s.chunks * s.G + w.g0;
     gn_join(sm, w.groups, s.chunks, stat, [&](int k, int g) {
-        return make_float2((__ldcg(p + (long long)k * s.G + g).x - __ldcg(p + g).x) * w.pixels(s, k), 0.0f);
+        return make_float2((p[(long long)k * s.G + g].x - p[g].x) * w.pixels(s, k), 0.0f);
     });
     const float over = 1.0f / s.P, values = (float)s.P * s.Cg;
     gn_join(sm, w.groups, s.chunks, join, [&](int k, int g) {
-        const float2 e = __ldcg(p + (long long)k * s.G + g);
-        const float d = e.x - (__ldcg(p + g).x + stat[g].x * over);
+        const float2 e = p[(long long)k * s.G + g];
+        const float d = e.x - (p[g].x + stat[g].x * over);
         return make_float2(fmaf(d * d, (float)w.pixels(s, k) * s.Cg, e.y), 0.0f);
     });
     for (int g = threadIdx.x; g < w.groups; g += GN_THREADS) {
-        const float m = __ldcg(p + g).x + stat[g].x * over, rs = 1.0f / sqrtf(join[g].x / values + eps);
+        const float m = p[g].x + stat[g].x * over, rs = 1.0f / sqrtf(join[g].x / values + eps);
         stat[g] = make_float2(m, rs);
         if (w.chunk == 0) {
             if (mean) mean[n * s.G + w.g0 + g] = m;
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(GN_THREADS, 2) gn_bwd_grid_kernel(View<const T
         }
     gn_meet(s);
     const float2* p = part + (long long)n * s.chunks * s.G + w.g0;
-    gn_join(sm, w.groups, s.chunks, stat, [&](int k, int g) { return __ldcg(p + (long long)k * s.G + g); });
+    gn_join(sm, w.groups, s.chunks, stat, [&](int k, int g) { return p[(long long)k * s.G + g]; });
     if (on) {
         const float over = 1.0f / ((float)s.P * s.Cg);
         float mq[V], mqx[V];
