@@ -56,6 +56,19 @@ __device__ __forceinline__ void gn_walk(int r, int n, int R, L&& load, F&& use) 
         for (int k = 0; k < U; k++) use(p + k * R, q[k], p + k * R < n);
     }
 }
+// The same as one loop of clamped turns: half the code, which a kernel that goes
+// through it a few times waits for more than for the loads.
+template <int U, typename L, typename F>
+__device__ __forceinline__ void gn_walk_short(int r, int n, int R, L&& load, F&& use) {
+#pragma unroll 1
+    for (int p = r; p < n; p += U * R) {
+        decltype(load(0)) q[U];
+#pragma unroll
+        for (int k = 0; k < U; k++) q[k] = load(min(p + k * R, n - 1));
+#pragma unroll
+        for (int k = 0; k < U; k++) use(p + k * R, q[k], p + k * R < n);
+    }
+}
 template <typename T, int V> struct Two {
     Pack<T, V> a, b;
 };
@@ -483,7 +496,7 @@ __global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x,
     for (int i = 0; i < V; i++) pivot[i] = sum[i] = sq[i] = 0.0f;
     if (on) {
         load_pack<T, V>(xb, pivot);
-        gn_walk<8>(r, w.cnt, s.R, [&](int p) { return load_raw<T, V>(xb + p * x.row); },
+        gn_walk_short<2>(r, w.cnt, s.R, [&](int p) { return load_raw<T, V>(xb + p * x.row); },
                    [&](int, const Pack<T, V>& q, bool in) {
                        float v[V];
                        unpack(q, v);
@@ -548,7 +561,7 @@ __global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x,
         T* yb = y.p + n * y.batch + w.p0 * y.row + w.c0 + c;
         // the pixels read last, which L2 still holds, first
         const int top = w.cnt - 1;
-        gn_walk<4>(r, w.cnt, s.R, [&](int p) { return load_raw_last<T, V>(xb + (top - p) * x.row); },
+        gn_walk_short<2>(r, w.cnt, s.R, [&](int p) { return load_raw_last<T, V>(xb + (top - p) * x.row); },
                    [&](int p, const Pack<T, V>& q, bool in) {
                        float v[V];
                        unpack(q, v);
@@ -593,7 +606,7 @@ __global__ void __launch_bounds__(GN_THREADS, 2) gn_bwd_grid_kernel(View<const T
         s1[i] = s2[i] = 0.0f;
     });
     if (on)
-        gn_walk<4>(r, w.cnt, s.R,
+        gn_walk_short<2>(r, w.cnt, s.R,
                    [&](int p) {
                        return Two<T, V>{load_raw<T, V>(xb + p * x.row), load_raw<T, V>(gb + p * gy.row)};
                    },
@@ -638,7 +651,7 @@ __global__ void __launch_bounds__(GN_THREADS, 2) gn_bwd_grid_kernel(View<const T
         });
         T* ob = gx.p + n * gx.batch + w.p0 * gx.row + w.c0 + c;
         const int top = w.cnt - 1;
-        gn_walk<2>(r, w.cnt, s.R,
+        gn_walk_short<2>(r, w.cnt, s.R,
                    [&](int p) {
                        return Two<T, V>{load_raw_last<T, V>(xb + (top - p) * x.row),
                                         load_raw_last<T, V>(gb + (top - p) * gy.row)};
@@ -664,7 +677,7 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 // where the three launches take the call: maps that L2 does not keep between the
 // two reads of `tensors` tensors (7 x 131072 x 256 bf16 image by image, a grid
 // meeting each: 336 us, three launches 262), or a run of whole groups and whole
-// vectors wider than a block's threads.  Slices of at least 128 bytes, a little
+// vectors wider than a block's threads.  Slices of at least 64 bytes, a little
 // wider where that makes them alike, and as many blocks as the GPU holds at once
 // unless a thread would be left with under two pixels.  Up to GN_CLUSTER chunks a
 // slice launch as clusters, which start 2 us sooner than a cooperative grid.
@@ -680,7 +693,7 @@ GnGrid gn_grid(const hc_groupnorm_desc* d, int V, int tensors, int blocks) {
     const long long unit = s.Cg / gcd(s.Cg, V);  // vectors
     if (unit > GN_THREADS || (double)d->N * d->P * d->C * dtype_size(d->dtype) * tensors > 64e6) return s;
     const long long units = s.cv / unit;
-    long long per = cdiv(128, unit * V * (long long)dtype_size(d->dtype));
+    long long per = cdiv(64, unit * V * (long long)dtype_size(d->dtype));
     if (per > units) per = units;
     for (long long q = per; q <= 2 * per && q <= units; q++)
         if (units % q == 0) {
