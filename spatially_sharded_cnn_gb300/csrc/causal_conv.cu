@@ -118,8 +118,9 @@ __device__ __forceinline__ void load_row(const T* xb, long long row, const T* st
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, View<T> y, const float* __restrict__ w,
                                                             const float* __restrict__ bias,
-                                                            const T* __restrict__ state_in, T* __restrict__ state_out,
-                                                            const int* __restrict__ lens, CcShape s) {
+                                                            const T* state_in, T* state_out,
+                                                            const int* lens, CcShape s) {
+    grid_begin();
     const int col = threadIdx.x % s.ncol, r = threadIdx.x / s.ncol;
     const int cvec = blockIdx.y * s.ncol + col;
     if (r >= s.R || cvec >= s.cv) return;
@@ -191,10 +192,11 @@ __global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, Vie
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, View<const T> gy, View<T> gx,
                                                             const float* __restrict__ w, const float* __restrict__ bias,
-                                                            const T* __restrict__ state_in,
-                                                            const T* __restrict__ gstate_out,
-                                                            T* __restrict__ gstate_in, float* __restrict__ part,
-                                                            const int* __restrict__ lens, CcShape s) {
+                                                            const T* state_in,
+                                                            const T* gstate_out,
+                                                            T* gstate_in, float* part,
+                                                            const int* lens, CcShape s) {
+    grid_begin();
     __shared__ float sm[CC_THREADS * V];
     const int col = threadIdx.x % s.ncol, r = threadIdx.x / s.ncol;
     const int cvec = blockIdx.y * s.ncol + col;
@@ -330,8 +332,9 @@ __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, Vie
 // One token: y from the carried rows and x, and the carried rows moved on.
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(128) cc_step_kernel(View<const T> x, View<T> y, const float* __restrict__ w,
-                                                      const float* __restrict__ bias, T* __restrict__ state, int B,
+                                                      const float* __restrict__ bias, T* state, int B,
                                                       int D, int cv) {
+    grid_begin();
     const long long q = blockIdx.x * 128LL + threadIdx.x;
     if (q >= (long long)B * cv) return;
     const int b = (int)(q / cv), c0 = (int)(q % cv) * V;
@@ -448,8 +451,7 @@ struct CcFwd {
     cudaStream_t st;
     template <typename T, int V, int K, int ACT> hc_status operator()() const {
         const CcShape s = cc_shape(d, V);
-        cc_fwd_kernel<T, V, K, ACT><<<dim3((unsigned)(s.B * s.blocks), cdiv(s.cv, s.ncol)), CC_THREADS, 0, st>>>(
-            view<const T>(x), view<T>(y), w, bias, (const T*)state_in, (T*)state_out, lens, s);
+        launch_next(cc_fwd_kernel<T, V, K, ACT>, dim3((unsigned)(s.B * s.blocks), cdiv(s.cv, s.ncol)), CC_THREADS, 0, st, view<const T>(x), view<T>(y), w, bias, (const T*)state_in, (T*)state_out, lens, s);
         return launched("cc_fwd_kernel", st);
     }
 };
@@ -467,8 +469,7 @@ struct CcBwd {
     template <typename T, int V, int K, int ACT> hc_status operator()() const {
         const CcShape s = cc_shape(d, V);
         const unsigned nb = (unsigned)(s.B * s.blocks);
-        cc_bwd_kernel<T, V, K, ACT><<<dim3(nb, cdiv(s.cv, s.ncol)), CC_THREADS, 0, st>>>(
-            view<const T>(x), view<const T>(gy), gx ? view<T>(gx) : View<T>{nullptr, 0, 0}, w, bias,
+        launch_next(cc_bwd_kernel<T, V, K, ACT>, dim3(nb, cdiv(s.cv, s.ncol)), CC_THREADS, 0, st, view<const T>(x), view<const T>(gy), gx ? view<T>(gx) : View<T>{nullptr, 0, 0}, w, bias,
             (const T*)state_in, (const T*)gstate_out, (T*)gstate_in, part, lens, s);
         hc_status e = launched("cc_bwd_kernel", st);
         if (e || !part) return e;
@@ -485,8 +486,7 @@ struct CcStep {
     cudaStream_t st;
     template <typename T, int V, int K, int ACT> hc_status operator()() const {
         const int cv = d->D / V;
-        cc_step_kernel<T, V, K, ACT><<<cdiv((long long)d->B * cv, 128), 128, 0, st>>>(
-            view<const T>(x), view<T>(y), w, bias, (T*)state, d->B, d->D, cv);
+        launch_next(cc_step_kernel<T, V, K, ACT>, cdiv((long long)d->B * cv, 128), 128, 0, st, view<const T>(x), view<T>(y), w, bias, (T*)state, d->B, d->D, cv);
         return launched("cc_step_kernel", st);
     }
 };

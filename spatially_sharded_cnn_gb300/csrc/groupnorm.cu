@@ -115,7 +115,8 @@ __device__ __forceinline__ void gn_block_sum(float2* sm, float (*tot)[GN_THREADS
 
 // part[n][chunk][c] = (mean, sum of squared deviations) of the chunk's pixels.
 template <typename T, int V>
-__global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(View<const T> x, float2* __restrict__ part, GnShape s) {
+__global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(View<const T> x, float2* part, GnShape s) {
+    grid_begin();
     __shared__ float2 sm[GN_THREADS * V];
     __shared__ float tot[2][GN_THREADS * V];
     const int col = threadIdx.x % s.ncol, r = threadIdx.x / s.ncol;
@@ -164,9 +165,10 @@ __device__ __forceinline__ float gn_reduce(float v, float* red) {
 
 // One block per (image, group): its chunks' and channels' means and squared
 // deviations combined.
-__global__ void __launch_bounds__(GN_THREADS) gn_combine_kernel(const float2* __restrict__ part, float eps,
-                                                                float* __restrict__ mean, float* __restrict__ rstd,
+__global__ void __launch_bounds__(GN_THREADS) gn_combine_kernel(const float2* part, float eps,
+                                                                float* mean, float* rstd,
                                                                 GnShape s) {
+    grid_begin();
     __shared__ float red[GN_THREADS / 32];
     const int n = blockIdx.x / s.G, g = blockIdx.x % s.G;
     const float2* pb = part + (long long)n * s.chunks * s.C + g * s.Cg;
@@ -196,8 +198,9 @@ __global__ void __launch_bounds__(GN_THREADS) gn_combine_kernel(const float2* __
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(View<const T> x, View<T> y, const float* __restrict__ gamma,
                                                               const float* __restrict__ beta,
-                                                              const float* __restrict__ mean,
-                                                              const float* __restrict__ rstd, GnShape s) {
+                                                              const float* mean,
+                                                              const float* rstd, GnShape s) {
+    grid_begin();
     const int col = threadIdx.x % s.ncol, r = threadIdx.x / s.ncol;
     const int cvec = blockIdx.z * s.ncol + col, n = s.N - 1 - blockIdx.y;
     if (r >= s.R || cvec >= s.cv) return;
@@ -229,9 +232,10 @@ template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS) gn_bwd_sums_kernel(View<const T> x, View<const T> gy,
                                                                  const float* __restrict__ gamma,
                                                                  const float* __restrict__ beta,
-                                                                 const float* __restrict__ mean,
-                                                                 const float* __restrict__ rstd,
-                                                                 float2* __restrict__ part, GnShape s) {
+                                                                 const float* mean,
+                                                                 const float* rstd,
+                                                                 float2* part, GnShape s) {
+    grid_begin();
     __shared__ float2 sm[GN_THREADS * V];
     __shared__ float tot[2][GN_THREADS * V];
     const int col = threadIdx.x % s.ncol, r = threadIdx.x / s.ncol;
@@ -283,11 +287,12 @@ __global__ void __launch_bounds__(GN_THREADS) gn_bwd_sums_kernel(View<const T> x
 // The others: a few channels' parameter gradients over every image and chunk,
 // thread rows taking every so many of them.
 constexpr int GN_PARAM_CHANNELS = 8;
-__global__ void __launch_bounds__(GN_THREADS) gn_bwd_combine_kernel(const float2* __restrict__ part,
+__global__ void __launch_bounds__(GN_THREADS) gn_bwd_combine_kernel(const float2* part,
                                                                     const float* __restrict__ gamma,
-                                                                    float2* __restrict__ gmean,
+                                                                    float2* gmean,
                                                                     float* __restrict__ ggamma,
                                                                     float* __restrict__ gbeta, GnShape s) {
+    grid_begin();
     __shared__ float red[GN_THREADS / 32];
     __shared__ float2 col[GN_THREADS / GN_PARAM_CHANNELS][GN_PARAM_CHANNELS + 1];
     if ((int)blockIdx.x < s.N * s.G) {
@@ -337,9 +342,10 @@ template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS) gn_bwd_apply_kernel(View<const T> x, View<const T> gy, View<T> gx,
                                                                   const float* __restrict__ gamma,
                                                                   const float* __restrict__ beta,
-                                                                  const float* __restrict__ mean,
-                                                                  const float* __restrict__ rstd,
-                                                                  const float2* __restrict__ gmean, GnShape s) {
+                                                                  const float* mean,
+                                                                  const float* rstd,
+                                                                  const float2* gmean, GnShape s) {
+    grid_begin();
     const int col = threadIdx.x % s.ncol, r = threadIdx.x / s.ncol;
     const int cvec = blockIdx.z * s.ncol + col, n = s.N - 1 - blockIdx.y;
     if (r >= s.R || cvec >= s.cv) return;
@@ -473,8 +479,9 @@ template <int V, typename F> __device__ __forceinline__ void gn_groups(int c, in
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x, View<T> y, const float* __restrict__ gamma,
                                                                 const float* __restrict__ beta, float eps,
-                                                                float* __restrict__ mean, float* __restrict__ rstd,
+                                                                float* mean, float* rstd,
                                                                 float2* part, GnGrid s) {
+    grid_begin();
     __shared__ float2 sm[GN_THREADS * V];
     __shared__ float tot[2][GN_THREADS * V];
     __shared__ float2 stat[GN_THREADS * V];
@@ -578,9 +585,10 @@ template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS, 2) gn_bwd_grid_kernel(View<const T> x, View<const T> gy, View<T> gx,
                                                                     const float* __restrict__ gamma,
                                                                     const float* __restrict__ beta,
-                                                                    const float* __restrict__ mean,
-                                                                    const float* __restrict__ rstd, float2* part,
-                                                                    float* __restrict__ param, GnGrid s) {
+                                                                    const float* mean,
+                                                                    const float* rstd, float2* part,
+                                                                    float* param, GnGrid s) {
+    grid_begin();
     __shared__ float2 sm[GN_THREADS * V];
     __shared__ float tot[2][GN_THREADS * V];
     float2* stat = reinterpret_cast<float2*>(tot);  // free once the block's groups are joined
@@ -673,6 +681,17 @@ __global__ void __launch_bounds__(GN_THREADS, 2) gn_bwd_grid_kernel(View<const T
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
+// SMs whose blocks can be there together: an imposed count (hc_set_sm_count) above
+// the device's does not make more.
+int gn_sms() {
+    const int sms = device_sm_count();
+    if (g_sm_override.load(std::memory_order_relaxed) <= 0) return sms;
+    int dev = 0, there = 0;
+    cudaGetDevice(&dev);
+    if (cudaDeviceGetAttribute(&there, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) cudaGetLastError();
+    return there > 0 && there < sms ? there : sms;
+}
+
 // The one-launch form's grid for kernels of `blocks` blocks an SM, or chunks = 0
 // where the three launches take the call: maps that L2 does not keep between the
 // two reads of `tensors` tensors (7 x 131072 x 256 bf16 image by image, a grid
@@ -705,7 +724,7 @@ GnGrid gn_grid(const hc_groupnorm_desc* d, int V, int tensors, int blocks) {
     s.R = GN_THREADS / s.ncol;
     s.slices = (int)cdiv(s.cv, s.ncol);
     const long long useful = cdiv(d->P, 2LL * s.R);
-    long long chunks = (long long)blocks * device_sm_count() / ((long long)s.slices * d->N);
+    long long chunks = (long long)blocks * gn_sms() / ((long long)s.slices * d->N);
     if (chunks > useful) chunks = useful;
     if (chunks < 1) return s;  // more (image, slice) pairs than blocks at once
     s.chunk = (int)cdiv(d->P, chunks);
@@ -720,17 +739,20 @@ void launch_grid(void (*k)(P...), const GnGrid& s, cudaStream_t st, A... args) {
     cfg.gridDim = dim3((unsigned)s.slices * s.chunks * s.N);
     cfg.blockDim = dim3(GN_THREADS);
     cfg.stream = st;
-    cudaLaunchAttribute at = {};
+    cudaLaunchAttribute at[2] = {};
     if (s.chunks <= GN_CLUSTER) {
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = s.chunks;
-        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = s.chunks;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
     } else {
-        at.id = cudaLaunchAttributeCooperative;
-        at.val.cooperative = 1;
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+        cfg.numAttrs = 1;
     }
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.attrs = at;
     cudaLaunchKernelEx(&cfg, k, P(args)...);
 }
 
@@ -810,13 +832,12 @@ struct GnFwd {
         }
         const GnShape s = gn_shape(d, V);
         const dim3 grid(s.chunks, s.N, cdiv(s.cv, s.ncol));
-        gn_stats_kernel<T, V><<<grid, GN_THREADS, 0, st>>>(view<const T>(x), part, s);
+        launch_next(gn_stats_kernel<T, V>, grid, GN_THREADS, 0, st, view<const T>(x), part, s);
         hc_status e = launched("gn_stats_kernel", st);
         if (e) return e;
-        gn_combine_kernel<<<s.N * s.G, GN_THREADS, 0, st>>>(part, d->eps, mean, rstd, s);
+        launch_next(gn_combine_kernel, s.N * s.G, GN_THREADS, 0, st, part, d->eps, mean, rstd, s);
         if ((e = launched("gn_combine_kernel", st))) return e;
-        gn_apply_kernel<T, V, ACT>
-            <<<grid, GN_THREADS, 0, st>>>(view<const T>(x), view<T>(y), gamma, beta, mean, rstd, s);
+        launch_next(gn_apply_kernel<T, V, ACT>, grid, GN_THREADS, 0, st, view<const T>(x), view<T>(y), gamma, beta, mean, rstd, s);
         return launched("gn_apply_kernel", st);
     }
 };
@@ -841,14 +862,13 @@ struct GnBwd {
         }
         const GnShape s = gn_shape(d, V);
         const dim3 grid(s.chunks, s.N, cdiv(s.cv, s.ncol));
-        gn_bwd_sums_kernel<T, V, ACT>
-            <<<grid, GN_THREADS, 0, st>>>(view<const T>(x), view<const T>(gy), gamma, beta, mean, rstd, part, s);
+        launch_next(gn_bwd_sums_kernel<T, V, ACT>, grid, GN_THREADS, 0, st, view<const T>(x), view<const T>(gy), gamma, beta, mean, rstd, part, s);
         hc_status e = launched("gn_bwd_sums_kernel", st);
         if (e) return e;
         const unsigned params = ggamma || gbeta ? cdiv(s.C, GN_PARAM_CHANNELS) : 0;
-        gn_bwd_combine_kernel<<<s.N * s.G + params, GN_THREADS, 0, st>>>(part, gamma, gmean, ggamma, gbeta, s);
+        launch_next(gn_bwd_combine_kernel, s.N * s.G + params, GN_THREADS, 0, st, part, gamma, gmean, ggamma, gbeta, s);
         if ((e = launched("gn_bwd_combine_kernel", st))) return e;
-        gn_bwd_apply_kernel<T, V, ACT><<<grid, GN_THREADS, 0, st>>>(view<const T>(x), view<const T>(gy), view<T>(gx),
+        launch_next(gn_bwd_apply_kernel<T, V, ACT>, grid, GN_THREADS, 0, st, view<const T>(x), view<const T>(gy), view<T>(gx),
                                                                    gamma, beta, mean, rstd, gmean, s);
         return launched("gn_bwd_apply_kernel", st);
     }

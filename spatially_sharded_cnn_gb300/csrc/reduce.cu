@@ -124,16 +124,16 @@ __global__ void column_group_kernel(const float* __restrict__ in, float* __restr
 
 // Column totals (launch_column_totals): a block takes 32 columns; warp w adds
 // rows w, w + 32, ..., then the warps' sums are added in order.
-__global__ void __launch_bounds__(1024) column_totals_kernel(const float* __restrict__ in, long long rows,
-                                                             float* __restrict__ a, int na, float* __restrict__ b,
-                                                             int nb, float* __restrict__ c, int nc) {
+__global__ void __launch_bounds__(1024) column_totals_kernel(const float* in, long long rows, float* a, int na,
+                                                             float* b, int nb, float* c, int nc) {
+    grid_begin();
     __shared__ float sm[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int k = blockIdx.x * 32 + lane, count = na + nb + nc;
     float t = 0.0f;
     if (k < count) {
 #pragma unroll 4
-        for (long long r = w; r < rows; r += 32) t += __ldg(in + r * count + k);
+        for (long long r = w; r < rows; r += 32) t += in[r * count + k];
     }
     sm[w][lane] = t;
     __syncthreads();
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(1024) column_totals_kernel(const float* __rest
 
 hc_status launch_column_totals(const float* in, long long rows, float* a, int na, float* b, int nb, float* c, int nc,
                                cudaStream_t st) {
-    column_totals_kernel<<<cdiv((long long)na + nb + nc, 32), 1024, 0, st>>>(in, rows, a, na, b, nb, c, nc);
+    launch_next(column_totals_kernel, cdiv((long long)na + nb + nc, 32), 1024, 0, st, in, rows, a, na, b, nb, c, nc);
     return launched("column_totals_kernel", st);
 }
 

@@ -33,6 +33,7 @@ template <int DT> __device__ __forceinline__ void st(void* p, long long i, float
 
 // gB and gC: the channel tiles' sums in tile order, Q states a thread.
 template <int DT, int Q> __global__ void __launch_bounds__(256) scan_bc_kernel(const __grid_constant__ ScanArgs a) {
+    grid_begin();
     const unsigned width = (unsigned)(a.G * 2 * a.N) / Q;
     const long long rows = (long long)a.B * a.L, per = rows * width * Q;
     for (long long q = blockIdx.x * 256LL + threadIdx.x; q < rows * width; q += gridDim.x * 256LL) {
@@ -61,14 +62,15 @@ template <int DT> void sum_bc(const ScanArgs& a, cudaStream_t st) {
     const long long blocks = (n + 255) / 256, most = 64LL * device_sm_count();
     const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     if (four)
-        scan_bc_kernel<DT, 4><<<grid, 256, 0, st>>>(a);
+        launch_next(scan_bc_kernel<DT, 4>, grid, 256, 0, st, a);
     else
-        scan_bc_kernel<DT, 1><<<grid, 256, 0, st>>>(a);
+        launch_next(scan_bc_kernel<DT, 1>, grid, 256, 0, st, a);
 }
 
 // One token: NL lanes a channel, 32 / NL channels a warp.
 template <int NL, int DT>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanArgs a, float* __restrict__ state) {
+    grid_begin();
     const int lane = threadIdx.x & 31, n = lane % NL;
     const long long q = (blockIdx.x * 4LL + (threadIdx.x >> 5)) * (32 / NL) + lane / NL;
     const bool on = q < (long long)a.B * a.Dm;
@@ -108,7 +110,7 @@ struct Step {
     float* state;
     cudaStream_t st;
     template <int NL, int DT> hc_status run() {
-        scan_step_kernel<NL, DT><<<cdiv((long long)a.B * a.Dm, 4 * (32 / NL)), 128, 0, st>>>(a, state);
+        launch_next(scan_step_kernel<NL, DT>, cdiv((long long)a.B * a.Dm, 4 * (32 / NL)), 128, 0, st, a, state);
         return launched("scan_step_kernel", st);
     }
 };

@@ -18,6 +18,7 @@ template <int NL> constexpr size_t bwd_smem() {
 constexpr int HALF = SC_T / 2;
 template <int NL, int DT>
 __global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREADS) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
+    grid_begin();
     using S = BwdTile<NL>;
     using T = typename EltOf<DT>::type;
     extern __shared__ float4 sm4[];
@@ -305,8 +306,7 @@ struct Launch {
             return cudaFuncSetAttribute(scan_bwd_kernel<NL, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)bwd_smem<NL>()) == cudaSuccess;
         });
-        scan_bwd_kernel<NL, DT>
-            <<<(unsigned)a.B * a.segs * a.G * a.ctiles, BwdTile<NL>::THREADS, bwd_smem<NL>(), st>>>(a);
+        launch_next(scan_bwd_kernel<NL, DT>, (unsigned)a.B * a.segs * a.G * a.ctiles, BwdTile<NL>::THREADS, bwd_smem<NL>(), st, a);
         return launched("scan_bwd_kernel", st);
     }
 };

@@ -14,6 +14,7 @@ template <int NL> constexpr size_t carry_smem() {
 }
 template <int NL, int DT, bool REV>
 __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_carry_kernel(const __grid_constant__ ScanArgs a) {
+    grid_begin();
     using S = FwdTile<NL>;
     extern __shared__ float4 sm4[];
     float* dl = reinterpret_cast<float*>(sm4);
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_carry_kernel(const 
 constexpr int SJ_THREADS = 256;
 template <bool REV, int R>
 __global__ void __launch_bounds__(SJ_THREADS) scan_join_kernel(const __grid_constant__ ScanArgs a, int NP) {
+    grid_begin();
     constexpr int S = SJ_THREADS / R;
     __shared__ float hs[R][S + 1], as[R][S + 1];
     const int col = threadIdx.x % S, r = threadIdx.x / S;
@@ -152,8 +154,7 @@ __global__ void __launch_bounds__(SJ_THREADS) scan_join_kernel(const __grid_cons
     }
 }
 template <bool REV, int R> void join(const ScanArgs& a, int NP, cudaStream_t st) {
-    scan_join_kernel<REV, R>
-        <<<dim3(cdiv((long long)a.Dm * NP, SJ_THREADS / R), a.B), SJ_THREADS, 0, st>>>(a, NP);
+    launch_next(scan_join_kernel<REV, R>, dim3(cdiv((long long)a.Dm * NP, SJ_THREADS / R), a.B), SJ_THREADS, 0, st, a, NP);
 }
 
 template <bool REV> struct Launch {
@@ -165,8 +166,7 @@ template <bool REV> struct Launch {
             return cudaFuncSetAttribute(scan_carry_kernel<NL, DT, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)carry_smem<NL>()) == cudaSuccess;
         });
-        scan_carry_kernel<NL, DT, REV>
-            <<<(unsigned)a.B * a.segs * a.G * a.ctiles, FwdTile<NL>::THREADS, carry_smem<NL>(), st>>>(a);
+        launch_next(scan_carry_kernel<NL, DT, REV>, (unsigned)a.B * a.segs * a.G * a.ctiles, FwdTile<NL>::THREADS, carry_smem<NL>(), st, a);
         const hc_status e = launched("scan_carry_kernel", st);
         if (e) return e;
         constexpr int NP = FwdTile<NL>::NP;

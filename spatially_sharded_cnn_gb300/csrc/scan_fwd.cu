@@ -9,6 +9,7 @@ template <int NL> constexpr size_t fwd_smem() {
     return sizeof(float) * (5 * S::PLANE + 2 * S::CT + 4 * SC_T * S::NP + 3 * S::PLANE);
 }
 template <int NL, int DT> __global__ void __launch_bounds__(FwdTile<NL>::THREADS) scan_fwd_kernel(const __grid_constant__ ScanArgs a) {
+    grid_begin();
     using S = FwdTile<NL>;
     extern __shared__ float4 sm4[];
     float* dl = reinterpret_cast<float*>(sm4);  // step sizes * log2 e
@@ -147,8 +148,7 @@ struct Launch {
             return cudaFuncSetAttribute(scan_fwd_kernel<NL, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)fwd_smem<NL>()) == cudaSuccess;
         });
-        scan_fwd_kernel<NL, DT>
-            <<<(unsigned)a.B * a.segs * a.G * a.ctiles, FwdTile<NL>::THREADS, fwd_smem<NL>(), st>>>(a);
+        launch_next(scan_fwd_kernel<NL, DT>, (unsigned)a.B * a.segs * a.G * a.ctiles, FwdTile<NL>::THREADS, fwd_smem<NL>(), st, a);
         return launched("scan_fwd_kernel", st);
     }
 };
