@@ -73,6 +73,22 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw_last
     u.w = __ldcs(reinterpret_cast<const W*>(p));
     return u.q;
 }
+// For rows that no cache holds until they are read again.
+template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw_stream(const T* p) {
+    if constexpr (sizeof(T) * V == 16) {
+        union U {
+            uint4 w;
+            Pack<T, V> q;
+            __device__ U() {}
+        } u;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.w.x), "=r"(u.w.y), "=r"(u.w.z), "=r"(u.w.w)
+                     : "l"(p));
+        return u.q;
+    } else {
+        return load_raw<T, V>(p);
+    }
+}
 template <typename T, int V> __device__ __forceinline__ void store_pack_last(T* p, const float (&f)[V]) {
     using W = typename Word<sizeof(T) * V>::type;
     union U {
