@@ -38,9 +38,14 @@ __device__ __forceinline__ void st1(void* p, long long i, int dt, float v) {
     else
         static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
-// States n0 .. n0 + 3 of a [..][N] fp32 row (past N: zeros / not written).
+// States n0 .. n0 + 3 of a [..][N] fp32 row (past N: zeros / not written): 16 bytes
+// at once where the row allows it -- a row of partial sums, (N + 2) * D floats
+// after the one before it, need not start on 16 bytes even if N is a multiple of 4.
+__device__ __forceinline__ bool states_vec(const float* p, int N) {
+    return N % 4 == 0 && ((uintptr_t)p & 15u) == 0;
+}
 __device__ __forceinline__ void ld_states(const float* p, int n0, int N, float (&f)[4]) {
-    if (N % 4 == 0 && n0 < N) {
+    if (states_vec(p, N) && n0 < N) {
         load_pack<float, 4>(p + n0, f);
         return;
     }
@@ -48,7 +53,7 @@ __device__ __forceinline__ void ld_states(const float* p, int n0, int N, float (
     for (int k = 0; k < 4; k++) f[k] = n0 + k < N ? p[n0 + k] : 0.0f;
 }
 __device__ __forceinline__ void st_states(float* p, int n0, int N, const float (&f)[4]) {
-    if (N % 4 == 0 && n0 < N) {
+    if (states_vec(p, N) && n0 < N) {
         store_pack<float, 4>(p + n0, f);
         return;
     }

@@ -177,3 +177,27 @@ def test_calls_back_to_back_see_each_other(hc):
                                gr, br, 4, 1e-5, "none")["y"]
             near("one round", cur, want, 1e-4)  # the norm divides by what the scan leaves
     assert torch.equal(first, cur)
+
+
+@pytest.mark.parametrize("D", [47, 1, 5, 130])
+@pytest.mark.parametrize("N", [4, 8, 16, 32, 64])
+def test_scan_odd_channels_many_sequences(hc, D, N):
+    """Channel counts whose rows of partial sums start off 16 bytes from the second sequence on."""
+    B, L, t, lens = 5, 6, torch.float32, [6, 0, 1, 3, 5]
+    x, r = scan_data(B, L, D, 1, N, t, True, True, lens, 0, seed=30)
+    ref = M.scan(r["u"], r["dt"], r["A"], r["Bm"], r["Cm"], 1, True, r["D"], r["z"], r["bias"], r["h0"], lens, r["gy"],
+                 r["ghT"])
+    d = hc.selective_scan_desc(B, L, D, N, t)
+    ws, nb = space(hc, hc.hc_selective_scan_workspace_size(d, 1))
+    saved = space(hc, hc.hc_selective_scan_saved_size(d))[0]
+    kw = dict(D=x["D"], z=x["z"], dt_bias=x["bias"], h0=x["h0"], ws=ws, ws_bytes=nb,
+              lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    args = (x["u"], x["dt"], x["A"], x["Bm"], x["Cm"])
+    y, hT = Out((B, L, D)), Out((B, D, N))
+    hc.check(hc.hc_selective_scan_fwd(d, *args, y.t, hT=hT.t, saved=saved, **kw))
+    o = dict(gu=Out((B, L, D)), gdt=Out((B, L, D)), gA=Out((D, N)), gB=Out((B, L, N)), gC=Out((B, L, N)))
+    rest = dict(gz=Out((B, L, D)), gD=Out((D,)), gdt_bias=Out((D,)), gh0=Out((B, D, N)))
+    hc.check(hc.hc_selective_scan_bwd(d, *args, x["gy"], saved, *(v.t for v in o.values()), ghT=x["ghT"],
+                                      **{k: v.t for k, v in rest.items()}, **kw))
+    for k, v in dict(o, y=y, state=hT, gstate=rest.pop("gh0"), **rest).items():
+        near(k, v, ref[k], 1e-4 if k in ("gA", "gD", "gdt_bias") else 1e-5)
