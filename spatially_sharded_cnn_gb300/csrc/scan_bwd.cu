@@ -10,6 +10,13 @@ namespace {
 // through them.  A tile's first state was saved; that of its later half is
 // recomputed from it.  Half tiles keep a thread at 168 registers, three blocks an
 // SM; whole tiles take 255 and two.
+//
+// A state takes 5 fp32 operations and an exponential on the way up, 3 and one more
+// in an earlier half's recomputation, 8 and one on the way down: 14.5 and 2.5 a row
+// on average.  224 x 1024 x 256 fp32, 16 states: 1190 us, a third of the fp32 pipe
+// and half of the issue slots; bound by the latency between dependent instructions
+// with three warps a scheduler (a warp's 32 channels x 8 rows are about 3500
+// instructions, a third of them the elementwise walks').
 template <int NL> constexpr size_t bwd_smem() {
     using S = BwdTile<NL>;
     return sizeof(float) * (9 * S::PLANE + 2 * S::CT + 2 * S::ROWS * S::CT + 4 * SC_T * S::NP + S::W * SC_T * 2 * S::NP +
@@ -17,7 +24,8 @@ template <int NL> constexpr size_t bwd_smem() {
 }
 constexpr int HALF = SC_T / 2;
 template <int NL, int DT>
-__global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREADS) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
+__global__ void __launch_bounds__(BwdTile<NL>::THREADS, 384 / BwdTile<NL>::THREADS)
+    scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
     grid_begin();
     using S = BwdTile<NL>;
     using T = typename EltOf<DT>::type;
@@ -306,7 +314,8 @@ struct Launch {
             return cudaFuncSetAttribute(scan_bwd_kernel<NL, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)bwd_smem<NL>()) == cudaSuccess;
         });
-        launch_next(scan_bwd_kernel<NL, DT>, (unsigned)a.B * a.segs * a.G * a.ctiles, BwdTile<NL>::THREADS, bwd_smem<NL>(), st, a);
+        launch_next(scan_bwd_kernel<NL, DT>, (unsigned)a.B * a.segs * a.G * a.ctiles, BwdTile<NL>::THREADS,
+                    bwd_smem<NL>(), st, a);
         return launched("scan_bwd_kernel", st);
     }
 };
