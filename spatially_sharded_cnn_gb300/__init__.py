@@ -3,6 +3,6 @@
 The compute path is the C-ABI library built from ``csrc/`` (hand-written CUDA);
 ``spatially_sharded_cnn_gb300.hc`` is its thin ctypes binding and raises at
 import when the library has not been built.  ``synth`` holds the seeded input
-generators.
+generators, ``mixer`` a temporal mixer built from the channels-last operators.
 """
-__all__ = ["hc", "synth"]
+__all__ = ["hc", "mixer", "synth"]
