@@ -446,6 +446,15 @@ def _addr(t) -> int:
     return 0 if t is None else t if isinstance(t, int) else t.data_ptr()
 
 
+def _lens(t) -> int:
+    """Sequence lengths: int32, one after another."""
+    if t is None or isinstance(t, int):
+        return t or 0
+    if str(t.dtype) != "torch.int32" or not t.is_contiguous():
+        raise HcError(HC_ERR_INVALID_ARG, "lengths are a contiguous int32 tensor")
+    return t.data_ptr()
+
+
 def _refuse(t, shape):
     if t.shape != shape:
         raise HcError(HC_ERR_INVALID_ARG, f"a tensor of shape {tuple(t.shape)} where {shape} is wanted")
@@ -512,7 +521,7 @@ def hc_causal_conv_fwd(d, x, w, bias, y, state_in=None, state_out=None, lens=Non
     """x and y are (B, L, D) tensors with adjacent channels; states (B, K - 1, D) contiguous; lens int32 (B,)."""
     s = d.B, d.L, d.D
     return _lib.hc_causal_conv_fwd(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _rows(y, *s), _addr(state_in),
-                                   _addr(state_out), _addr(lens), _stream(stream))
+                                   _addr(state_out), _lens(lens), _stream(stream))
 
 
 def hc_causal_conv_workspace_size(d: hc_causal_conv_desc):
@@ -527,7 +536,7 @@ def hc_causal_conv_bwd(d, x, w, bias, gy, gx, gw, gb, state_in=None, gstate_out=
     s = d.B, d.L, d.D
     return _lib.hc_causal_conv_bwd(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _rows(gy, *s),
                                    None if gx is None else _rows(gx, *s), _addr(gw), _addr(gb), _addr(state_in),
-                                   _addr(gstate_out), _addr(gstate_in), _addr(lens), _addr(ws), ws_bytes,
+                                   _addr(gstate_out), _addr(gstate_in), _lens(lens), _addr(ws), ws_bytes,
                                    _stream(stream))
 
 
@@ -563,7 +572,7 @@ def hc_selective_scan_fwd(d, u, dt, A, Bm, Cm, y, D=None, z=None, dt_bias=None, 
     """u, dt, z, y are (B, L, D) and Bm, Cm (B, L, groups * d_state) tensors with adjacent channels; lens int32 (B,)."""
     lead = (d.B, d.L)
     return _lib.hc_selective_scan_fwd(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(h0),
-                                      _addr(lens), _rows(y, *lead, d.D), _addr(hT), _addr(saved), _addr(ws), ws_bytes,
+                                      _lens(lens), _rows(y, *lead, d.D), _addr(hT), _addr(saved), _addr(ws), ws_bytes,
                                       _stream(stream))
 
 
@@ -576,7 +585,7 @@ def hc_selective_scan_bwd(d, u, dt, A, Bm, Cm, gy, saved, gu, gdt, gA, gB, gC, D
     grads = _pack_scan_grad(*_view(gu, *s), *_view(gdt, *s), *_view(gB, *m), *_view(gC, *m), *_view(gz, *s), _addr(gA),
                             _addr(gD), _addr(gdt_bias), _addr(gh0))
     return _lib.hc_selective_scan_bwd(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(h0),
-                                      _addr(lens), _addr(saved), _rows(gy, *s), _addr(ghT), grads, _addr(ws), ws_bytes,
+                                      _lens(lens), _addr(saved), _rows(gy, *s), _addr(ghT), grads, _addr(ws), ws_bytes,
                                       _stream(stream))
 
 

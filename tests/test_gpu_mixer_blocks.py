@@ -201,3 +201,38 @@ def test_scan_odd_channels_many_sequences(hc, D, N):
                                       **{k: v.t for k, v in rest.items()}, **kw))
     for k, v in dict(o, y=y, state=hT, gstate=rest.pop("gh0"), **rest).items():
         near(k, v, ref[k], 1e-4 if k in ("gA", "gD", "gdt_bias") else 1e-5)
+
+
+def test_captured_into_a_graph(hc):
+    """Convolution, scan in segments and norm (a cluster and a cooperative grid) replayed from a CUDA graph."""
+    B, L, D, N, t = 1, 512, 64, 16, torch.float32
+    x, _ = scan_data(B, L, D, 1, N, t, True, False, None, 0, seed=31)
+    w = Data(32, t).param(D, 4)[0]
+    gamma, beta = Data(33, t).param(D, shift=1.0)[0], Data(34, t).param(D)[0]
+    dc, ds = hc.causal_conv_desc(B, L, D, 4, t, hc.HC_PW_SILU), hc.selective_scan_desc(B, L, D, N, t)
+    big, small = hc.groupnorm_desc(B, L, D, 4, t), hc.groupnorm_desc(B, 32, D, 4, t)
+    ws, nb = space(hc, hc.hc_selective_scan_workspace_size(ds, 0))
+    ns, nn = space(hc, hc.hc_groupnorm_workspace_size(big, 0))
+    ms, nm = space(hc, hc.hc_groupnorm_workspace_size(small, 0))
+    a, b, c = (torch.empty(B, L, D, device="cuda") for _ in range(3))
+    e = torch.empty(B, 32, D, device="cuda")
+
+    def chain(stream=None):
+        hc.check(hc.hc_causal_conv_fwd(dc, x["u"], w, None, a, stream=stream))
+        hc.check(hc.hc_selective_scan_fwd(ds, a, x["dt"], x["A"], x["Bm"], x["Cm"], b, z=x["z"], ws=ws, ws_bytes=nb,
+                                          stream=stream))
+        hc.check(hc.hc_groupnorm_fwd(big, b, gamma, beta, c, ws=ns, ws_bytes=nn, stream=stream))
+        hc.check(hc.hc_groupnorm_fwd(small, c[:, :32], gamma, beta, e, ws=ms, ws_bytes=nm, stream=stream))
+
+    chain()
+    torch.cuda.synchronize()
+    want = [v.clone() for v in (a, b, c, e)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(torch.cuda.current_stream())
+    for v in (a, b, c, e):
+        v.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    for v, r in zip((a, b, c, e), want):
+        assert torch.equal(v, r)

@@ -138,3 +138,13 @@ def test_binding_checks_shapes_and_channels(hc):
     assert hc._dtype(torch.float64) == -1
     assert hc._view(x.half(), 2, 8, 8)[3] == hc.HC_DTYPE_F16
     assert hc._view(x[:, 0], 2, 8) == (x.data_ptr(), 64, 0, hc.HC_DTYPE_F32)
+
+
+def test_binding_checks_lengths(hc):
+    import torch
+    assert hc._lens(None) == 0
+    ok = torch.tensor([1, 2], dtype=torch.int32)
+    assert hc._lens(ok) == ok.data_ptr()
+    for bad in (torch.tensor([1, 2]), torch.zeros(4, dtype=torch.int32)[::2]):
+        with pytest.raises(hc.HcError):
+            hc._lens(bad)
