@@ -72,7 +72,7 @@ template <int DT> void sum_bc(const ScanArgs& a, cudaStream_t st) {
 // states (64 x 2048 x 16: 17 MB): 12 us from DRAM; called again and again, with the
 // states in L2, 8.5 us a call from Python, most of it the call.
 template <int NL, int DT>
-__global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanArgs a, float* __restrict__ state) {
+__global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanArgs a, float* state) {
     grid_begin();
     const int lane = threadIdx.x & 31, n = lane % NL;
     const long long q = (blockIdx.x * 4LL + (threadIdx.x >> 5)) * (32 / NL) + lane / NL;
