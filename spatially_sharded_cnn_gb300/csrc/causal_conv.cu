@@ -118,8 +118,8 @@ __device__ __forceinline__ void load_row(const T* xb, long long row, const T* st
 // 8 x 4096 x 1024 bf16, K = 4, SiLU (134 MB): 30 us a call, 4.5 TB/s; bound by
 // memory and the last wave of its blocks.
 template <typename T, int V, int K, int ACT>
-__global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, View<T> y, const float* __restrict__ w,
-                                                            const float* __restrict__ bias,
+__global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, View<T> y, const float* w,
+                                                            const float* bias,
                                                             const T* state_in, T* state_out,
                                                             const int* lens, CcShape s) {
     grid_begin();
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, Vie
 // registers; bound by the latency of its loads.
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, View<const T> gy, View<T> gx,
-                                                            const float* __restrict__ w, const float* __restrict__ bias,
+                                                            const float* w, const float* bias,
                                                             const T* state_in,
                                                             const T* gstate_out,
                                                             T* gstate_in, float* part,
@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, Vie
 // One token: y from the carried rows and x, and the carried rows moved on.  64 x
 // 2048 bf16: 5.9 us a call from Python, most of it the call.
 template <typename T, int V, int K, int ACT>
-__global__ void __launch_bounds__(128) cc_step_kernel(View<const T> x, View<T> y, const float* __restrict__ w,
-                                                      const float* __restrict__ bias, T* state, int B,
+__global__ void __launch_bounds__(128) cc_step_kernel(View<const T> x, View<T> y, const float* w,
+                                                      const float* bias, T* state, int B,
                                                       int D, int cv) {
     grid_begin();
     const long long q = blockIdx.x * 128LL + threadIdx.x;

@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_combine_kernel(const float2* pa
 // y = act((x - mean) * (rstd * gamma) + beta): the same map read again and y
 // written, 940 MB in 154 us, 6.1 TB/s; bound by memory.
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(View<const T> x, View<T> y, const float* __restrict__ gamma,
-                                                              const float* __restrict__ beta,
+__global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(View<const T> x, View<T> y, const float* gamma,
+                                                              const float* beta,
                                                               const float* mean,
                                                               const float* rstd, GnShape s) {
     grid_begin();
@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(View<const T> x, V
 // g = gy * act'(pre).  7 x 65536 x 256 fp32: x and gy, 940 MB, in 177 us, 5.3 TB/s.
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS) gn_bwd_sums_kernel(View<const T> x, View<const T> gy,
-                                                                 const float* __restrict__ gamma,
-                                                                 const float* __restrict__ beta,
+                                                                 const float* gamma,
+                                                                 const float* beta,
                                                                  const float* mean,
                                                                  const float* rstd,
                                                                  float2* part, GnShape s) {
@@ -308,10 +308,10 @@ __global__ void __launch_bounds__(GN_THREADS) gn_bwd_sums_kernel(View<const T> x
 // thread rows taking every so many of them.
 constexpr int GN_PARAM_CHANNELS = 8;
 __global__ void __launch_bounds__(GN_THREADS) gn_bwd_combine_kernel(const float2* part,
-                                                                    const float* __restrict__ gamma,
+                                                                    const float* gamma,
                                                                     float2* gmean,
-                                                                    float* __restrict__ ggamma,
-                                                                    float* __restrict__ gbeta, GnShape s) {
+                                                                    float* ggamma,
+                                                                    float* gbeta, GnShape s) {
     grid_begin();
     __shared__ float red[GN_THREADS / 32];
     __shared__ float2 col[GN_THREADS / GN_PARAM_CHANNELS][GN_PARAM_CHANNELS + 1];
@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_bwd_combine_kernel(const float2
 // and gx, 1410 MB at the same size in 215 us, 6.6 TB/s; bound by memory.
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS) gn_bwd_apply_kernel(View<const T> x, View<const T> gy, View<T> gx,
-                                                                  const float* __restrict__ gamma,
-                                                                  const float* __restrict__ beta,
+                                                                  const float* gamma,
+                                                                  const float* beta,
                                                                   const float* mean,
                                                                   const float* rstd,
                                                                   const float2* gmean, GnShape s) {
@@ -501,8 +501,8 @@ template <int V, typename F> __device__ __forceinline__ void gn_groups(int c, in
 // 512 x 256 bf16: 6.5 us a call; bound by its launch, two dependent reads and the
 // meeting (1.2 us for a cooperative grid).
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x, View<T> y, const float* __restrict__ gamma,
-                                                                const float* __restrict__ beta, float eps,
+__global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x, View<T> y, const float* gamma,
+                                                                const float* beta, float eps,
                                                                 float* mean, float* rstd,
                                                                 float2* part, GnGrid s) {
     grid_begin();
@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(GN_THREADS, 3) gn_grid_kernel(View<const T> x,
 // 3 x 10961 x 120 bf16 with GELU: 37 us.
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(GN_THREADS, 2) gn_bwd_grid_kernel(View<const T> x, View<const T> gy, View<T> gx,
-                                                                    const float* __restrict__ gamma,
-                                                                    const float* __restrict__ beta,
+                                                                    const float* gamma,
+                                                                    const float* beta,
                                                                     const float* mean,
                                                                     const float* rstd, float2* part,
                                                                     float* param, GnGrid s) {

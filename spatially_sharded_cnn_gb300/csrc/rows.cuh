@@ -70,7 +70,15 @@ template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw_last
         Pack<T, V> q;
         __device__ U() {}
     } u;
-    u.w = __ldcs(reinterpret_cast<const W*>(p));
+    // volatile: never ahead of grid_begin
+    if constexpr (sizeof(W) == 16)
+        asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.w.x), "=r"(u.w.y), "=r"(u.w.z), "=r"(u.w.w)
+                     : "l"(p));
+    else if constexpr (sizeof(W) == 4)
+        asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(u.w) : "l"(p));
+    else
+        asm volatile("ld.global.cs.u16 %0, [%1];" : "=h"(u.w) : "l"(p));
     return u.q;
 }
 // For rows that no cache holds until they are read again.
@@ -194,9 +202,9 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 // has several: ragged 5 x 1537 x 328 scan step 148 -> 130 us.  (Letting the next
 // kernel's blocks in before this one's begin to end made the 224 x 1024 x 256 step
 // 1.60 -> 1.74 ms: they take the shared memory that this one's later blocks want.)
-// What an earlier kernel may have written (anything but parameters) is read
-// through plain pointers: loads of the read-only path could be moved above the
-// wait.
+// Everything is read through plain pointers or volatile loads, parameters too (an
+// optimizer's kernel writes them just before the next call): loads through
+// __restrict__ pointers or of the read-only path could be moved above the wait.
 __device__ __forceinline__ void grid_begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
 void launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {

@@ -4,7 +4,7 @@ give the same bits."""
 import pytest
 import torch
 
-from test_gpu_mixer import scan_data
+from test_gpu_mixer import Data, scan_data, space
 
 pytestmark = pytest.mark.gpu
 
@@ -45,5 +45,89 @@ def test_scan_tokens_on_one_state(hc, B, D, N):
                                                z=row["z"], dt_bias=x["bias"]))
             after()
         return y, state
+
+    both(run)
+
+
+@pytest.mark.parametrize("B,D,K", [(1, 8, 4), (64, 256, 4), (64, 2048, 4), (3, 47, 3)])
+def test_conv_tokens_on_one_state(hc, B, D, K):
+    s = Data(41, torch.float32)
+    (x, _), (si, _), (w, _), (bias, _) = s.rows(CALLS, B, D), s.rows(B, K - 1, D), s.param(D, K), s.param(D)
+    d = hc.causal_conv_desc(B, 1, D, K, torch.float32, hc.HC_PW_SILU)
+
+    def run(after):
+        state, y = si.clone(), torch.empty(CALLS, B, D, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(CALLS):
+            hc.check(hc.hc_causal_conv_step(d, x[i], w, bias, state, y[i]))
+            after()
+        return y, state
+
+    both(run)
+
+
+@pytest.mark.parametrize("P,C,G", [(64, 32, 4), (3000, 96, 12), (17000, 1024, 32)])
+def test_norm_parameters_written_just_before(hc, P, C, G):
+    """Every call's gamma and beta come from the kernel ahead of it, as an optimizer's update does: maps that take a
+    cluster, a cooperative grid and three launches, forward and backward."""
+    calls = CALLS if P < 10000 else 20
+    s = Data(42, torch.float32)
+    (gamma0, _), (beta0, _) = s.param(C, shift=1.0), s.param(C)
+    g = torch.Generator(device="cuda").manual_seed(42)
+    x, gy = (torch.randn(1, P, C, device="cuda", generator=g) for _ in range(2))
+    d = hc.groupnorm_desc(1, P, C, G, torch.float32, act=hc.HC_PW_SILU)
+    ws, nb = space(hc, hc.hc_groupnorm_workspace_size(d, 1))
+
+    def run(after):
+        gamma, beta = gamma0.clone(), beta0.clone()
+        mean, rstd = torch.empty(1, G, device="cuda"), torch.empty(1, G, device="cuda")
+        y, gx = (torch.empty(1, P, C, device="cuda") for _ in range(2))
+        rows, grads, sums = [], torch.empty(calls, P, device="cuda"), torch.empty(calls, 2, C, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(calls):
+            gamma.add_(1.0)
+            after()
+            beta.sub_(0.25)
+            after()
+            hc.check(hc.hc_groupnorm_fwd(d, x, gamma, beta, y, mean, rstd, ws, nb))
+            after()
+            rows.append(y[0, ::7].clone())
+            gamma.mul_(0.5)
+            after()
+            beta.add_(0.125)
+            after()
+            hc.check(hc.hc_groupnorm_bwd(d, x, gamma, beta, mean, rstd, gy, gx, sums[i, 0], sums[i, 1], ws, nb))
+            after()
+            grads[i] = gx[0, :, i % C]
+        return [sums, grads, y, gx] + rows
+
+    both(run)
+
+
+@pytest.mark.parametrize("B,L,D", [(2, 40, 24), (8, 300, 264)])
+def test_conv_parameters_written_just_before(hc, B, L, D):
+    K, s = 4, Data(43, torch.float32)
+    (x, _), (gy, _), (w0, _), (bias0, _) = s.rows(B, L, D), s.rows(B, L, D), s.param(D, K), s.param(D)
+    d = hc.causal_conv_desc(B, L, D, K, torch.float32, hc.HC_PW_SILU)
+    ws, nb = space(hc, hc.hc_causal_conv_workspace_size(d))
+
+    def run(after):
+        w, bias = w0.clone(), bias0.clone()
+        y, gx, step = torch.empty(B, L, D, device="cuda"), torch.empty(B, L, D, device="cuda"), torch.empty(B, D, device="cuda")
+        state = torch.zeros(B, K - 1, D, device="cuda")
+        rows, sums = [], torch.empty(CALLS, D * K + D, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(CALLS):
+            for f in (lambda: bias.add_(0.01), lambda: w.mul_(-0.99),
+                      lambda: hc.check(hc.hc_causal_conv_fwd(d, x, w, bias, y)), lambda: rows.append(y[0].clone()),
+                      lambda: bias.sub_(0.02), lambda: w.add_(0.03),
+                      lambda: hc.check(hc.hc_causal_conv_bwd(d, x, w, bias, gy, gx, sums[i, :D * K], sums[i, D * K:],
+                                                             ws=ws, ws_bytes=nb)), lambda: rows.append(gx[0].clone()),
+                      lambda: bias.add_(0.01), lambda: w.sub_(0.03),
+                      lambda: hc.check(hc.hc_causal_conv_step(d, x[:, i % L], w, bias, state, step)),
+                      lambda: rows.append(step.clone())):
+                f()
+                after()
+        return [sums, state] + rows
 
     both(run)

@@ -29,7 +29,8 @@ def kernels(name):
     return found
 
 
-@pytest.mark.parametrize("source", ["scan.cu", "scan_fwd.cu", "scan_bwd.cu", "scan_carry.cu", "reduce.cu"])
+@pytest.mark.parametrize("source", ["groupnorm.cu", "causal_conv.cu", "scan.cu", "scan_fwd.cu", "scan_bwd.cu",
+                                    "scan_carry.cu", "reduce.cu"])
 def test_reads_stay_behind_the_wait(source):
     waiting = [k for k in kernels(source) if "grid_begin()" in k[2]]
     assert waiting
@@ -37,3 +38,14 @@ def test_reads_stay_behind_the_wait(source):
         assert body.lstrip("{ \n").startswith("grid_begin();"), f"{name} acts before its wait"
         assert "__restrict__" not in params + body, f"{name} has a __restrict__ pointer"
         assert "__ldg" not in body and "global.nc" not in body, f"{name} reads through the read-only path"
+
+
+@pytest.mark.parametrize("source", ["rows.cuh", "scan.cuh"])
+def test_shared_loads_stay_behind_the_wait(source):
+    """The functions that those kernels share: no such load, and no hinted one that the compiler may move."""
+    with open(os.path.join(CSRC, source)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    for word in ("__restrict__", "__ldg", "__ldcs", "__ldcg", "__ldca", "global.nc"):
+        assert word not in text, word
+    for m in re.finditer(r"asm( volatile)?\(\s*\"(ld|cp|prefetch)\b[^\"]*", text):
+        assert m.group(1), f"a load that may move: {m.group(0)}"
