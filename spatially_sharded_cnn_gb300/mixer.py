@@ -9,6 +9,7 @@ rows of the maps, (P, T, D) views of (T, P, D) tensors.
 ``forward`` / ``backward`` train on T frames at once, ``step`` takes one new frame and the carried
 states (a K - 1 row window and a D x N state a pixel) and gives the row that ``forward`` would.
 The operators are the library's kernels; torch holds the memory and multiplies by the projections.
+Both run on torch's current stream, which may be a side stream or one that a CUDA graph captures.
 
     python -m spatially_sharded_cnn_gb300.mixer      # a training step and a stream, timed
 """
@@ -48,13 +49,18 @@ class TemporalMixer:
     def _empty(self, *shape, dtype=None):
         return torch.empty(*shape, dtype=dtype or self.dtype, device=self.device)
 
+    def _stream(self):
+        """The stream of the library's calls: the one that torch's products before and after them are on."""
+        return torch.cuda.current_stream(self.device)
+
     def _norm(self, x, keep):
         T, P, C = x.shape
         d = hc.groupnorm_desc(T, P, C, self.groups, self.dtype, act=hc.HC_PW_SILU)
         ws, nb = self._space(hc.hc_groupnorm_workspace_size(d, int(keep)))
         y = torch.empty_like(x)
         mean, rstd = (self._empty(T, self.groups, dtype=torch.float32) for _ in range(2)) if keep else (None, None)
-        hc.check(hc.hc_groupnorm_fwd(d, x, self.p["gamma"], self.p["beta"], y, mean, rstd, ws, nb), "norm")
+        hc.check(hc.hc_groupnorm_fwd(d, x, self.p["gamma"], self.p["beta"], y, mean, rstd, ws, nb, self._stream()),
+                 "norm")
         return y, (d, mean, rstd, ws, nb)
 
     def _project(self, c):
@@ -71,14 +77,15 @@ class TemporalMixer:
         seq = lambda t: t.transpose(0, 1)  # (T, P, .) -> (P, T, .), in place
         dc = hc.causal_conv_desc(P, T, D, self.K, self.dtype, hc.HC_PW_SILU)
         c = self._empty(T, P, D)
-        hc.check(hc.hc_causal_conv_fwd(dc, seq(xz)[..., :D], p["conv"], p["conv_bias"], seq(c)), "conv")
+        hc.check(hc.hc_causal_conv_fwd(dc, seq(xz)[..., :D], p["conv"], p["conv_bias"], seq(c), stream=self._stream()), "conv")
         proj, dt, Bm, Cm = self._project(c)
         ds = hc.selective_scan_desc(P, T, D, self.N, self.dtype)
         ws, nb = self._space(hc.hc_selective_scan_workspace_size(ds, int(train)))
         saved = self._space(hc.hc_selective_scan_saved_size(ds))[0] if train else None
         s = self._empty(T, P, D)
         hc.check(hc.hc_selective_scan_fwd(ds, seq(c), seq(dt), p["A"], seq(Bm), seq(Cm), seq(s), D=p["D"],
-                                          z=seq(xz)[..., D:], dt_bias=p["dt_bias"], saved=saved, ws=ws, ws_bytes=nb), "scan")
+                                          z=seq(xz)[..., D:], dt_bias=p["dt_bias"], saved=saved, ws=ws, ws_bytes=nb,
+                                          stream=self._stream()), "scan")
         y = x + s @ p["w_out"]
         return (y, (x, n, norm, xz, dc, c, proj, dt, Bm, Cm, ds, ws, nb, saved, s)) if train else y
 
@@ -98,7 +105,7 @@ class TemporalMixer:
         hc.check(hc.hc_selective_scan_bwd(ds, seq(c), seq(dt), p["A"], seq(Bm), seq(Cm), seq(gs), saved, seq(gc), seq(gdt),
                                           g["A"], seq(gproj)[..., R:R + N], seq(gproj)[..., R + N:], D=p["D"],
                                           z=seq(xz)[..., D:], dt_bias=p["dt_bias"], gD=g["D"], gz=seq(gxz)[..., D:],
-                                          gdt_bias=g["dt_bias"], ws=ws, ws_bytes=nb), "scan backward")
+                                          gdt_bias=g["dt_bias"], ws=ws, ws_bytes=nb, stream=self._stream()), "scan backward")
         g["w_dt"] = flat(proj[..., :R]).T @ flat(gdt)
         gproj[..., :R] = gdt @ p["w_dt"].T
         g["w_x"] = flat(c).T @ flat(gproj)
@@ -106,12 +113,13 @@ class TemporalMixer:
         g["conv"], g["conv_bias"] = f32(D, self.K), f32(D)
         cws, cnb = self._space(hc.hc_causal_conv_workspace_size(dc))
         hc.check(hc.hc_causal_conv_bwd(dc, seq(xz)[..., :D], p["conv"], p["conv_bias"], seq(gc), seq(gxz)[..., :D],
-                                       g["conv"], g["conv_bias"], ws=cws, ws_bytes=cnb), "conv backward")
+                                       g["conv"], g["conv_bias"], ws=cws, ws_bytes=cnb, stream=self._stream()),
+                 "conv backward")
         g["w_in"] = flat(n).T @ flat(gxz)
         gn, gx = gxz @ p["w_in"].T, torch.empty_like(x)
         g["gamma"], g["beta"] = f32(self.C), f32(self.C)
-        hc.check(hc.hc_groupnorm_bwd(dn, x, p["gamma"], p["beta"], mean, rstd, gn, gx, g["gamma"], g["beta"], nws, nnb),
-                 "norm backward")
+        hc.check(hc.hc_groupnorm_bwd(dn, x, p["gamma"], p["beta"], mean, rstd, gn, gx, g["gamma"], g["beta"], nws, nnb,
+                                     self._stream()), "norm backward")
         return gx + gy, g
 
     def states(self, P):
@@ -127,10 +135,11 @@ class TemporalMixer:
         dc, ds = (hc.causal_conv_desc(P, 1, D, self.K, self.dtype, hc.HC_PW_SILU),
                   hc.selective_scan_desc(P, 1, D, self.N, self.dtype))
         c, s = self._empty(P, D), self._empty(P, D)
-        hc.check(hc.hc_causal_conv_step(dc, xz[:, :D], p["conv"], p["conv_bias"], states[0], c), "conv step")
+        st = self._stream()
+        hc.check(hc.hc_causal_conv_step(dc, xz[:, :D], p["conv"], p["conv_bias"], states[0], c, st), "conv step")
         _, dt, Bm, Cm = self._project(c)
         hc.check(hc.hc_selective_scan_step(ds, c, dt, p["A"], Bm, Cm, states[1], s, D=p["D"], z=xz[:, D:],
-                                           dt_bias=p["dt_bias"]), "scan step")
+                                           dt_bias=p["dt_bias"], stream=st), "scan step")
         return x + s @ p["w_out"]
 
 

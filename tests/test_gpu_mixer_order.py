@@ -131,3 +131,59 @@ def test_conv_parameters_written_just_before(hc, B, L, D):
         return [sums, state] + rows
 
     both(run)
+
+
+# ---------------------------------------------------------------- the temporal mixer
+
+@pytest.fixture(scope="module")
+def mixer(hc):
+    from spatially_sharded_cnn_gb300.mixer import TemporalMixer
+    T, P = 6, 512
+    m = TemporalMixer(C=64, D=128, groups=8, seed=5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, gy = (torch.randn(T, P, 64, device="cuda", generator=g).to(m.dtype) for _ in range(2))
+    return m, x, gy
+
+
+def mixed(m, x, gy):
+    y, kept = m.forward(x, train=True)
+    gx, g = m.backward(gy, kept)
+    states = m.states(x.shape[1])
+    rows = torch.stack([m.step(f, states) for f in x])
+    return [y, gx, rows, *states] + [g[k] for k in sorted(g)]
+
+
+def test_mixer_on_a_side_stream(mixer):
+    """Training and single frames on a side stream, many in a row, against the default stream."""
+    m, x, gy = mixer
+    want = mixed(m, x, gy)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [mixed(m, x, gy) for _ in range(20)]
+    side.synchronize()
+    for one in got:
+        for a, b in zip(one, want):
+            assert torch.equal(a, b)
+
+
+def test_mixer_in_a_graph(mixer):
+    """A training step and a frame captured from torch's stream, replayed on new values."""
+    m, x, gy = mixer
+    x, gy = x.clone(), gy.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            mixed(m, x, gy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mixed(m, x, gy)
+    x.copy_(x.flip(0))
+    gy.copy_(gy.flip(1))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, mixed(m, x, gy)):
+        assert torch.equal(a, b)
