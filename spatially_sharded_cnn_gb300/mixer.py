@@ -15,12 +15,22 @@ Both run on torch's current stream, which may be a side stream or one that a CUD
 """
 from __future__ import annotations
 
+import functools
 import math
 import time
 
 import torch
 
 from . import hc
+
+
+def _on_device(method):
+    """Runs a method with the mixer's device as the current one: the library launches on the current device."""
+    @functools.wraps(method)
+    def run(self, *args, **kwargs):
+        with torch.cuda.device(self.device):
+            return method(self, *args, **kwargs)
+    return run
 
 
 class TemporalMixer:
@@ -68,6 +78,7 @@ class TemporalMixer:
         R, N = self.R, self.N
         return proj, proj[..., :R] @ self.p["w_dt"], proj[..., R:R + N], proj[..., R + N:]
 
+    @_on_device
     def forward(self, x, train=False):
         """x (T, P, C) -> (T, P, C); with `train`, also what `backward` needs."""
         T, P, _ = x.shape
@@ -89,6 +100,7 @@ class TemporalMixer:
         y = x + s @ p["w_out"]
         return (y, (x, n, norm, xz, dc, c, proj, dt, Bm, Cm, ds, ws, nb, saved, s)) if train else y
 
+    @_on_device
     def backward(self, gy, kept):
         """The gradients of every parameter, and of x, from the gradient of forward's result."""
         x, n, (dn, mean, rstd, nws, nnb), xz, dc, c, proj, dt, Bm, Cm, ds, ws, nb, saved, s = kept
@@ -127,6 +139,7 @@ class TemporalMixer:
         return (torch.zeros(P, self.K - 1, self.D, dtype=self.dtype, device=self.device),
                 torch.zeros(P, self.D, self.N, device=self.device))
 
+    @_on_device
     def step(self, x, states):
         """One frame x (P, C) -> (P, C); the states move on in place."""
         P, D, p = x.shape[0], self.D, self.p

@@ -1,5 +1,6 @@
-"""The host side of the temporal mixer (no GPU): which stream its library calls go to, with the
-library's calls replaced by ones that take note of it."""
+"""The host side of the temporal mixer (no GPU): which stream and device its library calls go to, with
+the library's calls replaced by ones that take note of it."""
+import contextlib
 import inspect
 
 import pytest
@@ -17,14 +18,22 @@ def mod(monkeypatch):
     return mixer
 
 
-def test_library_calls_take_torchs_stream(mod, monkeypatch):
-    seen, asked, current = [], [], object()
+def test_library_calls_take_torchs_stream_and_the_mixers_device(mod, monkeypatch):
+    seen, asked, current, entered = [], [], object(), []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(str(d))
+        yield
+        entered.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", device)
 
     def note(name, real):
         where = inspect.signature(real)
 
         def call(*a, **k):
-            seen.append((name, where.bind(*a, **k).arguments.get("stream")))
+            seen.append((name, where.bind(*a, **k).arguments.get("stream"), list(entered)))
             return 0
         return call
 
@@ -37,7 +46,8 @@ def test_library_calls_take_torchs_stream(mod, monkeypatch):
     m.backward(x, kept)
     m.forward(x)
     m.step(x[0], m.states(6))
-    assert {n for n, _ in seen} == set(CALLS)
-    for name, stream in seen:
+    assert {s[0] for s in seen} == set(CALLS)
+    for name, stream, on in seen:
         assert stream is current, f"{name} is not on torch's current stream"
+        assert on == ["cpu"], f"{name} is not on the mixer's device"
     assert {str(d) for d in asked} == {"cpu"}  # the mixer's own device
