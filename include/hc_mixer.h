@@ -106,7 +106,9 @@ hc_status hc_causal_conv_workspace_size(const hc_causal_conv_desc* d, size_t* by
  * gw[d][k] = sum over b, t of g_t * x_{t-(K-1)+k}, gb[d] = sum g_t.
  * gstate_out (may be NULL): the gradient of state_out, which joins that of the
  * rows it holds.  gstate_in (may be NULL): the gradient of state_in.  Both are
- * [B][K-1][D] in the desc's type.  gx, gw, gb may each be NULL. */
+ * [B][K-1][D] in the desc's type.  gstate_in may be neither gstate_out's nor
+ * state_in's own buffer: other blocks still read those.  gx, gw, gb may each be
+ * NULL. */
 hc_status hc_causal_conv_bwd(const hc_causal_conv_desc* d, const hc_rows* x, const float* w, const float* bias,
                              const hc_rows* gy, const hc_rows* gx, float* gw, float* gb, const void* state_in,
                              const void* gstate_out, void* gstate_in, const int* lens, void* ws, size_t ws_bytes,

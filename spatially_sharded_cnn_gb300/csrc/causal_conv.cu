@@ -539,7 +539,7 @@ hc_status hc_causal_conv_bwd(const hc_causal_conv_desc* d, const hc_rows* x, con
     if (!rows_in_ok(x, d->dtype, d->L) || !rows_in_ok(gy, d->dtype, d->L) ||
         (gx && (!rows_out_ok(gx, d->dtype, d->B, d->L, d->D) || rows_same(gx, x) || rows_same(gx, gy))) || !f32_ok(w) ||
         !f32_opt_ok(bias) || !f32_opt_ok(gw) || !f32_opt_ok(gb) || !ptr_al(state_in, 16) || !ptr_al(gstate_out, 16) ||
-        !ptr_al(gstate_in, 16) || !ptr_al(lens, 4))
+        !ptr_al(gstate_in, 16) || (gstate_in && (gstate_in == gstate_out || gstate_in == state_in)) || !ptr_al(lens, 4))
         return HC_ERR_INVALID_ARG;
     const bool params = gw || gb;
     if (params && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
