@@ -30,6 +30,10 @@
  *     used, whatever they hold; their outputs and gradients are zeros.
  *   - L = 0 is a valid call: states pass through, nothing else is written
  *     (parameter gradients become zero).
+ *   - Sizes past these limits are HC_ERR_UNSUPPORTED.  Norm: N <= 65535,
+ *     C <= 2^20, N * groups < 2^30.  Convolution: 2 <= K <= 8, D <= 2^20,
+ *     B * (L / 4 + 1) < 2^31, L < 2^31 - 64.  Scan: d_state <= 64, D <= 2^20,
+ *     B * D < 2^31, L < 2^31 - 64.
  */
 #ifndef HC_MIXER_H
 #define HC_MIXER_H

@@ -133,10 +133,10 @@ bool scan_desc_ok(const hc_selective_scan_desc* d) {
     return d && d->B > 0 && d->L >= 0 && d->D > 0 && d->groups > 0 && d->D % d->groups == 0 && d->d_state > 0 &&
            (d->softplus == 0 || d->softplus == 1) && dtype_ok(d->dtype);
 }
-// Launch limits: (sequence, segment, channel tile) on grid x, sequences on grid y.
+// Launch limits: (sequence, segment, channel tile) on grid x; segments are joined
+// with sequences on grid y (scan_segs).
 bool scan_size_ok(const hc_selective_scan_desc* d) {
-    return d->d_state <= 64 && d->D <= (1 << 20) && d->B <= 65535 && (long long)d->B * d->D < (1LL << 31) &&
-           d->L <= 0x7fffffff - 64;
+    return d->d_state <= 64 && d->D <= (1 << 20) && (long long)d->B * d->D < (1LL << 31) && d->L <= 0x7fffffff - 64;
 }
 // Channel tiles a group in the forward and segment kernels, and in the backward kernel.
 struct TileChannels {
@@ -171,7 +171,8 @@ Segs scan_segs(const hc_selective_scan_desc* d, int ctiles, int want, bool ragge
     const int tiles = (int)cdiv(d->L, SC_T);
     const long long blocks = (long long)d->B * d->groups * ctiles;
     const long long full = (long long)want * device_sm_count() * (ragged ? 2 : 1);
-    if (blocks * 3 > full || tiles < 16) return {1, tiles > 0 ? tiles : 1};
+    // (more than 65535 sequences, which the join's grid does not take, only an imposed SM count would cut)
+    if (blocks * 3 > full || tiles < 16 || d->B > 65535) return {1, tiles > 0 ? tiles : 1};
     long long n = full / blocks;
     if (n > tiles / 2) n = tiles / 2;
     const int per = (int)cdiv(tiles, n);
