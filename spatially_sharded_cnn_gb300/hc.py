@@ -398,7 +398,10 @@ def hc_trace_collect(max_entries: int = 256):
 # ---- channels-last sequence-mixer operators (include/hc_mixer.h) ------------
 HC_DTYPE_F32, HC_DTYPE_BF16, HC_DTYPE_F16 = range(3)
 HC_PW_NONE, HC_PW_SILU, HC_PW_GELU = range(3)
+
+
 _DTYPES = {"torch.float32": HC_DTYPE_F32, "torch.bfloat16": HC_DTYPE_BF16, "torch.float16": HC_DTYPE_F16}
+_TORCH = {}  # torch's dtype of each hc_dtype that was met
 
 
 class hc_groupnorm_desc(C.Structure):
@@ -421,6 +424,7 @@ def _dtype(t) -> int:
     v = _DTYPES.get(t)
     if v is None:
         v = _DTYPES[t] = _DTYPES.get(str(t), -1)
+        _TORCH[v] = t
     return v
 
 
@@ -436,22 +440,56 @@ def selective_scan_desc(B, L, D, d_state, dtype, groups=1, softplus=1) -> hc_sel
     return hc_selective_scan_desc(B, L, D, groups, d_state, softplus, _dtype(dtype))
 
 
+# A call's marshalling is most of what one token costs: descriptors are read at once, and a tensor's
+# attributes once each.
 _ABSENT = (0, 0, 0, 0)
+_groupnorm = struct.Struct("@4ifii").unpack
+_causal_conv = struct.Struct("@6i").unpack
+_selective_scan = struct.Struct("@7i").unpack
 _pack_rows = struct.Struct("@Pqqq").pack
 _pack_scan_in = struct.Struct("@" + "Pqqq" * 5 + "PPP").pack
 _pack_scan_grad = struct.Struct("@" + "Pqqq" * 5 + "PPPP").pack
 
 
-def _addr(t) -> int:
-    return 0 if t is None else t if isinstance(t, int) else t.data_ptr()
+def _fault(t, what):
+    raise HcError(HC_ERR_INVALID_ARG, f"a tensor of shape {tuple(t.shape)}, {t.dtype}, on {t.device} where {what} is wanted")
 
 
-def _lens(t) -> int:
-    """Sequence lengths: int32, one after another."""
+def _array(t, n, dtype=HC_DTYPE_F32) -> int:
+    """The address of n elements of a type, one after another on the device, whatever shape they have."""
+    if t is None:
+        return 0
+    try:
+        if t.dtype is _TORCH[dtype] and t.numel() == n and t.is_contiguous() and t.is_cuda:
+            return t.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    if isinstance(t, int):
+        return t
+    if _dtype(t.dtype) != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        _fault(t, f"a contiguous device array of {n} elements of hc_dtype {dtype}")
+    return t.data_ptr()
+
+
+def _bytes(t, n) -> int:
+    """The address of n bytes or more."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
+    if t.nbytes < n or not t.is_contiguous() or not t.is_cuda:
+        _fault(t, f"a contiguous device buffer of {n} bytes")
+    return t.data_ptr()
+
+
+def _lens(t, B=None) -> int:
+    """Sequence lengths: int32, one after another, one for each of B sequences."""
     if t is None or isinstance(t, int):
         return t or 0
     if str(t.dtype) != "torch.int32" or not t.is_contiguous():
         raise HcError(HC_ERR_INVALID_ARG, "lengths are a contiguous int32 tensor")
+    if B is not None and (t.numel() != B or not t.is_cuda):
+        _fault(t, f"a device array of {B} lengths")
     return t.data_ptr()
 
 
@@ -461,21 +499,38 @@ def _refuse(t, shape):
     raise HcError(HC_ERR_INVALID_ARG, "a channels-last tensor needs adjacent channels")
 
 
-def _view(t, *shape):
-    """The fields of an hc_rows for a torch tensor (batch, row, channel) or (batch, channel) with adjacent channels."""
+def _view(t, b, l, c=None):
+    """The fields of an hc_rows for a torch tensor (b, l, c) -- batch, row, channel -- or one token's (b, l), with adjacent
+    channels."""
     if t is None:
         return _ABSENT
-    s = t.stride()
-    if t.shape != shape or (s[-1] != 1 and shape[-1] > 1):
-        _refuse(t, shape)
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        dt = _dtype(t.dtype)
-    return t.data_ptr(), s[0], s[1] if len(s) == 3 else 0, dt
+    if c is None:
+        if t.shape != (b, l):
+            _refuse(t, (b, l))
+        batch, w = t.stride()
+        row, c = 0, l
+    else:
+        if t.shape != (b, l, c):
+            _refuse(t, (b, l, c))
+        batch, row, w = t.stride()
+    if w != 1 and c > 1:
+        _refuse(t, t.shape)
+    try:
+        return t.data_ptr(), batch, row, _DTYPES[t.dtype]
+    except KeyError:
+        return t.data_ptr(), batch, row, _dtype(t.dtype)
 
 
-def _rows(t, *shape) -> bytes:
-    return _pack_rows(*_view(t, *shape))
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            _fault(t, "a device tensor")
+
+
+def _rows(t, b, l, c=None) -> bytes:
+    if t is not None and not t.is_cuda:
+        _on_gpu(t)
+    return _pack_rows(*_view(t, b, l, c))
 
 
 _R, _Z = C.c_char_p, C.c_size_t  # a packed hc_rows (or hc_scan_in, hc_scan_grad)
@@ -504,24 +559,27 @@ def hc_groupnorm_workspace_size(d: hc_groupnorm_desc, pass_: int):
 
 def hc_groupnorm_fwd(d, x, gamma, beta, y, mean=None, rstd=None, ws=None, ws_bytes=0, stream=None) -> int:
     """y = act(group norm of x); x and y are (N, P, C) tensors with adjacent channels."""
-    s = d.N, d.P, d.C
-    return _lib.hc_groupnorm_fwd(C.byref(d), _rows(x, *s), _addr(gamma), _addr(beta), _rows(y, *s), _addr(mean),
-                                 _addr(rstd), _addr(ws), ws_bytes, _stream(stream))
+    n, p, c, g, _, _, _ = _groupnorm(d)
+    g *= n
+    return _lib.hc_groupnorm_fwd(C.byref(d), _rows(x, n, p, c), _array(gamma, c), _array(beta, c), _rows(y, n, p, c),
+                                 _array(mean, g), _array(rstd, g), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
 
 
 def hc_groupnorm_bwd(d, x, gamma, beta, mean, rstd, gy, gx, ggamma=None, gbeta=None, ws=None, ws_bytes=0,
                      stream=None) -> int:
-    s = d.N, d.P, d.C
-    return _lib.hc_groupnorm_bwd(C.byref(d), _rows(x, *s), _addr(gamma), _addr(beta), _addr(mean), _addr(rstd),
-                                 _rows(gy, *s), _rows(gx, *s), _addr(ggamma), _addr(gbeta), _addr(ws), ws_bytes,
-                                 _stream(stream))
+    n, p, c, g, _, _, _ = _groupnorm(d)
+    g *= n
+    return _lib.hc_groupnorm_bwd(C.byref(d), _rows(x, n, p, c), _array(gamma, c), _array(beta, c), _array(mean, g),
+                                 _array(rstd, g), _rows(gy, n, p, c), _rows(gx, n, p, c), _array(ggamma, c), _array(gbeta, c),
+                                 _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
 
 
 def hc_causal_conv_fwd(d, x, w, bias, y, state_in=None, state_out=None, lens=None, stream=None) -> int:
     """x and y are (B, L, D) tensors with adjacent channels; states (B, K - 1, D) contiguous; lens int32 (B,)."""
-    s = d.B, d.L, d.D
-    return _lib.hc_causal_conv_fwd(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _rows(y, *s), _addr(state_in),
-                                   _addr(state_out), _lens(lens), _stream(stream))
+    b, l, c, k, _, t = _causal_conv(d)
+    n = b * (k - 1) * c
+    return _lib.hc_causal_conv_fwd(C.byref(d), _rows(x, b, l, c), _array(w, c * k), _array(bias, c), _rows(y, b, l, c),
+                                   _array(state_in, n, t), _array(state_out, n, t), _lens(lens, b), _stream(stream))
 
 
 def hc_causal_conv_workspace_size(d: hc_causal_conv_desc):
@@ -533,18 +591,19 @@ def hc_causal_conv_workspace_size(d: hc_causal_conv_desc):
 
 def hc_causal_conv_bwd(d, x, w, bias, gy, gx, gw, gb, state_in=None, gstate_out=None, gstate_in=None, lens=None,
                        ws=None, ws_bytes=0, stream=None) -> int:
-    s = d.B, d.L, d.D
-    return _lib.hc_causal_conv_bwd(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _rows(gy, *s),
-                                   None if gx is None else _rows(gx, *s), _addr(gw), _addr(gb), _addr(state_in),
-                                   _addr(gstate_out), _addr(gstate_in), _lens(lens), _addr(ws), ws_bytes,
-                                   _stream(stream))
+    b, l, c, k, _, t = _causal_conv(d)
+    n = b * (k - 1) * c
+    return _lib.hc_causal_conv_bwd(C.byref(d), _rows(x, b, l, c), _array(w, c * k), _array(bias, c), _rows(gy, b, l, c),
+                                   None if gx is None else _rows(gx, b, l, c), _array(gw, c * k), _array(gb, c),
+                                   _array(state_in, n, t), _array(gstate_out, n, t), _array(gstate_in, n, t),
+                                   _lens(lens, b), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
 
 
 def hc_causal_conv_step(d, x, w, bias, state, y, stream=None) -> int:
     """One token: x and y are (B, D) tensors; state is moved on in place."""
-    s = d.B, d.D
-    return _lib.hc_causal_conv_step(C.byref(d), _rows(x, *s), _addr(w), _addr(bias), _addr(state), _rows(y, *s),
-                                    _stream(stream))
+    b, _, c, k, _, t = _causal_conv(d)
+    return _lib.hc_causal_conv_step(C.byref(d), _rows(x, b, c), _array(w, c * k), _array(bias, c),
+                                    _array(state, b * (k - 1) * c, t), _rows(y, b, c), _stream(stream))
 
 
 def hc_selective_scan_workspace_size(d: hc_selective_scan_desc, pass_: int):
@@ -561,39 +620,57 @@ def hc_selective_scan_saved_size(d: hc_selective_scan_desc):
     return st, b.value
 
 
-def _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias) -> bytes:
-    s, m = lead + (d.D,), lead + (d.groups * d.d_state,)
-    return _pack_scan_in(*_view(u, *s), *_view(dt, *s), *_view(Bm, *m), *_view(Cm, *m), *_view(z, *s), _addr(A),
-                         _addr(D), _addr(dt_bias))
+def _scan_in(b, l, c, g, n, u, dt, A, Bm, Cm, D, z, dt_bias) -> bytes:
+    """An hc_scan_in of rows (b, l, c), n states a channel and g groups; l None: one token's rows (b, c)."""
+    try:
+        there = u.is_cuda and dt.is_cuda and Bm.is_cuda and Cm.is_cuda and (z is None or z.is_cuda)
+    except AttributeError:  # an absent tensor, which the library answers for
+        there = False
+    if not there:
+        _on_gpu(u, dt, Bm, Cm, z)
+    m = g * n
+    if l is None:
+        rows = (*_view(u, b, c), *_view(dt, b, c), *_view(Bm, b, m), *_view(Cm, b, m), *_view(z, b, c))
+    else:
+        rows = (*_view(u, b, l, c), *_view(dt, b, l, c), *_view(Bm, b, l, m), *_view(Cm, b, l, m), *_view(z, b, l, c))
+    return _pack_scan_in(*rows, _array(A, c * n), _array(D, c), _array(dt_bias, c))
+
+
+def _saved(d, t) -> int:
+    """The address of the states that the forward pass saves: as many bytes as it does, or more."""
+    return 0 if t is None else t if isinstance(t, int) else _bytes(t, hc_selective_scan_saved_size(d)[1])
 
 
 def hc_selective_scan_fwd(d, u, dt, A, Bm, Cm, y, D=None, z=None, dt_bias=None, h0=None, hT=None, lens=None,
                           saved=None, ws=None, ws_bytes=0, stream=None) -> int:
     """u, dt, z, y are (B, L, D) and Bm, Cm (B, L, groups * d_state) tensors with adjacent channels; lens int32 (B,)."""
-    lead = (d.B, d.L)
-    return _lib.hc_selective_scan_fwd(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(h0),
-                                      _lens(lens), _rows(y, *lead, d.D), _addr(hT), _addr(saved), _addr(ws), ws_bytes,
-                                      _stream(stream))
+    b, l, c, g, n, _, _ = _selective_scan(d)
+    states = b * c * n
+    return _lib.hc_selective_scan_fwd(C.byref(d), _scan_in(b, l, c, g, n, u, dt, A, Bm, Cm, D, z, dt_bias),
+                                      _array(h0, states), _lens(lens, b), _rows(y, b, l, c), _array(hT, states),
+                                      _saved(d, saved), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
 
 
 def hc_selective_scan_bwd(d, u, dt, A, Bm, Cm, gy, saved, gu, gdt, gA, gB, gC, D=None, z=None, dt_bias=None, h0=None,
                           lens=None, ghT=None, gD=None, gz=None, gdt_bias=None, gh0=None, ws=None, ws_bytes=0,
                           stream=None) -> int:
     """The gradients of hc_selective_scan_fwd on the same inputs, from the states it saved."""
-    lead = (d.B, d.L)
-    s, m = lead + (d.D,), lead + (d.groups * d.d_state,)
-    grads = _pack_scan_grad(*_view(gu, *s), *_view(gdt, *s), *_view(gB, *m), *_view(gC, *m), *_view(gz, *s), _addr(gA),
-                            _addr(gD), _addr(gdt_bias), _addr(gh0))
-    return _lib.hc_selective_scan_bwd(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(h0),
-                                      _lens(lens), _addr(saved), _rows(gy, *s), _addr(ghT), grads, _addr(ws), ws_bytes,
-                                      _stream(stream))
+    b, l, c, g, n, _, _ = _selective_scan(d)
+    m, states = g * n, b * c * n
+    _on_gpu(gu, gdt, gB, gC, gz)
+    grads = _pack_scan_grad(*_view(gu, b, l, c), *_view(gdt, b, l, c), *_view(gB, b, l, m), *_view(gC, b, l, m),
+                            *_view(gz, b, l, c), _array(gA, c * n), _array(gD, c), _array(gdt_bias, c),
+                            _array(gh0, states))
+    return _lib.hc_selective_scan_bwd(C.byref(d), _scan_in(b, l, c, g, n, u, dt, A, Bm, Cm, D, z, dt_bias),
+                                      _array(h0, states), _lens(lens, b), _saved(d, saved), _rows(gy, b, l, c),
+                                      _array(ghT, states), grads, _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
 
 
 def hc_selective_scan_step(d, u, dt, A, Bm, Cm, state, y, D=None, z=None, dt_bias=None, stream=None) -> int:
     """One token: u, dt, z, y are (B, D) and Bm, Cm (B, groups * d_state) tensors; state is updated in place."""
-    lead = (d.B,)
-    return _lib.hc_selective_scan_step(C.byref(d), _scan_in(d, lead, u, dt, A, Bm, Cm, D, z, dt_bias), _addr(state),
-                                       _rows(y, d.B, d.D), _stream(stream))
+    b, _, c, g, n, _, _ = _selective_scan(d)
+    return _lib.hc_selective_scan_step(C.byref(d), _scan_in(b, None, c, g, n, u, dt, A, Bm, Cm, D, z, dt_bias),
+                                       _array(state, b * c * n), _rows(y, b, c), _stream(stream))
 
 
 def check(status: int, what: str = "hc call") -> None:
