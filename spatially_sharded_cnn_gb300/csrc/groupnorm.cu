@@ -178,7 +178,8 @@ __device__ __forceinline__ float gn_reduce(float v, float* red) {
 }
 
 // One block per (image, group): its chunks' and channels' means and squared
-// deviations combined.
+// deviations combined.  The means are summed as offsets from the first one: sums of
+// the means themselves lose up to three units in the mean's last place.
 __global__ void __launch_bounds__(GN_THREADS) gn_combine_kernel(const float2* part, float eps,
                                                                 float* mean, float* rstd,
                                                                 GnShape s) {
@@ -188,13 +189,13 @@ __global__ void __launch_bounds__(GN_THREADS) gn_combine_kernel(const float2* pa
     const float2* pb = part + (long long)n * s.chunks * s.C + g * s.Cg;
     const int total = s.chunks * s.Cg;
     const int last = s.P - (s.chunks - 1) * s.chunk;  // pixels of the last chunk
-    const float values = (float)s.P * s.Cg;
+    const float values = (float)s.P * s.Cg, pivot = pb[0].x;
     float a = 0.0f;
     for (int q = threadIdx.x; q < total; q += GN_THREADS) {
         const int k = q / s.Cg;
-        a += pb[(long long)k * s.C + (q - k * s.Cg)].x * (k == s.chunks - 1 ? last : s.chunk);
+        a = fmaf(pb[(long long)k * s.C + (q - k * s.Cg)].x - pivot, (float)(k == s.chunks - 1 ? last : s.chunk), a);
     }
-    const float m = gn_reduce(a, red) / values;
+    const float m = pivot + gn_reduce(a, red) / values;
     float b = 0.0f;
     for (int q = threadIdx.x; q < total; q += GN_THREADS) {
         const int k = q / s.Cg;
