@@ -48,7 +48,8 @@ extern "C" {
 
 typedef enum { HC_DTYPE_F32 = 0, HC_DTYPE_BF16 = 1, HC_DTYPE_F16 = 2 } hc_dtype;
 /* Activations of the norm and the convolution: x, x / (1 + exp(-x)) and
- * x * (1 + erf(x / sqrt 2)) / 2 (the normal distribution function within 1.5e-7). */
+ * x * (1 + erf(x / sqrt 2)) / 2 (no further from it than hc_gelu_fwd, and with
+ * its negative tail to a relative 1e-5). */
 typedef enum { HC_PW_NONE = 0, HC_PW_SILU = 1, HC_PW_GELU = 2 } hc_pw_act;
 
 typedef struct {

@@ -138,30 +138,44 @@ __device__ __forceinline__ float softplus_f(float x) {
     return fmaf(2.0f * v, p, fmaxf(x, 0.0f));
 }
 
-// Phi(x) and e = exp(-x^2 / 2) by Abramowitz and Stegun 7.1.26: erfc(z) =
-// (a1 t + ... + a5 t^5) exp(-z^2), t = 1 / (1 + 0.3275911 z), z = |x| / sqrt 2, within
-// 1.5e-7; no branch, and the exponential serves the slope Phi(x) + x phi(x).
-__device__ __forceinline__ float normal_cdf(float x, float& e) {
-    const float t = rcpf(fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
+// GELU x Phi(x) and its slope Phi(x) + x phi(x) from a = |x| (up to 14, where e ends),
+// e = exp(-x^2 / 2) and R, Phi(-a) = e * R: the function R, a scaled complementary error
+// function, falls from 1/2 like 1 / a.  It is a polynomial of degree 7 in
+// s = a / (1 + 0.33 a), fitted here in 64 bits (least squares, reweighted until the
+// largest error of e * R is level: 4e-9).  s = 0 at x = 0, so that the last addition
+// alone rounds there, and the tail keeps its relative accuracy.
+// GELU of normal values is 1.8e-8 off (rms; 2.4e-8 in the form with erff, which took
+// 361 us where this takes 291 on 7 x 131072 x 256 bf16), its slope 2.4e-8 (2.7e-8).
+__device__ __forceinline__ float normal_tail(float x, float& a, float& e) {
+    a = fminf(fabsf(x), 14.0f);
+    const float s = a * rcpf(fmaf(0.33f, a, 1.0f));
     e = ex2f(-0.5f * kLog2e * x * x);
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
-    const float half = 0.5f * t * p * e;  // Phi(-|x|)
-    return x >= 0.0f ? 1.0f - half : half;
+    float p = fmaf(s, -1.96299188e-05f, 0.000127479288f);
+    p = fmaf(s, p, 0.000140480028f);
+    p = fmaf(s, p, -0.0017548654f);
+    p = fmaf(s, p, -0.0114476355f);
+    p = fmaf(s, p, 0.118352972f);
+    p = fmaf(s, p, -0.3989425f);
+    return fmaf(s, p, 0.5f);
+}
+// max(x, 0) - a Phi(-a)
+__device__ __forceinline__ float pw_gelu_f(float x) {
+    float a, e;
+    const float r = normal_tail(x, a, e);
+    return fmaf(-a, r * e, fmaxf(x, 0.0f));
+}
+// Phi(-a) - a phi(a), or 1 less that for x >= 0
+__device__ __forceinline__ float pw_gelu_d(float x) {
+    float a, e;
+    const float r = normal_tail(x, a, e), g = e * fmaf(-0.39894228040143268f, a, r);
+    return x >= 0.0f ? 1.0f - g : g;
 }
 
 template <int ACT> __device__ __forceinline__ float act_f(float x) {
-    float e;
-    return ACT == HC_PW_SILU ? silu_f(x) : ACT == HC_PW_GELU ? x * normal_cdf(x, e) : x;
+    return ACT == HC_PW_SILU ? silu_f(x) : ACT == HC_PW_GELU ? pw_gelu_f(x) : x;
 }
 template <int ACT> __device__ __forceinline__ float act_d(float x) {
-    if (ACT == HC_PW_SILU) return silu_d(x);
-    if (ACT != HC_PW_GELU) return 1.0f;
-    float e;
-    const float c = normal_cdf(x, e);
-    return fmaf(x * 0.39894228040143268f, e, c);
+    return ACT == HC_PW_SILU ? silu_d(x) : ACT == HC_PW_GELU ? pw_gelu_d(x) : 1.0f;
 }
 
 // Column sums of in[rows][na + nb + nc] in a fixed order: the first na columns

@@ -1,5 +1,7 @@
 """Where the mixer operators' rounding shows, against 64 bits: bounds derived from the formats, beside
 each test."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -36,3 +38,44 @@ def test_groupnorm_mean_under_a_large_offset(hc, P, C, G):
     assert ("gn_combine_kernel" in hc.hc_trace_collect()[1]) == (P > 4096)
     ref = x.double().view(P, G, C // G).mean((0, 2)).cpu().numpy()
     assert np.abs(mean[0].double().cpu().numpy() - ref).max() <= 2.0 ** -14 + 1e-6
+
+
+def gelu_of(hc, v):
+    """GELU and its slope at v through the norm (gamma 0, beta v: the activation's argument is v), and by the library's
+    elementwise calls (the form with erff)."""
+    C = v.numel()
+    x, z = torch.randn(1, 2, C, device="cuda", generator=torch.Generator(device="cuda").manual_seed(61)), torch.zeros_like(v)
+    d = hc.groupnorm_desc(1, 2, C, C // 16, torch.float32, act=hc.HC_PW_GELU)
+    ws, nb = space(hc, hc.hc_groupnorm_workspace_size(d, 1))
+    y, gx, one = torch.empty_like(x), torch.empty_like(x), torch.ones_like(x)
+    mean, rstd = torch.empty(1, C // 16, device="cuda"), torch.empty(1, C // 16, device="cuda")
+    gg, gb, ey, es = (torch.empty_like(v) for _ in range(4))
+    hc.check(hc.hc_groupnorm_fwd(d, x, z, v, y, mean, rstd, ws, nb))
+    hc.check(hc.hc_groupnorm_bwd(d, x, z, v, mean, rstd, one, gx, gg, gb, ws, nb))
+    hc.check(hc.hc_gelu_fwd(C, v, ey))
+    hc.check(hc.hc_gelu_bwd(C, v, torch.ones_like(v), es))
+    torch.cuda.synchronize()
+    vd = v.double()
+    cdf = torch.special.ndtr(vd)
+    return (y[0, 0], gb / 2, ey, es), (vd * cdf, cdf + vd * torch.exp(-0.5 * vd * vd) / math.sqrt(2 * math.pi))
+
+
+def test_gelu_is_as_accurate_as_the_error_function_form(hc):
+    """rms errors over 65536 normal values, a sample's rms being within a few per cent of the distribution's: at most a
+    quarter above those of the plain fp32 form."""
+    v = torch.randn(1 << 16, device="cuda", generator=torch.Generator(device="cuda").manual_seed(62))
+    (y, slope, ey, es), (ref, sref) = gelu_of(hc, v)
+    rms = lambda a, b: float((a.double() - b).square().mean().sqrt())
+    assert rms(y, ref) <= 1.25 * rms(ey, ref)
+    assert rms(slope, sref) <= 1.25 * rms(es, sref)
+
+
+def test_gelu_far_from_zero(hc):
+    """The negative tail to a relative 1e-5: exp(-x^2 / 2)'s argument, up to 18 at -5, is rounded twice (2e-6), the scaled
+    function, 0.08 there, is off by a few roundings below 0.5 (1e-6 to 2e-6).  Beyond the format's range: 0 and x."""
+    v = torch.cat([torch.linspace(-5, -1, 4080, device="cuda"), torch.linspace(-40, 40, 16, device="cuda")])
+    (y, slope, _, _), (ref, sref) = gelu_of(hc, v)
+    assert ((y.double() - ref).abs() <= 1e-5 * ref.abs())[:4080].all()
+    assert ((y.double() - ref).abs()[4080:] <= 1e-6 * v.abs().double()[4080:]).all()
+    assert ((slope.double() - sref).abs() <= 1e-6).all()
+    assert torch.isinf(gelu_of(hc, torch.full((16,), float("inf"), device="cuda"))[0][0]).all()
