@@ -92,11 +92,15 @@ __device__ __forceinline__ int lanes_sum(float (&v)[M], int n) {
     return first;
 }
 
-// 2^(s * A).  The special function unit's 2^x is low by 1.7e-8 to 2e-8 on
-// average over the arguments of slow states (-0.1 to -0.001; measured over 2^20
-// arguments a decade, rms error 3.5e-8), the same way in every row, which a state
-// with a memory of hundreds of rows adds up: gA of 1024 rows was 1.4e-6 off.
-// The multiply-add that forms the argument adds the mean back before it rounds.
+// 2^(s * A).  The special function unit's 2^x is low on average, the same way in
+// every row, which a state with a memory of hundreds of rows adds up: gA of 1024 rows
+// was 1.4e-6 off.  The multiply-add that forms the argument adds a mean back before it
+// rounds.  Mean error over 2^20 arguments from a third of x to x, without it and with
+// it, in 1e-8: x = -0.3 -1.9, +0.1; -0.1 -1.8, -0.2; -0.03 -2.6, -1.0; -0.01 -2.1, -0.5;
+// slower states, whose result comes to a few spacings (6e-8) below 1: -1e-3 -0.5, +1.1;
+// -1e-4 -0.7, +0.9; -1e-5 -1.0, +0.6; -1e-6 -1.2, +0.4; -3e-7 -0.7, +1.8 (rms 3 to 4 for
+// all; correctly rounded results 1.7).  An argument of 0 gives 1, and one below -1 takes
+// no part of it (-5.0).
 constexpr float kEx2Mean = 2.3e-8f;  // 1.6e-8 / ln 2
 __device__ __forceinline__ f32x2 decay2(f32x2 s, f32x2 A) {
     float a, b;

@@ -79,3 +79,31 @@ def test_gelu_far_from_zero(hc):
     assert ((y.double() - ref).abs()[4080:] <= 1e-6 * v.abs().double()[4080:]).all()
     assert ((slope.double() - sref).abs() <= 1e-6).all()
     assert torch.isinf(gelu_of(hc, torch.full((16,), float("inf"), device="cuda"))[0][0]).all()
+
+
+@pytest.mark.parametrize("sms", [1, 0])
+def test_slow_states_keep_their_decay(hc, sms):
+    """A state that only decays, over 4096 rows with steps of a third to all of 3e-7 ... 1e-2 (times log2 e), uncut and cut
+    into segments.  A row's decay is off by 1.2e-8 on average where that is above 3e-7, by 2e-8 below, the same way in every
+    row, and by 5e-8 (rms) at random; the state's own rounding adds 3e-8 (rms)."""
+    B, L, N, t = 4, 4096, 4, torch.float32
+    tops = 10.0 ** np.arange(-6.5, -1.99, 0.25)
+    D = tops.size
+    r = np.random.default_rng(63)
+    dt = torch.from_numpy(tops * r.uniform(1 / 3, 1, size=(B, L, D)) / math.log2(math.e)).float().cuda()
+    zero, y, hT = torch.zeros(B, L, D, device="cuda"), torch.empty(B, L, D, device="cuda"), torch.empty(B, D, N, device="cuda")
+    Bm = torch.zeros(B, L, N, device="cuda")
+    A = -torch.ones(D, N, device="cuda")
+    h0 = torch.ones(B, D, N, device="cuda")
+    hc.check(hc.hc_set_sm_count(sms))
+    try:
+        d = hc.selective_scan_desc(B, L, D, N, t, softplus=0)
+        ws, nb = space(hc, hc.hc_selective_scan_workspace_size(d, 0))
+        hc.check(hc.hc_selective_scan_fwd(d, zero, dt, A, Bm, Bm, y, h0=h0, hT=hT, ws=ws, ws_bytes=nb))
+        torch.cuda.synchronize()
+    finally:
+        hc.check(hc.hc_set_sm_count(0))
+    want = torch.exp(-dt.double().sum(1))[..., None]
+    off = ((hT.double() - want) / want).abs().amax((0, 2)).cpu().numpy()
+    mean = np.where(tops > 6e-7, 1.2e-8, 2e-8)
+    assert (off <= mean * L + 5 * math.hypot(5e-8, 3e-8) * math.sqrt(L)).all(), off
