@@ -54,13 +54,12 @@ __device__ __forceinline__ float rcpf(float x) {
     return r;
 }
 
-// The same for data that is not read again soon: evicted first.
 template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw(const T* p) {
     return *reinterpret_cast<const Pack<T, V>*>(p);
 }
+// The same for data that is not read again soon: evicted first.
 template <int BYTES> struct Word;
 template <> struct Word<16> { using type = uint4; };
-template <> struct Word<8> { using type = uint2; };
 template <> struct Word<4> { using type = unsigned; };
 template <> struct Word<2> { using type = unsigned short; };
 template <typename T, int V> __device__ __forceinline__ Pack<T, V> load_raw_last(const T* p) {

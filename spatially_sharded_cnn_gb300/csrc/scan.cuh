@@ -25,19 +25,6 @@ struct ScanArgs {
     float* dsum;          // [B][segs][D]: its sum of step sizes * log2 e
 };
 
-__device__ __forceinline__ float ld1(const void* p, long long i, int dt) {
-    if (dt == HC_DTYPE_F32) return static_cast<const float*>(p)[i];
-    if (dt == HC_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void st1(void* p, long long i, int dt, float v) {
-    if (dt == HC_DTYPE_F32)
-        static_cast<float*>(p)[i] = v;
-    else if (dt == HC_DTYPE_BF16)
-        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 // States n0 .. n0 + 3 of a [..][N] fp32 row (past N: zeros / not written): 16 bytes
 // at once where the row allows it -- a row of partial sums, (N + 2) * D floats
 // after the one before it, need not start on 16 bytes even if N is a multiple of 4.

@@ -398,8 +398,6 @@ def hc_trace_collect(max_entries: int = 256):
 # ---- channels-last sequence-mixer operators (include/hc_mixer.h) ------------
 HC_DTYPE_F32, HC_DTYPE_BF16, HC_DTYPE_F16 = range(3)
 HC_PW_NONE, HC_PW_SILU, HC_PW_GELU = range(3)
-
-
 _DTYPES = {"torch.float32": HC_DTYPE_F32, "torch.bfloat16": HC_DTYPE_BF16, "torch.float16": HC_DTYPE_F16}
 _TORCH = {}  # torch's dtype of each hc_dtype that was met
 
