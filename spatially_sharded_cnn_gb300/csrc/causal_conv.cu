@@ -115,8 +115,9 @@ __device__ __forceinline__ void load_row(const T* xb, long long row, const T* st
         load_or_zero<T, V>(state + (t + K - 1) * D, on && state != nullptr, f);
 }
 
-// 8 x 4096 x 1024 bf16, K = 4, SiLU (134 MB): 30 us a call, 4.5 TB/s; bound by
-// memory and the last wave of its blocks.
+// 8 x 4096 x 1024 bf16, K = 4, SiLU (134 MB): 30 us a call, 4.5 TB/s; bound by the bytes
+// it has in flight: its rows ahead are in registers, and 122 of those leave four blocks
+// an SM, 32 KB of loads (1216 blocks, two full waves).
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, View<T> y, const float* w,
                                                             const float* bias,
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(CC_THREADS) cc_fwd_kernel(View<const T> x, Vie
 // A run's rows [t0, t1): g_t for t in [t0, t1 + K - 1) recomputed, gx_t from
 // the K-row window of g, gw and gb summed over its own rows; the block's sums
 // go to part[block][(K + 1) * D]: K weights a channel, then the bias sums.
-// 56 x 1023 x 264 fp32, ragged: 50 us (181 MB were every row there, 3.6 TB/s), 166
-// registers; bound by the latency of its loads.
+// 56 x 1023 x 264 fp32, ragged: 50 us (121 MB with half of the rows there), 166
+// registers, three blocks an SM; bound by the bytes in flight as the forward kernel is.
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, View<const T> gy, View<T> gx,
                                                             const float* w, const float* bias,
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(CC_THREADS) cc_bwd_kernel(View<const T> x, Vie
 }
 
 // One token: y from the carried rows and x, and the carried rows moved on.  64 x
-// 2048 bf16: 5.9 us a call from Python, most of it the call.
+// 2048 bf16: 5.5 to 5.9 us a call from Python, most of it the call; replayed from a graph
+// with the carried rows in DRAM 3.0 us.
 template <typename T, int V, int K, int ACT>
 __global__ void __launch_bounds__(128) cc_step_kernel(View<const T> x, View<T> y, const float* w,
                                                       const float* bias, T* state, int B,
@@ -386,8 +388,9 @@ CcShape cc_shape(const hc_causal_conv_desc* d, int V) {
     s.cv = d->D / V;
     s.ncol = cc_columns(s.cv);
     s.R = CC_THREADS / s.ncol;
-    // runs of CC_RUN rows, shorter where that leaves the GPU without eight blocks an
-    // SM (backward as above: runs of 16, 32, 64 rows 82, 66, 61 us)
+    // runs of CC_RUN rows, shorter where that leaves the launch under eight blocks an
+    // SM, two rounds of the four (backward: three) that are resident (backward as above:
+    // runs of 16, 32, 64 rows 82, 66, 61 us)
     const long long cols = cdiv(s.cv, s.ncol);
     long long runs = cdiv(s.L, CC_RUN);
     const long long want = cdiv(8LL * device_sm_count() * s.R, (long long)s.B * cols);

@@ -212,7 +212,8 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 // blocks of the kernel before it in the stream are finishing: a kernel's first act
 // is grid_begin, which waits until that kernel is complete and its writes are
 // visible.  Hides most of a launch's latency (about 2 us), of which a short call
-// has several: ragged 5 x 1537 x 328 scan step 148 -> 130 us.  (Letting the next
+// has several: the ragged 5 x 1537 x 328 scan training took 148 us before and 130 after,
+// 121 with later changes.  (Letting the next
 // kernel's blocks in before this one's begin to end made the 224 x 1024 x 256 step
 // 1.60 -> 1.74 ms: they take the shared memory that this one's later blocks want.)
 // Everything is read through plain pointers or volatile loads, parameters too (an

@@ -69,8 +69,10 @@ template <int DT> void sum_bc(const ScanArgs& a, cudaStream_t st) {
 }
 
 // One token: NL lanes a channel, 32 / NL channels a warp.  Reads and writes the
-// states (64 x 2048 x 16: 17 MB): 12 us from DRAM; called again and again, with the
-// states in L2, 8.5 us a call from Python, most of it the call.
+// states.  64 x 2048 x 16 (17 MB): replayed from a graph with the states in DRAM 7.3 us,
+// 2.3 TB/s; called from Python with the states in L2 8.7 us, most of it the call.
+// 2048 x 512 x 16 (134 MB): 48 us, 2.8 TB/s; bound by latency, one 16-byte load of states
+// a thread in flight.
 template <int NL, int DT>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanArgs a, float* state) {
     grid_begin();
@@ -163,7 +165,8 @@ int bwd_ctiles(const hc_selective_scan_desc* d) {
 // two extra launches as long as a dozen), else as many as make up for it, of two
 // tiles at least.  Ragged sequences are cut twice as fine: blocks without rows end
 // at once, and half of them have none where lengths are spread evenly.
-// (16384 x 512 forward: 4, 6, 8 blocks an SM 114, 105, 113 us.)
+// (16384 x 512 forward: cut for 4, 6, 8 blocks an SM 114, 105, 113 us; four of its blocks
+// are resident at once, three of the backward kernel's.)
 struct Segs {
     int n, tiles;
 };

@@ -9,7 +9,7 @@ namespace {
 // registers (H), with y and gC on the way, then the state's gradient runs back
 // through them.  A tile's first state was saved; that of its later half is
 // recomputed from it.  Half tiles keep a thread at 168 registers, three blocks an
-// SM; whole tiles take 255 and two.
+// SM, with 28 to 112 bytes of it spilled; whole tiles take 255 and two.
 //
 // A state takes 5 fp32 operations and an exponential on the way up, 3 and one more
 // in an earlier half's recomputation, 8 and one on the way down: 14.5 and 2.5 a row

@@ -8,8 +8,9 @@ namespace {
 // the walk over them makes step sizes, step * u, D * u and silu(z), the recurrence
 // reads those as channel pairs, and a second walk writes y.  224 x 1024 x 256 fp32,
 // 16 states, saving the states: 396 us, 3.6 TB/s (1.4 GB), a third of the fp32
-// pipe; 16384 x 512 bf16 in segments 58 us.  Bound by instruction issue: half of
-// the 160 instructions a channel and row are the walks'.
+// pipe; 16384 x 512 bf16 in segments 58 us.  Bound by instruction issue with four
+// blocks an SM (123 to 128 registers): half of the 160 instructions a channel and row
+// are the walks', which are not packed as the recurrence is.
 template <int NL> constexpr size_t fwd_smem() {
     using S = FwdTile<NL>;
     return sizeof(float) * (5 * S::PLANE + 2 * S::CT + 4 * SC_T * S::NP + 3 * S::PLANE);
