@@ -84,7 +84,9 @@ template <typename T> __device__ __forceinline__ bool gn_kept(const GnShape& s, 
 }
 
 // The R rows of threads' two sums of every channel, to tot[0 | 1][ncol * V]: rows
-// in order, in as many runs as there are threads for, then the runs in order.
+// in order, in as many runs as there are threads for but no more than sixteen, then
+// the runs in order.  (256 runs of one row, which a single channel has threads for,
+// would be one sum of 256 in order: three times the rounding error.)
 template <int V>
 __device__ __forceinline__ void gn_block_sum(float2* sm, float (*tot)[GN_THREADS * V], int ncol, int R, int col, int r,
                                              bool on, const float (&a)[V], const float (&b)[V]) {
@@ -95,7 +97,7 @@ __device__ __forceinline__ void gn_block_sum(float2* sm, float (*tot)[GN_THREADS
     }
     __syncthreads();
     int rows = R;
-    const int parts = w < GN_THREADS ? min(GN_THREADS / w, R) : 1;
+    const int parts = w < GN_THREADS ? min(min(GN_THREADS / w, 16), R) : 1;
     if (parts > 1) {
         const int c = tid % w, q = tid / w;
         float2 t = make_float2(0.0f, 0.0f);

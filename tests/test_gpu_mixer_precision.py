@@ -40,6 +40,29 @@ def test_groupnorm_mean_under_a_large_offset(hc, P, C, G):
     assert np.abs(mean[0].double().cpu().numpy() - ref).max() <= 2.0 ** -14 + 1e-6
 
 
+def test_groupnorm_sums_of_one_channel(hc):
+    """The sums of a block whose 256 rows of threads all have the same channel.  Adding m values of spread s in order leaves
+    0.29 * m * 2^-24 * s (rms: sum k is off by 0.4 units of its own size sqrt(k) s).  512 values, two a thread, in sixteen
+    runs of sixteen rows and then the runs: 16 runs of 0.29 * 16 * sqrt(2) and one of 0.29 * 16 * sqrt(32), 37 in all;
+    the values' own rounding 23.  In one run of 256 the sum alone would leave 105.  Held to 75 over 60 inputs."""
+    P, off, spread = 512, [], []
+    one, zero = torch.ones(4, device="cuda")[:1], torch.zeros(4, device="cuda")[:1]
+    d = hc.groupnorm_desc(1, P, 1, 1, torch.float32)
+    ws, nb = space(hc, hc.hc_groupnorm_workspace_size(d, 1))
+    g = torch.Generator(device="cuda").manual_seed(64)
+    for _ in range(60):
+        x, gy = (torch.randn(1, P, 1, device="cuda", generator=g) for _ in range(2))
+        y, gx = torch.empty_like(x), torch.empty_like(x)
+        mean, rstd = torch.empty(1, 1, device="cuda"), torch.empty(1, 1, device="cuda")
+        gg, gb = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+        hc.check(hc.hc_groupnorm_fwd(d, x, one, zero, y, mean, rstd, ws, nb))
+        hc.check(hc.hc_groupnorm_bwd(d, x, one, zero, mean, rstd, gy, gx, gg, gb, ws, nb))
+        t = gy.double() * (x.double() - mean.double()) * rstd.double()
+        off.append(float(gg.double() - t.sum()))
+        spread.append(float(t.square().mean().sqrt()))
+    assert np.sqrt(np.mean(np.square(off))) <= 75 * 2.0 ** -24 * np.mean(spread)
+
+
 def gelu_of(hc, v):
     """GELU and its slope at v through the norm (gamma 0, beta v: the activation's argument is v), and by the library's
     elementwise calls (the form with erff)."""
