@@ -497,4 +497,8 @@ hc_status hc_trace_collect(hc_trace_entry* out, int max_entries, int* n_entries)
  * short causal convolution and a selective state-space scan. */
 #include "hc_mixer.h"
 
+/* Operators of a channels-last sequence block: layer norm, linear attention
+ * with a decay for each head and the gated feed-forward product. */
+#include "hc_block.h"
+
 #endif /* HC_H */

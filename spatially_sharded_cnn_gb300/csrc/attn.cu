@@ -1,0 +1,244 @@
+// attn.cu -- linear attention with a decay for each head: the join of segments, the form
+// for one token, and the entry points (hc_linear_attn_*).
+#include <math.h>
+
+#include "attn.cuh"
+
+namespace hc {
+namespace {
+
+// One thread an element of the state: carry[seg] becomes the state ahead of segment
+// seg, and z1 the one behind the last.  Grid: (elements of a state, pairs, passes).
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int T) {
+    grid_begin();
+    const AttnPass& p = a.p[blockIdx.z];
+    if (!p.keep) return;
+    const int e = blockIdx.y * 256 + threadIdx.x, pair = blockIdx.x, size = p.Dk * p.Dv;
+    if (e >= size) return;
+    const int b = pair / a.H, h = pair - b * a.H;
+    const int len = attn_len(a.lens, b, a.L), chunks = (len + T - 1) / T;
+    const float l2 = attn_log2_decay(a.decay, h);
+    float z = p.z0 ? p.z0[(long long)pair * size + e] : 0.0f;
+    float* c = p.carry + (long long)pair * a.segs * size + e;
+    const int part = chunks * T - len;  // rows that the chunk with the first row lacks
+    for (int s = 0; s < a.segs; s++) {
+        const int c0 = min(chunks, s * a.per), c1 = min(chunks, c0 + a.per);
+        const bool first = c1 > c0 && (p.back ? c1 == chunks : c0 == 0);
+        const float own = c[(long long)s * size];
+        c[(long long)s * size] = z;
+        z = fmaf(z, exp2f(l2 * ((c1 - c0) * T - (first ? part : 0))), own);
+    }
+    if (p.z1) p.z1[(long long)pair * size + e] = z;
+}
+
+// One token: a block a (sequence, head).  Thread (r, c) takes columns c * V .. of rows
+// r, r + R, ...; bound by the states, read and written once.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) attn_step_kernel(View<const T> q, View<const T> k, View<const T> v,
+                                                        const float* decay, float* state, View<T> y, int H, int Dk,
+                                                        int Dv, float scale) {
+    grid_begin();
+    __shared__ float sm[256 * V];
+    const int pair = blockIdx.x, b = pair / H, h = pair - b * H;
+    const int cols = (Dv + V - 1) / V, R = 256 / cols;
+    const int r = threadIdx.x / cols, c = (threadIdx.x - r * cols) * V;
+    const float w = exp2f(attn_log2_decay(decay, h));
+    const T* qr = q.p + b * q.batch + (long long)h * Dk;
+    const T* kr = k.p + b * k.batch + (long long)h * Dk;
+    const T* vr = v.p + b * v.batch + (long long)h * Dv;
+    float* z = state + (long long)pair * Dk * Dv + c;
+    float acc[V], vf[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        acc[i] = 0.0f;
+        vf[i] = r < R ? to_f(vr[c + i]) : 0.0f;
+    }
+    if (r < R) {
+#pragma unroll 4
+        for (int d = r; d < Dk; d += R) {
+            const float kf = to_f(kr[d]), qf = to_f(qr[d]);
+            float s[V];
+            load_pack<float, V>(z + (long long)d * Dv, s);
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                s[i] = fmaf(s[i], w, kf * vf[i]);
+                acc[i] = fmaf(qf, s[i], acc[i]);
+            }
+            store_pack<float, V>(z + (long long)d * Dv, s);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) sm[threadIdx.x * V + i] = acc[i];
+    __syncthreads();
+    for (int n = threadIdx.x; n < Dv; n += 256) {
+        float t = 0.0f;
+        for (int j = 0; j < R; j++) t += sm[j * cols * V + n];
+        y.p[b * y.batch + (long long)h * Dv + n] = from_f<T>(scale * t);
+    }
+}
+
+template <typename T>
+hc_status attn_step(const hc_linear_attn_desc* d, const hc_rows* q, const hc_rows* k, const hc_rows* v,
+                    const float* decay, float* state, const hc_rows* y, cudaStream_t st) {
+    const dim3 grid((unsigned)((long long)d->B * d->H));
+    if (d->Dv % 4 == 0)
+        launch_next(attn_step_kernel<T, 4>, grid, dim3(256), 0, st, view<const T>(q), view<const T>(k),
+                    view<const T>(v), decay, state, view<T>(y), d->H, d->Dk, d->Dv, d->scale);
+    else
+        launch_next(attn_step_kernel<T, 1>, grid, dim3(256), 0, st, view<const T>(q), view<const T>(k),
+                    view<const T>(v), decay, state, view<T>(y), d->H, d->Dk, d->Dv, d->scale);
+    return launched("attn_step_kernel", st);
+}
+
+bool attn_desc_ok(const hc_linear_attn_desc* d) {
+    return d && d->B >= 1 && d->L >= 0 && d->H >= 1 && d->Dk >= 1 && d->Dv >= 1 && isfinite(d->scale) &&
+           dtype_ok(d->dtype);
+}
+bool attn_size_ok(const hc_linear_attn_desc* d) {
+    return d->Dk <= 128 && d->Dv <= 128 && d->L < 0x7fffffff - 256 && (long long)d->H * d->Dk <= 1 << 20 &&
+           (long long)d->H * d->Dv <= 1 << 20 && (long long)d->B * d->H < 0x7fffffffLL / 3;
+}
+
+struct Cut {
+    int segs, per;
+};
+// Segments of a sequence in chunks of T rows: as many as give `want` blocks in all, two
+// chunks each at least.
+Cut attn_cut(const hc_linear_attn_desc* d, int T, int passes) {
+    const long long pairs = (long long)d->B * d->H * passes, want = 2LL * device_sm_count();
+    const int chunks = (int)(((long long)d->L + T - 1) / T);
+    long long segs = pairs < want ? want / pairs : 1;
+    if (segs > chunks / 2) segs = chunks / 2;
+    if (segs < 1) segs = 1;
+    const int per = (int)((chunks + segs - 1) / segs);
+    return {per > 0 ? (chunks + per - 1) / per : 1, per};
+}
+
+size_t carry_floats(const hc_linear_attn_desc* d, const Cut& c) {
+    return c.segs > 1 ? (size_t)d->B * d->H * c.segs * d->Dk * d->Dv : 0;
+}
+
+AttnArgs attn_args(const hc_linear_attn_desc* d, const float* decay, const int* lens, const Cut& c) {
+    AttnArgs a = {};
+    a.decay = decay;
+    a.lens = lens;
+    a.B = d->B;
+    a.L = d->L;
+    a.H = d->H;
+    a.dtype = d->dtype;
+    a.segs = c.segs;
+    a.per = c.per;
+    return a;
+}
+
+hc_status attn_run(const AttnArgs& a, cudaStream_t st) {
+    hc_status e = HC_OK;
+    if (a.segs > 1 && ((e = launch_attn_fp32(a, true, st)) || (e = launch_attn_join(a, AT_T, st)))) return e;
+    return launch_attn_fp32(a, false, st);
+}
+
+}  // namespace
+
+hc_status launch_attn_join(const AttnArgs& a, int T, cudaStream_t st) {
+    const int size = a.p[0].Dk * a.p[0].Dv;  // the same for every pass
+    launch_next(attn_join_kernel, dim3((unsigned)((long long)a.B * a.H), cdiv(size, 256), a.passes), dim3(256), 0, st, a,
+                T);
+    return launched("attn_join_kernel", st);
+}
+
+}  // namespace hc
+
+using namespace hc;
+
+extern "C" {
+
+// Segments' states: of S forward; of S and of G backward.
+hc_status hc_linear_attn_workspace_size(const hc_linear_attn_desc* d, int pass, size_t* bytes) {
+    if (!attn_desc_ok(d) || pass < 0 || pass > 1 || !bytes) return HC_ERR_INVALID_ARG;
+    if (!attn_size_ok(d)) return HC_ERR_UNSUPPORTED;
+    size_t n = carry_floats(d, attn_cut(d, AT_T, 1));
+    if (pass == 1) {
+        const size_t b = 2 * carry_floats(d, attn_cut(d, AT_T, 3));
+        if (b > n) n = b;
+    }
+    *bytes = n * sizeof(float);
+    return HC_OK;
+}
+
+hc_status hc_linear_attn_fwd(const hc_linear_attn_desc* d, const hc_rows* q, const hc_rows* k, const hc_rows* v,
+                             const float* log_decay, const hc_rows* y, const float* h0, float* hT, const int* lens,
+                             void* ws, size_t ws_bytes, void* stream) {
+    size_t need = 0;
+    const hc_status e = hc_linear_attn_workspace_size(d, 0, &need);
+    if (e) return e;
+    if (!rows_in_ok(q, d->dtype, d->L) || !rows_in_ok(k, d->dtype, d->L) || !rows_in_ok(v, d->dtype, d->L) ||
+        !rows_out_ok(y, d->dtype, d->B, d->L, (long long)d->H * d->Dv) || rows_same(y, q) || rows_same(y, k) ||
+        rows_same(y, v) || !f32_opt_ok(log_decay) || !f32_opt_ok(h0) || !f32_opt_ok(hT) || (h0 && h0 == hT) ||
+        !ptr_al(lens, 4))
+        return HC_ERR_INVALID_ARG;
+    if (need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
+    const cudaStream_t st = (cudaStream_t)stream;
+    traced_begin(st);
+    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, AT_T, 1));
+    a.passes = 1;
+    a.p[0] = {*q, *k, *v, *y, d->Dk, d->Dv, d->scale, d->scale, 1.0f, 0, h0, hT, d->Dv, 1,
+              a.segs > 1 ? (float*)ws : nullptr, 1};
+    return attn_run(a, st);
+}
+
+hc_status hc_linear_attn_bwd(const hc_linear_attn_desc* d, const hc_rows* q, const hc_rows* k, const hc_rows* v,
+                             const float* log_decay, const float* h0, const hc_rows* gy, const float* ghT,
+                             const hc_rows* gq, const hc_rows* gk, const hc_rows* gv, float* gh0, const int* lens,
+                             void* ws, size_t ws_bytes, void* stream) {
+    size_t need = 0;
+    const hc_status e = hc_linear_attn_workspace_size(d, 1, &need);
+    if (e) return e;
+    for (const hc_rows* r : {q, k, v, gy})
+        if (!rows_in_ok(r, d->dtype, d->L)) return HC_ERR_INVALID_ARG;
+    if (!rows_out_ok(gq, d->dtype, d->B, d->L, (long long)d->H * d->Dk) ||
+        !rows_out_ok(gk, d->dtype, d->B, d->L, (long long)d->H * d->Dk) ||
+        !rows_out_ok(gv, d->dtype, d->B, d->L, (long long)d->H * d->Dv) || !f32_opt_ok(log_decay) || !f32_opt_ok(h0) ||
+        !f32_opt_ok(ghT) || !f32_opt_ok(gh0) || (ghT && ghT == gh0) || (h0 && h0 == gh0) || !ptr_al(lens, 4))
+        return HC_ERR_INVALID_ARG;
+    for (const hc_rows* o : {gq, gk, gv})
+        for (const hc_rows* r : {q, k, v, gy})
+            if (rows_same(o, r)) return HC_ERR_INVALID_ARG;
+    if (rows_same(gq, gk) || rows_same(gq, gv) || rows_same(gk, gv)) return HC_ERR_INVALID_ARG;
+    if (need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
+    const cudaStream_t st = (cudaStream_t)stream;
+    traced_begin(st);
+    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, AT_T, 3));
+    float *cs = nullptr, *cg = nullptr;
+    if (a.segs > 1) {
+        cs = (float*)ws;
+        cg = cs + carry_floats(d, {a.segs, a.per});
+    }
+    const float s = d->scale;
+    // the states of gv's pass are those of gk's, transposed; S comes from k and v, whose
+    // pass is not run: gq's takes S^T (v, k)
+    const AttnPass pq = {*gy, *v, *k, *gq, d->Dv, d->Dk, s, s, 1.0f, 0, h0, nullptr, 1, d->Dv, cs, 1};
+    const AttnPass pv = {*k, *q, *gy, *gv, d->Dk, d->Dv, s, 1.0f, s, 1, ghT, gh0, d->Dv, 1, cg, 1};
+    const AttnPass pk = {*v, *gy, *q, *gk, d->Dv, d->Dk, s, 1.0f, s, 1, ghT, nullptr, 1, d->Dv, cg, 0};
+    a.passes = 3;
+    a.p[0] = pq;
+    a.p[1] = pv;
+    a.p[2] = pk;
+    return attn_run(a, st);
+}
+
+hc_status hc_linear_attn_step(const hc_linear_attn_desc* d, const hc_rows* q, const hc_rows* k, const hc_rows* v,
+                              const float* log_decay, float* state, const hc_rows* y, void* stream) {
+    if (!attn_desc_ok(d)) return HC_ERR_INVALID_ARG;
+    if (!attn_size_ok(d)) return HC_ERR_UNSUPPORTED;
+    if (!rows_in_ok(q, d->dtype) || !rows_in_ok(k, d->dtype) || !rows_in_ok(v, d->dtype) ||
+        !rows_out_ok(y, d->dtype, d->B, 1, (long long)d->H * d->Dv) || rows_same(y, q) || rows_same(y, k) ||
+        rows_same(y, v) || !f32_opt_ok(log_decay) || !f32_ok(state))
+        return HC_ERR_INVALID_ARG;
+    const cudaStream_t st = (cudaStream_t)stream;
+    traced_begin(st);
+    if (d->dtype == HC_DTYPE_F32) return attn_step<float>(d, q, k, v, log_decay, state, y, st);
+    if (d->dtype == HC_DTYPE_BF16) return attn_step<__nv_bfloat16>(d, q, k, v, log_decay, state, y, st);
+    return attn_step<__half>(d, q, k, v, log_decay, state, y, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,79 @@
+// attn.cuh -- shared by the linear attention kernels (attn.cu, attn_fp32.cu, attn_tc.cu).
+//
+// One computation serves the forward pass and the three gradients.  A pass takes rows
+// q, k ([Dk] a head) and v ([Dv]) and a state Z ([Dk][Dv]), and walks over the rows in
+// chunks of T, forwards or backwards.  With w(n) = lambda^n, for rows i, j of a chunk
+// whose first row that exists is lo (chunks end at the sequence's end, so the
+// chunk with the first row may begin before it):
+//   forwards   y_i = si sum_{j <= i} w(i-j) (q_i . k_j) v_j + sx w(i-lo+1) q_i Z
+//              Z   <- w(T-lo) Z + su sum_j w(T-1-j) k_j v_j^T
+//   backwards  y_i = si sum_{j >= i} w(j-i) (q_i . k_j) v_j + sx w(T-1-i) q_i Z
+//              Z   <- w(T-lo) Z + su sum_j w(j-lo+1) k_j v_j^T
+// Then, with the state S and the state's gradient G,
+//   y  = forwards (q, k, v; S),              si = sx = scale, su = 1
+//   gq = forwards (gy, v, k; S^T),           si = sx = scale, su = 1
+//   gv = backwards(k, q, gy; G),             si = su = scale, sx = 1
+//   gk = backwards(v, gy, q; G^T),           si = su = scale, sx = 1
+// (a row j of the sum is then a later row, whose gradient it carries back).
+//
+// Where sequences times heads leave the GPU idle, a sequence's chunks are cut into
+// segments: every segment's own sum of k v^T (the carry pass), a join in order, and
+// then all segments at once, each from the state ahead of it.
+#pragma once
+
+#include "rows.cuh"
+
+namespace hc {
+
+constexpr float kLowDecay = -1e30f;  // stands for a log decay of minus infinity: 0 * it is 0
+
+struct AttnPass {
+    hc_rows q, k, v, y;
+    int Dk, Dv;         // of this pass: the widths of q, k and of v, y
+    float si, sx, su;
+    int back;           // 1: backwards
+    const float* z0;    // the state ahead of the first chunk, element (m, n) of pair p at p * Dk * Dv + m * zm + n * zn
+    float* z1;          // where the state behind the last chunk goes, laid out so; NULL: nowhere
+    int zm, zn;
+    float* carry;       // segments' states [pair][seg], laid out so; NULL: one segment
+    int keep;           // the carry pass fills `carry` from this pass's k and v (su in them)
+};
+
+struct AttnArgs {
+    AttnPass p[3];
+    int passes;
+    const float* decay;
+    const int* lens;
+    int B, L, H, dtype;
+    int segs, per;  // segments of a sequence, chunks of a segment
+};
+
+__host__ __device__ inline int attn_len(const int* lens, int b, int L) {
+    if (!lens) return L;
+    const int n = lens[b];
+    return n < 0 ? 0 : n > L ? L : n;
+}
+__device__ __forceinline__ float attn_log2_decay(const float* decay, int h) {
+    if (!decay) return 0.0f;
+    const float a = decay[h];
+    return (a < kLowDecay ? kLowDecay : a) * kLog2e;
+}
+
+// Rows past the sequence's end: zeros, a share for each of `segs` blocks.
+template <typename T>
+__device__ __forceinline__ void attn_blank(const AttnPass& p, int b, int h, int len, int L, int seg, int segs) {
+    const long long gone = (long long)(L - len), r0 = len + gone * seg / segs, r1 = len + gone * (seg + 1) / segs;
+    T* y = static_cast<T*>(p.y.p) + b * p.y.batch + (long long)h * p.Dv;
+    for (long long e = threadIdx.x; e < (r1 - r0) * p.Dv; e += blockDim.x) {
+        const long long r = e / p.Dv;
+        y[(r0 + r) * p.y.row + (e - r * p.Dv)] = from_f<T>(0.0f);
+    }
+}
+
+// The kernels in fp32 (any type of row): 32-row chunks.
+constexpr int AT_T = 32;
+hc_status launch_attn_fp32(const AttnArgs& a, bool carry, cudaStream_t st);
+// Segments joined in order, in place: carry[seg] becomes the state ahead of it.
+hc_status launch_attn_join(const AttnArgs& a, int T, cudaStream_t st);
+
+}  // namespace hc

@@ -1,0 +1,447 @@
+// layernorm.cu -- layer norm over the channels of each row, forward and backward
+// (hc_layernorm_*).
+//
+// TPR threads hold one row in registers: its values are read once, the mean and then
+// the squared deviations from it are summed from registers (two passes over values
+// that do not move, so no cancellation), and the row is written.  Bound by memory:
+// x in and y out, and for the backward pass x and gy in and gx out.
+#include "rows.cuh"
+
+namespace hc {
+namespace {
+
+constexpr int LN_THREADS = 256;
+
+struct LnShape {
+    int L, C;
+    int rows;    // B * L
+    float eps;
+    const int* lens;
+};
+
+// Threads of a block: rows of up to a warp share one, a longer row has its own.
+__host__ __device__ constexpr int ln_block(int tpr) { return tpr > 32 ? tpr : LN_THREADS; }
+
+// V parameters; their array is aligned to 16 bytes.
+template <int V> __device__ __forceinline__ void ln_param(const float* p, float (&f)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + i);
+            f[i] = q.x;
+            f[i + 1] = q.y;
+            f[i + 2] = q.z;
+            f[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) f[i] = p[i];
+    }
+}
+
+// Sum over the TPR threads of a row; every one of them gets it, added in the same
+// order.  red: a slot for each warp of the block, for rows that take several warps.
+template <int TPR> __device__ __forceinline__ float ln_sum(float v, float* red) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (TPR > 32) {
+        const int w = threadIdx.x >> 5;
+        __syncthreads();  // the sum before has been read
+        if ((threadIdx.x & 31) == 0) red[w] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < TPR / 32; k++) v += red[k];
+    }
+    return v;
+}
+
+__device__ __forceinline__ bool ln_live(const LnShape& s, int b, int l) { return !s.lens || l < s.lens[b]; }
+
+// NV packs of V values a thread: channels (i * TPR + lane) * V of pack i.  Blocks
+// walk over the rows, ROWS at a time.
+template <typename T, int V, int TPR, int NV>
+__global__ void __launch_bounds__(ln_block(TPR))
+    ln_fwd_kernel(View<const T> x, const float* gamma, const float* beta, View<T> y, float* mean, float* rstd,
+                  LnShape s) {
+    grid_begin();
+    constexpr int ROWS = ln_block(TPR) / TPR;
+    __shared__ float red[32];
+    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const float inv = 1.0f / s.C;
+    // every thread takes every turn: the sums are of whole warps
+    for (long long r0 = (long long)blockIdx.x * ROWS; r0 < s.rows; r0 += (long long)gridDim.x * ROWS) {
+        const long long r = r0 + sub;
+        const bool there = r < s.rows;
+        const int b = there ? (int)(r / s.L) : 0, l = there ? (int)(r - (long long)b * s.L) : 0;
+        const bool live = there && ln_live(s, b, l);
+        const T* xr = x.p + b * x.batch + l * x.row;
+        float v[NV][V];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+            if (live && c < s.C) {
+                unpack(load_raw_stream<T, V>(xr + c), v[i]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; k++) v[i][k] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < V; k++) sum += v[i][k];
+        }
+        const float m = __fmul_rn(ln_sum<TPR>(sum, red), inv);  // rounded alike wherever it is used
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if ((i * TPR + lane) * V < s.C) {
+#pragma unroll
+                for (int k = 0; k < V; k++) {
+                    v[i][k] -= m;
+                    sq = fmaf(v[i][k], v[i][k], sq);
+                }
+            }
+        }
+        const float rs = __frcp_rn(__fsqrt_rn(ln_sum<TPR>(sq, red) * inv + s.eps));
+        if (!there) continue;
+        if (lane == 0) {
+            if (mean) mean[r] = live ? m : 0.0f;
+            if (rstd) rstd[r] = live ? rs : 0.0f;
+        }
+        T* yr = y.p + b * y.batch + l * y.row;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+            if (c < s.C) {
+                float g[V], o[V];
+                ln_param<V>(gamma + c, g);
+                ln_param<V>(beta + c, o);
+#pragma unroll
+                for (int k = 0; k < V; k++) o[k] = live ? fmaf(v[i][k] * rs, g[k], o[k]) : 0.0f;
+                store_pack<T, V>(yr + c, o);
+            }
+        }
+    }
+}
+
+// A block of LN_THREADS a row that no variant above holds: read three times.
+template <typename T>
+__global__ void __launch_bounds__(LN_THREADS) ln_fwd_long_kernel(View<const T> x, const float* gamma, const float* beta,
+                                                                 View<T> y, float* mean, float* rstd, LnShape s) {
+    grid_begin();
+    __shared__ float red[32];
+    for (long long r = blockIdx.x; r < s.rows; r += gridDim.x) {
+        const int b = (int)(r / s.L), l = (int)(r - (long long)b * s.L);
+        const bool live = ln_live(s, b, l);
+        const T* xr = x.p + b * x.batch + l * x.row;
+        float sum = 0.0f, sq = 0.0f;
+        if (live)
+            for (int c = threadIdx.x; c < s.C; c += LN_THREADS) sum += to_f(xr[c]);
+        const float m = ln_sum<LN_THREADS>(sum, red) / s.C;
+        if (live)
+            for (int c = threadIdx.x; c < s.C; c += LN_THREADS) {
+                const float d = to_f(xr[c]) - m;
+                sq = fmaf(d, d, sq);
+            }
+        const float rs = __frcp_rn(__fsqrt_rn(ln_sum<LN_THREADS>(sq, red) / s.C + s.eps));
+        if (threadIdx.x == 0) {
+            if (mean) mean[r] = live ? m : 0.0f;
+            if (rstd) rstd[r] = live ? rs : 0.0f;
+        }
+        T* yr = y.p + b * y.batch + l * y.row;
+        for (int c = threadIdx.x; c < s.C; c += LN_THREADS)
+            yr[c] = from_f<T>(live ? fmaf((to_f(xr[c]) - m) * rs, gamma[c], beta[c]) : 0.0f);
+    }
+}
+
+// Backward: a thread keeps the sums for gamma and beta of its channels over the rows
+// that its block walks; the block's row groups are then added in order into
+// part[block][ggamma C | gbeta C].  gy * gamma is rounded (__fmul_rn) before its mean is
+// taken from it, as it was in that mean: where a row's gradient cancels to zero, it is zero.
+template <typename T, int V, int TPR, int NV>
+__global__ void __launch_bounds__(ln_block(TPR))
+    ln_bwd_kernel(View<const T> x, const float* gamma, const float* mean, const float* rstd, View<const T> gy,
+                  View<T> gx, float* part, LnShape s) {
+    grid_begin();
+    constexpr int ROWS = ln_block(TPR) / TPR;
+    __shared__ float red[32];
+    extern __shared__ float own[];  // [ROWS][2][C], rows of several groups
+    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const float inv = 1.0f / s.C;
+    float gg[NV][V], gb[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int k = 0; k < V; k++) gg[i][k] = gb[i][k] = 0.0f;
+    for (long long r0 = (long long)blockIdx.x * ROWS; r0 < s.rows; r0 += (long long)gridDim.x * ROWS) {
+        const long long r = r0 + sub;
+        const bool there = r < s.rows;
+        const int b = there ? (int)(r / s.L) : 0, l = there ? (int)(r - (long long)b * s.L) : 0;
+        const bool live = there && ln_live(s, b, l);
+        const T* xr = x.p + b * x.batch + l * x.row;
+        const T* gr = gy.p + b * gy.batch + l * gy.row;
+        const float m = live ? mean[r] : 0.0f, rs = live ? rstd[r] : 0.0f;
+        Pack<T, V> xq[NV], gq[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+            if (live && c < s.C) {
+                xq[i] = load_raw_stream<T, V>(xr + c);
+                gq[i] = load_raw_stream<T, V>(gr + c);
+            }
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+            if (live && c < s.C) {
+                float xv[V], gv[V], ga[V];
+                unpack(xq[i], xv);
+                unpack(gq[i], gv);
+                ln_param<V>(gamma + c, ga);
+#pragma unroll
+                for (int k = 0; k < V; k++) {
+                    const float xh = (xv[k] - m) * rs, q = __fmul_rn(gv[k], ga[k]);
+                    gg[i][k] = fmaf(gv[k], xh, gg[i][k]);
+                    gb[i][k] += gv[k];
+                    s1 += q;
+                    s2 = fmaf(q, xh, s2);
+                }
+            }
+        }
+        const float m1 = __fmul_rn(ln_sum<TPR>(s1, red), inv), m2 = __fmul_rn(ln_sum<TPR>(s2, red), inv);
+        if (!there) continue;
+        T* or_ = gx.p + b * gx.batch + l * gx.row;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+            if (c < s.C) {
+                float o[V];
+                if (live) {
+                    float xv[V], gv[V], ga[V];
+                    unpack(xq[i], xv);
+                    unpack(gq[i], gv);
+                    ln_param<V>(gamma + c, ga);
+#pragma unroll
+                    for (int k = 0; k < V; k++) o[k] = rs * (__fmul_rn(gv[k], ga[k]) - m1 - (xv[k] - m) * rs * m2);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; k++) o[k] = 0.0f;
+                }
+                store_pack<T, V>(or_ + c, o);
+            }
+        }
+    }
+    if (!part) return;
+    float* p = part + (long long)blockIdx.x * 2 * s.C;
+    if constexpr (ROWS == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+#pragma unroll
+            for (int k = 0; k < V; k++)
+                if (c + k < s.C) {
+                    p[c + k] = gg[i][k];
+                    p[s.C + c + k] = gb[i][k];
+                }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * TPR + lane) * V;
+#pragma unroll
+            for (int k = 0; k < V; k++)
+                if (c + k < s.C) {
+                    own[sub * 2 * s.C + c + k] = gg[i][k];
+                    own[sub * 2 * s.C + s.C + c + k] = gb[i][k];
+                }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * s.C; c += LN_THREADS) {
+            float t = own[c];
+#pragma unroll 4
+            for (int k = 1; k < ROWS; k++) t += own[k * 2 * s.C + c];
+            p[c] = t;
+        }
+    }
+}
+
+// Rows that no variant above holds: a block's sums stay in its row of `part`.
+template <typename T>
+__global__ void __launch_bounds__(LN_THREADS)
+    ln_bwd_long_kernel(View<const T> x, const float* gamma, const float* mean, const float* rstd, View<const T> gy,
+                       View<T> gx, float* part, LnShape s) {
+    grid_begin();
+    __shared__ float red[32];
+    float* p = part ? part + (long long)blockIdx.x * 2 * s.C : nullptr;
+    if (p)
+        for (int c = threadIdx.x; c < s.C; c += LN_THREADS) p[c] = p[s.C + c] = 0.0f;
+    for (long long r = blockIdx.x; r < s.rows; r += gridDim.x) {
+        const int b = (int)(r / s.L), l = (int)(r - (long long)b * s.L);
+        const bool live = ln_live(s, b, l);
+        const T* xr = x.p + b * x.batch + l * x.row;
+        const T* gr = gy.p + b * gy.batch + l * gy.row;
+        const float m = live ? mean[r] : 0.0f, rs = live ? rstd[r] : 0.0f;
+        float s1 = 0.0f, s2 = 0.0f;
+        if (live)
+            for (int c = threadIdx.x; c < s.C; c += LN_THREADS) {
+                const float xh = (to_f(xr[c]) - m) * rs, g = to_f(gr[c]), q = __fmul_rn(g, gamma[c]);
+                if (p) {
+                    p[c] = fmaf(g, xh, p[c]);
+                    p[s.C + c] += g;
+                }
+                s1 += q;
+                s2 = fmaf(q, xh, s2);
+            }
+        const float m1 = ln_sum<LN_THREADS>(s1, red) / s.C, m2 = ln_sum<LN_THREADS>(s2, red) / s.C;
+        T* o = gx.p + b * gx.batch + l * gx.row;
+        for (int c = threadIdx.x; c < s.C; c += LN_THREADS)
+            o[c] = from_f<T>(live ? rs * (__fmul_rn(to_f(gr[c]), gamma[c]) - m1 - (to_f(xr[c]) - m) * rs * m2) : 0.0f);
+    }
+}
+
+// The threads of a row and the packs a thread, MOST values or fewer: the first that
+// hold C channels.  False: none does.
+template <int V, int MOST, int TPR, int NV, typename F> bool ln_try(int C, F& f) {
+    if constexpr (NV * V <= MOST)
+        if (C <= TPR * NV * V) {
+            f.template run<V, TPR, NV>();
+            return true;
+        }
+    return false;
+}
+template <int V, int MOST, typename F> bool ln_dispatch(int C, F& f) {
+    return ln_try<V, MOST, 8, 1>(C, f) || ln_try<V, MOST, 8, 2>(C, f) || ln_try<V, MOST, 32, 1>(C, f) ||
+           ln_try<V, MOST, 32, 2>(C, f) || ln_try<V, MOST, 32, 4>(C, f) || ln_try<V, MOST, 32, 8>(C, f) ||
+           ln_try<V, MOST, 128, 4>(C, f) || ln_try<V, MOST, 128, 8>(C, f) || ln_try<V, MOST, 512, 2>(C, f) ||
+           ln_try<V, MOST, 512, 4>(C, f) || ln_try<V, MOST, 512, 8>(C, f) || ln_try<V, MOST, 512, 16>(C, f);
+}
+
+// Blocks of the backward pass: each leaves a row of sums.
+long long ln_blocks(const hc_layernorm_desc* d) {
+    const long long rows = (long long)d->B * d->L, most = 4LL * device_sm_count();
+    return rows < most ? rows : most;
+}
+
+bool ln_desc_ok(const hc_layernorm_desc* d) {
+    return d && d->B >= 1 && d->L >= 0 && d->C >= 1 && d->eps >= 0.0f && dtype_ok(d->dtype);
+}
+bool ln_size_ok(const hc_layernorm_desc* d) { return d->C <= 1 << 20 && (long long)d->B * d->L < 1LL << 31; }
+
+template <typename T> struct LnFwd {
+    const hc_rows *x, *y;
+    const float *gamma, *beta;
+    float *mean, *rstd;
+    LnShape s;
+    cudaStream_t st;
+    template <int V, int TPR, int NV> void run() {
+        constexpr int threads = ln_block(TPR), rows = threads / TPR;
+        const long long want = cdiv(s.rows, rows), most = 16LL * device_sm_count();
+        launch_next(ln_fwd_kernel<T, V, TPR, NV>, dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, st,
+                    view<const T>(x), gamma, beta, view<T>(y), mean, rstd, s);
+    }
+};
+
+template <typename T> struct LnBwd {
+    const hc_rows *x, *gy, *gx;
+    const float *gamma, *mean, *rstd;
+    float* part;
+    LnShape s;
+    long long blocks;
+    cudaStream_t st;
+    template <int V, int TPR, int NV> void run() {
+        constexpr int threads = ln_block(TPR);
+        const size_t smem = threads > TPR ? (size_t)(threads / TPR) * 2 * s.C * sizeof(float) : 0;
+        launch_next(ln_bwd_kernel<T, V, TPR, NV>, dim3((unsigned)blocks), dim3(threads), smem, st, view<const T>(x),
+                    gamma, mean, rstd, view<const T>(gy), view<T>(gx), part, s);
+    }
+};
+
+// Wide accesses: whole packs in a row, and every row on a 16-byte boundary.
+template <int V> bool ln_wide(int C, const hc_rows* a, const hc_rows* b, const hc_rows* c) {
+    return C % V == 0 && rows_vec(a, V) && rows_vec(b, V) && (!c || rows_vec(c, V));
+}
+
+template <typename T>
+hc_status ln_fwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamma, const float* beta, const hc_rows* y,
+                 float* mean, float* rstd, const int* lens, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    LnFwd<T> f{x, y, gamma, beta, mean, rstd, {d->L, d->C, d->B * d->L, d->eps, lens}, st};
+    if (!(ln_wide<W>(d->C, x, y, nullptr) ? ln_dispatch<W, 32>(d->C, f) : ln_dispatch<1, 16>(d->C, f))) {
+        const long long most = 8LL * device_sm_count();
+        launch_next(ln_fwd_long_kernel<T>, dim3((unsigned)(f.s.rows < most ? f.s.rows : most)), dim3(LN_THREADS), 0, st,
+                    view<const T>(x), gamma, beta, view<T>(y), mean, rstd, f.s);
+    }
+    return launched("ln_fwd_kernel", st);
+}
+
+template <typename T>
+hc_status ln_bwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamma, const float* mean, const float* rstd,
+                 const hc_rows* gy, const hc_rows* gx, float* part, const int* lens, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    LnBwd<T> f{x, gy, gx, gamma, mean, rstd, part, {d->L, d->C, d->B * d->L, d->eps, lens}, ln_blocks(d), st};
+    if (!(ln_wide<W>(d->C, x, gy, gx) ? ln_dispatch<W, 16>(d->C, f) : ln_dispatch<1, 16>(d->C, f)))
+        launch_next(ln_bwd_long_kernel<T>, dim3((unsigned)f.blocks), dim3(LN_THREADS), 0, st, view<const T>(x), gamma,
+                    mean, rstd, view<const T>(gy), view<T>(gx), part, f.s);
+    return launched("ln_bwd_kernel", st);
+}
+
+}  // namespace
+}  // namespace hc
+
+using namespace hc;
+
+extern "C" {
+
+hc_status hc_layernorm_fwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamma, const float* beta,
+                           const hc_rows* y, float* mean, float* rstd, const int* lens, void* stream) {
+    if (!ln_desc_ok(d)) return HC_ERR_INVALID_ARG;
+    if (!ln_size_ok(d)) return HC_ERR_UNSUPPORTED;
+    if (!rows_in_ok(x, d->dtype, d->L) || !rows_out_ok(y, d->dtype, d->B, d->L, d->C) || rows_same(x, y) ||
+        !f32_ok(gamma) || !f32_ok(beta) || !f32_opt_ok(mean) || !f32_opt_ok(rstd) || !ptr_al(lens, 4))
+        return HC_ERR_INVALID_ARG;
+    if (d->L == 0) return HC_OK;
+    const cudaStream_t st = (cudaStream_t)stream;
+    traced_begin(st);
+    if (d->dtype == HC_DTYPE_F32) return ln_fwd<float>(d, x, gamma, beta, y, mean, rstd, lens, st);
+    if (d->dtype == HC_DTYPE_BF16) return ln_fwd<__nv_bfloat16>(d, x, gamma, beta, y, mean, rstd, lens, st);
+    return ln_fwd<__half>(d, x, gamma, beta, y, mean, rstd, lens, st);
+}
+
+// [blocks][ggamma C | gbeta C]
+hc_status hc_layernorm_workspace_size(const hc_layernorm_desc* d, size_t* bytes) {
+    if (!ln_desc_ok(d) || !bytes) return HC_ERR_INVALID_ARG;
+    if (!ln_size_ok(d)) return HC_ERR_UNSUPPORTED;
+    *bytes = (size_t)ln_blocks(d) * 2 * d->C * sizeof(float);
+    return HC_OK;
+}
+
+hc_status hc_layernorm_bwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamma, const float* mean,
+                           const float* rstd, const hc_rows* gy, const hc_rows* gx, float* ggamma, float* gbeta,
+                           const int* lens, void* ws, size_t ws_bytes, void* stream) {
+    size_t need = 0;
+    hc_status e = hc_layernorm_workspace_size(d, &need);
+    if (e) return e;
+    if (!rows_in_ok(x, d->dtype, d->L) || !rows_in_ok(gy, d->dtype, d->L) ||
+        !rows_out_ok(gx, d->dtype, d->B, d->L, d->C) || rows_same(gx, x) || rows_same(gx, gy) || !f32_ok(gamma) ||
+        (d->L > 0 && (!f32_ok(mean) || !f32_ok(rstd))) || !f32_opt_ok(ggamma) || !f32_opt_ok(gbeta) || !ptr_al(lens, 4))
+        return HC_ERR_INVALID_ARG;
+    const bool sums = ggamma || gbeta;
+    if (sums && need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
+    const cudaStream_t st = (cudaStream_t)stream;
+    traced_begin(st);
+    float* part = sums ? (float*)ws : nullptr;
+    if (d->L > 0) {
+        if (d->dtype == HC_DTYPE_F32)
+            e = ln_bwd<float>(d, x, gamma, mean, rstd, gy, gx, part, lens, st);
+        else if (d->dtype == HC_DTYPE_BF16)
+            e = ln_bwd<__nv_bfloat16>(d, x, gamma, mean, rstd, gy, gx, part, lens, st);
+        else
+            e = ln_bwd<__half>(d, x, gamma, mean, rstd, gy, gx, part, lens, st);
+        if (e) return e;
+    }
+    if (!sums) return HC_OK;
+    return launch_column_totals(part, d->L > 0 ? ln_blocks(d) : 0, ggamma, d->C, gbeta, d->C, nullptr, 0, st);
+}
+
+}  // extern "C"

@@ -137,6 +137,9 @@ EXPORTS = [
     "hc_groupnorm_workspace_size", "hc_groupnorm_fwd", "hc_groupnorm_bwd", "hc_causal_conv_fwd",
     "hc_causal_conv_workspace_size", "hc_causal_conv_bwd", "hc_causal_conv_step", "hc_selective_scan_workspace_size",
     "hc_selective_scan_saved_size", "hc_selective_scan_fwd", "hc_selective_scan_bwd", "hc_selective_scan_step",
+    "hc_layernorm_workspace_size", "hc_layernorm_fwd", "hc_layernorm_bwd", "hc_linear_attn_workspace_size",
+    "hc_linear_attn_fwd", "hc_linear_attn_bwd", "hc_linear_attn_step", "hc_gated_ffn_workspace_size",
+    "hc_gated_ffn_fwd", "hc_gated_ffn_bwd",
 ]
 
 
@@ -669,6 +672,140 @@ def hc_selective_scan_step(d, u, dt, A, Bm, Cm, state, y, D=None, z=None, dt_bia
     b, _, c, g, n, _, _ = _selective_scan(d)
     return _lib.hc_selective_scan_step(C.byref(d), _scan_in(b, None, c, g, n, u, dt, A, Bm, Cm, D, z, dt_bias),
                                        _array(state, b * c * n), _rows(y, b, c), _stream(stream))
+
+
+# ---- operators of a channels-last sequence block (include/hc_block.h) ---------
+class hc_layernorm_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "L", "C")] + [("eps", C.c_float), ("dtype", C.c_int)]
+
+
+class hc_linear_attn_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "L", "H", "Dk", "Dv")] + [("scale", C.c_float), ("dtype", C.c_int)]
+
+
+class hc_gated_ffn_desc(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("M", "C", "F", "act", "dtype")]
+
+
+def layernorm_desc(B, L, C, dtype, eps=1e-5) -> hc_layernorm_desc:
+    return hc_layernorm_desc(B, L, C, eps, _dtype(dtype))
+
+
+def linear_attn_desc(B, L, H, Dk, Dv, dtype, scale=None) -> hc_linear_attn_desc:
+    """scale None: Dk ** -0.5."""
+    return hc_linear_attn_desc(B, L, H, Dk, Dv, max(Dk, 1) ** -0.5 if scale is None else scale, _dtype(dtype))
+
+
+def gated_ffn_desc(M, C, F, dtype, act=HC_PW_SILU) -> hc_gated_ffn_desc:
+    return hc_gated_ffn_desc(M, C, F, act, _dtype(dtype))
+
+
+_layernorm = struct.Struct("@3ifi").unpack
+_linear_attn = struct.Struct("@5ifi").unpack
+_gated_ffn = struct.Struct("@5i").unpack
+
+for _n, _a in (("hc_layernorm_workspace_size", [_P, C.POINTER(_Z)]),
+               ("hc_layernorm_fwd", [_P, _R, _P, _P, _R, _P, _P, _P, _P]),
+               ("hc_layernorm_bwd", [_P, _R, _P, _P, _P, _R, _R, _P, _P, _P, _P, _Z, _P]),
+               ("hc_linear_attn_workspace_size", [_P, _I, C.POINTER(_Z)]),
+               ("hc_linear_attn_fwd", [_P, _R, _R, _R, _P, _R, _P, _P, _P, _P, _Z, _P]),
+               ("hc_linear_attn_bwd", [_P, _R, _R, _R, _P, _P, _R, _P, _R, _R, _R, _P, _P, _P, _Z, _P]),
+               ("hc_linear_attn_step", [_P, _R, _R, _R, _P, _P, _R, _P]),
+               ("hc_gated_ffn_workspace_size", [_P, _I, C.POINTER(_Z)]),
+               ("hc_gated_ffn_fwd", [_P, _R, _P, _P, _R, _P, _Z, _P]),
+               ("hc_gated_ffn_bwd", [_P, _R, _P, _P, _R, _R, _P, _P, _P, _Z, _P])):
+    getattr(_lib, _n).argtypes = _a
+    getattr(_lib, _n).restype = C.c_int
+
+
+def hc_layernorm_workspace_size(d: hc_layernorm_desc):
+    """Returns (status, bytes) of the backward pass."""
+    b = C.c_size_t(0)
+    st = _lib.hc_layernorm_workspace_size(C.byref(d), C.byref(b))
+    return st, b.value
+
+
+def hc_layernorm_fwd(d, x, gamma, beta, y, mean=None, rstd=None, lens=None, stream=None) -> int:
+    """y = layer norm of each row of x; x and y are (B, L, C) tensors with adjacent channels; lens int32 (B,)."""
+    b, l, c, _, _ = _layernorm(d)
+    return _lib.hc_layernorm_fwd(C.byref(d), _rows(x, b, l, c), _array(gamma, c), _array(beta, c), _rows(y, b, l, c),
+                                 _array(mean, b * l), _array(rstd, b * l), _lens(lens, b), _stream(stream))
+
+
+def hc_layernorm_bwd(d, x, gamma, mean, rstd, gy, gx, ggamma=None, gbeta=None, lens=None, ws=None, ws_bytes=0,
+                     stream=None) -> int:
+    b, l, c, _, _ = _layernorm(d)
+    return _lib.hc_layernorm_bwd(C.byref(d), _rows(x, b, l, c), _array(gamma, c), _array(mean, b * l),
+                                 _array(rstd, b * l), _rows(gy, b, l, c), _rows(gx, b, l, c), _array(ggamma, c),
+                                 _array(gbeta, c), _lens(lens, b), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
+
+
+def hc_linear_attn_workspace_size(d: hc_linear_attn_desc, pass_: int):
+    """Returns (status, bytes): pass 0 for the forward pass, 1 for both."""
+    b = C.c_size_t(0)
+    st = _lib.hc_linear_attn_workspace_size(C.byref(d), int(pass_), C.byref(b))
+    return st, b.value
+
+
+def hc_linear_attn_fwd(d, q, k, v, y, log_decay=None, h0=None, hT=None, lens=None, ws=None, ws_bytes=0,
+                       stream=None) -> int:
+    """q, k are (B, L, H * Dk) and v, y (B, L, H * Dv) tensors with adjacent channels; log_decay (H,), states
+    (B, H, Dk, Dv) fp32; lens int32 (B,)."""
+    b, l, h, dk, dv, _, _ = _linear_attn(d)
+    n = b * h * dk * dv
+    return _lib.hc_linear_attn_fwd(C.byref(d), _rows(q, b, l, h * dk), _rows(k, b, l, h * dk), _rows(v, b, l, h * dv),
+                                   _array(log_decay, h), _rows(y, b, l, h * dv), _array(h0, n), _array(hT, n),
+                                   _lens(lens, b), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
+
+
+def hc_linear_attn_bwd(d, q, k, v, gy, gq, gk, gv, log_decay=None, h0=None, ghT=None, gh0=None, lens=None, ws=None,
+                       ws_bytes=0, stream=None) -> int:
+    """The gradients of hc_linear_attn_fwd on the same inputs."""
+    b, l, h, dk, dv, _, _ = _linear_attn(d)
+    n, wk, wv = b * h * dk * dv, h * dk, h * dv
+    return _lib.hc_linear_attn_bwd(C.byref(d), _rows(q, b, l, wk), _rows(k, b, l, wk), _rows(v, b, l, wv),
+                                   _array(log_decay, h), _array(h0, n), _rows(gy, b, l, wv), _array(ghT, n),
+                                   _rows(gq, b, l, wk), _rows(gk, b, l, wk), _rows(gv, b, l, wv), _array(gh0, n),
+                                   _lens(lens, b), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
+
+
+def hc_linear_attn_step(d, q, k, v, state, y, log_decay=None, stream=None) -> int:
+    """One token: q, k are (B, H * Dk) and v, y (B, H * Dv) tensors; state is updated in place."""
+    b, _, h, dk, dv, _, _ = _linear_attn(d)
+    return _lib.hc_linear_attn_step(C.byref(d), _rows(q, b, h * dk), _rows(k, b, h * dk), _rows(v, b, h * dv),
+                                    _array(log_decay, h), _array(state, b * h * dk * dv), _rows(y, b, h * dv),
+                                    _stream(stream))
+
+
+def hc_gated_ffn_workspace_size(d: hc_gated_ffn_desc, pass_: int):
+    """Returns (status, bytes): pass 0 for the forward pass, 1 for both."""
+    b = C.c_size_t(0)
+    st = _lib.hc_gated_ffn_workspace_size(C.byref(d), int(pass_), C.byref(b))
+    return st, b.value
+
+
+def _flat(t, m, c) -> bytes:
+    """An hc_rows of (m, c) rows: their stride is the row stride."""
+    if t is not None and not t.is_cuda:
+        _on_gpu(t)
+    p, row, _, dtype = _view(t, m, c)
+    return _pack_rows(p, 0, row, dtype)
+
+
+def hc_gated_ffn_fwd(d, x, w_in, w_out, y, ws=None, ws_bytes=0, stream=None) -> int:
+    """x, y are (M, C) tensors with adjacent channels, w_in (C, 2 F) and w_out (F, C) contiguous, all of the desc's type."""
+    m, c, f, _, t = _gated_ffn(d)
+    return _lib.hc_gated_ffn_fwd(C.byref(d), _flat(x, m, c), _array(w_in, 2 * c * f, t), _array(w_out, c * f, t),
+                                 _flat(y, m, c), _bytes(ws, ws_bytes), ws_bytes, _stream(stream))
+
+
+def hc_gated_ffn_bwd(d, x, w_in, w_out, gy, gx=None, gw_in=None, gw_out=None, ws=None, ws_bytes=0, stream=None) -> int:
+    """The gradients of hc_gated_ffn_fwd on the same inputs; the weights' gradients are laid out as the weights."""
+    m, c, f, _, t = _gated_ffn(d)
+    return _lib.hc_gated_ffn_bwd(C.byref(d), _flat(x, m, c), _array(w_in, 2 * c * f, t), _array(w_out, c * f, t),
+                                 _flat(gy, m, c), None if gx is None else _flat(gx, m, c),
+                                 _array(gw_in, 2 * c * f, t), _array(gw_out, c * f, t), _bytes(ws, ws_bytes), ws_bytes,
+                                 _stream(stream))
 
 
 def check(status: int, what: str = "hc call") -> None:
