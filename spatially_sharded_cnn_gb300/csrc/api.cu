@@ -514,8 +514,9 @@ hc_status hc_sync_check(void* stream) {
         return HC_ERR_CUDA;
     }
     if (cudaGetLastError() != cudaSuccess) return HC_ERR_CUDA;
-    const hc_status a = dw_take_status(), b = tc_take_status(), c = pw_take_status(), d = ffn_take_status();
-    return a ? a : b ? b : c ? c : d;
+    const hc_status a = dw_take_status(), b = tc_take_status(), c = pw_take_status(), d = ffn_take_status(),
+                    e = attn_take_status();
+    return a ? a : b ? b : c ? c : d ? d : e;
 }
 
 hc_status hc_selftest_timeout(int wait_us, void* stream) {

@@ -99,13 +99,24 @@ bool attn_size_ok(const hc_linear_attn_desc* d) {
            (long long)d->H * d->Dv <= 1 << 20 && (long long)d->B * d->H < 0x7fffffffLL / 3;
 }
 
+// Whether a call may run on the tensor cores, as far as its sizes say.
+bool attn_tc_sizes(const hc_linear_attn_desc* d) {
+    return d->dtype == HC_DTYPE_BF16 && d->Dk % 8 == 0 && d->Dv % 8 == 0 && d->L >= 32;
+}
+// And its rows: the copy engine wants 16-byte boundaries and strides that are not 0.
+bool attn_tc_rows(const hc_linear_attn_desc* d, const hc_rows* r) {
+    return ptr_al(r->p, 16) && (d->L <= 1 || (r->row > 0 && r->row % 8 == 0)) &&
+           (d->B <= 1 || (r->batch > 0 && r->batch % 8 == 0));
+}
+
 struct Cut {
     int segs, per;
 };
-// Segments of a sequence in chunks of T rows: as many as give `want` blocks in all, two
-// chunks each at least.
-Cut attn_cut(const hc_linear_attn_desc* d, int T, int passes) {
-    const long long pairs = (long long)d->B * d->H * passes, want = 2LL * device_sm_count();
+// Segments of a sequence: as many as give the GPU `passes` passes of blocks to fill it,
+// two chunks each at least.
+Cut attn_cut(const hc_linear_attn_desc* d, bool tc, int passes) {
+    const int T = tc ? AT_TC : AT_T, per_sm = tc && (d->Dk > 64 || d->Dv > 64) ? 1 : 2;
+    const long long pairs = (long long)d->B * d->H * passes, want = (long long)per_sm * device_sm_count();
     const int chunks = (int)(((long long)d->L + T - 1) / T);
     long long segs = pairs < want ? want / pairs : 1;
     if (segs > chunks / 2) segs = chunks / 2;
@@ -131,10 +142,11 @@ AttnArgs attn_args(const hc_linear_attn_desc* d, const float* decay, const int* 
     return a;
 }
 
-hc_status attn_run(const AttnArgs& a, cudaStream_t st) {
+hc_status attn_run(const AttnArgs& a, bool tc, cudaStream_t st) {
+    const auto launch = tc ? launch_attn_tc : launch_attn_fp32;
     hc_status e = HC_OK;
-    if (a.segs > 1 && ((e = launch_attn_fp32(a, true, st)) || (e = launch_attn_join(a, AT_T, st)))) return e;
-    return launch_attn_fp32(a, false, st);
+    if (a.segs > 1 && ((e = launch(a, true, st)) || (e = launch_attn_join(a, tc ? AT_TC : AT_T, st)))) return e;
+    return launch(a, false, st);
 }
 
 }  // namespace
@@ -152,14 +164,16 @@ using namespace hc;
 
 extern "C" {
 
-// Segments' states: of S forward; of S and of G backward.
+// Segments' states: of S forward; of S and of G backward; whichever way the rows of the
+// call let it run.
 hc_status hc_linear_attn_workspace_size(const hc_linear_attn_desc* d, int pass, size_t* bytes) {
     if (!attn_desc_ok(d) || pass < 0 || pass > 1 || !bytes) return HC_ERR_INVALID_ARG;
     if (!attn_size_ok(d)) return HC_ERR_UNSUPPORTED;
-    size_t n = carry_floats(d, attn_cut(d, AT_T, 1));
-    if (pass == 1) {
-        const size_t b = 2 * carry_floats(d, attn_cut(d, AT_T, 3));
-        if (b > n) n = b;
+    size_t n = 0;
+    for (int tc = 0; tc <= (int)attn_tc_sizes(d); tc++) {
+        const size_t f = carry_floats(d, attn_cut(d, tc, 1)), b = pass ? 2 * carry_floats(d, attn_cut(d, tc, 3)) : 0;
+        n = n > f ? n : f;
+        n = n > b ? n : b;
     }
     *bytes = n * sizeof(float);
     return HC_OK;
@@ -179,11 +193,13 @@ hc_status hc_linear_attn_fwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     if (need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
     const cudaStream_t st = (cudaStream_t)stream;
     traced_begin(st);
-    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, AT_T, 1));
+    bool tc = attn_tc_sizes(d);
+    for (const hc_rows* r : {q, k, v, y}) tc = tc && attn_tc_rows(d, r);
+    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, 1));
     a.passes = 1;
     a.p[0] = {*q, *k, *v, *y, d->Dk, d->Dv, d->scale, d->scale, 1.0f, 0, h0, hT, d->Dv, 1,
               a.segs > 1 ? (float*)ws : nullptr, 1};
-    return attn_run(a, st);
+    return attn_run(a, tc, st);
 }
 
 hc_status hc_linear_attn_bwd(const hc_linear_attn_desc* d, const hc_rows* q, const hc_rows* k, const hc_rows* v,
@@ -207,7 +223,9 @@ hc_status hc_linear_attn_bwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     if (need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
     const cudaStream_t st = (cudaStream_t)stream;
     traced_begin(st);
-    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, AT_T, 3));
+    bool tc = attn_tc_sizes(d);
+    for (const hc_rows* r : {q, k, v, gy, gq, gk, gv}) tc = tc && attn_tc_rows(d, r);
+    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, 3));
     float *cs = nullptr, *cg = nullptr;
     if (a.segs > 1) {
         cs = (float*)ws;
@@ -223,7 +241,7 @@ hc_status hc_linear_attn_bwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     a.p[0] = pq;
     a.p[1] = pv;
     a.p[2] = pk;
-    return attn_run(a, st);
+    return attn_run(a, tc, st);
 }
 
 hc_status hc_linear_attn_step(const hc_linear_attn_desc* d, const hc_rows* q, const hc_rows* k, const hc_rows* v,

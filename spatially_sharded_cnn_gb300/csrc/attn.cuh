@@ -70,9 +70,29 @@ __device__ __forceinline__ void attn_blank(const AttnPass& p, int b, int h, int 
     }
 }
 
-// The kernels in fp32 (any type of row): 32-row chunks.
-constexpr int AT_T = 32;
+// Runs f on the passes of each shape (Dk, Dv) together; of a carry pass on those that
+// fill one.
+template <typename F> hc_status attn_by_shape(const AttnArgs& all, bool carry, F&& f) {
+    bool done[3] = {};
+    for (int i = 0; i < all.passes; i++) {
+        if (done[i] || (carry && !all.p[i].keep)) continue;
+        AttnArgs a = all;
+        a.passes = 0;
+        for (int j = i; j < all.passes; j++)
+            if (!done[j] && (!carry || all.p[j].keep) && all.p[j].Dk == all.p[i].Dk && all.p[j].Dv == all.p[i].Dv) {
+                a.p[a.passes++] = all.p[j];
+                done[j] = true;
+            }
+        const hc_status e = f(a);
+        if (e) return e;
+    }
+    return HC_OK;
+}
+
+// The kernels in fp32 (any type of row): 32-row chunks.  On the tensor cores (bf16): 128.
+constexpr int AT_T = 32, AT_TC = 128;
 hc_status launch_attn_fp32(const AttnArgs& a, bool carry, cudaStream_t st);
+hc_status launch_attn_tc(const AttnArgs& a, bool carry, cudaStream_t st);
 // Segments joined in order, in place: carry[seg] becomes the state ahead of it.
 hc_status launch_attn_join(const AttnArgs& a, int T, cudaStream_t st);
 

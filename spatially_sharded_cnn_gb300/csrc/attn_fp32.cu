@@ -244,24 +244,12 @@ template <typename T> hc_status launch_type(const AttnArgs& a, bool carry, cudaS
 
 }  // namespace
 
-// Passes of one shape share a launch; the others follow.
 hc_status launch_attn_fp32(const AttnArgs& all, bool carry, cudaStream_t st) {
-    bool done[3] = {};
-    for (int i = 0; i < all.passes; i++) {
-        if (done[i] || (carry && !all.p[i].keep)) continue;
-        AttnArgs a = all;
-        a.passes = 0;
-        for (int j = i; j < all.passes; j++)
-            if (!done[j] && (!carry || all.p[j].keep) && all.p[j].Dk == all.p[i].Dk && all.p[j].Dv == all.p[i].Dv) {
-                a.p[a.passes++] = all.p[j];
-                done[j] = true;
-            }
-        const hc_status e = a.dtype == HC_DTYPE_F32    ? launch_type<float>(a, carry, st)
-                            : a.dtype == HC_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, carry, st)
-                                                       : launch_type<__half>(a, carry, st);
-        if (e) return e;
-    }
-    return HC_OK;
+    return attn_by_shape(all, carry, [&](const AttnArgs& a) {
+        return a.dtype == HC_DTYPE_F32    ? launch_type<float>(a, carry, st)
+               : a.dtype == HC_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, carry, st)
+                                          : launch_type<__half>(a, carry, st);
+    });
 }
 
 }  // namespace hc

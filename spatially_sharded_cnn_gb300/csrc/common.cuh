@@ -98,6 +98,7 @@ hc_status make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const
 hc_status dw_take_status();
 hc_status tc_take_status();
 hc_status ffn_take_status();
+hc_status attn_take_status();
 hc_status launch_selftest_timeout(int wait_us, cudaStream_t st);
 
 // GELU, exact form: x * Phi(x), Phi(x) = (1 + erf(x / sqrt 2)) / 2.

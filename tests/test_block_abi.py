@@ -141,7 +141,7 @@ def test_binding_checks(hc):
         hc.hc_gated_ffn_fwd(hc.gated_ffn_desc(16, 8, 8, torch.bfloat16), x[0], x, x, x[0])
 
 
-@pytest.mark.parametrize("source", ["layernorm.cu", "attn.cu", "attn_fp32.cu", "ffn.cu"])
+@pytest.mark.parametrize("source", ["layernorm.cu", "attn.cu", "attn_fp32.cu", "attn_tc.cu", "ffn.cu"])
 def test_reads_stay_behind_the_wait(source):
     """As test_mixer_sources.py, for the kernels of this set."""
     found = kernels(source)
