@@ -75,6 +75,27 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     return r;
 }
 
+// Two bf16 values times w as three pieces each: 24 bits.
+__device__ __forceinline__ void split_pair(uint32_t v, float w, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+    float a = __uint_as_float(v << 16) * w, b = __uint_as_float(v & 0xffff0000u) * w;
+    p0 = bf2(a, b);
+    a -= __uint_as_float(p0 << 16);
+    b -= __uint_as_float(p0 & 0xffff0000u);
+    p1 = bf2(a, b);
+    p2 = bf2(a - __uint_as_float(p1 << 16), b - __uint_as_float(p1 & 0xffff0000u));
+}
+// 16 bf16 values: a whole 32-byte sector where the address allows.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&v)[8], bool whole, int left) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (left > 8) *reinterpret_cast<uint4*>(p + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 template <int DK, int DV, bool CARRY>
 __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
     attn_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ AttnArgs a) {
@@ -160,6 +181,7 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
     put_state();
     fence_async_smem();
 
+    const bool whole = Dv % 16 == 0 && ((uintptr_t)p.y.p & 31) == 0 && p.y.row % 16 == 0 && p.y.batch % 16 == 0;
     constexpr uint32_t id_scores = idesc_bf16(TT, TT, 0, 0), id_rows = idesc_bf16(TT, DV, 0, 1),
                        id_part = idesc_bf16(TT, DV, 1, 1);
     const int ksteps = (Dk + 15) / 16;
@@ -254,39 +276,39 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                 tc_commit(&sh.rows);
             }
             __syncwarp();
-            wait_all(&sh.rows, ph);
-            tc_fence_after();
         }
+        // ---- v times its weight in the state, as three pieces, over v, q and the state's copy:
+        // taken while product 3 runs, stored behind it.  16 bytes a time, all of one row; rows
+        // (tid >> 3) + 32 i of each 64-column block.
         wait_all(&sh.full[it & 1], full_ph);
-        // ---- v times its weight in the state, as three pieces, over v, q and the state's copy
-        // (16 bytes a time, all of one row; rows (tid >> 3) + 32 i of each 64-column block)
-#pragma unroll
-        for (int nb = 0; nb < DV / 64; nb++) {
-            uint4 x[4];
+        {
+            constexpr int NB = DV / 64;
+            uint4 p0[4 * NB], p1[4 * NB], p2[4 * NB];
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int j = (tid >> 3) + 32 * i;
-                x[i] = *reinterpret_cast<const uint4*>(sv + nb * TBLOCK + 16 * (tid + 256 * i));
                 w[i] = j < lo ? 0.0f : p.su * ex2f(l2 * (float)(back ? j - lo + 1 : TT - 1 - j));
             }
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t p0[4], p1[4], p2[4];
+            for (int i = 0; i < 4 * NB; i++) p0[i] = *reinterpret_cast<const uint4*>(sv + 16 * (tid + 256 * i));
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    float f0 = __uint_as_float(in[k] << 16) * w[i], f1 = __uint_as_float(in[k] & 0xffff0000u) * w[i];
-                    p0[k] = bf2(f0, f1);
-                    f0 -= __uint_as_float(p0[k] << 16);
-                    f1 -= __uint_as_float(p0[k] & 0xffff0000u);
-                    p1[k] = bf2(f0, f1);
-                    p2[k] = bf2(f0 - __uint_as_float(p1[k] << 16), f1 - __uint_as_float(p1[k] & 0xffff0000u));
-                }
-                const uint32_t at = nb * TBLOCK + 16 * (tid + 256 * i);
-                *reinterpret_cast<uint4*>(sv + at) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
-                *reinterpret_cast<uint4*>(slo + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                *reinterpret_cast<uint4*>(zop + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+            for (int i = 0; i < 4 * NB; i++) {
+                split_pair(p0[i].x, w[i & 3], p0[i].x, p1[i].x, p2[i].x);
+                split_pair(p0[i].y, w[i & 3], p0[i].y, p1[i].y, p2[i].y);
+                split_pair(p0[i].z, w[i & 3], p0[i].z, p1[i].z, p2[i].z);
+                split_pair(p0[i].w, w[i & 3], p0[i].w, p1[i].w, p2[i].w);
+            }
+            if (!CARRY) {
+                wait_all(&sh.rows, ph);
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int i = 0; i < 4 * NB; i++) {
+                const uint32_t at = 16 * (tid + 256 * i);
+                *reinterpret_cast<uint4*>(sv + at) = p0[i];
+                *reinterpret_cast<uint4*>(slo + at) = p1[i];
+                *reinterpret_cast<uint4*>(zop + at) = p2[i];
             }
         }
         fence_async_smem();
@@ -319,11 +341,12 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
 #pragma unroll
                     for (int i = 0; i < 32; i++) o[i] = fmaf(w, r[i], p.si * o[i]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
+                    for (int i = 0; i < 32; i += 16) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; j++) v[j] = bf2(o[i + 2 * j], o[i + 2 * j + 1]);
                         const int n = half * ZC + cc + i;
-                        if (n < Dv)
-                            *reinterpret_cast<uint4*>(y + n) = make_uint4(bf2(o[i], o[i + 1]), bf2(o[i + 2], o[i + 3]),
-                                                                          bf2(o[i + 4], o[i + 5]), bf2(o[i + 6], o[i + 7]));
+                        store16(y + n, v, whole && n < Dv, Dv - n);
                     }
                 }
             }
