@@ -7,8 +7,9 @@
 namespace hc {
 namespace {
 
-// One thread an element of the state: carry[seg] becomes the state ahead of segment
-// seg, and z1 the one behind the last.  Grid: (elements of a state, pairs, passes).
+// One thread an element of the state: carry[seg], the sum of segment seg alone, becomes the
+// state ahead of it.  Eight segments' sums are read before the first is replaced.  Grid:
+// (pairs, elements of a state, passes).
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int T) {
     grid_begin();
     const AttnPass& p = a.p[blockIdx.z];
@@ -21,14 +22,20 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int T) {
     float z = p.z0 ? p.z0[(long long)pair * size + e] : 0.0f;
     float* c = p.carry + (long long)pair * a.segs * size + e;
     const int part = chunks * T - len;  // rows that the chunk with the first row lacks
-    for (int s = 0; s < a.segs; s++) {
-        const int c0 = min(chunks, s * a.per), c1 = min(chunks, c0 + a.per);
-        const bool first = c1 > c0 && (p.back ? c1 == chunks : c0 == 0);
-        const float own = c[(long long)s * size];
-        c[(long long)s * size] = z;
-        z = fmaf(z, exp2f(l2 * ((c1 - c0) * T - (first ? part : 0))), own);
+    for (int s0 = 0; s0 < a.segs; s0 += 8) {
+        float own[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) own[i] = s0 + i < a.segs - 1 ? c[(long long)(s0 + i) * size] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int s = s0 + i;
+            if (s >= a.segs) break;
+            const int c0 = min(chunks, s * a.per), c1 = min(chunks, c0 + a.per);
+            const bool first = c1 > c0 && (p.back ? c1 == chunks : c0 == 0);
+            c[(long long)s * size] = z;
+            z = fmaf(z, exp2f(l2 * ((c1 - c0) * T - (first ? part : 0))), own[i]);
+        }
     }
-    if (p.z1) p.z1[(long long)pair * size + e] = z;
 }
 
 // One token: a block a (sequence, head).  Thread (r, c) takes columns c * V .. of rows

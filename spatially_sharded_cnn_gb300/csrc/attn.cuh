@@ -17,8 +17,8 @@
 // (a row j of the sum is then a later row, whose gradient it carries back).
 //
 // Where sequences times heads leave the GPU idle, a sequence's chunks are cut into
-// segments: every segment's own sum of k v^T (the carry pass), a join in order, and
-// then all segments at once, each from the state ahead of it.
+// segments: every segment's own sum of k v^T but the last one's (the carry pass), a join in
+// order, and then all segments at once, each from the state ahead of it.
 #pragma once
 
 #include "rows.cuh"

@@ -38,6 +38,8 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const AttnPass& p = a.p[blockIdx.y];
     const int seg = blockIdx.x % a.segs, pair = blockIdx.x / a.segs;
+    const bool last = seg == a.segs - 1;
+    if (CARRY && last) return;  // its state is the pass's own
     const int b = pair / a.H, h = pair - b * a.H;
     const int len = attn_len(a.lens, b, a.L), chunks = (len + AT_T - 1) / AT_T;
     const int c0 = min(chunks, seg * a.per), c1 = min(chunks, c0 + a.per);
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
     }
     if (c0 == c1) __syncthreads();  // the state as it was loaded
     float* z1 = CARRY ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                      : p.z1 && a.segs == 1 ? p.z1 + pair * zsize
+                      : p.z1 && last ? p.z1 + pair * zsize
                                             : nullptr;
     if (z1)
         for (int e = tid; e < PK * PV; e += 256) {

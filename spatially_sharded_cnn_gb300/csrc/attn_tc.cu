@@ -3,20 +3,31 @@
 //
 // A block walks over one segment of one (sequence, head) in chunks of 128 rows, four
 // products a chunk, all accumulated in fp32 in tensor memory:
-//   1  scores = q k^T                             [128 x 128 x DK]
-//   2  rows on the state: q Z                     [128 x DV x DK]
-//   3  (scores * powers of lambda) v              [128 x DV x 128], scores in tensor memory
-//   4  the state's part: k^T (weights * v)        [DK x DV x 128], three times
-// The state stays in registers in fp32: a thread holds a row of it (half of the columns),
-// adds product 4 to it and leaves a copy rounded to bf16 in shared memory for product 2.
+//   1  scores = q k^T                                    [128 x 128 x DK]
+//   2  rows on the state: q Z                            [128 x DV x DK]
+//   3  (scores * powers of lambda) v                     [128 x DV x 128], scores in tensor memory
+//   4  the state's part, transposed: v^T (weights * k)   [DV x DK x 128], three times
+// The state stays in registers in fp32, transposed: a thread holds a column n of Z (half
+// of the DK values), adds product 4 to it and leaves a copy rounded to bf16 in shared memory for
+// product 2.
 // Roundings: scores and that copy once each to bf16 (y, whose terms have random
-// signs, is then off by 2.3e-3 instead of the 1.7e-3 of its own rounding).  v times its
+// signs, is then off by 2.3e-3 instead of the 1.7e-3 of its own rounding).  k times its
 // weight goes into the state as three bf16 pieces (24 bits): states are fp32 outputs, which
 // one rounding would leave 1.7e-3 off and two pieces 2.4e-6.
 //
-// All 256 threads work on every step and one of warp 0 issues copies and products, so that a
-// block of 64-wide heads has 128 registers a thread, 112 KB of shared memory and 256
-// columns of tensor memory, and two run on an SM, one computing while the other waits.
+// What a product of M = 128, K = 16 costs, measured: 42 + 0.46 N cycles with A in shared
+// memory, 12 + 0.46 N with A in tensor memory.  So products that share A are issued as one
+// wider one where the buffers can lie side by side.
+//   64-wide heads (Shape::pair): two blocks an SM, one computing while the other waits, with
+// 113 KB of shared memory, 256 columns of tensor memory and 128 registers a thread each.
+// Products 1 and 2 are one (N = 192: the copy of Z lies behind or ahead of k's rows),
+// and so are the three of 4 (the pieces go over q, over k and into the copy's place, next to one
+// another), which takes the columns of 1 and 2 once everything has been read from them.
+//   Wider heads: one block an SM, and product 4 runs while the scores are read and scaled
+// (its pieces only replace what products 1 and 2 have read), product 3 while the state is
+// added up, products 1 and 2 while the rows before are stored.
+// All 256 threads work on every step and one of warp 0 issues copies and products.
+//
 // Chunks end at the sequence's end: rows past it are never read, and those ahead of its
 // first row are the copy engine's zero fill (negative row coordinates).  Every wait is
 // bounded, and the threads agree on giving up at the next barrier.
@@ -32,21 +43,23 @@ constexpr uint32_t TBLOCK = TT * 128;  // 128 rows x 64 values, 128-byte swizzle
 __device__ int g_attn_status;
 
 template <int DK, int DV> struct Shape {
+    static constexpr bool pair = DK == 64 && DV == 64;
     static constexpr uint32_t q = DK / 64 * TBLOCK, v = DV / 64 * TBLOCK;
-    static constexpr uint32_t stage = 2 * q + v;                  // [q][k][v]
-    // the state in bf16 (DK rows x DV), and between its reads the third piece of v
-    static constexpr uint32_t z = DV / 64 * DK * 128 > v ? DV / 64 * DK * 128 : v;
-    static constexpr uint32_t lo = DK < DV ? v : 0;               // second pieces of v (else over q)
-    static constexpr uint32_t smem = 2 * stage + z + lo;
-    static constexpr uint32_t cols = DV == 128 ? 512 : 256;
-    // tensor memory columns: scores 0 .. 127 (as bf16: 0 .. 63), then rows on the chunk, rows on
-    // the state; the state's part over the scores' upper half, or behind
-    static constexpr uint32_t o1 = 128, o2 = 128 + DV, kv = DV == 128 ? 384 : 64;
-    static constexpr int per_sm = DK == 64 && DV == 64 ? 2 : 1;
+    // x: the state's copy in bf16 (DV rows x DK), and between its reads the third piece of k
+    static constexpr uint32_t zblock = DV * 128, z = DK / 64 * zblock, x = z > q ? z : q;
+    // shared memory: v1 v0 q0 k0 x k1 q1 (the digit is the stage)
+    static constexpr uint32_t smem = 2 * v + 4 * q + x;
+    static constexpr uint32_t stage = 2 * q + v;  // bytes of a stage's copies
+    // tensor memory columns.  pair: products 1 and 2 and product 4 0 .. 191, product 3 behind.
+    // Else scores 0 .. 127, rows on the chunk, rows on the state, the state's part.
+    // The scores go back as bf16 over their own first 64 columns.
+    static constexpr uint32_t cols = pair ? 256 : 512;
+    static constexpr uint32_t o1 = pair ? 192 : 128, o2 = pair ? 0 : 128 + DV, part = pair ? 0 : 384;
+    static constexpr int per_sm = pair ? 2 : 1;
 };
 
 struct TcMaps {
-    CUtensorMap q[3], k[3], v[3];
+    CUtensorMap q[3], k[3], v[3], y[3];
 };
 
 struct AttnSh {
@@ -54,8 +67,10 @@ struct AttnSh {
     uint64_t scores, rows, part;
     uint32_t tmem_base;
     int abort_flag;
-    float pw[64];                  // lambda^n at 31 + n, n = 0 .. 31, and zeros ahead of it
-    alignas(16) float col[32];     // a score block's columns: lambda^(31 - j), backwards lambda^j
+    // si times: lambda^n at 31 + n, n = 0 .. 31, and zeros ahead of it; a score block's columns,
+    // lambda^(31 - j), backwards lambda^j
+    float pw[64];
+    alignas(16) float col[32];
 };
 
 // The two warps of a lane quarter.
@@ -76,24 +91,38 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
 }
 
 // Two bf16 values times w as three pieces each: 24 bits.
-__device__ __forceinline__ void split_pair(uint32_t v, float w, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-    float a = __uint_as_float(v << 16) * w, b = __uint_as_float(v & 0xffff0000u) * w;
-    p0 = bf2(a, b);
-    a -= __uint_as_float(p0 << 16);
-    b -= __uint_as_float(p0 & 0xffff0000u);
-    p1 = bf2(a, b);
-    p2 = bf2(a - __uint_as_float(p1 << 16), b - __uint_as_float(p1 & 0xffff0000u));
+__device__ __forceinline__ f32x2 widen(uint32_t v) { return pk2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t narrow(f32x2 v) {
+    float a, b;
+    unpk2(v, a, b);
+    return bf2(a, b);
 }
-// 16 bf16 values: a whole 32-byte sector where the address allows.
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&v)[8], bool whole, int left) {
-    if (whole) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-    } else {
-        if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
-        if (left > 8) *reinterpret_cast<uint4*>(p + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-    }
+__device__ __forceinline__ void split_pair(uint32_t v, f32x2 w, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+    const f32x2 minus = pk2(-1.0f, -1.0f);
+    f32x2 f = mul2(widen(v), w);
+    p0 = narrow(f);
+    f = fma2(widen(p0), minus, f);
+    p1 = narrow(f);
+    p2 = narrow(fma2(widen(p1), minus, f));
+}
+
+struct Unit {  // a segment of one (sequence, head) of one pass
+    int ip, seg, pair, b, h, len, chunks, c0, count;
+};
+template <bool CARRY> __device__ __forceinline__ Unit unit_of(const AttnArgs& a, long long u) {
+    Unit r;
+    r.ip = (int)(u % a.passes);
+    const int rest = (int)(u / a.passes);
+    r.seg = rest % a.segs;
+    r.pair = rest / a.segs;
+    r.b = r.pair / a.H;
+    r.h = r.pair - r.b * a.H;
+    r.len = attn_len(a.lens, r.b, a.L);
+    r.chunks = (r.len + TT - 1) / TT;
+    r.c0 = min(r.chunks, r.seg * a.per);
+    r.count = min(r.chunks, r.c0 + a.per) - r.c0;
+    if (CARRY && r.seg == a.segs - 1) r.count = 0;  // its state is the pass's own
+    return r;
 }
 
 template <int DK, int DV, bool CARRY>
@@ -101,22 +130,12 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
     attn_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ AttnArgs a) {
     grid_begin();
     using S = Shape<DK, DV>;
-    extern __shared__ __align__(1024) unsigned char ring[];  // swizzle atoms are 1 KB
-    unsigned char *zop = ring + 2 * S::stage, *lobuf = zop + S::z;
+    extern __shared__ __align__(1024) unsigned char smem[];  // swizzle atoms are 1 KB
     __shared__ AttnSh sh;
     volatile int* abort_flag = &sh.abort_flag;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: see elect_one
     const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
-
-    const int ip = blockIdx.x % a.passes, rest = blockIdx.x / a.passes;
-    const int seg = rest % a.segs, pair = rest / a.segs, b = pair / a.H, h = pair - b * a.H;
-    const AttnPass& p = a.p[ip];
-    const int len = attn_len(a.lens, b, a.L), chunks = (len + TT - 1) / TT;
-    const int c0 = min(chunks, seg * a.per), c1 = min(chunks, c0 + a.per), count = c1 - c0;
-    const float l2 = attn_log2_decay(a.decay, h);
-    const int Dk = p.Dk, Dv = p.Dv, back = p.back;
-    const long long zsize = (long long)Dk * Dv;
 
     if (tid == 0) {
         mbar_init(&sh.full[0], 1);
@@ -128,132 +147,158 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 0) tc_alloc(&sh.tmem_base, S::cols);
-    if (warp == 1) {
-        sh.pw[31 + lane] = ex2f(l2 * (float)lane);
-        if (lane < 31) sh.pw[lane] = 0.0f;
-        sh.col[lane] = ex2f(l2 * (float)(back ? lane : 31 - lane));
-    }
+    if (warp == 1 && lane < 31) sh.pw[lane] = 0.0f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base, lanes = (uint32_t)(32 * quarter) << 16;
 
-    const auto first_row = [&](int it) { return len - (back ? c0 + it + 1 : chunks - c0 - it) * TT; };
-    const auto load = [&](int it) {
-        unsigned char* st = ring + (it & 1) * S::stage;
-        const int t0 = first_row(it);
-        mbar_expect_tx(&sh.full[it & 1], CARRY ? S::q + S::v : S::stage);
-        for (int i = 0; i < (int)(S::q / TBLOCK); i++) {
-            if (!CARRY) tma_4d(st + i * TBLOCK, &maps.q[ip], 64 * i, h, t0, b, &sh.full[it & 1]);
-            tma_4d(st + S::q + i * TBLOCK, &maps.k[ip], 64 * i, h, t0, b, &sh.full[it & 1]);
-        }
-        for (int i = 0; i < (int)(S::v / TBLOCK); i++)
-            tma_4d(st + 2 * S::q + i * TBLOCK, &maps.v[ip], 64 * i, h, t0, b, &sh.full[it & 1]);
-    };
-    int issued = count < 2 ? count : 2;  // chunks whose copies were issued
-    if (warp == 0 && elect_one())
-        for (int it = 0; it < issued; it++) load(it);
-    __syncwarp();
+    unsigned char* const sx = smem + 2 * S::v + 2 * S::q;
+    const auto buf_v = [&](int s) { return smem + (s ? 0 : S::v); };
+    const auto buf_q = [&](int s) { return s ? sx + S::x + S::q : sx - 2 * S::q; };
+    const auto buf_k = [&](int s) { return s ? sx + S::x : sx - S::q; };
+    // pair: the copy of Z lies behind k's rows in stage 0, ahead of them in stage 1
+    const auto buf_z = [&](int s) { return S::pair && s ? sx + S::x - S::z : sx; };
 
-    // ---- the state: row `row`, columns half * DV / 2 ..
-    constexpr int ZC = DV / 2;
-    const bool zrow = row < DK;
-    float z[ZC];
-    {
-        const float* z0 = CARRY ? nullptr : p.carry ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                                          : p.z0    ? p.z0 + pair * zsize
-                                                    : nullptr;
-#pragma unroll
-        for (int i = 0; i < ZC; i++) {
-            const int n = half * ZC + i;
-            z[i] = z0 && row < Dk && n < Dv ? z0[(long long)row * p.zm + (long long)n * p.zn] : 0.0f;
+    // ---- copies: warp 0 keeps two chunks ahead, over the ends of units
+    const long long units = (long long)a.B * a.H * a.segs * a.passes;
+    long long lu = blockIdx.x;  // the unit and chunk to load next, and how many were loaded
+    int lit = 0, loaded = 0;
+    Unit ln = unit_of<CARRY>(a, lu < units ? lu : 0);
+    const auto load_next = [&] {  // the stage's rows out have been read, too
+        if (warp != 0) return;
+        if constexpr (!CARRY) {
+            if (elect_one()) bulk_wait_read();
+            __syncwarp();
         }
-    }
-    const auto put_state = [&] {
-        if (CARRY || !zrow) return;
-#pragma unroll
-        for (int i = 0; i < ZC; i += 8) {
-            const int n = half * ZC + i, ch = (n & 63) >> 3;
-            *reinterpret_cast<uint4*>(zop + (n >> 6) * (DK * 128) + row * 128 + ((ch ^ (row & 7)) << 4)) =
-                make_uint4(bf2(z[i], z[i + 1]), bf2(z[i + 2], z[i + 3]), bf2(z[i + 4], z[i + 5]), bf2(z[i + 6], z[i + 7]));
+        while (lu < units && lit >= ln.count) {
+            lu += gridDim.x;
+            lit = 0;
+            if (lu < units) ln = unit_of<CARRY>(a, lu);
         }
-    };
-    put_state();
-    fence_async_smem();
-
-    const bool whole = Dv % 16 == 0 && ((uintptr_t)p.y.p & 31) == 0 && p.y.row % 16 == 0 && p.y.batch % 16 == 0;
-    constexpr uint32_t id_scores = idesc_bf16(TT, TT, 0, 0), id_rows = idesc_bf16(TT, DV, 0, 1),
-                       id_part = idesc_bf16(TT, DV, 1, 1);
-    const int ksteps = (Dk + 15) / 16;
-    bool fail = false;
-    const auto wait = [&](uint64_t* bar, unsigned parity) {
-        if (!fail && !mbar_wait(bar, parity, abort_flag, &g_attn_status)) fail = true;
-    };
-    const auto wait_all = [&](uint64_t* bar, unsigned parity) {  // every thread of the warp
-        wait(bar, parity);
+        if (lu < units) {
+            if (elect_one()) {
+                const AttnPass& lp = a.p[ln.ip];
+                const int s = loaded & 1, t0 = ln.len - (lp.back ? ln.c0 + lit + 1 : ln.chunks - ln.c0 - lit) * TT;
+                mbar_expect_tx(&sh.full[s], CARRY ? S::q + S::v : S::stage);
+                for (int i = 0; i < (int)(S::q / TBLOCK); i++) {
+                    if constexpr (!CARRY) tma_4d(buf_q(s) + i * TBLOCK, &maps.q[ln.ip], 64 * i, ln.h, t0, ln.b, &sh.full[s]);
+                    tma_4d(buf_k(s) + i * TBLOCK, &maps.k[ln.ip], 64 * i, ln.h, t0, ln.b, &sh.full[s]);
+                }
+                for (int i = 0; i < (int)(S::v / TBLOCK); i++)
+                    tma_4d(buf_v(s) + i * TBLOCK, &maps.v[ln.ip], 64 * i, ln.h, t0, ln.b, &sh.full[s]);
+            }
+            lit++;
+            loaded++;
+        }
         __syncwarp();
     };
-    for (int it = 0; it < count; it++) {
-        unsigned char* st = ring + (it & 1) * S::stage;
-        unsigned char *sq = st, *sk = st + S::q, *sv = st + 2 * S::q, *slo = S::lo ? lobuf : sq;
-        const unsigned full_ph = (it >> 1) & 1, ph = it & 1;
-        const int t0 = first_row(it), lo = t0 < 0 ? -t0 : 0;
-        if (!CARRY) {
-            // the state's copy is there and the last chunk's results were read
-            tc_fence_before();
-            if (__syncthreads_or(fail)) break;
-            wait_all(&sh.full[it & 1], full_ph);
+    load_next();
+    load_next();
+
+    bool fail = false, stop = false;
+    const auto wait_all = [&](uint64_t* bar, unsigned parity) {  // every thread of the warp
+        if (!fail && !mbar_wait(bar, parity, abort_flag, &g_attn_status)) fail = true;
+        __syncwarp();
+    };
+    int g = 0;  // chunks walked over
+    for (long long un = blockIdx.x; un < units && !stop; un += gridDim.x) {
+        const Unit u = unit_of<CARRY>(a, un);
+        const int pair = u.pair, seg = u.seg, b = u.b, h = u.h, len = u.len, count = u.count;
+        const AttnPass& p = a.p[u.ip];
+        const int Dk = p.Dk, Dv = p.Dv, back = p.back;
+        const float l2 = attn_log2_decay(a.decay, h);
+        const long long zsize = (long long)Dk * Dv;
+        const bool last = seg == a.segs - 1;
+        if (CARRY && last) continue;
+        if (!CARRY && warp == 1) {
+            // (every warp is past a barrier behind its last read of these)
+            sh.pw[31 + lane] = p.si * ex2f(l2 * (float)lane);
+            sh.col[lane] = p.si * ex2f(l2 * (float)(back ? lane : 31 - lane));
+        }
+        const auto first_row = [&](int it) { return len - (back ? u.c0 + it + 1 : u.chunks - u.c0 - it) * TT; };
+
+        // ---- the state: column zn of Z, rows zm ..  With DV = 64 product 4 gives every column
+        // twice (lanes 0 .. 63 and 64 .. 127), and four threads share one.
+        constexpr int ZC = DK * DV / 256;
+        const int zn = row % DV, zm = (DV == 64 ? half + 2 * (quarter >> 1) : half) * ZC;
+        f32x2 z[ZC / 2];
+        {
+            const float* z0 = CARRY ? nullptr : p.carry ? p.carry + ((long long)pair * a.segs + seg) * zsize
+                                              : p.z0    ? p.z0 + pair * zsize
+                                                        : nullptr;
+#pragma unroll
+            for (int i = 0; i < ZC; i += 2) {
+                const int m = zm + i;  // Dk is even
+                const bool in = z0 && m < Dk && zn < Dv;
+                const float* zp = z0 + (long long)m * p.zm + (long long)zn * p.zn;
+                z[i / 2] = in ? pk2(zp[0], zp[p.zm]) : pk2(0.0f, 0.0f);
+            }
+        }
+        const auto put_state = [&](int s) {
+            if (CARRY) return;
+#pragma unroll
+            for (int i = 0; i < ZC; i += 8) {
+                const int m = zm + i, ch = (m & 63) >> 3;
+                *reinterpret_cast<uint4*>(buf_z(s) + (m >> 6) * S::zblock + zn * 128 + ((ch ^ (zn & 7)) << 4)) =
+                    make_uint4(narrow(z[i / 2]), narrow(z[i / 2 + 1]), narrow(z[i / 2 + 2]), narrow(z[i / 2 + 3]));
+            }
+        };
+        put_state(g & 1);
+        fence_async_smem();
+
+        constexpr uint32_t id_scores = idesc_bf16(TT, S::pair ? 192 : TT, 0, 0), id_state = idesc_bf16(TT, DV, 0, 0),
+                           id_rows = idesc_bf16(TT, DV, 0, 1), id_part = idesc_bf16(TT, S::pair ? 192 : DK, 1, 1);
+        const int ksteps = (Dk + 15) / 16;
+        // The steps of a chunk (s its stage, ph its parity, lo the rows that it lacks).
+        const auto issue_scores = [&](int s) {  // products 1 and 2
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                const uint64_t dq = sdesc(sq, 16, 1024), dk = sdesc(sk, 16, 1024), dz = sdesc(zop, DK * 128, 1024);
+                const uint64_t dq = sdesc(buf_q(s), 16, 1024), dz = sdesc(buf_z(s), 16, 1024);
+                const uint64_t dk = S::pair && s ? dz : sdesc(buf_k(s), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < DK / 16; k++)
                     if (k < ksteps) {
                         const uint32_t off = (k >> 2) * (TBLOCK >> 4) + (k & 3) * 2;
                         tc_mma_bf16(tmem, dq + off, dk + off, id_scores, k > 0);
                     }
-                tc_commit(&sh.scores);
+                if constexpr (!S::pair) {
 #pragma unroll
-                for (int k = 0; k < DK / 16; k++)
-                    if (k < ksteps)
-                        tc_mma_bf16(tmem + S::o2, dq + (k >> 2) * (TBLOCK >> 4) + (k & 3) * 2, dz + k * 128, id_rows,
-                                    k > 0);
+                    for (int k = 0; k < DK / 16; k++)
+                        if (k < ksteps)
+                            tc_mma_bf16(tmem + S::o2, dq + (k >> 2) * (TBLOCK >> 4) + (k & 3) * 2,
+                                        dz + (k >> 2) * (S::zblock >> 4) + (k & 3) * 2, id_state, k > 0);
+                }
+                tc_commit(&sh.scores);
             }
             __syncwarp();
-            // ---- scores times powers of lambda, in bf16, back to tensor memory.  This warp
-            // takes column blocks half and half + 2 of its rows' four.
-            wait_all(&sh.scores, ph);
-            tc_fence_after();
+        };
+        const auto scale_scores = [&](uint32_t at) {
+            // scores times powers of lambda, in bf16, back over themselves.  This warp takes column
+            // blocks half and half + 2 of its rows' four.
             uint32_t pk[2][16];
 #pragma unroll
             for (int u = 0; u < 2; u++) {
                 const int cb = half + 2 * u;
-                const bool diag = cb == quarter;
-                if (diag) {
+                if (cb == quarter) {
                     float s[32];
-                    tc_ld32(tmem + lanes + 32 * cb, s);
-                    // (a factor of 0 beside a score that is not finite would not do)
+                    tc_ld32(at + 32 * cb, s);
 #pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const float f = s[j] * sh.pw[31 + (back ? j - lane : lane - j)];
-                        s[j] = (back ? j >= lane : j <= lane) ? f : 0.0f;
-                    }
+                    for (int j = 0; j < 32; j++) s[j] *= sh.pw[31 + (back ? j - lane : lane - j)];
 #pragma unroll
                     for (int j = 0; j < 16; j++) pk[u][j] = bf2(s[2 * j], s[2 * j + 1]);
                 } else if (back ? cb > quarter : cb < quarter) {
                     // lambda^(rows apart) = one power of the row's, 1 at least, and one of the column's
                     float s[32];
-                    tc_ld32(tmem + lanes + 32 * cb, s);
+                    tc_ld32(at + 32 * cb, s);
                     const float f = ex2f(l2 * (float)(back ? 32 * cb - row : row - 32 * cb - 31));
                     const f32x2 ff = pk2(f, f);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 c = *reinterpret_cast<const float4*>(&sh.col[j]);
-                        unpk2(mul2(mul2(pk2(s[j], s[j + 1]), ff), pk2(c.x, c.y)), s[j], s[j + 1]);
-                        unpk2(mul2(mul2(pk2(s[j + 2], s[j + 3]), ff), pk2(c.z, c.w)), s[j + 2], s[j + 3]);
+                        pk[u][j / 2] = narrow(mul2(mul2(pk2(s[j], s[j + 1]), ff), pk2(c.x, c.y)));
+                        pk[u][j / 2 + 1] = narrow(mul2(mul2(pk2(s[j + 2], s[j + 3]), ff), pk2(c.z, c.w)));
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; j++) pk[u][j] = bf2(s[2 * j], s[2 * j + 1]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; j++) pk[u][j] = 0;
@@ -263,35 +308,34 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
             tc_fence_before();
             pair_sync(quarter);
             tc_fence_after();
-            tc_st16(tmem + lanes + 16 * half, pk[0]);
-            tc_st16(tmem + lanes + 16 * (half + 2), pk[1]);
+            tc_st16(at + 16 * half, pk[0]);
+            tc_st16(at + 16 * (half + 2), pk[1]);
             tc_wait_st();
-            tc_fence_before();
-            if (__syncthreads_or(fail)) break;
+        };
+        const auto issue_rows = [&](int s, uint32_t at) {  // product 3
             if (warp == 0 && elect_one()) {
                 tc_fence_after();
-                const uint64_t dv = sdesc(sv, TBLOCK, 1024);
+                const uint64_t dv = sdesc(buf_v(s), TBLOCK, 1024);
 #pragma unroll
-                for (int k = 0; k < TT / 16; k++) tc_mma_ts(tmem + S::o1, tmem + 8 * k, dv + k * 128, id_rows, k > 0);
+                for (int k = 0; k < TT / 16; k++) tc_mma_ts(tmem + S::o1, at + 8 * k, dv + k * 128, id_rows, k > 0);
                 tc_commit(&sh.rows);
             }
             __syncwarp();
-        }
-        // ---- v times its weight in the state, as three pieces, over v, q and the state's copy:
-        // taken while product 3 runs, stored behind it.  16 bytes a time, all of one row; rows
-        // (tid >> 3) + 32 i of each 64-column block.
-        wait_all(&sh.full[it & 1], full_ph);
-        {
-            constexpr int NB = DV / 64;
-            uint4 p0[4 * NB], p1[4 * NB], p2[4 * NB];
-            float w[4];
+        };
+        // k times its weight in the state as three pieces, p0 over k, p1 over q, p2 over the
+        // state's copy: 16 bytes a time, all of one row; rows (tid >> 3) + 32 i of each 64-column block
+        constexpr int NB = DK / 64;
+        uint4 p0[4 * NB], p1[4 * NB], p2[4 * NB];
+        const auto split_k = [&](int s, int lo) {
+            f32x2 w[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const int j = (tid >> 3) + 32 * i;
-                w[i] = j < lo ? 0.0f : p.su * ex2f(l2 * (float)(back ? j - lo + 1 : TT - 1 - j));
+                const float f = j < lo ? 0.0f : p.su * ex2f(l2 * (float)(back ? j - lo + 1 : TT - 1 - j));
+                w[i] = pk2(f, f);
             }
 #pragma unroll
-            for (int i = 0; i < 4 * NB; i++) p0[i] = *reinterpret_cast<const uint4*>(sv + 16 * (tid + 256 * i));
+            for (int i = 0; i < 4 * NB; i++) p0[i] = *reinterpret_cast<const uint4*>(buf_k(s) + 16 * (tid + 256 * i));
 #pragma unroll
             for (int i = 0; i < 4 * NB; i++) {
                 split_pair(p0[i].x, w[i & 3], p0[i].x, p1[i].x, p2[i].x);
@@ -299,102 +343,210 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                 split_pair(p0[i].z, w[i & 3], p0[i].z, p1[i].z, p2[i].z);
                 split_pair(p0[i].w, w[i & 3], p0[i].w, p1[i].w, p2[i].w);
             }
-            if (!CARRY) {
-                wait_all(&sh.rows, ph);
-                tc_fence_after();
-            }
+        };
+        const auto put_pieces = [&](int s) {
 #pragma unroll
             for (int i = 0; i < 4 * NB; i++) {
                 const uint32_t at = 16 * (tid + 256 * i);
-                *reinterpret_cast<uint4*>(sv + at) = p0[i];
-                *reinterpret_cast<uint4*>(slo + at) = p1[i];
-                *reinterpret_cast<uint4*>(zop + at) = p2[i];
+                *reinterpret_cast<uint4*>(buf_k(s) + at) = p0[i];
+                *reinterpret_cast<uint4*>(buf_q(s) + at) = p1[i];
+                *reinterpret_cast<uint4*>(sx + at) = p2[i];
             }
-        }
-        fence_async_smem();
-        if (__syncthreads_or(fail)) break;
-        if (warp == 0 && elect_one()) {
-            tc_fence_after();
-            const uint64_t dk = sdesc(sk, TBLOCK, 1024);
+            fence_async_smem();
+        };
+        const auto issue_part = [&](int s) {  // product 4
+            if (warp == 0 && elect_one()) {
+                tc_fence_after();
+                // (DV = 64: both 64-row blocks of v^T are the one there is)
+                const uint64_t dv = sdesc(buf_v(s), DV == 64 ? 0 : TBLOCK, 1024);
+                if constexpr (S::pair) {
+                    const uint64_t dp = sdesc(s ? sx : buf_q(s), TBLOCK, 1024);
 #pragma unroll
-            for (int u = 0; u < 3; u++) {
-                const uint64_t dv = sdesc(u == 2 ? zop : u ? slo : sv, TBLOCK, 1024);
+                    for (int k = 0; k < TT / 16; k++) tc_mma_bf16(tmem + S::part, dv + k * 128, dp + k * 128, id_part, k > 0);
+                } else {
 #pragma unroll
-                for (int k = 0; k < TT / 16; k++)
-                    tc_mma_bf16(tmem + S::kv, dk + k * 128, dv + k * 128, id_part, u > 0 || k > 0);
+                    for (int u = 0; u < 3; u++) {
+                        const uint64_t dp = sdesc(u == 0 ? sx : u == 1 ? buf_q(s) : buf_k(s), TBLOCK, 1024);
+#pragma unroll
+                        for (int k = 0; k < TT / 16; k++)
+                            tc_mma_bf16(tmem + S::part, dv + k * 128, dp + k * 128, id_part, u > 0 || k > 0);
+                    }
+                }
+                tc_commit(&sh.part);
             }
-            tc_commit(&sh.part);
-        }
-        __syncwarp();
-        if (!CARRY) {
-            // ---- rows out, while the state's part is multiplied
-            tc_fence_after();
-            const float w = p.sx * ex2f(l2 * (float)(back ? TT - 1 - row : row >= lo ? row - lo + 1 : 0));
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y.p) + b * p.y.batch + (long long)(t0 + row) * p.y.row +
-                               (long long)h * Dv;
+            __syncwarp();
+        };
+        const auto add_part = [&](int lo) {  // the state behind the chunk
+            const float wz = ex2f(l2 * (float)(TT - lo));
+            const f32x2 ww = pk2(wz, wz);
+            constexpr int PARTS = S::pair ? 3 : 1;
 #pragma unroll
-            for (int cc = 0; cc < ZC; cc += 32) {
-                float o[32], r[32];
-                tc_ld32(tmem + lanes + S::o1 + half * ZC + cc, o);
-                tc_ld32(tmem + lanes + S::o2 + half * ZC + cc, r);
-                if (row >= lo) {
+            for (int cc = 0; cc < ZC; cc += 16) {
+                float s[PARTS][16];
 #pragma unroll
-                    for (int i = 0; i < 32; i++) o[i] = fmaf(w, r[i], p.si * o[i]);
+                for (int u = 0; u < PARTS; u++) tc_ld16_async(tmem + lanes + S::part + 64 * u + zm + cc, s[u]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 16) {
-                        uint32_t v[8];
+                for (int u = 0; u < PARTS; u++) {
+                    tc_wait_ld(s[u]);
 #pragma unroll
-                        for (int j = 0; j < 8; j++) v[j] = bf2(o[i + 2 * j], o[i + 2 * j + 1]);
-                        const int n = half * ZC + cc + i;
-                        store16(y + n, v, whole && n < Dv, Dv - n);
+                    for (int i = 0; i < 8; i++) {
+                        const f32x2 t = pk2(s[u][2 * i], s[u][2 * i + 1]);
+                        f32x2& zz = z[cc / 2 + i];
+                        zz = u ? add2(zz, t) : fma2(zz, ww, t);
                     }
                 }
             }
+        };
+        constexpr int OC = DV / 2;  // output columns of a thread
+        uint32_t out[OC / 2];
+        const auto read_rows = [&](int lo, uint32_t o2) {
+            const float w = p.sx * ex2f(l2 * (float)(back ? TT - 1 - row : row >= lo ? row - lo + 1 : 0));
+            const f32x2 ww = pk2(w, w);
+#pragma unroll
+            for (int cc = 0; cc < OC; cc += 32) {
+                float o[32], r[32];
+                tc_ld32(tmem + lanes + S::o1 + half * OC + cc, o);
+                tc_ld32(o2 + lanes + half * OC + cc, r);
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    out[cc / 2 + i] = narrow(fma2(ww, pk2(r[2 * i], r[2 * i + 1]), pk2(o[2 * i], o[2 * i + 1])));
+            }
+        };
+        // Rows out: over v's buffer, which every product has read, and from there by the copy
+        // engine; a chunk that begins before the sequence straight from the registers (a copy
+        // may not start at a negative row).
+        const auto put_rows = [&](int s, int lo, int t0) {
+            if (lo == 0) {
+#pragma unroll
+                for (int i = 0; i < OC; i += 8) {
+                    const int n = half * OC + i, ch = (n & 63) >> 3;
+                    *reinterpret_cast<uint4*>(buf_v(s) + (n >> 6) * TBLOCK + row * 128 + ((ch ^ (row & 7)) << 4)) =
+                        make_uint4(out[i / 2], out[i / 2 + 1], out[i / 2 + 2], out[i / 2 + 3]);
+                }
+                fence_async_smem();
+            } else if (row >= lo) {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y.p) + b * p.y.batch + (long long)(t0 + row) * p.y.row +
+                                   (long long)h * Dv;
+#pragma unroll
+                for (int i = 0; i < OC; i += 8)
+                    if (half * OC + i < Dv)
+                        *reinterpret_cast<uint4*>(y + half * OC + i) =
+                            make_uint4(out[i / 2], out[i / 2 + 1], out[i / 2 + 2], out[i / 2 + 3]);
+            }
+        };
+        const auto store_rows = [&](int it, int s) {  // behind a barrier; warp 0's elected thread
+            const int t0 = first_row(it);
+            if (t0 < 0) return;
+            for (int i = 0; i < (int)(S::v / TBLOCK); i++)
+                if (64 * i < Dv) tma_store_4d(&maps.y[u.ip], buf_v(s) + i * TBLOCK, 64 * i, h, t0, b);
+            bulk_commit();
+        };
+
+        for (int it = 0; it < count; it++, g++) {
+            const int s = g & 1, t0 = first_row(it), lo = t0 < 0 ? -t0 : 0;
+            const unsigned full_ph = (g >> 1) & 1, ph = g & 1;
+            stop = true;
+            if constexpr (CARRY) {
+                wait_all(&sh.full[s], full_ph);
+                split_k(s, lo);
+                put_pieces(s);
+                tc_fence_before();
+                if (__syncthreads_or(fail)) break;
+                issue_part(s);
+                wait_all(&sh.part, ph);
+                tc_fence_after();
+                load_next();  // this chunk's stage is free
+                add_part(lo);
+            } else if constexpr (S::pair) {
+                const uint32_t scores = tmem + (s ? 64 : 0), o2 = tmem + (s ? 0 : 128);
+                wait_all(&sh.full[s], full_ph);
+                tc_fence_before();
+                if (__syncthreads_or(fail)) break;  // the state's copy is there, the last chunk's results were read
+                if (it > 0 && warp == 0 && elect_one()) store_rows(it - 1, s ^ 1);
+                __syncwarp();
+                issue_scores(s);
+                if (g > 0) load_next();
+                split_k(s, lo);
+                wait_all(&sh.scores, ph);
+                tc_fence_after();
+                put_pieces(s);
+                scale_scores(scores + lanes);
+                tc_fence_before();
+                if (__syncthreads_or(fail)) break;
+                issue_rows(s, scores);
+                wait_all(&sh.rows, ph);
+                tc_fence_after();
+                read_rows(lo, o2);
+                tc_fence_before();
+                if (__syncthreads_or(fail)) break;
+                issue_part(s);
+                wait_all(&sh.part, ph);
+                tc_fence_after();
+                put_rows(s, lo, t0);
+                add_part(lo);
+                if (it + 1 < count) {
+                    put_state(s ^ 1);
+                    fence_async_smem();
+                }
+            } else {
+                wait_all(&sh.full[s], full_ph);
+                tc_fence_before();
+                if (__syncthreads_or(fail)) break;
+                if (it > 0 && warp == 0 && elect_one()) store_rows(it - 1, s ^ 1);
+                __syncwarp();
+                issue_scores(s);
+                split_k(s, lo);
+                wait_all(&sh.scores, ph);
+                tc_fence_after();
+                put_pieces(s);
+                if (__syncthreads_or(fail)) break;
+                issue_part(s);
+                if (g > 0) load_next();
+                scale_scores(tmem + lanes);
+                tc_fence_before();
+                if (__syncthreads_or(fail)) break;
+                issue_rows(s, tmem);
+                wait_all(&sh.part, ph);
+                tc_fence_after();
+                add_part(lo);
+                if (it + 1 < count) {
+                    put_state(s ^ 1);
+                    fence_async_smem();
+                }
+                wait_all(&sh.rows, ph);
+                tc_fence_after();
+                read_rows(lo, tmem + S::o2);
+                put_rows(s, lo, t0);
+            }
+            stop = false;
         }
-        wait_all(&sh.part, ph);
-        tc_fence_after();
-        if (issued < count && !fail) {
-            if (warp == 0 && elect_one()) load(issued);
+        if (stop) break;
+        if (!CARRY && count > 0) {
+            if (__syncthreads_or(fail)) break;
+            if (warp == 0 && elect_one()) store_rows(count - 1, (g - 1) & 1);
             __syncwarp();
-            issued++;
         }
-        // ---- the state behind the chunk
-        const float wz = ex2f(l2 * (float)(TT - lo));
-        if (32 * quarter < DK) {
+
+        float* z1 = CARRY ? p.carry + ((long long)pair * a.segs + seg) * zsize
+                          : p.z1 && last ? p.z1 + pair * zsize
+                                                : nullptr;
+        if (z1 && zn < Dv) {
 #pragma unroll
-            for (int cc = 0; cc < ZC; cc += 32) {
-                float s[32];
-                tc_ld32(tmem + lanes + S::kv + half * ZC + cc, s);
-#pragma unroll
-                for (int i = 0; i < 32; i++) z[cc + i] = fmaf(z[cc + i], wz, s[i]);
+            for (int i = 0; i < ZC; i += 2) {
+                const int m = zm + i;
+                float* zp = z1 + (long long)m * p.zm + (long long)zn * p.zn;
+                if (m < Dk) unpk2(z[i / 2], zp[0], zp[p.zm]);
             }
         }
-        if (it + 1 < count) {
-            put_state();
-            fence_async_smem();
-        }
-        if (CARRY) {
-            tc_fence_before();
-            if (__syncthreads_or(fail)) break;
-        }
+        if constexpr (!CARRY) attn_blank<__nv_bfloat16>(p, b, h, len, a.L, seg, a.segs);
     }
-
-    float* z1 = CARRY ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                      : p.z1 && a.segs == 1 ? p.z1 + pair * zsize
-                                            : nullptr;
-    if (z1 && row < Dk) {
-#pragma unroll
-        for (int i = 0; i < ZC; i++) {
-            const int n = half * ZC + i;
-            if (n < Dv) z1[(long long)row * p.zm + (long long)n * p.zn] = z[i];
-        }
-    }
-    if (!CARRY) attn_blank<__nv_bfloat16>(p, b, h, len, a.L, seg, a.segs);
+    if (!CARRY && warp == 0 && elect_one()) bulk_wait_all();
+    __syncwarp();
     // copies and products under way end before their memory is given back (after a wait that
     // ran out; otherwise every one of them has been waited for)
     if (tid == 0 && *abort_flag) {
         int zero = 0;
-        for (int k = issued > 2 ? issued - 2 : 0; k < issued; k++)
+        for (int k = loaded > 2 ? loaded - 2 : 0; k < loaded; k++)
             mbar_wait(&sh.full[k & 1], (unsigned)((k >> 1) & 1), &zero, &g_attn_status);
         tc_commit(&sh.rows);
         for (int i = 0; i < 2; i++) mbar_wait(&sh.rows, (unsigned)i, &zero, &g_attn_status);
@@ -426,11 +578,12 @@ template <int DK, int DV> hc_status launch_shape(const AttnArgs& a, bool carry, 
     TcMaps m;
     for (int i = 0; i < a.passes; i++) {
         hc_status e;
-        if ((e = rows_map(&m.q[i], a.p[i].q, a.p[i].Dk, a)) || (e = rows_map(&m.k[i], a.p[i].k, a.p[i].Dk, a)) ||
+        if ((e = rows_map(&m.y[i], a.p[i].y, a.p[i].Dv, a)) || (e = rows_map(&m.q[i], a.p[i].q, a.p[i].Dk, a)) || (e = rows_map(&m.k[i], a.p[i].k, a.p[i].Dk, a)) ||
             (e = rows_map(&m.v[i], a.p[i].v, a.p[i].Dv, a)))
             return e;
     }
-    const dim3 grid((unsigned)((long long)a.B * a.H * a.segs * a.passes));
+    const long long units = (long long)a.B * a.H * a.segs * a.passes, most = (long long)S::per_sm * device_sm_count();
+    const dim3 grid((unsigned)(units < most ? units : most));
     if (carry)
         launch_next(attn_tc_kernel<DK, DV, true>, grid, dim3(256), S::smem, st, m, a);
     else
