@@ -160,24 +160,20 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
     // pair: the copy of Z lies behind k's rows in stage 0, ahead of them in stage 1
     const auto buf_z = [&](int s) { return S::pair && s ? sx + S::x - S::z : sx; };
 
-    // ---- copies: warp 0 keeps two chunks ahead, over the ends of units
+    // ---- copies, two chunks ahead, over the ends of units, by warp `mover`
     const long long units = (long long)a.B * a.H * a.segs * a.passes;
     long long lu = blockIdx.x;  // the unit and chunk to load next, and how many were loaded
     int lit = 0, loaded = 0;
     Unit ln = unit_of<CARRY>(a, lu < units ? lu : 0);
-    const auto load_next = [&] {  // the stage's rows out have been read, too
-        if (warp != 0) return;
-        if constexpr (!CARRY) {
-            if (elect_one()) bulk_wait_read();
-            __syncwarp();
-        }
+    const auto load_next = [&](int mover) {
         while (lu < units && lit >= ln.count) {
             lu += gridDim.x;
             lit = 0;
             if (lu < units) ln = unit_of<CARRY>(a, lu);
         }
         if (lu < units) {
-            if (elect_one()) {
+            if (warp == mover && elect_one()) {
+                if constexpr (!CARRY) bulk_wait_read();  // the stage's rows out have been read, too
                 const AttnPass& lp = a.p[ln.ip];
                 const int s = loaded & 1, t0 = ln.len - (lp.back ? ln.c0 + lit + 1 : ln.chunks - ln.c0 - lit) * TT;
                 mbar_expect_tx(&sh.full[s], CARRY ? S::q + S::v : S::stage);
@@ -193,8 +189,8 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         }
         __syncwarp();
     };
-    load_next();
-    load_next();
+    load_next(0);
+    load_next(0);
 
     bool fail = false, stop = false;
     const auto wait_all = [&](uint64_t* bar, unsigned parity) {  // every thread of the warp
@@ -211,6 +207,8 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         const long long zsize = (long long)Dk * Dv;
         const bool last = seg == a.segs - 1;
         if (CARRY && last) continue;
+        // the warp whose rows have no scores in its column blocks moves data meanwhile
+        const int mover = back ? 3 : 4;
         if (!CARRY && warp == 1) {
             // (every warp is past a barrier behind its last read of these)
             sh.pw[31 + lane] = p.si * ex2f(l2 * (float)lane);
@@ -455,21 +453,21 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                 issue_part(s);
                 wait_all(&sh.part, ph);
                 tc_fence_after();
-                load_next();  // this chunk's stage is free
+                load_next(mover);  // this chunk's stage is free
                 add_part(lo);
             } else if constexpr (S::pair) {
                 const uint32_t scores = tmem + (s ? 64 : 0), o2 = tmem + (s ? 0 : 128);
                 wait_all(&sh.full[s], full_ph);
                 tc_fence_before();
                 if (__syncthreads_or(fail)) break;  // the state's copy is there, the last chunk's results were read
-                if (it > 0 && warp == 0 && elect_one()) store_rows(it - 1, s ^ 1);
+                if (it > 0 && warp == mover && elect_one()) store_rows(it - 1, s ^ 1);
                 __syncwarp();
                 issue_scores(s);
-                if (g > 0) load_next();
                 split_k(s, lo);
                 wait_all(&sh.scores, ph);
                 tc_fence_after();
                 put_pieces(s);
+                if (g > 0) load_next(mover);
                 scale_scores(scores + lanes);
                 tc_fence_before();
                 if (__syncthreads_or(fail)) break;
@@ -492,7 +490,7 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                 wait_all(&sh.full[s], full_ph);
                 tc_fence_before();
                 if (__syncthreads_or(fail)) break;
-                if (it > 0 && warp == 0 && elect_one()) store_rows(it - 1, s ^ 1);
+                if (it > 0 && warp == mover && elect_one()) store_rows(it - 1, s ^ 1);
                 __syncwarp();
                 issue_scores(s);
                 split_k(s, lo);
@@ -501,7 +499,7 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                 put_pieces(s);
                 if (__syncthreads_or(fail)) break;
                 issue_part(s);
-                if (g > 0) load_next();
+                if (g > 0) load_next(mover);
                 scale_scores(tmem + lanes);
                 tc_fence_before();
                 if (__syncthreads_or(fail)) break;
@@ -523,7 +521,10 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         if (stop) break;
         if (!CARRY && count > 0) {
             if (__syncthreads_or(fail)) break;
-            if (warp == 0 && elect_one()) store_rows(count - 1, (g - 1) & 1);
+            if (warp == mover && elect_one()) {
+                store_rows(count - 1, (g - 1) & 1);
+                bulk_wait_read();  // the next unit's mover may be another one
+            }
             __syncwarp();
         }
 
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         }
         if constexpr (!CARRY) attn_blank<__nv_bfloat16>(p, b, h, len, a.L, seg, a.segs);
     }
-    if (!CARRY && warp == 0 && elect_one()) bulk_wait_all();
+    if (!CARRY && (warp == 3 || warp == 4) && elect_one()) bulk_wait_all();
     __syncwarp();
     // copies and products under way end before their memory is given back (after a wait that
     // ran out; otherwise every one of them has been waited for)
