@@ -17,9 +17,10 @@
 //
 // Operands come by TMA in 128-byte swizzled tiles, K-major or MN-major as the arrays lie,
 // so that nothing is transposed or copied; edges are the copy engine's zero fill.
-// Warp roles (320 threads, one CTA an SM): warp 0 loads, warp 1 issues the MMAs, warps 2-9
-// drain finished accumulators (two per TMEM lane quarter, half of the columns each) and
-// store through TMA.  Every wait is bounded, as in tc.cu.
+// Warp roles (576 threads, one CTA an SM): warp 0 loads, warp 1 issues the MMAs, warps 2-17
+// drain finished accumulators (four per TMEM lane quarter, 32 columns at a time: with two
+// the activations' latency was longer than a tile's products at C = 512) and store through TMA.
+// Every wait is bounded, as in tc.cu.
 #include "rows.cuh"
 #include "tcgen.cuh"
 
@@ -32,23 +33,45 @@ constexpr uint32_t FF_A_BYTES = FF_BM * FF_BK * 2;         // 16 KB
 constexpr uint32_t FF_STAGE = FF_A_BYTES + 256 * FF_BK * 2;  // and 32 KB of B
 constexpr uint32_t FF_MN_BLOCK = FF_BK * 128;              // 64 MN values x 64 k-values
 constexpr int FF_BOX = 32 * 64;                            // 32 rows x 32 values: an output box
-constexpr int FF_EPI = 8;
+constexpr int FF_EPI = 16;
 constexpr int FF_THREADS = 32 * (2 + FF_EPI);
-constexpr int FF_SMEM = 1024 + FF_STAGES * FF_STAGE + FF_EPI * 2 * FF_BOX;
+constexpr int FF_SMEM = 1024 + FF_STAGES * FF_STAGE + FF_EPI * FF_BOX;
 
 enum FfnMode { FF_IN, FF_MID, FF_MM };
 
 __device__ int g_ffn_status;
 
 struct FfnParams {
-    int units, tiles_m, tiles_n, splits;
-    int chunks;     // k-chunks of a product
-    int per;        // k-chunks of a split
-    int bn;         // accumulator columns a tile
-    int amn, bmn;   // operand majors (FF_MM)
-    int M, N, F;    // output rows and columns; F for IN and MID
-    float* part;    // splits > 1: [split][M][N]
+    // Tiles 0 .. full - 1 are one unit each.  The `rest` that would leave SMs idle in the last
+    // round are cut into `splits` runs of `per` k-chunks, a unit each, and joined afterwards.
+    int units, tiles_n, full, rest, splits;
+    int chunks, per;  // k-chunks of a product, of a split
+    int bn;           // accumulator columns a tile
+    int amn, bmn;     // operand majors (FF_MM)
+    int M, N, F;      // output rows and columns; F for IN and MID
+    float* part;      // [split][rest][128][bn]
 };
+struct FfnUnit {
+    int m0, n0, c0, c1;
+    long long slot;  // of `part`, or -1: a whole tile
+};
+__device__ __forceinline__ FfnUnit ffn_unit(const FfnParams& p, int u, int width) {
+    FfnUnit r;
+    int tile = u;
+    r.c0 = 0;
+    r.c1 = p.chunks;
+    r.slot = -1;
+    if (u >= p.full) {
+        r.slot = u - p.full;
+        const int split = (u - p.full) / p.rest;
+        tile = p.full + (u - p.full) - split * p.rest;
+        r.c0 = split * p.per;
+        r.c1 = min(p.chunks, r.c0 + p.per);
+    }
+    r.m0 = tile / p.tiles_n * FF_BM;
+    r.n0 = tile % p.tiles_n * width;
+    return r;
+}
 
 struct FfnSmem {
     uint64_t full[FF_STAGES], empty[FF_STAGES];
@@ -86,30 +109,30 @@ template <typename T> __device__ __forceinline__ uint32_t pack_pair(float a, flo
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// One warp's output boxes: 32 rows (a lane each) x 32 values, 64-byte swizzle, in two
-// buffers in turn.
-struct BoxOut {
-    unsigned char* buf;
-    int turn;
-};
-template <typename T>
-__device__ __forceinline__ void box_store(BoxOut& o, const CUtensorMap* map, const float (&v)[32], int lane, int col,
-                                          int part, int row, int cols, int rows) {
-    unsigned char* box = o.buf + o.turn * FF_BOX;
-    o.turn ^= 1;
-    if (lane == 0) bulk_wait_read1();  // the store before the last one has read this buffer
+// One warp's output box: 32 rows (a lane each) x 32 values, 64-byte swizzle.
+__device__ __forceinline__ void box_free(int lane) {  // the store before has read it
+    if (lane == 0) bulk_wait_read();
     __syncwarp();
+}
+// 16 values of the lane's row, columns 16 half ..
+template <typename T> __device__ __forceinline__ void box_put(unsigned char* box, const uint32_t (&v)[8], int half, int lane) {
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-        *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(pack_pair<T>(v[8 * j], v[8 * j + 1]), pack_pair<T>(v[8 * j + 2], v[8 * j + 3]),
-                       pack_pair<T>(v[8 * j + 4], v[8 * j + 5]), pack_pair<T>(v[8 * j + 6], v[8 * j + 7]));
+    for (int j = 0; j < 2; j++)
+        *reinterpret_cast<uint4*>(box + lane * 64 + (((2 * half + j) ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void box_store(const unsigned char* box, const CUtensorMap* map, int lane, int col, int part,
+                                          int row, int cols, int rows) {
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
         if (col < cols && row < rows) tma_store_3d(map, box, col, part, row);
         bulk_commit();
     }
+}
+template <typename T> __device__ __forceinline__ void pack16(const float (&v)[16], uint32_t (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) o[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
 }
 
 // amap, bmap: operands; a2map, b2map: gy and w_out of MID; omap: y, h or a gradient; o2map:
@@ -124,7 +147,7 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     unsigned char* ring = (unsigned char*)(((uintptr_t)dsmem + 1023) & ~(uintptr_t)1023);
     unsigned char* boxes = ring + FF_STAGES * FF_STAGE;
     __shared__ FfnSmem sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // see elect_one
     volatile int* abort_flag = &sh.abort_flag;
     if (threadIdx.x == 0) {
         for (int s = 0; s < FF_STAGES; s++) {
@@ -146,23 +169,22 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     const uint32_t tmem = sh.tmem_base;
     const int hw = p.bn / 2;  // IN, MID: columns of each of a and u
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         // ---------------- loads ----------------
         long long it = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < p.units && ok; t += gridDim.x) {
-            const int n0 = (t % p.tiles_n) * (MODE == FF_MM ? p.bn : hw);
-            const int rest = t / p.tiles_n, m0 = (rest % p.tiles_m) * FF_BM, split = rest / p.tiles_m;
-            const int c0 = split * p.per, c1 = min(p.chunks, c0 + p.per);
+            const FfnUnit un = ffn_unit(p, t, MODE == FF_MM ? p.bn : hw);
+            const int m0 = un.m0, n0 = un.n0;
             for (int second = 0; second < (MODE == FF_MID ? 2 : 1) && ok; second++)
-                for (int c = c0; c < c1; c++, it++) {
+                for (int c = un.c0; c < un.c1; c++, it++) {
                     const int s = (int)(it % FF_STAGES), k = c * FF_BK;
                     if (it >= FF_STAGES && !ff_wait(&sh.empty[s], (unsigned)((it / FF_STAGES - 1) & 1), abort_flag)) {
                         ok = false;
                         break;
                     }
                     unsigned char *sa = ring + s * FF_STAGE, *sb = sa + FF_A_BYTES;
-                    if (MODE == FF_MID && second) {
+                    if (MODE == FF_MID && !second) {  // gh first
                         mbar_expect_tx(&sh.full[s], FF_A_BYTES + 128 * FF_BK * 2);
                         tma_2d(sa, &a2map, k, m0, &sh.full[s]);
                         tma_2d(sb, &b2map, k, n0, &sh.full[s]);
@@ -196,11 +218,11 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
             for (long long k = it > FF_STAGES ? it - FF_STAGES : 0; k < it; k++)
                 ff_wait(&sh.full[k % FF_STAGES], (unsigned)((k / FF_STAGES) & 1), &zero);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         // ---------------- MMAs ----------------
-        // IN, MM: tile t accumulates in half t & 1 of the 512 columns.  MID: a | u in half
-        // t & 1 and gh in the first 128 columns of the other one, which the drain of the
-        // tile before frees in the order gh, then a | u.
+        // IN, MM: tile t accumulates in half t & 1 of the 512 columns.  MID: a | u in the first
+        // half and gh in 128 columns of the second, in turn: the next tile's gh is multiplied
+        // while this one is drained.
         const uint32_t fmt = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
         const auto idesc = [&](int n, int amn, int bmn) {
             return (1u << 4) | fmt | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16) | ((uint32_t)(n >> 3) << 17) |
@@ -226,25 +248,22 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
             return true;
         };
         for (int t = blockIdx.x; t < p.units && ok; t += gridDim.x, tile++) {
-            const int split = t / p.tiles_n / p.tiles_m;
-            const int c0 = split * p.per, c1 = min(p.chunks, c0 + p.per);
+            const FfnUnit un = ffn_unit(p, t, MODE == FF_MM ? p.bn : hw);
             const int b = tile & 1;
             if (MODE == FF_MID) {
-                // acc_empty[0]: gh drained, acc_empty[1]: a | u drained
-                if (tile > 0 && !ff_wait(&sh.acc_empty[0], (unsigned)((tile - 1) & 1), abort_flag)) break;
+                // (the tile before last was drained before a | u of the last)
+                ok = product(tmem + 256 + b * 128, idesc(128, 0, 0), un.c0, un.c1, 0, 0);
+                if (!ok || (tile > 0 && !ff_wait(&sh.acc_empty[0], (unsigned)((tile - 1) & 1), abort_flag))) break;
                 tc_fence_after();
-                ok = product(tmem + b * 256, idesc(p.bn, 0, 1), c0, c1, 0, 1);
-                if (!ok || (tile > 0 && !ff_wait(&sh.acc_empty[1], (unsigned)((tile - 1) & 1), abort_flag))) break;
-                tc_fence_after();
-                ok = product(tmem + (b ^ 1) * 256, idesc(128, 0, 0), c0, c1, 0, 0);
+                ok = product(tmem, idesc(p.bn, 0, 1), un.c0, un.c1, 0, 1);
                 if (ok) tc_commit(&sh.acc_full[0]);
             } else {
                 if (tile >= 2 && !ff_wait(&sh.acc_empty[b], (unsigned)((tile / 2 - 1) & 1), abort_flag)) break;
                 tc_fence_after();
                 if (MODE == FF_IN)
-                    ok = product(tmem + b * 256, idesc(p.bn, 0, 1), c0, c1, 0, 1);
+                    ok = product(tmem + b * 256, idesc(p.bn, 0, 1), un.c0, un.c1, 0, 1);
                 else
-                    ok = product(tmem + b * 256, idesc(p.bn, p.amn, p.bmn), c0, c1, p.amn, p.bmn);
+                    ok = product(tmem + b * 256, idesc(p.bn, p.amn, p.bmn), un.c0, un.c1, p.amn, p.bmn);
                 if (ok) tc_commit(&sh.acc_full[b]);
             }
         }
@@ -254,75 +273,91 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
         ff_wait(&sh.drain, 0, &zero);
     } else if (warp >= 2) {
         // ---------------- drain ----------------
-        const int ew = warp - 2, q = warp & 3, half = ew >> 2;
+        const int ew = warp - 2, q = warp & 3, part = ew >> 2;
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
-        BoxOut box{boxes + ew * 2 * FF_BOX, 0};
+        unsigned char* box = boxes + ew * FF_BOX;
         int tile = 0;
         for (int t = blockIdx.x; t < p.units; t += gridDim.x, tile++) {
-            const int n0 = (t % p.tiles_n) * (MODE == FF_MM ? p.bn : hw);
-            const int rest = t / p.tiles_n, m0 = (rest % p.tiles_m) * FF_BM, split = rest / p.tiles_m;
-            const int b = tile & 1, row = m0 + 32 * q;
+            const FfnUnit un = ffn_unit(p, t, MODE == FF_MM ? p.bn : hw);
+            const int b = MODE == FF_MID ? 0 : tile & 1, row = un.m0 + 32 * q;
+            if (!ff_wait(&sh.acc_full[b], (unsigned)((MODE == FF_MID ? tile : tile >> 1) & 1), abort_flag)) break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t base = tmem + lanes + b * 256;
             if (MODE == FF_MID) {
-                if (!ff_wait(&sh.acc_full[0], (unsigned)(tile & 1), abort_flag)) break;
-                tc_fence_after();
-                float g[2][32];
-                const uint32_t gbase = tmem + lanes + (b ^ 1) * 256 + half * 64, base = tmem + lanes + b * 256 + half * 64;
-                tc_ld32(gbase, g[0]);
-                tc_ld32(gbase + 32, g[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.acc_empty[0]);
+                const uint32_t gbase = tmem + lanes + 256 + (tile & 1) * 128 + 32 * part;
+                uint32_t ga[2][8], gu[2][8];
+                box_free(lane);
 #pragma unroll
                 for (int cc = 0; cc < 2; cc++) {
-                    float a[32], u[32];
-                    tc_ld32(base + 32 * cc, a);
-                    tc_ld32(base + 128 + 32 * cc, u);
+                    float g[16], a[16], u[16];
+                    tc_ld16_async(gbase + 16 * cc, g);
+                    tc_ld16_async(base + 32 * part + 16 * cc, a);
+                    tc_ld16_async(base + 128 + 32 * part + 16 * cc, u);
+                    tc_wait_ld(g);
+                    tc_wait_ld(a);
+                    tc_wait_ld(u);
                     if (cc == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.acc_empty[1]);
+                        if (lane == 0) mbar_arrive(&sh.acc_empty[0]);
                     }
+                    uint32_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        float f, s;
-                        act_both<ACT>(a[i], f, s);
-                        const float gh = g[cc][i];
-                        a[i] = gh * u[i] * s;
+                    for (int i = 0; i < 16; i++) {
+                        float f, d;
+                        act_both<ACT>(a[i], f, d);
+                        a[i] = g[i] * u[i] * d;
                         u[i] *= f;
-                        g[cc][i] = gh * f;
+                        g[i] *= f;
                     }
-                    const int col = n0 + 64 * half + 32 * cc;
-                    box_store<T>(box, &omap, u, lane, col, 0, row, p.F, p.M);
-                    box_store<T>(box, &o2map, a, lane, col, 0, row, p.F, p.M);
-                    box_store<T>(box, &o2map, g[cc], lane, col, 1, row, p.F, p.M);
+                    pack16<T>(u, h);
+                    pack16<T>(a, ga[cc]);
+                    pack16<T>(g, gu[cc]);
+                    box_put<T>(box, h, cc, lane);
                 }
+                const int col = un.n0 + 32 * part;
+                box_store(box, &omap, lane, col, 0, row, p.F, p.M);
+                box_free(lane);
+                box_put<T>(box, ga[0], 0, lane);
+                box_put<T>(box, ga[1], 1, lane);
+                box_store(box, &o2map, lane, col, 0, row, p.F, p.M);
+                box_free(lane);
+                box_put<T>(box, gu[0], 0, lane);
+                box_put<T>(box, gu[1], 1, lane);
+                box_store(box, &o2map, lane, col, 1, row, p.F, p.M);
                 continue;
             }
-            if (!ff_wait(&sh.acc_full[b], (unsigned)((tile >> 1) & 1), abort_flag)) break;
-            tc_fence_after();
-            const uint32_t base = tmem + lanes + b * 256;
-            const int own = (MODE == FF_IN ? hw : p.bn) / 2;  // columns of this warp
-            for (int cc = half * own; cc < (half + 1) * own; cc += 32) {
-                float v[32];
-                tc_ld32(base + cc, v);
-                if (MODE == FF_IN) {
-                    float u[32];
-                    tc_ld32(base + hw + cc, u);
+            for (int bx = part; bx < (MODE == FF_IN ? hw : p.bn) / 32; bx += 4) {
+                const int col = un.n0 + 32 * bx;
+                const bool whole = MODE != FF_MM || un.slot < 0;
+                if (whole) box_free(lane);
 #pragma unroll
-                    for (int i = 0; i < 32; i++) v[i] = act_f<ACT>(v[i]) * u[i];
-                }
-                if (MODE == FF_MM && p.splits > 1) {
-                    const int r = row + lane;
-                    if (r < p.M) {
-                        float* o = p.part + ((long long)split * p.M + r) * p.N + n0 + cc;
+                for (int cc = 0; cc < 2; cc++) {
+                    float v[16];
+                    tc_ld16_async(base + 32 * bx + 16 * cc, v);
+                    if (MODE == FF_IN) {
+                        float u[16];
+                        tc_ld16_async(base + hw + 32 * bx + 16 * cc, u);
+                        tc_wait_ld(v);
+                        tc_wait_ld(u);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            if (n0 + cc + i < p.N)
-                                *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        for (int i = 0; i < 16; i++) v[i] = act_f<ACT>(v[i]) * u[i];
+                    } else {
+                        tc_wait_ld(v);
                     }
-                } else {
-                    box_store<T>(box, &omap, v, lane, n0 + cc, 0, row, p.N, p.M);
+                    if (whole) {
+                        uint32_t o[8];
+                        pack16<T>(v, o);
+                        box_put<T>(box, o, cc, lane);
+                    } else {
+                        float* o = p.part + (un.slot * FF_BM + 32 * q + lane) * p.bn + 32 * bx + 16 * cc;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
                 }
+                if (whole) box_store(box, &omap, lane, col, 0, row, p.N, p.M);
             }
             tc_fence_before();
             __syncwarp();
@@ -336,46 +371,72 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     if (warp == 0) tc_dealloc(tmem, 512);
 }
 
-// out[r][c] = sum over splits, in order, of part[split][r][c]; four values a thread.
+// The tiles that were cut: out = sum over splits, in order.  Grid: (rest, groups of 8 rows).
 template <typename T>
-__global__ void __launch_bounds__(256) ffn_join_kernel(const float* part, int splits, int M, int N, T* out,
-                                                       long long row) {
+__global__ void __launch_bounds__(256) ffn_join_kernel(FfnParams p, T* out, long long row) {
     grid_begin();
-    const long long total = (long long)M * (N / 4);
-    for (long long e = blockIdx.x * 256LL + threadIdx.x; e < total; e += gridDim.x * 256LL) {
-        const long long r = e / (N / 4), c = (e - r * (N / 4)) * 4;
+    const int tile = p.full + blockIdx.x, m0 = tile / p.tiles_n * FF_BM + blockIdx.y * 8, n0 = tile % p.tiles_n * p.bn;
+    const long long stride = (long long)p.rest * FF_BM * p.bn;
+    for (int e = threadIdx.x; e < 8 * p.bn / 4; e += 256) {
+        const int r = e / (p.bn / 4), c = (e - r * (p.bn / 4)) * 4;
+        if (m0 + r >= p.M || n0 + c >= p.N) continue;
+        const float* in = p.part + ((long long)blockIdx.x * FF_BM + blockIdx.y * 8 + r) * p.bn + c;
         float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < splits; s++) {
-            const float4 v = *reinterpret_cast<const float4*>(part + ((long long)s * M + r) * N + c);
+#pragma unroll 4
+        for (int s = 0; s < p.splits; s++) {
+            const float4 v = *reinterpret_cast<const float4*>(in + s * stride);
             f[0] += v.x;
             f[1] += v.y;
             f[2] += v.z;
             f[3] += v.w;
         }
-        store_pack<T, 4>(out + r * row + c, f);
+        store_pack<T, 4>(out + (m0 + r) * row + n0 + c, f);
     }
+}
+template <typename T> __global__ void __launch_bounds__(256) ffn_zero_kernel(T* out, long long n) {
+    grid_begin();
+    for (long long e = blockIdx.x * 256LL + threadIdx.x; e < n; e += gridDim.x * 256LL) out[e] = from_f<T>(0.0f);
 }
 
 // ---------------------------------------------------------------------------
-// A product's shape: M x N outputs over K.
-struct MmPlan {
-    int bn, tiles_m, tiles_n, chunks, splits, per;
-};
-MmPlan ffn_plan(int M, int N, int K, bool may_split) {
-    MmPlan p;
-    p.bn = N > 128 ? 256 : N > 64 ? 128 : 64;
-    p.tiles_m = (int)cdiv(M, FF_BM);
-    p.tiles_n = (int)cdiv(N, p.bn);
+// The shape and cut of a product: M x N outputs over K, tiles of 128 x bn.
+FfnParams ffn_plan(int M, int N, int K, int bn) {
+    FfnParams p = {};
+    p.bn = bn;
+    p.M = M;
+    p.N = N;
+    p.tiles_n = (int)cdiv(N, bn);
     p.chunks = (int)cdiv(K, FF_BK);
-    const long long tiles = (long long)p.tiles_m * p.tiles_n, sms = device_sm_count();
-    long long s = may_split && tiles > 0 && tiles < sms ? sms / tiles : 1;
-    if (s > p.chunks / 4) s = p.chunks / 4;  // four chunks a split at least
-    if (s < 1) s = 1;
-    p.per = (int)((p.chunks + s - 1) / s);
-    p.splits = p.per > 0 ? (p.chunks + p.per - 1) / p.per : 1;
+    p.per = p.chunks;
+    p.splits = 1;
+    p.units = p.full = (int)cdiv(M, FF_BM) * p.tiles_n;
     return p;
 }
-size_t part_bytes(const MmPlan& p, int M, int N) { return p.splits > 1 ? sizeof(float) * p.splits * (size_t)M * N : 0; }
+// The same for FF_MM.  What whole rounds over the SMs leave is cut in the way that takes the
+// least time, at 0.4 us a k-chunk (measured; 128 x 256) and 0.04 us to write and read a partial
+// tile: 176 tiles of 512 chunks (gw_in of 32768 rows, 1024 x 5632) run in 1.17 rounds, not 2.
+FfnParams ffn_mm_plan(int M, int N, int K) {
+    FfnParams p = ffn_plan(M, N, K, N > 128 ? 256 : N > 64 ? 128 : 64);
+    const int sms = device_sm_count(), rest = p.full % sms;
+    double best = 1e30;
+    for (int s = 1; s <= 32 && rest > 0 && p.chunks > 0; s++) {
+        if (s > 1 && p.chunks / s < 4) break;
+        const int per = (p.chunks + s - 1) / s, n = (p.chunks + per - 1) / per;
+        const double t = 0.4 * per * ((rest * n + sms - 1) / sms) + (n > 1 ? 4.0 + 0.04 * rest * n : 0.0);
+        if (t < best) {
+            best = t;
+            p.per = per;
+            p.splits = n;
+        }
+    }
+    if (p.splits > 1) {
+        p.rest = rest;
+        p.full -= rest;
+        p.units = p.full + p.rest * p.splits;
+    }
+    return p;
+}
+size_t part_bytes(const FfnParams& p) { return sizeof(float) * p.rest * p.splits * FF_BM * (size_t)p.bn; }
 size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Mat {
@@ -418,44 +479,29 @@ template <typename T, int MODE> hc_status ffn_act(int act, const Maps& m, const 
     return ffn_launch<T, MODE, HC_PW_NONE>(m, p, st);
 }
 
-FfnParams params(const MmPlan& p, int M, int N, int F) {
-    FfnParams q = {};
-    q.units = p.tiles_m * p.tiles_n * p.splits;
-    q.tiles_m = p.tiles_m;
-    q.tiles_n = p.tiles_n;
-    q.splits = p.splits;
-    q.chunks = p.chunks;
-    q.per = p.per;
-    q.bn = p.bn;
-    q.M = M;
-    q.N = N;
-    q.F = F;
-    return q;
-}
-
 // out (M x N, T) = A B over K.  A: [M][K] rows, or with amn [K][M]; B: [N][K] rows, or with bmn [K][N].
 template <typename T>
 hc_status ffn_mm(const Mat& A, bool amn, const Mat& B, bool bmn, int M, int N, int K, T* out, long long row, float* part,
                  cudaStream_t st) {
-    const MmPlan pl = ffn_plan(M, N, K, true);
-    FfnParams p = params(pl, M, N, 0);
+    FfnParams p = ffn_mm_plan(M, N, K);
     p.amn = amn;
     p.bmn = bmn;
     p.part = part;
-    hc_status e = HC_OK;
-    if (K > 0) {
-        Maps m;
-        if ((e = in_map(&m.a, A, amn ? FF_BK : FF_BM)) || (e = in_map(&m.b, B, bmn ? FF_BK : pl.bn)) ||
-            (e = out_map(&m.o, out, row, N, 1, M)))
-            return e;
-        m.a2 = m.a;
-        m.b2 = m.b;
-        m.o2 = m.o;
-        if ((e = ffn_launch<T, FF_MM, HC_PW_NONE>(m, p, st)) || p.splits == 1) return e;
+    if (K == 0) {  // no rows: the weights' gradients (contiguous) are zeros
+        const long long n = (long long)M * N, want = (n + 255) / 256, most = 16LL * device_sm_count();
+        launch_next(ffn_zero_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, out, n);
+        return launched("ffn_zero_kernel", st);
     }
-    const long long want = cdiv((long long)M * (N / 4), 256), most = 16LL * device_sm_count();
-    launch_next(ffn_join_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, (const float*)part,
-                K > 0 ? p.splits : 0, M, N, out, row);
+    Maps m;
+    hc_status e;
+    if ((e = in_map(&m.a, A, amn ? FF_BK : FF_BM)) || (e = in_map(&m.b, B, bmn ? FF_BK : p.bn)) ||
+        (e = out_map(&m.o, out, row, N, 1, M)))
+        return e;
+    m.a2 = m.a;
+    m.b2 = m.b;
+    m.o2 = m.o;
+    if ((e = ffn_launch<T, FF_MM, HC_PW_NONE>(m, p, st)) || p.rest == 0) return e;
+    launch_next(ffn_join_kernel<T>, dim3(p.rest, FF_BM / 8), dim3(256), 0, st, p, out, row);
     return launched("ffn_join_kernel", st);
 }
 
@@ -478,7 +524,7 @@ Space ffn_space(const hc_gated_ffn_desc* d, int pass) {
     const size_t m = (size_t)d->M;
     Space s = {pad16(m * d->F * 2), 0, 0};
     const auto part = [&](int M, int N, int K) {
-        const size_t b = part_bytes(ffn_plan(M, N, K, true), M, N);
+        const size_t b = part_bytes(ffn_mm_plan(M, N, K));
         if (b > s.part) s.part = b;
     };
     if (pass == 0) {
@@ -497,11 +543,11 @@ hc_status ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
                   char* ws, cudaStream_t st) {
     const int M = d->M, C = d->C, F = d->F;
     void* h = ws;
-    MmPlan pl = ffn_plan(M, 2 * F, C, false);
     // columns of a and u each a tile: 64 where 128 would leave SMs without one
-    const int hw = (long long)pl.tiles_m * cdiv(F, 128) >= device_sm_count() ? 128 : 64;
-    pl.bn = 2 * hw;
-    pl.tiles_n = (int)cdiv(F, hw);
+    const int hw = (long long)cdiv(M, FF_BM) * cdiv(F, 128) >= device_sm_count() ? 128 : 64;
+    FfnParams p = ffn_plan(M, F, C, hw);
+    p.bn = 2 * hw;
+    p.F = F;
     Maps m;
     hc_status e;
     if ((e = in_map(&m.a, {x->p, row_of(x, d), C, M}, FF_BM)) || (e = in_map(&m.b, {w_in, 2LL * F, 2 * F, C}, FF_BK)) ||
@@ -510,7 +556,7 @@ hc_status ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
     m.a2 = m.a;
     m.b2 = m.b;
     m.o2 = m.o;
-    if ((e = ffn_act<T, FF_IN>(d->act, m, params(pl, M, F, F), st))) return e;
+    if ((e = ffn_act<T, FF_IN>(d->act, m, p, st))) return e;
     return ffn_mm<T>({h, F, F, M}, false, {w_out, C, C, F}, true, M, C, F, (T*)y->p, row_of(y, d),
                      (float*)(ws + ffn_space(d, 0).h), st);
 }
@@ -525,15 +571,15 @@ hc_status ffn_bwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
     const Mat xm = {x->p, row_of(x, d), C, M}, gym = {gy->p, row_of(gy, d), C, M};
     hc_status e = HC_OK;
     if (M > 0) {
-        MmPlan pl = ffn_plan(M, 2 * F, C, false);
-        pl.bn = 256;
-        pl.tiles_n = (int)cdiv(F, 128);
+        FfnParams p = ffn_plan(M, F, C, 128);
+        p.bn = 256;
+        p.F = F;
         Maps m;
         if ((e = in_map(&m.a, xm, FF_BM)) || (e = in_map(&m.b, {w_in, 2LL * F, 2 * F, C}, FF_BK)) ||
             (e = in_map(&m.a2, gym, FF_BM)) || (e = in_map(&m.b2, {w_out, C, C, F}, 128)) ||
             (e = out_map(&m.o, h, F, F, 1, M)) || (e = out_map(&m.o2, pre, 2LL * F, F, 2, M)))
             return e;
-        if ((e = ffn_act<T, FF_MID>(d->act, m, params(pl, M, F, F), st))) return e;
+        if ((e = ffn_act<T, FF_MID>(d->act, m, p, st))) return e;
         if (gx && gx->p &&
             (e = ffn_mm<T>({pre, 2LL * F, 2 * F, M}, false, {w_in, 2LL * F, 2 * F, C}, false, M, C, 2 * F, (T*)gx->p,
                            row_of(gx, d), part, st)))
