@@ -122,7 +122,7 @@ struct Cut {
 // Segments of a sequence: as many as give the GPU `passes` passes of blocks to fill it,
 // two chunks each at least.
 Cut attn_cut(const hc_linear_attn_desc* d, bool tc, int passes) {
-    const int T = tc ? AT_TC : AT_T, per_sm = tc && (d->Dk > 64 || d->Dv > 64) ? 1 : 2;
+    const int T = tc ? AT_TC : AT_T, per_sm = tc ? d->Dk > 64 || d->Dv > 64 ? 1 : 2 : d->Dk > 96 && d->Dv > 64 ? 2 : 3;
     const long long pairs = (long long)d->B * d->H * passes, want = (long long)per_sm * device_sm_count();
     const int chunks = (int)(((long long)d->L + T - 1) / T);
     long long segs = pairs < want ? want / pairs : 1;

@@ -3,7 +3,7 @@
 //
 // A block walks over one segment of one (sequence, head): 32 rows of q, k and v go to
 // shared memory, the state stays there, and 16 x 16 threads take each of the four
-// products in register tiles.  Bound by the multiply-adds and the shared-memory reads
+// products in register tiles, two values an instruction.  Bound by the multiply-adds and the shared-memory reads
 // that feed them.
 #include "attn.cuh"
 
@@ -13,9 +13,9 @@ namespace {
 constexpr int TP = AT_T + 2;  // pitch of a transposed tile: pairs of rows stay aligned
 
 template <int PK, int PV> struct AttnSmem {
-    float qt[PK][TP], kt[PK][TP];  // transposed
-    float k[AT_T][PK], v[AT_T][PV];
+    alignas(16) float k[AT_T][PK], v[AT_T][PV];
     float z[PK][PV];
+    float qt[PK][TP], kt[PK][TP];  // transposed
     float pt[AT_T][TP];            // scores, transposed: [j][i]
     float wj[AT_T];                // what row j weighs in the state
 };
@@ -64,68 +64,86 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
         sm.z[m][n] = z0 && m < Dk && n < Dv ? z0[(long long)m * p.zm + (long long)n * p.zn] : 0.0f;
     }
 
-    for (int idx = c0; idx < c1; idx++) {
-        const int c = p.back ? chunks - 1 - idx : idx;
-        const int t0 = len - (chunks - c) * AT_T, lo = t0 < 0 ? -t0 : 0;
-        // ---- rows in; those ahead of the sequence are zeros
-        for (int e = tid; e < AT_T * (PK / 4); e += 256) {
-            const int i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
-            float qf[4] = {0, 0, 0, 0}, kf[4] = {0, 0, 0, 0};
-            if (i >= lo && d < Dk) {
-                if (!CARRY) load4(qb + (long long)(t0 + i) * p.q.row, d, Dk, wq, qf);
-                load4(kb + (long long)(t0 + i) * p.k.row, d, Dk, wk, kf);
-            }
+    // A chunk's rows wait in registers while the chunk before is multiplied: four values of row
+    // (e / (P / 4)) each.
+    constexpr int NK = PK / 32, NV = PV / 32;
+    float qr[NK][4], kr[NK][4], vr[NV][4];
+    const auto first_row = [&](int idx) { return len - (p.back ? idx + 1 : chunks - idx) * AT_T; };
+    const auto fetch = [&](int t0) {
 #pragma unroll
-            for (int s = 0; s < 4; s++) {
-                if (!CARRY) {
-                    sm.qt[d + s][i] = qf[s];
-                    sm.kt[d + s][i] = kf[s];
-                }
-                sm.k[i][d + s] = kf[s];
-            }
+        for (int u = 0; u < NK; u++) {
+            const int e = tid + 256 * u, i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
+            const bool in = t0 + i >= 0 && d < Dk;  // rows ahead of the sequence are zeros
+#pragma unroll
+            for (int s = 0; s < 4; s++) qr[u][s] = kr[u][s] = 0.0f;
+            if (in && !CARRY) load4(qb + (long long)(t0 + i) * p.q.row, d, Dk, wq, qr[u]);
+            if (in) load4(kb + (long long)(t0 + i) * p.k.row, d, Dk, wk, kr[u]);
         }
-        for (int e = tid; e < AT_T * (PV / 4); e += 256) {
-            const int i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
-            float vf[4] = {0, 0, 0, 0};
-            if (i >= lo && d < Dv) load4(vb + (long long)(t0 + i) * p.v.row, d, Dv, wv, vf);
 #pragma unroll
-            for (int s = 0; s < 4; s++) sm.v[i][d + s] = vf[s];
+        for (int u = 0; u < NV; u++) {
+            const int e = tid + 256 * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
+#pragma unroll
+            for (int s = 0; s < 4; s++) vr[u][s] = 0.0f;
+            if (t0 + i >= 0 && d < Dv) load4(vb + (long long)(t0 + i) * p.v.row, d, Dv, wv, vr[u]);
+        }
+    };
+    if (c0 < c1) fetch(first_row(c0));
+
+    for (int idx = c0; idx < c1; idx++) {
+        const int t0 = first_row(idx), lo = t0 < 0 ? -t0 : 0;
+#pragma unroll
+        for (int u = 0; u < NK; u++) {
+            const int e = tid + 256 * u, i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
+            if (!CARRY) {
+#pragma unroll
+                for (int s = 0; s < 4; s++) {
+                    sm.qt[d + s][i] = qr[u][s];
+                    sm.kt[d + s][i] = kr[u][s];
+                }
+            }
+            *reinterpret_cast<float4*>(&sm.k[i][d]) = make_float4(kr[u][0], kr[u][1], kr[u][2], kr[u][3]);
+        }
+#pragma unroll
+        for (int u = 0; u < NV; u++) {
+            const int e = tid + 256 * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
+            *reinterpret_cast<float4*>(&sm.v[i][d]) = make_float4(vr[u][0], vr[u][1], vr[u][2], vr[u][3]);
         }
         if (tid < AT_T) sm.wj[tid] = tid < lo ? 0.0f : p.su * exp2f(l2 * (p.back ? tid - lo + 1 : AT_T - 1 - tid));
         __syncthreads();
+        if (idx + 1 < c1) fetch(first_row(idx + 1));
         if (!CARRY) {
             // ---- scores of rows 2 ty, + 1 on rows 2 tx, + 1
-            float s[2][2] = {};
-#pragma unroll 4
+            f32x2 s[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
+#pragma unroll 8
             for (int d = 0; d < Dk; d++) {
                 const float2 q2 = *reinterpret_cast<const float2*>(&sm.qt[d][2 * ty]);
-                const float2 k2 = *reinterpret_cast<const float2*>(&sm.kt[d][2 * tx]);
-                s[0][0] = fmaf(q2.x, k2.x, s[0][0]);
-                s[0][1] = fmaf(q2.x, k2.y, s[0][1]);
-                s[1][0] = fmaf(q2.y, k2.x, s[1][0]);
-                s[1][1] = fmaf(q2.y, k2.y, s[1][1]);
+                const f32x2 k2 = *reinterpret_cast<const f32x2*>(&sm.kt[d][2 * tx]);
+                s[0] = fma2(pk2(q2.x, q2.x), k2, s[0]);
+                s[1] = fma2(pk2(q2.y, q2.y), k2, s[1]);
             }
 #pragma unroll
-            for (int u = 0; u < 2; u++)
+            for (int u = 0; u < 2; u++) {
+                float sc[2];
+                unpk2(s[u], sc[0], sc[1]);
 #pragma unroll
                 for (int w = 0; w < 2; w++) {
                     const int i = 2 * ty + u, j = 2 * tx + w, n = p.back ? j - i : i - j;
-                    sm.pt[j][i] = n >= 0 ? s[u][w] * (p.si * exp2f(l2 * n)) : 0.0f;
+                    sm.pt[j][i] = n >= 0 ? sc[w] * (p.si * exp2f(l2 * n)) : 0.0f;
                 }
+            }
             // ---- rows on the state
-            float o[2][PV / 16];
+            f32x2 o[2][NV];
 #pragma unroll
-            for (int n = 0; n < PV / 16; n++) o[0][n] = o[1][n] = 0.0f;
-#pragma unroll 2
+            for (int n = 0; n < NV; n++) o[0][n] = o[1][n] = pk2(0.0f, 0.0f);
+#pragma unroll 4
             for (int d = 0; d < Dk; d++) {
                 const float2 q2 = *reinterpret_cast<const float2*>(&sm.qt[d][2 * ty]);
+                const f32x2 qa = pk2(q2.x, q2.x), qc = pk2(q2.y, q2.y);
 #pragma unroll
-                for (int n = 0; n < PV / 32; n++) {
-                    const float2 z2 = *reinterpret_cast<const float2*>(&sm.z[d][2 * tx + 32 * n]);
-                    o[0][2 * n] = fmaf(q2.x, z2.x, o[0][2 * n]);
-                    o[0][2 * n + 1] = fmaf(q2.x, z2.y, o[0][2 * n + 1]);
-                    o[1][2 * n] = fmaf(q2.y, z2.x, o[1][2 * n]);
-                    o[1][2 * n + 1] = fmaf(q2.y, z2.y, o[1][2 * n + 1]);
+                for (int n = 0; n < NV; n++) {
+                    const f32x2 z2 = *reinterpret_cast<const f32x2*>(&sm.z[d][2 * tx + 32 * n]);
+                    o[0][n] = fma2(qa, z2, o[0][n]);
+                    o[1][n] = fma2(qc, z2, o[1][n]);
                 }
             }
 #pragma unroll
@@ -133,20 +151,19 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
                 const int i = 2 * ty + u;
                 const float w = p.sx * exp2f(l2 * (p.back ? AT_T - 1 - i : i >= lo ? i - lo + 1 : 0));
 #pragma unroll
-                for (int n = 0; n < PV / 16; n++) o[u][n] *= w;
+                for (int n = 0; n < NV; n++) o[u][n] = mul2(o[u][n], pk2(w, w));
             }
             __syncthreads();
             // ---- and on the chunk's rows
-#pragma unroll 2
+#pragma unroll 4
             for (int j = 0; j < AT_T; j++) {
                 const float2 p2 = *reinterpret_cast<const float2*>(&sm.pt[j][2 * ty]);
+                const f32x2 pa = pk2(p2.x, p2.x), pc = pk2(p2.y, p2.y);
 #pragma unroll
-                for (int n = 0; n < PV / 32; n++) {
-                    const float2 v2 = *reinterpret_cast<const float2*>(&sm.v[j][2 * tx + 32 * n]);
-                    o[0][2 * n] = fmaf(p2.x, v2.x, o[0][2 * n]);
-                    o[0][2 * n + 1] = fmaf(p2.x, v2.y, o[0][2 * n + 1]);
-                    o[1][2 * n] = fmaf(p2.y, v2.x, o[1][2 * n]);
-                    o[1][2 * n + 1] = fmaf(p2.y, v2.y, o[1][2 * n + 1]);
+                for (int n = 0; n < NV; n++) {
+                    const f32x2 v2 = *reinterpret_cast<const f32x2*>(&sm.v[j][2 * tx + 32 * n]);
+                    o[0][n] = fma2(pa, v2, o[0][n]);
+                    o[1][n] = fma2(pc, v2, o[1][n]);
                 }
             }
 #pragma unroll
@@ -155,47 +172,44 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
                 if (i < lo) continue;
                 T* yr = yb + (long long)(t0 + i) * p.y.row;
 #pragma unroll
-                for (int n = 0; n < PV / 32; n++) {
+                for (int n = 0; n < NV; n++) {
                     const int m = 2 * tx + 32 * n;
-                    if (m < Dv) yr[m] = from_f<T>(o[u][2 * n]);
-                    if (m + 1 < Dv) yr[m + 1] = from_f<T>(o[u][2 * n + 1]);
+                    float f0, f1;
+                    unpk2(o[u][n], f0, f1);
+                    if (m < Dv) yr[m] = from_f<T>(f0);
+                    if (m + 1 < Dv) yr[m + 1] = from_f<T>(f1);
                 }
             }
         }
         // ---- the state behind the chunk: rows 2 ty + 32 r, + 1, columns 2 tx + 32 n, + 1
+        // (every row has read the state ahead of the barrier above)
         const float w = exp2f(l2 * (AT_T - lo));
+        const f32x2 ww = pk2(w, w);
 #pragma unroll
-        for (int r = 0; r < PK / 32; r++) {
-            float z[2][PV / 16];
+        for (int r = 0; r < NK; r++) {
+            f32x2 z[2][NV];
             const int m = 2 * ty + 32 * r;
 #pragma unroll
-            for (int n = 0; n < PV / 32; n++) {
-                const float2 a0 = *reinterpret_cast<const float2*>(&sm.z[m][2 * tx + 32 * n]);
-                const float2 a1 = *reinterpret_cast<const float2*>(&sm.z[m + 1][2 * tx + 32 * n]);
-                z[0][2 * n] = w * a0.x;
-                z[0][2 * n + 1] = w * a0.y;
-                z[1][2 * n] = w * a1.x;
-                z[1][2 * n + 1] = w * a1.y;
+            for (int n = 0; n < NV; n++) {
+                z[0][n] = mul2(ww, *reinterpret_cast<const f32x2*>(&sm.z[m][2 * tx + 32 * n]));
+                z[1][n] = mul2(ww, *reinterpret_cast<const f32x2*>(&sm.z[m + 1][2 * tx + 32 * n]));
             }
-#pragma unroll 2
+#pragma unroll 4
             for (int j = 0; j < AT_T; j++) {
                 const float f = sm.wj[j];
                 const float2 k2 = *reinterpret_cast<const float2*>(&sm.k[j][m]);
-                const float ka = k2.x * f, kc = k2.y * f;
+                const f32x2 ka = pk2(k2.x * f, k2.x * f), kc = pk2(k2.y * f, k2.y * f);
 #pragma unroll
-                for (int n = 0; n < PV / 32; n++) {
-                    const float2 v2 = *reinterpret_cast<const float2*>(&sm.v[j][2 * tx + 32 * n]);
-                    z[0][2 * n] = fmaf(ka, v2.x, z[0][2 * n]);
-                    z[0][2 * n + 1] = fmaf(ka, v2.y, z[0][2 * n + 1]);
-                    z[1][2 * n] = fmaf(kc, v2.x, z[1][2 * n]);
-                    z[1][2 * n + 1] = fmaf(kc, v2.y, z[1][2 * n + 1]);
+                for (int n = 0; n < NV; n++) {
+                    const f32x2 v2 = *reinterpret_cast<const f32x2*>(&sm.v[j][2 * tx + 32 * n]);
+                    z[0][n] = fma2(ka, v2, z[0][n]);
+                    z[1][n] = fma2(kc, v2, z[1][n]);
                 }
             }
-            // (every row has read the state ahead of the barrier above)
 #pragma unroll
-            for (int n = 0; n < PV / 32; n++) {
-                *reinterpret_cast<float2*>(&sm.z[m][2 * tx + 32 * n]) = make_float2(z[0][2 * n], z[0][2 * n + 1]);
-                *reinterpret_cast<float2*>(&sm.z[m + 1][2 * tx + 32 * n]) = make_float2(z[1][2 * n], z[1][2 * n + 1]);
+            for (int n = 0; n < NV; n++) {
+                *reinterpret_cast<f32x2*>(&sm.z[m][2 * tx + 32 * n]) = z[0][n];
+                *reinterpret_cast<f32x2*>(&sm.z[m + 1][2 * tx + 32 * n]) = z[1][n];
             }
         }
         __syncthreads();
