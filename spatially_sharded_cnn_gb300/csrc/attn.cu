@@ -7,33 +7,39 @@
 namespace hc {
 namespace {
 
-// One thread an element of the state: carry[seg], the sum of segment seg alone, becomes the
-// state ahead of it.  Eight segments' sums are read before the first is replaced.  Grid:
-// (pairs, elements of a state, passes).
+// One thread an element of the state: carry[s - 1] becomes the state ahead of segment s.
+// 32 cells' sums are read before the first is replaced (one after another, 32 segments took
+// 16 us for a load's latency each).  Grid: (pairs, elements of a state, passes).
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int T) {
     grid_begin();
     const AttnPass& p = a.p[blockIdx.z];
     if (!p.keep) return;
-    const int e = blockIdx.y * 256 + threadIdx.x, pair = blockIdx.x, size = p.Dk * p.Dv;
-    if (e >= size) return;
+    __shared__ float w[32];
+    const int e = blockIdx.y * 256 + threadIdx.x, pair = blockIdx.x, size = p.Dk * p.Dv, cells = a.cells();
+    const bool in = e < size;
     const int b = pair / a.H, h = pair - b * a.H;
-    const int len = attn_len(a.lens, b, a.L), chunks = (len + T - 1) / T;
+    const int len = attn_len(a.lens, b, a.L), chunks = (len + T - 1) / T, part = chunks * T - len;
     const float l2 = attn_log2_decay(a.decay, h);
-    float z = p.z0 ? p.z0[(long long)pair * size + e] : 0.0f;
-    float* c = p.carry + (long long)pair * a.segs * size + e;
-    const int part = chunks * T - len;  // rows that the chunk with the first row lacks
-    for (int s0 = 0; s0 < a.segs; s0 += 8) {
-        float own[8];
+    float z = in && p.z0 ? p.z0[(long long)pair * size + e] : 0.0f;
+    float* c = p.carry + (long long)pair * cells * size + e;
+    int cell = 0, seg = 0;
+    for (int s0 = 0; s0 < cells; s0 += 32) {
+        float own[32];
 #pragma unroll
-        for (int i = 0; i < 8; i++) own[i] = s0 + i < a.segs - 1 ? c[(long long)(s0 + i) * size] : 0.0f;
+        for (int i = 0; i < 32; i++) own[i] = in && s0 + i < cells ? c[(long long)(s0 + i) * size] : 0.0f;
+        __syncthreads();
+        if (threadIdx.x < 32 && s0 + (int)threadIdx.x < cells)
+            w[threadIdx.x] = attn_cell_decay(l2, a, s0 + threadIdx.x, chunks, T, part, p.back);
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < 32; i++) {
             const int s = s0 + i;
-            if (s >= a.segs) break;
-            const int c0 = min(chunks, s * a.per), c1 = min(chunks, c0 + a.per);
-            const bool first = c1 > c0 && (p.back ? c1 == chunks : c0 == 0);
-            c[(long long)s * size] = z;
-            z = fmaf(z, exp2f(l2 * ((c1 - c0) * T - (first ? part : 0))), own[i]);
+            if (s >= cells) break;
+            z = fmaf(z, w[i], own[i]);
+            if (++cell == a.split) {  // a segment ends
+                cell = 0;
+                if (in) c[(long long)seg++ * size] = z;
+            }
         }
     }
 }
@@ -117,23 +123,36 @@ bool attn_tc_rows(const hc_linear_attn_desc* d, const hc_rows* r) {
 }
 
 struct Cut {
-    int segs, per;
+    int segs, per, split, cell_per;
 };
-// Segments of a sequence: as many as give the GPU `passes` passes of blocks to fill it,
-// two chunks each at least.
-Cut attn_cut(const hc_linear_attn_desc* d, bool tc, int passes) {
+// Segments of a sequence: as many as give the GPU enough blocks to fill it in launches of
+// `passes` passes, two chunks each at least; then cells, so that the carry pass, which the last
+// segments are no part of, fills it too.
+Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd) {
     const int T = tc ? AT_TC : AT_T, per_sm = tc ? d->Dk > 64 || d->Dv > 64 ? 1 : 2 : d->Dk > 96 && d->Dv > 64 ? 2 : 3;
-    const long long pairs = (long long)d->B * d->H * passes, want = (long long)per_sm * device_sm_count();
+    const int pad = tc ? 64 : 32;
+    // (passes of another shape are another launch)
+    const int passes = bwd && cdiv(d->Dk, pad) == cdiv(d->Dv, pad) ? 3 : 1, kept = passes == 3 ? 2 : 1;
+    const long long pairs = (long long)d->B * d->H, want = (long long)per_sm * device_sm_count();
     const int chunks = (int)(((long long)d->L + T - 1) / T);
-    long long segs = pairs < want ? want / pairs : 1;
+    long long segs = pairs * passes < want ? want / (pairs * passes) : 1;
     if (segs > chunks / 2) segs = chunks / 2;
     if (segs < 1) segs = 1;
     const int per = (int)((chunks + segs - 1) / segs);
-    return {per > 0 ? (chunks + per - 1) / per : 1, per};
+    Cut c = {per > 0 ? (chunks + per - 1) / per : 1, per, 1, per};
+    if (c.segs > 1) {
+        long long split = want / (pairs * kept * (c.segs - 1));
+        if (split > per) split = per;
+        if (split > 1) {
+            c.cell_per = (int)((per + split - 1) / split);
+            c.split = (per + c.cell_per - 1) / c.cell_per;
+        }
+    }
+    return c;
 }
 
 size_t carry_floats(const hc_linear_attn_desc* d, const Cut& c) {
-    return c.segs > 1 ? (size_t)d->B * d->H * c.segs * d->Dk * d->Dv : 0;
+    return (size_t)d->B * d->H * (c.segs - 1) * c.split * d->Dk * d->Dv;
 }
 
 AttnArgs attn_args(const hc_linear_attn_desc* d, const float* decay, const int* lens, const Cut& c) {
@@ -146,13 +165,16 @@ AttnArgs attn_args(const hc_linear_attn_desc* d, const float* decay, const int* 
     a.dtype = d->dtype;
     a.segs = c.segs;
     a.per = c.per;
+    a.split = c.split;
+    a.cell_per = c.cell_per;
     return a;
 }
 
 hc_status attn_run(const AttnArgs& a, bool tc, cudaStream_t st) {
     const auto launch = tc ? launch_attn_tc : launch_attn_fp32;
     hc_status e = HC_OK;
-    if (a.segs > 1 && ((e = launch(a, true, st)) || (e = launch_attn_join(a, tc ? AT_TC : AT_T, st)))) return e;
+    if (a.segs > 1 && (e = launch(a, true, st))) return e;
+    if (a.cells() > kFewCells && (e = launch_attn_join(a, tc ? AT_TC : AT_T, st))) return e;
     return launch(a, false, st);
 }
 
@@ -171,14 +193,14 @@ using namespace hc;
 
 extern "C" {
 
-// Segments' states: of S forward; of S and of G backward; whichever way the rows of the
+// Cells' sums: of S forward; of S and of G backward; whichever way the rows of the
 // call let it run.
 hc_status hc_linear_attn_workspace_size(const hc_linear_attn_desc* d, int pass, size_t* bytes) {
     if (!attn_desc_ok(d) || pass < 0 || pass > 1 || !bytes) return HC_ERR_INVALID_ARG;
     if (!attn_size_ok(d)) return HC_ERR_UNSUPPORTED;
     size_t n = 0;
     for (int tc = 0; tc <= (int)attn_tc_sizes(d); tc++) {
-        const size_t f = carry_floats(d, attn_cut(d, tc, 1)), b = pass ? 2 * carry_floats(d, attn_cut(d, tc, 3)) : 0;
+        const size_t f = carry_floats(d, attn_cut(d, tc, false)), b = pass ? 2 * carry_floats(d, attn_cut(d, tc, true)) : 0;
         n = n > f ? n : f;
         n = n > b ? n : b;
     }
@@ -202,7 +224,7 @@ hc_status hc_linear_attn_fwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     traced_begin(st);
     bool tc = attn_tc_sizes(d);
     for (const hc_rows* r : {q, k, v, y}) tc = tc && attn_tc_rows(d, r);
-    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, 1));
+    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, false));
     a.passes = 1;
     a.p[0] = {*q, *k, *v, *y, d->Dk, d->Dv, d->scale, d->scale, 1.0f, 0, h0, hT, d->Dv, 1,
               a.segs > 1 ? (float*)ws : nullptr, 1};
@@ -232,11 +254,12 @@ hc_status hc_linear_attn_bwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     traced_begin(st);
     bool tc = attn_tc_sizes(d);
     for (const hc_rows* r : {q, k, v, gy, gq, gk, gv}) tc = tc && attn_tc_rows(d, r);
-    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, 3));
+    const Cut cut = attn_cut(d, tc, true);
+    AttnArgs a = attn_args(d, log_decay, lens, cut);
     float *cs = nullptr, *cg = nullptr;
     if (a.segs > 1) {
         cs = (float*)ws;
-        cg = cs + carry_floats(d, {a.segs, a.per});
+        cg = cs + carry_floats(d, cut);
     }
     const float s = d->scale;
     // the states of gv's pass are those of gk's, transposed; S comes from k and v, whose

@@ -17,8 +17,10 @@
 // (a row j of the sum is then a later row, whose gradient it carries back).
 //
 // Where sequences times heads leave the GPU idle, a sequence's chunks are cut into
-// segments: every segment's own sum of k v^T but the last one's (the carry pass), a join in
-// order, and then all segments at once, each from the state ahead of it.
+// segments, and the segments but the last into cells: every cell's own sum of k v^T (the
+// carry pass), and then all segments at once, each from the state ahead of it, which it adds up
+// from the cells, in order, where they are few, and finds joined (attn_join_kernel) where they
+// are many.
 #pragma once
 
 #include "rows.cuh"
@@ -35,9 +37,10 @@ struct AttnPass {
     const float* z0;    // the state ahead of the first chunk, element (m, n) of pair p at p * Dk * Dv + m * zm + n * zn
     float* z1;          // where the state behind the last chunk goes, laid out so; NULL: nowhere
     int zm, zn;
-    float* carry;       // segments' states [pair][seg], laid out so; NULL: one segment
+    float* carry;       // cells' sums [pair][cell], laid out so; NULL: one segment
     int keep;           // the carry pass fills `carry` from this pass's k and v (su in them)
 };
+constexpr int kFewCells = 4;  // that a segment adds up itself (8 x 4096 x 8 heads of 128: a join of 2 took 20 us)
 
 struct AttnArgs {
     AttnPass p[3];
@@ -45,7 +48,9 @@ struct AttnArgs {
     const float* decay;
     const int* lens;
     int B, L, H, dtype;
-    int segs, per;  // segments of a sequence, chunks of a segment
+    int segs, per;         // segments of a sequence, chunks of a segment
+    int split, cell_per;   // cells of a segment, chunks of a cell (split * cell_per = per)
+    __host__ __device__ int cells() const { return (segs - 1) * split; }  // of a sequence
 };
 
 __host__ __device__ inline int attn_len(const int* lens, int b, int L) {
@@ -57,6 +62,52 @@ __device__ __forceinline__ float attn_log2_decay(const float* decay, int h) {
     if (!decay) return 0.0f;
     const float a = decay[h];
     return (a < kLowDecay ? kLowDecay : a) * kLog2e;
+}
+
+// What a state loses over cell c of a sequence of `chunks` chunks of T rows: lambda^rows.
+// `part`: rows that the chunk with the first row lacks.
+__device__ __forceinline__ float attn_cell_decay(float l2, const AttnArgs& a, int c, int chunks, int T, int part,
+                                                 int back) {
+    const int seg = c / a.split, c0 = min(chunks, seg * a.per + (c - seg * a.split) * a.cell_per);
+    const int c1 = min(chunks, min(c0 + a.cell_per, (seg + 1) * a.per));
+    const bool first = c1 > c0 && (back ? c1 == chunks : c0 == 0);
+    return exp2f(l2 * (float)((c1 - c0) * T - (first ? part : 0)));
+}
+// The state ahead of segment seg, N elements of it a thread: `at` gives element i's place in
+// the array (below 0: none).  The loads of all elements are under way at once: none is
+// behind a branch (that took 40 us of 80 on 8 x 4096 x 8 heads of 128).
+template <int N, typename F>
+__device__ __forceinline__ void attn_state_ahead(const AttnPass& p, const AttnArgs& a, long long pair, int seg, float l2,
+                                                 int chunks, int T, int part, F&& at, float (&z)[N]) {
+    const long long size = (long long)p.Dk * p.Dv;
+    const bool joined = seg > 0 && a.cells() > kFewCells;
+    const float* from = joined ? p.carry + (pair * a.cells() + seg - 1) * size : p.z0 ? p.z0 + pair * size : nullptr;
+    int place[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        place[i] = max(at(i), 0);
+        z[i] = 0.0f;
+    }
+    if (from) {
+#pragma unroll
+        for (int i = 0; i < N; i++) z[i] = from[place[i]];
+    }
+    if (joined) {
+#pragma unroll
+        for (int i = 0; i < N; i++) z[i] = at(i) >= 0 ? z[i] : 0.0f;
+        return;
+    }
+    for (int c = 0; c < seg * a.split; c++) {
+        const float w = attn_cell_decay(l2, a, c, chunks, T, part, p.back);
+        const float* own = p.carry + (pair * a.cells() + c) * size;
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = own[place[i]];
+#pragma unroll
+        for (int i = 0; i < N; i++) z[i] = fmaf(z[i], w, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) z[i] = at(i) >= 0 ? z[i] : 0.0f;
 }
 
 // Rows past the sequence's end: zeros, a share for each of `segs` blocks.
@@ -93,7 +144,7 @@ template <typename F> hc_status attn_by_shape(const AttnArgs& all, bool carry, F
 constexpr int AT_T = 32, AT_TC = 128;
 hc_status launch_attn_fp32(const AttnArgs& a, bool carry, cudaStream_t st);
 hc_status launch_attn_tc(const AttnArgs& a, bool carry, cudaStream_t st);
-// Segments joined in order, in place: carry[seg] becomes the state ahead of it.
+// Cells joined in order, in place: carry[s - 1] becomes the state ahead of segment s.
 hc_status launch_attn_join(const AttnArgs& a, int T, cudaStream_t st);
 
 }  // namespace hc

@@ -37,12 +37,12 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
     AttnSmem<PK, PV>& sm = *reinterpret_cast<AttnSmem<PK, PV>*>(raw);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const AttnPass& p = a.p[blockIdx.y];
-    const int seg = blockIdx.x % a.segs, pair = blockIdx.x / a.segs;
-    const bool last = seg == a.segs - 1;
-    if (CARRY && last) return;  // its state is the pass's own
+    const int runs = CARRY ? a.cells() : a.segs, run = blockIdx.x % runs, pair = blockIdx.x / runs;  // a cell or a segment
+    const int seg = CARRY ? run / a.split : run;
     const int b = pair / a.H, h = pair - b * a.H;
     const int len = attn_len(a.lens, b, a.L), chunks = (len + AT_T - 1) / AT_T;
-    const int c0 = min(chunks, seg * a.per), c1 = min(chunks, c0 + a.per);
+    const int c0 = min(chunks, seg * a.per + (CARRY ? run - seg * a.split : 0) * a.cell_per);
+    const int c1 = min(chunks, min(CARRY ? c0 + a.cell_per : 0x7fffffff, (seg + 1) * a.per));
     const float l2 = attn_log2_decay(a.decay, h);
     const int Dk = p.Dk, Dv = p.Dv;
     const long long zsize = (long long)Dk * Dv;
@@ -56,12 +56,18 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
     const bool wq = wide4(p.q, Dk), wk = wide4(p.k, Dk), wv = wide4(p.v, Dv);
 
     // the state ahead of the segment
-    const float* z0 = CARRY ? nullptr : p.carry ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                                      : p.z0    ? p.z0 + pair * zsize
-                                                : nullptr;
-    for (int e = tid; e < PK * PV; e += 256) {
-        const int m = e / PV, n = e - m * PV;
-        sm.z[m][n] = z0 && m < Dk && n < Dv ? z0[(long long)m * p.zm + (long long)n * p.zn] : 0.0f;
+    for (int e0 = 0; e0 < PK * PV; e0 += 256 * 16) {
+        float z[16] = {};
+        const auto place = [&](int i) {
+            const int e = e0 + tid + 256 * i, m = e / PV, n = e - m * PV;
+            return e < PK * PV && m < Dk && n < Dv ? m * p.zm + n * p.zn : -1;
+        };
+        if (!CARRY) attn_state_ahead<16>(p, a, pair, seg, l2, chunks, AT_T, chunks * AT_T - len, place, z);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const int e = e0 + tid + 256 * i;
+            if (e < PK * PV) sm.z[e / PV][e % PV] = z[i];
+        }
     }
 
     // A chunk's rows wait in registers while the chunk before is multiplied: four values of row
@@ -215,8 +221,8 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
         __syncthreads();
     }
     if (c0 == c1) __syncthreads();  // the state as it was loaded
-    float* z1 = CARRY ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                      : p.z1 && last ? p.z1 + pair * zsize
+    float* z1 = CARRY ? p.carry + ((long long)pair * runs + run) * zsize
+                      : p.z1 && seg == a.segs - 1 ? p.z1 + pair * zsize
                                             : nullptr;
     if (z1)
         for (int e = tid; e < PK * PV; e += 256) {
@@ -235,7 +241,7 @@ template <typename T, int PK, int PV> hc_status launch_pads(const AttnArgs& a, b
                cudaFuncSetAttribute(attn_fp32_kernel<T, PK, PV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     smem) == cudaSuccess;
     });
-    const dim3 grid((unsigned)((long long)a.B * a.H * a.segs), a.passes);
+    const dim3 grid((unsigned)((long long)a.B * a.H * (carry ? a.cells() : a.segs)), a.passes);
     if (carry)
         launch_next(attn_fp32_kernel<T, PK, PV, true>, grid, dim3(256), smem, st, a);
     else

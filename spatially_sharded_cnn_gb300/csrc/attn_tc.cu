@@ -106,22 +106,24 @@ __device__ __forceinline__ void split_pair(uint32_t v, f32x2 w, uint32_t& p0, ui
     p2 = narrow(fma2(widen(p1), minus, f));
 }
 
-struct Unit {  // a segment of one (sequence, head) of one pass
-    int ip, seg, pair, b, h, len, chunks, c0, count;
+struct Unit {  // a segment (or, carrying, a cell) of one (sequence, head) of one pass
+    int ip, seg, run, pair, b, h, len, chunks, c0, count;
 };
 template <bool CARRY> __device__ __forceinline__ Unit unit_of(const AttnArgs& a, long long u) {
     Unit r;
     r.ip = (int)(u % a.passes);
     const int rest = (int)(u / a.passes);
-    r.seg = rest % a.segs;
-    r.pair = rest / a.segs;
+    const int runs = CARRY ? a.cells() : a.segs;
+    r.run = rest % runs;
+    r.seg = CARRY ? r.run / a.split : r.run;
+    r.pair = rest / runs;
     r.b = r.pair / a.H;
     r.h = r.pair - r.b * a.H;
     r.len = attn_len(a.lens, r.b, a.L);
     r.chunks = (r.len + TT - 1) / TT;
-    r.c0 = min(r.chunks, r.seg * a.per);
-    r.count = min(r.chunks, r.c0 + a.per) - r.c0;
-    if (CARRY && r.seg == a.segs - 1) r.count = 0;  // its state is the pass's own
+    r.c0 = min(r.chunks, r.seg * a.per + (CARRY ? r.run - r.seg * a.split : 0) * a.cell_per);
+    r.count = min(r.chunks, min(CARRY ? r.c0 + a.cell_per : 0x7fffffff, (r.seg + 1) * a.per)) - r.c0;
+    if (r.count < 0) r.count = 0;
     return r;
 }
 
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
     const auto buf_z = [&](int s) { return S::pair && s ? sx + S::x - S::z : sx; };
 
     // ---- copies, two chunks ahead, over the ends of units, by warp `mover`
-    const long long units = (long long)a.B * a.H * a.segs * a.passes;
+    const long long units = (long long)a.B * a.H * (CARRY ? a.cells() : a.segs) * a.passes;
     long long lu = blockIdx.x;  // the unit and chunk to load next, and how many were loaded
     int lit = 0, loaded = 0;
     Unit ln = unit_of<CARRY>(a, lu < units ? lu : 0);
@@ -205,8 +207,6 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         const int Dk = p.Dk, Dv = p.Dv, back = p.back;
         const float l2 = attn_log2_decay(a.decay, h);
         const long long zsize = (long long)Dk * Dv;
-        const bool last = seg == a.segs - 1;
-        if (CARRY && last) continue;
         // the warp whose rows have no scores in its column blocks moves data meanwhile
         const int mover = back ? 3 : 4;
         if (!CARRY && warp == 1) {
@@ -222,16 +222,12 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         const int zn = row % DV, zm = (DV == 64 ? half + 2 * (quarter >> 1) : half) * ZC;
         f32x2 z[ZC / 2];
         {
-            const float* z0 = CARRY ? nullptr : p.carry ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                                              : p.z0    ? p.z0 + pair * zsize
-                                                        : nullptr;
+            float z0[ZC] = {};
+            const auto place = [&](int i) { return zm + i < Dk && zn < Dv ? (zm + i) * p.zm + zn * p.zn : -1; };
+            if (!CARRY)
+                attn_state_ahead<ZC>(p, a, pair, seg, l2, u.chunks, TT, u.chunks * TT - len, place, z0);
 #pragma unroll
-            for (int i = 0; i < ZC; i += 2) {
-                const int m = zm + i;  // Dk is even
-                const bool in = z0 && m < Dk && zn < Dv;
-                const float* zp = z0 + (long long)m * p.zm + (long long)zn * p.zn;
-                z[i / 2] = in ? pk2(zp[0], zp[p.zm]) : pk2(0.0f, 0.0f);
-            }
+            for (int i = 0; i < ZC; i += 2) z[i / 2] = pk2(z0[i], z0[i + 1]);
         }
         const auto put_state = [&](int s) {
             if (CARRY) return;
@@ -528,8 +524,8 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
             __syncwarp();
         }
 
-        float* z1 = CARRY ? p.carry + ((long long)pair * a.segs + seg) * zsize
-                          : p.z1 && last ? p.z1 + pair * zsize
+        float* z1 = CARRY ? p.carry + ((long long)pair * a.cells() + u.run) * zsize
+                          : p.z1 && seg == a.segs - 1 ? p.z1 + pair * zsize
                                                 : nullptr;
         if (z1 && zn < Dv) {
 #pragma unroll
@@ -583,7 +579,7 @@ template <int DK, int DV> hc_status launch_shape(const AttnArgs& a, bool carry, 
             (e = rows_map(&m.v[i], a.p[i].v, a.p[i].Dv, a)))
             return e;
     }
-    const long long units = (long long)a.B * a.H * a.segs * a.passes, most = (long long)S::per_sm * device_sm_count();
+    const long long units = (long long)a.B * a.H * (carry ? a.cells() : a.segs) * a.passes, most = (long long)S::per_sm * device_sm_count();
     const dim3 grid((unsigned)(units < most ? units : most));
     if (carry)
         launch_next(attn_tc_kernel<DK, DV, true>, grid, dim3(256), S::smem, st, m, a);
