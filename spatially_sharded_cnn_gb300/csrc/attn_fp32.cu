@@ -2,23 +2,47 @@
 // every type, head sizes up to 128 and any strides.
 //
 // A block walks over one segment of one (sequence, head): 32 rows of q, k and v go to
-// shared memory, the state stays there, and 16 x 16 threads take each of the four
-// products in register tiles, two values an instruction.  Bound by the multiply-adds and the shared-memory reads
-// that feed them.
+// shared memory, the state stays there, and 8 x 16 threads take each of the four products in
+// register tiles of 4 rows x pairs of columns, four steps of the sum at a time (one 16-byte read
+// a row serves all of a thread's columns).  Bound by the multiply-adds, two an instruction, and the
+// shared-memory reads that feed them.
 #include "attn.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int TP = AT_T + 2;  // pitch of a transposed tile: pairs of rows stay aligned
+constexpr int FT = 128;  // threads of a block
 
+// Pitches keep rows on 16 bytes and spread neighbours over the banks.
 template <int PK, int PV> struct AttnSmem {
-    alignas(16) float k[AT_T][PK], v[AT_T][PV];
+    alignas(16) float q[AT_T][PK + 4];
+    float k[AT_T][PK + 4];
+    float v[AT_T][PV];
     float z[PK][PV];
-    float qt[PK][TP], kt[PK][TP];  // transposed
-    float pt[AT_T][TP];            // scores, transposed: [j][i]
-    float wj[AT_T];                // what row j weighs in the state
+    float p[AT_T][AT_T + 4];  // scores
+    float wj[AT_T];           // what row j weighs in the state
 };
+
+// acc[r][n] += a[r][0 .. 3] . b[0 .. 3][n]: rows of `a` in shared memory, `pitch` floats apart,
+// four rows of `b` (`step` floats apart) of which a thread takes the pairs 32 columns apart.
+template <int R, int N> __device__ __forceinline__ void mul4(f32x2 (&acc)[R][N], const float* a, int pitch, const float* b, int step) {
+    float4 x[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) x[r] = *reinterpret_cast<const float4*>(a + r * pitch);
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        f32x2 y[N];
+#pragma unroll
+        for (int n = 0; n < N; n++) y[n] = *reinterpret_cast<const f32x2*>(b + u * step + 32 * n);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const float f = u == 0 ? x[r].x : u == 1 ? x[r].y : u == 2 ? x[r].z : x[r].w;
+            const f32x2 ff = pk2(f, f);
+#pragma unroll
+            for (int n = 0; n < N; n++) acc[r][n] = fma2(ff, y[n], acc[r][n]);
+        }
+    }
+}
 
 // Four elements of a row from channel c on, zeros past D.
 template <typename T> __device__ __forceinline__ void load4(const T* row, int c, int D, bool wide, float (&f)[4]) {
@@ -31,7 +55,7 @@ template <typename T> __device__ __forceinline__ void load4(const T* row, int c,
 }
 
 template <typename T, int PK, int PV, bool CARRY>
-__global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
     grid_begin();
     extern __shared__ __align__(16) unsigned char raw[];
     AttnSmem<PK, PV>& sm = *reinterpret_cast<AttnSmem<PK, PV>*>(raw);
@@ -56,29 +80,29 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
     const bool wq = wide4(p.q, Dk), wk = wide4(p.k, Dk), wv = wide4(p.v, Dv);
 
     // the state ahead of the segment
-    for (int e0 = 0; e0 < PK * PV; e0 += 256 * 16) {
+    for (int e0 = 0; e0 < PK * PV; e0 += FT * 16) {
         float z[16] = {};
         const auto place = [&](int i) {
-            const int e = e0 + tid + 256 * i, m = e / PV, n = e - m * PV;
+            const int e = e0 + tid + FT * i, m = e / PV, n = e - m * PV;
             return e < PK * PV && m < Dk && n < Dv ? m * p.zm + n * p.zn : -1;
         };
         if (!CARRY) attn_state_ahead<16>(p, a, pair, seg, l2, chunks, AT_T, chunks * AT_T - len, place, z);
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-            const int e = e0 + tid + 256 * i;
+            const int e = e0 + tid + FT * i;
             if (e < PK * PV) sm.z[e / PV][e % PV] = z[i];
         }
     }
 
     // A chunk's rows wait in registers while the chunk before is multiplied: four values of row
     // (e / (P / 4)) each.
-    constexpr int NK = PK / 32, NV = PV / 32;
+    constexpr int NK = PK / 16, NV = PV / 16;
     float qr[NK][4], kr[NK][4], vr[NV][4];
     const auto first_row = [&](int idx) { return len - (p.back ? idx + 1 : chunks - idx) * AT_T; };
     const auto fetch = [&](int t0) {
 #pragma unroll
         for (int u = 0; u < NK; u++) {
-            const int e = tid + 256 * u, i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
+            const int e = tid + FT * u, i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
             const bool in = t0 + i >= 0 && d < Dk;  // rows ahead of the sequence are zeros
 #pragma unroll
             for (int s = 0; s < 4; s++) qr[u][s] = kr[u][s] = 0.0f;
@@ -87,7 +111,7 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int u = 0; u < NV; u++) {
-            const int e = tid + 256 * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
+            const int e = tid + FT * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
 #pragma unroll
             for (int s = 0; s < 4; s++) vr[u][s] = 0.0f;
             if (t0 + i >= 0 && d < Dv) load4(vb + (long long)(t0 + i) * p.v.row, d, Dv, wv, vr[u]);
@@ -95,90 +119,77 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
     };
     if (c0 < c1) fetch(first_row(c0));
 
+    constexpr int N = PV / 32;  // pairs of columns 2 tx + 32 n, + 1
+    const f32x2 none = pk2(0.0f, 0.0f);
     for (int idx = c0; idx < c1; idx++) {
         const int t0 = first_row(idx), lo = t0 < 0 ? -t0 : 0;
 #pragma unroll
         for (int u = 0; u < NK; u++) {
-            const int e = tid + 256 * u, i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
-            if (!CARRY) {
-#pragma unroll
-                for (int s = 0; s < 4; s++) {
-                    sm.qt[d + s][i] = qr[u][s];
-                    sm.kt[d + s][i] = kr[u][s];
-                }
-            }
+            const int e = tid + FT * u, i = e / (PK / 4), d = (e - i * (PK / 4)) * 4;
+            if (!CARRY) *reinterpret_cast<float4*>(&sm.q[i][d]) = make_float4(qr[u][0], qr[u][1], qr[u][2], qr[u][3]);
             *reinterpret_cast<float4*>(&sm.k[i][d]) = make_float4(kr[u][0], kr[u][1], kr[u][2], kr[u][3]);
         }
 #pragma unroll
         for (int u = 0; u < NV; u++) {
-            const int e = tid + 256 * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
+            const int e = tid + FT * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
             *reinterpret_cast<float4*>(&sm.v[i][d]) = make_float4(vr[u][0], vr[u][1], vr[u][2], vr[u][3]);
         }
         if (tid < AT_T) sm.wj[tid] = tid < lo ? 0.0f : p.su * exp2f(l2 * (p.back ? tid - lo + 1 : AT_T - 1 - tid));
         __syncthreads();
         if (idx + 1 < c1) fetch(first_row(idx + 1));
         if (!CARRY) {
-            // ---- scores of rows 2 ty, + 1 on rows 2 tx, + 1
-            f32x2 s[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
-#pragma unroll 8
-            for (int d = 0; d < Dk; d++) {
-                const float2 q2 = *reinterpret_cast<const float2*>(&sm.qt[d][2 * ty]);
-                const f32x2 k2 = *reinterpret_cast<const f32x2*>(&sm.kt[d][2 * tx]);
-                s[0] = fma2(pk2(q2.x, q2.x), k2, s[0]);
-                s[1] = fma2(pk2(q2.y, q2.y), k2, s[1]);
+            // ---- scores of rows 4 ty .. on rows 2 tx, + 1
+            float s[4][2] = {};
+#pragma unroll 4
+            for (int d = 0; d < Dk; d += 4) {
+                float4 k2[2];
+#pragma unroll
+                for (int w = 0; w < 2; w++) k2[w] = *reinterpret_cast<const float4*>(&sm.k[2 * tx + w][d]);
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[4 * ty + u][d]);
+#pragma unroll
+                    for (int w = 0; w < 2; w++)
+                        s[u][w] = fmaf(q4.x, k2[w].x, fmaf(q4.y, k2[w].y, fmaf(q4.z, k2[w].z, fmaf(q4.w, k2[w].w, s[u][w]))));
+                }
             }
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-                float sc[2];
-                unpk2(s[u], sc[0], sc[1]);
+            for (int u = 0; u < 4; u++) {
+                const int i = 4 * ty + u, j = 2 * tx;
+                float f[2];
 #pragma unroll
                 for (int w = 0; w < 2; w++) {
-                    const int i = 2 * ty + u, j = 2 * tx + w, n = p.back ? j - i : i - j;
-                    sm.pt[j][i] = n >= 0 ? sc[w] * (p.si * exp2f(l2 * n)) : 0.0f;
+                    const int n = p.back ? j + w - i : i - j - w;
+                    f[w] = n >= 0 ? s[u][w] * (p.si * exp2f(l2 * n)) : 0.0f;
                 }
+                *reinterpret_cast<float2*>(&sm.p[i][j]) = make_float2(f[0], f[1]);
             }
             // ---- rows on the state
-            f32x2 o[2][NV];
+            f32x2 o[4][N];
 #pragma unroll
-            for (int n = 0; n < NV; n++) o[0][n] = o[1][n] = pk2(0.0f, 0.0f);
-#pragma unroll 4
-            for (int d = 0; d < Dk; d++) {
-                const float2 q2 = *reinterpret_cast<const float2*>(&sm.qt[d][2 * ty]);
-                const f32x2 qa = pk2(q2.x, q2.x), qc = pk2(q2.y, q2.y);
+            for (int u = 0; u < 4; u++)
 #pragma unroll
-                for (int n = 0; n < NV; n++) {
-                    const f32x2 z2 = *reinterpret_cast<const f32x2*>(&sm.z[d][2 * tx + 32 * n]);
-                    o[0][n] = fma2(qa, z2, o[0][n]);
-                    o[1][n] = fma2(qc, z2, o[1][n]);
-                }
-            }
+                for (int n = 0; n < N; n++) o[u][n] = none;
+#pragma unroll 2
+            for (int d = 0; d < Dk; d += 4) mul4<4, N>(o, &sm.q[4 * ty][d], PK + 4, &sm.z[d][2 * tx], PV);
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-                const int i = 2 * ty + u;
+            for (int u = 0; u < 4; u++) {
+                const int i = 4 * ty + u;
                 const float w = p.sx * exp2f(l2 * (p.back ? AT_T - 1 - i : i >= lo ? i - lo + 1 : 0));
 #pragma unroll
-                for (int n = 0; n < NV; n++) o[u][n] = mul2(o[u][n], pk2(w, w));
+                for (int n = 0; n < N; n++) o[u][n] = mul2(o[u][n], pk2(w, w));
             }
             __syncthreads();
             // ---- and on the chunk's rows
-#pragma unroll 4
-            for (int j = 0; j < AT_T; j++) {
-                const float2 p2 = *reinterpret_cast<const float2*>(&sm.pt[j][2 * ty]);
-                const f32x2 pa = pk2(p2.x, p2.x), pc = pk2(p2.y, p2.y);
+#pragma unroll 2
+            for (int j = 0; j < AT_T; j += 4) mul4<4, N>(o, &sm.p[4 * ty][j], AT_T + 4, &sm.v[j][2 * tx], PV);
 #pragma unroll
-                for (int n = 0; n < NV; n++) {
-                    const f32x2 v2 = *reinterpret_cast<const f32x2*>(&sm.v[j][2 * tx + 32 * n]);
-                    o[0][n] = fma2(pa, v2, o[0][n]);
-                    o[1][n] = fma2(pc, v2, o[1][n]);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; u++) {
-                const int i = 2 * ty + u;
+            for (int u = 0; u < 4; u++) {
+                const int i = 4 * ty + u;
                 if (i < lo) continue;
                 T* yr = yb + (long long)(t0 + i) * p.y.row;
 #pragma unroll
-                for (int n = 0; n < NV; n++) {
+                for (int n = 0; n < N; n++) {
                     const int m = 2 * tx + 32 * n;
                     float f0, f1;
                     unpk2(o[u][n], f0, f1);
@@ -187,36 +198,35 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
                 }
             }
         }
-        // ---- the state behind the chunk: rows 2 ty + 32 r, + 1, columns 2 tx + 32 n, + 1
+        // ---- the state behind the chunk: rows 4 ty .. + 32 r
         // (every row has read the state ahead of the barrier above)
         const float w = exp2f(l2 * (AT_T - lo));
         const f32x2 ww = pk2(w, w);
 #pragma unroll
-        for (int r = 0; r < NK; r++) {
-            f32x2 z[2][NV];
-            const int m = 2 * ty + 32 * r;
+        for (int r = 0; r < PK / 32; r++) {
+            f32x2 z[4][N];
+            const int m = 4 * ty + 32 * r;
 #pragma unroll
-            for (int n = 0; n < NV; n++) {
-                z[0][n] = mul2(ww, *reinterpret_cast<const f32x2*>(&sm.z[m][2 * tx + 32 * n]));
-                z[1][n] = mul2(ww, *reinterpret_cast<const f32x2*>(&sm.z[m + 1][2 * tx + 32 * n]));
-            }
+            for (int u = 0; u < 4; u++)
+#pragma unroll
+                for (int n = 0; n < N; n++) z[u][n] = mul2(ww, *reinterpret_cast<const f32x2*>(&sm.z[m + u][2 * tx + 32 * n]));
 #pragma unroll 4
             for (int j = 0; j < AT_T; j++) {
                 const float f = sm.wj[j];
-                const float2 k2 = *reinterpret_cast<const float2*>(&sm.k[j][m]);
-                const f32x2 ka = pk2(k2.x * f, k2.x * f), kc = pk2(k2.y * f, k2.y * f);
+                const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[j][m]);
+                const float kw[4] = {k4.x * f, k4.y * f, k4.z * f, k4.w * f};
+                f32x2 v2[N];
 #pragma unroll
-                for (int n = 0; n < NV; n++) {
-                    const f32x2 v2 = *reinterpret_cast<const f32x2*>(&sm.v[j][2 * tx + 32 * n]);
-                    z[0][n] = fma2(ka, v2, z[0][n]);
-                    z[1][n] = fma2(kc, v2, z[1][n]);
-                }
+                for (int n = 0; n < N; n++) v2[n] = *reinterpret_cast<const f32x2*>(&sm.v[j][2 * tx + 32 * n]);
+#pragma unroll
+                for (int u = 0; u < 4; u++)
+#pragma unroll
+                    for (int n = 0; n < N; n++) z[u][n] = fma2(pk2(kw[u], kw[u]), v2[n], z[u][n]);
             }
 #pragma unroll
-            for (int n = 0; n < NV; n++) {
-                *reinterpret_cast<f32x2*>(&sm.z[m][2 * tx + 32 * n]) = z[0][n];
-                *reinterpret_cast<f32x2*>(&sm.z[m + 1][2 * tx + 32 * n]) = z[1][n];
-            }
+            for (int u = 0; u < 4; u++)
+#pragma unroll
+                for (int n = 0; n < N; n++) *reinterpret_cast<f32x2*>(&sm.z[m + u][2 * tx + 32 * n]) = z[u][n];
         }
         __syncthreads();
     }
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(256) attn_fp32_kernel(AttnArgs a) {
                       : p.z1 && seg == a.segs - 1 ? p.z1 + pair * zsize
                                             : nullptr;
     if (z1)
-        for (int e = tid; e < PK * PV; e += 256) {
+        for (int e = tid; e < PK * PV; e += FT) {
             const int m = e / PV, n = e - m * PV;
             if (m < Dk && n < Dv) z1[(long long)m * p.zm + (long long)n * p.zn] = sm.z[m][n];
         }
@@ -243,9 +253,9 @@ template <typename T, int PK, int PV> hc_status launch_pads(const AttnArgs& a, b
     });
     const dim3 grid((unsigned)((long long)a.B * a.H * (carry ? a.cells() : a.segs)), a.passes);
     if (carry)
-        launch_next(attn_fp32_kernel<T, PK, PV, true>, grid, dim3(256), smem, st, a);
+        launch_next(attn_fp32_kernel<T, PK, PV, true>, grid, dim3(FT), smem, st, a);
     else
-        launch_next(attn_fp32_kernel<T, PK, PV, false>, grid, dim3(256), smem, st, a);
+        launch_next(attn_fp32_kernel<T, PK, PV, false>, grid, dim3(FT), smem, st, a);
     return launched(carry ? "attn_fp32_carry_kernel" : "attn_fp32_kernel", st);
 }
 
