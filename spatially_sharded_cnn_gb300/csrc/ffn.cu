@@ -371,6 +371,156 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     if (warp == 0) tc_dealloc(tmem, 512);
 }
 
+// Few rows (one token of some streams): every tile's product is cut along k over the CTAs of a
+// cluster, so that all SMs read weights at once; each leaves its fp32 tile in its own shared memory
+// and then takes a share of the rows from everyone's, summed in the order of the ranks.  MODE
+// FF_IN (out: h) or FF_MM (out: y).  Warps: 0 loads, 1 multiplies, all eight add up.
+constexpr int FS_THREADS = 256;
+constexpr int FS_SPLITS = 6;  // CTAs of a cluster at most: of eight, the sixteen clusters of 16 tiles ran in two rounds
+constexpr int FS_STAGES = 6;
+constexpr uint32_t FS_STAGE = FF_A_BYTES + 128 * FF_BK * 2;  // 128 accumulator columns at most
+constexpr int FS_SMEM = FS_STAGES * FS_STAGE;                // and the tile in fp32 (64 KB) over it
+
+struct FfnFewParams {
+    int chunks, per, bn, tiles_n, splits;
+    int M, N, F;  // rows and columns out; F of FF_IN
+    void* out;
+    long long row;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ float4 peer_load(uint32_t addr, int rank) {
+    uint32_t at;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at));
+    return v;
+}
+
+template <typename T, int MODE, int ACT>
+__global__ void __launch_bounds__(FS_THREADS, 1)
+    ffn_few_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, FfnFewParams p) {
+    grid_begin();
+    extern __shared__ __align__(1024) unsigned char ring[];
+    __shared__ uint64_t full[FS_STAGES], empty[FS_STAGES], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
+    const int hw = p.bn / 2, n0 = tile % p.tiles_n * (MODE == FF_IN ? hw : p.bn), m0 = tile / p.tiles_n * FF_BM;
+    const int c0 = min(p.chunks, rank * p.per), c1 = min(p.chunks, c0 + p.per);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < FS_STAGES; s++) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&done, 1);
+        abort_word = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 0) tc_alloc(&tmem_base, 128);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    if (warp == 0 && elect_one()) {
+        int it = 0;
+        for (int c = c0; c < c1; c++, it++) {
+            const int s = it % FS_STAGES, k = c * FF_BK;
+            if (it >= FS_STAGES && !ff_wait(&empty[s], (unsigned)((it / FS_STAGES - 1) & 1), abort_flag)) break;
+            unsigned char *sa = ring + s * FS_STAGE, *sb = sa + FF_A_BYTES;
+            mbar_expect_tx(&full[s], FF_A_BYTES + (uint32_t)p.bn * FF_BK * 2);
+            tma_2d(sa, &amap, k, m0, &full[s]);
+            for (int i = 0; i < p.bn / 64; i++)
+                tma_2d(sb + i * FF_MN_BLOCK, &bmap,
+                       MODE == FF_IN ? (i < hw / 64 ? n0 + 64 * i : p.F + n0 + 64 * (i - hw / 64)) : n0 + 64 * i, k, &full[s]);
+        }
+        if (*abort_flag) {  // the last copy issued into each stage lands before the tile takes its place
+            int zero = 0;
+            for (int k = it > FS_STAGES ? it - FS_STAGES : 0; k < it; k++)
+                ff_wait(&full[k % FS_STAGES], (unsigned)((k / FS_STAGES) & 1), &zero);
+        }
+    } else if (warp == 1 && elect_one()) {
+        const uint32_t fmt = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
+        const uint32_t id = (1u << 4) | fmt | (1u << 16) | ((uint32_t)(p.bn >> 3) << 17) | ((uint32_t)(FF_BM >> 4) << 24);
+        for (int c = c0; c < c1; c++) {
+            const int it = c - c0, s = it % FS_STAGES;
+            if (!ff_wait(&full[s], (unsigned)((it / FS_STAGES) & 1), abort_flag)) break;
+            tc_fence_after();
+            const uint64_t a0 = sdesc(ring + s * FS_STAGE, 16, 1024), b0 = sdesc(ring + s * FS_STAGE + FF_A_BYTES, FF_MN_BLOCK, 1024);
+#pragma unroll
+            for (int k = 0; k < FF_BK / 16; k++) tc_mma_bf16(tmem, a0 + 2 * k, b0 + 128 * k, id, it > 0 || k > 0);
+            tc_commit(&empty[s]);
+        }
+        tc_commit(&done);
+    }
+    __syncwarp();
+    int zero = 0;
+    ff_wait(&done, 0, &zero);  // every copy has landed and every product has read it
+    __syncwarp();
+    tc_fence_after();
+    __syncthreads();
+    // ---- the tile to shared memory, 16-byte chunks of a row rotated by the row
+    float* own = reinterpret_cast<float*>(ring);
+    const int row = 32 * (warp & 3) + lane, quads = p.bn / 4;
+    for (int cc = (warp >> 2) * (p.bn / 2); cc < ((warp >> 2) + 1) * (p.bn / 2); cc += 16) {
+        float v[16];
+        tc_ld16_async(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cc, v);
+        tc_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(own + row * p.bn + ((((cc + i) >> 2) + row) % quads) * 4) =
+                c0 < c1 ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 0) tc_dealloc(tmem, 128);
+    // ---- rows rank, rank + splits, ... of everyone's tile
+    const int rows = min(FF_BM, p.M - m0), cols = MODE == FF_IN ? hw : p.bn;
+    const uint32_t base = su32(own);
+    for (int e = threadIdx.x; e < (rows - rank + p.splits - 1) / p.splits * (cols / 4); e += FS_THREADS) {
+        const int r = rank + e / (cols / 4) * p.splits, c = e % (cols / 4);
+        const uint32_t fa = base + (uint32_t)(r * p.bn + (c + r) % quads * 4) * 4;
+        const uint32_t ga = base + (uint32_t)(r * p.bn + (c + hw / 4 + r) % quads * 4) * 4;
+        float4 v[FS_SPLITS], w[FS_SPLITS];  // (all under way at once)
+#pragma unroll
+        for (int k = 0; k < FS_SPLITS; k++)
+            if (k < p.splits) {
+                v[k] = peer_load(fa, k);
+                if (MODE == FF_IN) w[k] = peer_load(ga, k);
+            }
+        float f[4] = {}, g[4] = {};
+#pragma unroll
+        for (int k = 0; k < FS_SPLITS; k++)
+            if (k < p.splits) {
+                f[0] += v[k].x;
+                f[1] += v[k].y;
+                f[2] += v[k].z;
+                f[3] += v[k].w;
+                if (MODE == FF_IN) {
+                    g[0] += w[k].x;
+                    g[1] += w[k].y;
+                    g[2] += w[k].z;
+                    g[3] += w[k].w;
+                }
+            }
+        if (MODE == FF_IN) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) f[i] = act_f<ACT>(f[i]) * g[i];
+        }
+        if (n0 + 4 * c < p.N) store_pack<T, 4>(static_cast<T*>(p.out) + (long long)(m0 + r) * p.row + n0 + 4 * c, f);
+    }
+    __syncwarp();
+    cluster_sync();  // nobody's tile goes while it is read
+}
+
 // The tiles that were cut: out = sum over splits, in order.  Grid: (rest, groups of 8 rows).
 template <typename T>
 __global__ void __launch_bounds__(256) ffn_join_kernel(FfnParams p, T* out, long long row) {
@@ -479,6 +629,57 @@ template <typename T, int MODE> hc_status ffn_act(int act, const Maps& m, const 
     return ffn_launch<T, MODE, HC_PW_NONE>(m, p, st);
 }
 
+// The cut of a product with few rows: columns a tile and CTAs a cluster, or splits = 0 where the
+// tiles alone fill the GPU.
+struct FewPlan {
+    int bn, tiles_n, splits, per, chunks;
+};
+FewPlan ffn_few_plan(int M, int N, int K, bool gated) {
+    FewPlan p = {gated ? 128 : 64, 0, 0, 0, (int)cdiv(K, FF_BK)};
+    p.tiles_n = (int)cdiv(N, 64);
+    const long long tiles = (long long)cdiv(M, FF_BM) * p.tiles_n, sms = device_sm_count();
+    if (tiles * 2 > sms) return p;
+    long long s = sms / tiles;
+    if (s > FS_SPLITS) s = FS_SPLITS;
+    if (s > p.chunks) s = p.chunks;
+    p.splits = (int)s;
+    p.per = (int)cdiv(p.chunks, s);
+    return p;
+}
+template <typename T, int MODE, int ACT>
+hc_status ffn_few(const FewPlan& pl, const Mat& A, const Mat& B, int M, int N, int F, T* out, long long row, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    once_per_device(done, [] {
+        return cudaFuncSetAttribute(ffn_few_kernel<T, MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, FS_SMEM) ==
+               cudaSuccess;
+    });
+    CUtensorMap a, b;
+    hc_status e;
+    if ((e = in_map(&a, A, FF_BM)) || (e = in_map(&b, B, FF_BK))) return e;
+    const FfnFewParams p = {pl.chunks, pl.per, pl.bn, pl.tiles_n, pl.splits, M, N, F, out, row};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cdiv(M, FF_BM) * pl.tiles_n * pl.splits);
+    cfg.blockDim = dim3(FS_THREADS);
+    cfg.dynamicSmemBytes = FS_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = pl.splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, ffn_few_kernel<T, MODE, ACT>, a, b, p);
+    return launched("ffn_few_kernel", st);
+}
+template <typename T>
+hc_status ffn_few_in(int act, const FewPlan& pl, const Mat& A, const Mat& B, int M, int F, T* out, cudaStream_t st) {
+    if (act == HC_PW_SILU) return ffn_few<T, FF_IN, HC_PW_SILU>(pl, A, B, M, F, F, out, F, st);
+    if (act == HC_PW_GELU) return ffn_few<T, FF_IN, HC_PW_GELU>(pl, A, B, M, F, F, out, F, st);
+    return ffn_few<T, FF_IN, HC_PW_NONE>(pl, A, B, M, F, F, out, F, st);
+}
+
 // out (M x N, T) = A B over K.  A: [M][K] rows, or with amn [K][M]; B: [N][K] rows, or with bmn [K][N].
 template <typename T>
 hc_status ffn_mm(const Mat& A, bool amn, const Mat& B, bool bmn, int M, int N, int K, T* out, long long row, float* part,
@@ -548,17 +749,23 @@ hc_status ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
     FfnParams p = ffn_plan(M, F, C, hw);
     p.bn = 2 * hw;
     p.F = F;
+    const Mat xm = {x->p, row_of(x, d), C, M}, wi = {w_in, 2LL * F, 2 * F, C}, hm = {h, F, F, M}, wo = {w_out, C, C, F};
     Maps m;
     hc_status e;
-    if ((e = in_map(&m.a, {x->p, row_of(x, d), C, M}, FF_BM)) || (e = in_map(&m.b, {w_in, 2LL * F, 2 * F, C}, FF_BK)) ||
-        (e = out_map(&m.o, h, F, F, 1, M)))
-        return e;
+    const FewPlan few = ffn_few_plan(M, F, C, true), few_out = ffn_few_plan(M, C, F, false);
+    if (few.splits > 0) {
+        if ((e = ffn_few_in<T>(d->act, few, xm, wi, M, F, (T*)h, st))) return e;
+        if (few_out.splits > 0)
+            return ffn_few<T, FF_MM, HC_PW_NONE>(few_out, hm, wo, M, C, 0, (T*)y->p, row_of(y, d), st);
+        return ffn_mm<T>(hm, false, wo, true, M, C, F, (T*)y->p, row_of(y, d), (float*)(ws + ffn_space(d, 0).h), st);
+    }
+    if ((e = in_map(&m.a, xm, FF_BM)) || (e = in_map(&m.b, wi, FF_BK)) || (e = out_map(&m.o, h, F, F, 1, M))) return e;
     m.a2 = m.a;
     m.b2 = m.b;
     m.o2 = m.o;
     if ((e = ffn_act<T, FF_IN>(d->act, m, p, st))) return e;
-    return ffn_mm<T>({h, F, F, M}, false, {w_out, C, C, F}, true, M, C, F, (T*)y->p, row_of(y, d),
-                     (float*)(ws + ffn_space(d, 0).h), st);
+    if (few_out.splits > 0) return ffn_few<T, FF_MM, HC_PW_NONE>(few_out, hm, wo, M, C, 0, (T*)y->p, row_of(y, d), st);
+    return ffn_mm<T>(hm, false, wo, true, M, C, F, (T*)y->p, row_of(y, d), (float*)(ws + ffn_space(d, 0).h), st);
 }
 
 template <typename T>
