@@ -17,6 +17,8 @@
 //
 // Operands come by TMA in 128-byte swizzled tiles, K-major or MN-major as the arrays lie,
 // so that nothing is transposed or copied; edges are the copy engine's zero fill.
+// Large products take pairs of CTAs (Shape 256 x 256, the two SMs of a cluster): each holds its 128
+// rows of A and accumulators, and half of B's columns.
 // Warp roles (576 threads, one CTA an SM): warp 0 loads, warp 1 issues the MMAs, warps 2-17
 // drain finished accumulators (four per TMEM lane quarter, 32 columns at a time: with two
 // the activations' latency was longer than a tile's products at C = 512) and store through TMA.
@@ -28,14 +30,17 @@ namespace hc {
 namespace {
 
 constexpr int FF_BM = 128, FF_BK = 64;
-constexpr int FF_STAGES = 4;
-constexpr uint32_t FF_A_BYTES = FF_BM * FF_BK * 2;         // 16 KB
-constexpr uint32_t FF_STAGE = FF_A_BYTES + 256 * FF_BK * 2;  // and 32 KB of B
+constexpr uint32_t FF_A_BYTES = FF_BM * FF_BK * 2;  // 16 KB
+// One CTA a tile: 32 KB of B beside it, four stages; a pair: 16 KB in each CTA, six stages.
+constexpr int FF_MAX_STAGES = 6;
+__host__ __device__ constexpr int ff_stages(int ctas) { return ctas == 2 ? 6 : 4; }
+__host__ __device__ constexpr uint32_t ff_stage(int ctas) { return FF_A_BYTES + 256 / ctas * FF_BK * 2; }
 constexpr uint32_t FF_MN_BLOCK = FF_BK * 128;              // 64 MN values x 64 k-values
 constexpr int FF_BOX = 32 * 64;                            // 32 rows x 32 values: an output box
 constexpr int FF_EPI = 16;
 constexpr int FF_THREADS = 32 * (2 + FF_EPI);
-constexpr int FF_SMEM = 1024 + FF_STAGES * FF_STAGE + FF_EPI * FF_BOX;
+constexpr int FF_SMEM = 1024 + 192 * 1024 + FF_EPI * FF_BOX;
+static_assert(ff_stages(1) * ff_stage(1) == 192 * 1024 && ff_stages(2) * ff_stage(2) == 192 * 1024, "");
 
 enum FfnMode { FF_IN, FF_MID, FF_MM };
 
@@ -49,32 +54,34 @@ struct FfnParams {
     int bn;           // accumulator columns a tile
     int amn, bmn;     // operand majors (FF_MM)
     int M, N, F;      // output rows and columns; F for IN and MID
-    float* part;      // [split][rest][128][bn]
+    int ctas;         // CTAs a tile: 128 rows each
+    float* part;      // [split][rest][ctas][128][bn]
 };
 struct FfnUnit {
     int m0, n0, c0, c1;
     long long slot;  // of `part`, or -1: a whole tile
 };
-__device__ __forceinline__ FfnUnit ffn_unit(const FfnParams& p, int u, int width) {
+template <int CTAS> __device__ __forceinline__ FfnUnit ffn_unit(const FfnParams& p, int u, int width) {
+    const int rank = CTAS == 2 ? blockIdx.x & 1 : 0;
     FfnUnit r;
     int tile = u;
     r.c0 = 0;
     r.c1 = p.chunks;
     r.slot = -1;
     if (u >= p.full) {
-        r.slot = u - p.full;
+        r.slot = (long long)(u - p.full) * CTAS + rank;
         const int split = (u - p.full) / p.rest;
         tile = p.full + (u - p.full) - split * p.rest;
         r.c0 = split * p.per;
         r.c1 = min(p.chunks, r.c0 + p.per);
     }
-    r.m0 = tile / p.tiles_n * FF_BM;
+    r.m0 = (tile / p.tiles_n * CTAS + rank) * FF_BM;
     r.n0 = tile % p.tiles_n * width;
     return r;
 }
 
 struct FfnSmem {
-    uint64_t full[FF_STAGES], empty[FF_STAGES];
+    uint64_t full[FF_MAX_STAGES], empty[FF_MAX_STAGES];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t drain;
     uint32_t tmem_base;
@@ -137,7 +144,7 @@ template <typename T> __device__ __forceinline__ void pack16(const float (&v)[16
 
 // amap, bmap: operands; a2map, b2map: gy and w_out of MID; omap: y, h or a gradient; o2map:
 // [ga | gu] of MID.
-template <typename T, int MODE, int ACT>
+template <typename T, int MODE, int ACT, int CTAS>
 __global__ void __launch_bounds__(FF_THREADS, 1)
     ffn_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap a2map, const __grid_constant__ CUtensorMap b2map,
@@ -145,26 +152,36 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     grid_begin();
     extern __shared__ __align__(1024) unsigned char dsmem[];
     unsigned char* ring = (unsigned char*)(((uintptr_t)dsmem + 1023) & ~(uintptr_t)1023);
-    unsigned char* boxes = ring + FF_STAGES * FF_STAGE;
+    constexpr int STAGES = ff_stages(CTAS);
+    constexpr uint32_t STAGE = ff_stage(CTAS);
+    unsigned char* boxes = ring + STAGES * STAGE;
     __shared__ FfnSmem sh;
+    const int rank = CTAS == 2 ? blockIdx.x & 1 : 0;  // of a pair; 0 leads
+    const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // see elect_one
     volatile int* abort_flag = &sh.abort_flag;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < FF_STAGES; s++) {
+        for (int s = 0; s < STAGES; s++) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&sh.acc_full[b], 1);
-            mbar_init(&sh.acc_empty[b], FF_EPI);
+            mbar_init(&sh.acc_empty[b], FF_EPI * CTAS);
         }
         mbar_init(&sh.drain, 1);
         sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 0) tc_alloc(&sh.tmem_base, 512);
+    if (warp == 0) {
+        if constexpr (CTAS == 2)
+            tc_alloc_pair(&sh.tmem_base, 512);
+        else
+            tc_alloc(&sh.tmem_base, 512);
+    }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync();  // the other's barriers are there
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const int hw = p.bn / 2;  // IN, MID: columns of each of a and u
@@ -173,52 +190,59 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
         // ---------------- loads ----------------
         long long it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.units && ok; t += gridDim.x) {
-            const FfnUnit un = ffn_unit(p, t, MODE == FF_MM ? p.bn : hw);
+        for (int t = first; t < p.units && ok; t += step) {
+            const FfnUnit un = ffn_unit<CTAS>(p, t, MODE == FF_MM ? p.bn : hw);
             const int m0 = un.m0, n0 = un.n0;
             for (int second = 0; second < (MODE == FF_MID ? 2 : 1) && ok; second++)
                 for (int c = un.c0; c < un.c1; c++, it++) {
-                    const int s = (int)(it % FF_STAGES), k = c * FF_BK;
-                    if (it >= FF_STAGES && !ff_wait(&sh.empty[s], (unsigned)((it / FF_STAGES - 1) & 1), abort_flag)) {
+                    const int s = (int)(it % STAGES), k = c * FF_BK;
+                    if (it >= STAGES && !ff_wait(&sh.empty[s], (unsigned)((it / STAGES - 1) & 1), abort_flag)) {
                         ok = false;
                         break;
                     }
-                    unsigned char *sa = ring + s * FF_STAGE, *sb = sa + FF_A_BYTES;
-                    if (MODE == FF_MID && !second) {  // gh first
-                        mbar_expect_tx(&sh.full[s], FF_A_BYTES + 128 * FF_BK * 2);
-                        tma_2d(sa, &a2map, k, m0, &sh.full[s]);
-                        tma_2d(sb, &b2map, k, n0, &sh.full[s]);
-                        continue;
-                    }
-                    mbar_expect_tx(&sh.full[s], FF_A_BYTES + (uint32_t)p.bn * FF_BK * 2);
-                    if (MODE != FF_MM) {
-                        tma_2d(sa, &amap, k, m0, &sh.full[s]);
-                        for (int i = 0; i < hw / 64; i++) {
-                            tma_2d(sb + i * FF_MN_BLOCK, &bmap, n0 + 64 * i, k, &sh.full[s]);
-                            tma_2d(sb + (hw / 64 + i) * FF_MN_BLOCK, &bmap, p.F + n0 + 64 * i, k, &sh.full[s]);
+                    unsigned char *sa = ring + s * STAGE, *sb = sa + FF_A_BYTES;
+                    // the copies of both CTAs of a pair count on the leader's barrier; each brings
+                    // its own rows of A and half of B's columns
+                    const bool gh = MODE == FF_MID && !second;  // gh first
+                    const int bn = (gh ? 128 : p.bn) / CTAS;    // columns of B here
+                    if (rank == 0) mbar_expect_tx(&sh.full[s], CTAS * (FF_A_BYTES + (uint32_t)bn * FF_BK * 2));
+                    const uint32_t bar = CTAS == 2 ? peer_addr(su32(&sh.full[s]), 0) : 0;
+                    const auto copy = [&](unsigned char* dst, const CUtensorMap* m, int x, int y) {
+                        if constexpr (CTAS == 2)
+                            tma_2d_pair(dst, m, x, y, bar);
+                        else
+                            tma_2d(dst, m, x, y, &sh.full[s]);
+                    };
+                    if (gh) {
+                        copy(sa, &a2map, k, m0);
+                        copy(sb, &b2map, k, n0 + rank * bn);
+                    } else if (MODE != FF_MM) {
+                        copy(sa, &amap, k, m0);
+                        for (int i = 0; i < bn / 64; i++) {
+                            const int j = rank * (bn / 64) + i;  // 64-column block of a | u
+                            copy(sb + i * FF_MN_BLOCK, &bmap, j < hw / 64 ? n0 + 64 * j : p.F + n0 + 64 * (j - hw / 64), k);
                         }
                     } else {
                         if (p.amn) {
-                            tma_2d(sa, &amap, m0, k, &sh.full[s]);
-                            tma_2d(sa + FF_MN_BLOCK, &amap, m0 + 64, k, &sh.full[s]);
+                            copy(sa, &amap, m0, k);
+                            copy(sa + FF_MN_BLOCK, &amap, m0 + 64, k);
                         } else {
-                            tma_2d(sa, &amap, k, m0, &sh.full[s]);
+                            copy(sa, &amap, k, m0);
                         }
                         if (p.bmn)
-                            for (int i = 0; i < p.bn / 64; i++)
-                                tma_2d(sb + i * FF_MN_BLOCK, &bmap, n0 + 64 * i, k, &sh.full[s]);
+                            for (int i = 0; i < bn / 64; i++) copy(sb + i * FF_MN_BLOCK, &bmap, n0 + rank * bn + 64 * i, k);
                         else
-                            tma_2d(sb, &bmap, k, n0, &sh.full[s]);
+                            copy(sb, &bmap, k, n0 + rank * bn);
                     }
                 }
         }
-        if (*abort_flag) {
-            // wait (bounded, ignoring the abort flag) for the last copy issued into each stage
+        if (rank == 0 && *abort_flag) {
+            // wait (bounded, ignoring the abort flag) for the last copies issued into each stage
             int zero = 0;
-            for (long long k = it > FF_STAGES ? it - FF_STAGES : 0; k < it; k++)
-                ff_wait(&sh.full[k % FF_STAGES], (unsigned)((k / FF_STAGES) & 1), &zero);
+            for (long long k = it > STAGES ? it - STAGES : 0; k < it; k++)
+                ff_wait(&sh.full[k % STAGES], (unsigned)((k / STAGES) & 1), &zero);
         }
-    } else if (warp == 1 && elect_one()) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
         // ---------------- MMAs ----------------
         // IN, MM: tile t accumulates in half t & 1 of the 512 columns.  MID: a | u in the first
         // half and gh in 128 columns of the second, in turn: the next tile's gh is multiplied
@@ -226,49 +250,63 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
         const uint32_t fmt = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
         const auto idesc = [&](int n, int amn, int bmn) {
             return (1u << 4) | fmt | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16) | ((uint32_t)(n >> 3) << 17) |
-                   ((uint32_t)(FF_BM >> 4) << 24);
+                   ((uint32_t)(FF_BM * CTAS >> 4) << 24);
         };
         long long it = 0;
         int tile = 0;
         bool ok = true;
+        const auto commit = [&](uint64_t* b) {
+            if constexpr (CTAS == 2)
+                tc_commit_pair(b);
+            else
+                tc_commit(b);
+        };
+        const auto drained = [&](int b, unsigned parity) {  // by both CTAs
+            return mbar_wait_on([&] { return CTAS == 2 ? mbar_try_cluster(&sh.acc_empty[b], parity) : mbar_try(&sh.acc_empty[b], parity); },
+                                abort_flag, &g_ffn_status);
+        };
         const auto product = [&](uint32_t d, uint32_t id, int c0, int c1, int amn, int bmn) {
             for (int c = c0; c < c1; c++, it++) {
-                const int s = (int)(it % FF_STAGES);
-                if (!ff_wait(&sh.full[s], (unsigned)((it / FF_STAGES) & 1), abort_flag)) return false;
+                const int s = (int)(it % STAGES);
+                if (!ff_wait(&sh.full[s], (unsigned)((it / STAGES) & 1), abort_flag)) return false;
                 tc_fence_after();
-                unsigned char* sa = ring + s * FF_STAGE;
+                unsigned char* sa = ring + s * STAGE;
                 const uint64_t a0 = sdesc(sa, amn ? FF_MN_BLOCK : 16, 1024);
                 const uint64_t b0 = sdesc(sa + FF_A_BYTES, bmn ? FF_MN_BLOCK : 16, 1024);
                 const uint32_t ak = amn ? 2048 >> 4 : 32 >> 4, bk = bmn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
-                for (int k = 0; k < FF_BK / 16; k++)
-                    tc_mma_bf16(d, a0 + k * ak, b0 + k * bk, id, c > c0 || k > 0 ? 1u : 0u);
-                tc_commit(&sh.empty[s]);
+                for (int k = 0; k < FF_BK / 16; k++) {
+                    if constexpr (CTAS == 2)
+                        tc_mma_pair(d, a0 + k * ak, b0 + k * bk, id, c > c0 || k > 0 ? 1u : 0u);
+                    else
+                        tc_mma_bf16(d, a0 + k * ak, b0 + k * bk, id, c > c0 || k > 0 ? 1u : 0u);
+                }
+                commit(&sh.empty[s]);
             }
             return true;
         };
-        for (int t = blockIdx.x; t < p.units && ok; t += gridDim.x, tile++) {
-            const FfnUnit un = ffn_unit(p, t, MODE == FF_MM ? p.bn : hw);
+        for (int t = first; t < p.units && ok; t += step, tile++) {
+            const FfnUnit un = ffn_unit<CTAS>(p, t, MODE == FF_MM ? p.bn : hw);
             const int b = tile & 1;
             if (MODE == FF_MID) {
                 // (the tile before last was drained before a | u of the last)
                 ok = product(tmem + 256 + b * 128, idesc(128, 0, 0), un.c0, un.c1, 0, 0);
-                if (!ok || (tile > 0 && !ff_wait(&sh.acc_empty[0], (unsigned)((tile - 1) & 1), abort_flag))) break;
+                if (!ok || (tile > 0 && !drained(0, (unsigned)((tile - 1) & 1)))) break;
                 tc_fence_after();
                 ok = product(tmem, idesc(p.bn, 0, 1), un.c0, un.c1, 0, 1);
-                if (ok) tc_commit(&sh.acc_full[0]);
+                if (ok) commit(&sh.acc_full[0]);
             } else {
-                if (tile >= 2 && !ff_wait(&sh.acc_empty[b], (unsigned)((tile / 2 - 1) & 1), abort_flag)) break;
+                if (tile >= 2 && !drained(b, (unsigned)((tile / 2 - 1) & 1))) break;
                 tc_fence_after();
                 if (MODE == FF_IN)
                     ok = product(tmem + b * 256, idesc(p.bn, 0, 1), un.c0, un.c1, 0, 1);
                 else
                     ok = product(tmem + b * 256, idesc(p.bn, p.amn, p.bmn), un.c0, un.c1, p.amn, p.bmn);
-                if (ok) tc_commit(&sh.acc_full[b]);
+                if (ok) commit(&sh.acc_full[b]);
             }
         }
         // every MMA issued has completed before tensor memory is released
-        tc_commit(&sh.drain);
+        commit(&sh.drain);
         int zero = 0;
         ff_wait(&sh.drain, 0, &zero);
     } else if (warp >= 2) {
@@ -276,9 +314,15 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
         const int ew = warp - 2, q = warp & 3, part = ew >> 2;
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         unsigned char* box = boxes + ew * FF_BOX;
+        const auto release = [&](int b) {
+            if constexpr (CTAS == 2)
+                peer_arrive(peer_addr(su32(&sh.acc_empty[b]), 0));
+            else
+                mbar_arrive(&sh.acc_empty[b]);
+        };
         int tile = 0;
-        for (int t = blockIdx.x; t < p.units; t += gridDim.x, tile++) {
-            const FfnUnit un = ffn_unit(p, t, MODE == FF_MM ? p.bn : hw);
+        for (int t = first; t < p.units; t += step, tile++) {
+            const FfnUnit un = ffn_unit<CTAS>(p, t, MODE == FF_MM ? p.bn : hw);
             const int b = MODE == FF_MID ? 0 : tile & 1, row = un.m0 + 32 * q;
             if (!ff_wait(&sh.acc_full[b], (unsigned)((MODE == FF_MID ? tile : tile >> 1) & 1), abort_flag)) break;
             __syncwarp();
@@ -300,7 +344,7 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                     if (cc == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.acc_empty[0]);
+                        if (lane == 0) release(0);
                     }
                     uint32_t h[8];
 #pragma unroll
@@ -361,14 +405,20 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.acc_empty[b]);
+            if (lane == 0) release(b);
         }
         if (lane == 0) bulk_wait_all();  // output boxes written out
     }
     tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    if (warp == 0) tc_dealloc(tmem, 512);
+    if constexpr (CTAS == 2) {
+        cluster_sync();  // the leader's products are done, and nobody arrives here any more
+        tc_fence_after();
+        if (warp == 0) tc_dealloc_pair(tmem, 512);
+    } else {
+        tc_fence_after();
+        if (warp == 0) tc_dealloc(tmem, 512);
+    }
 }
 
 // Few rows (one token of some streams): every tile's product is cut along k over the CTAs of a
@@ -388,16 +438,11 @@ struct FfnFewParams {
     long long row;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
 __device__ __forceinline__ float4 peer_load(uint32_t addr, int rank) {
-    uint32_t at;
     float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(at));
+                 : "r"(peer_addr(addr, rank)));
     return v;
 }
 
@@ -521,16 +566,17 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
     cluster_sync();  // nobody's tile goes while it is read
 }
 
-// The tiles that were cut: out = sum over splits, in order.  Grid: (rest, groups of 8 rows).
+// The tiles that were cut: out = sum over splits, in order.  Grid: (rest, groups of 8 rows of a
+// tile's ctas * 128).
 template <typename T>
 __global__ void __launch_bounds__(256) ffn_join_kernel(FfnParams p, T* out, long long row) {
     grid_begin();
-    const int tile = p.full + blockIdx.x, m0 = tile / p.tiles_n * FF_BM + blockIdx.y * 8, n0 = tile % p.tiles_n * p.bn;
-    const long long stride = (long long)p.rest * FF_BM * p.bn;
+    const int tile = p.full + blockIdx.x, rows = FF_BM * p.ctas, m0 = tile / p.tiles_n * rows + blockIdx.y * 8, n0 = tile % p.tiles_n * p.bn;
+    const long long stride = (long long)p.rest * rows * p.bn;
     for (int e = threadIdx.x; e < 8 * p.bn / 4; e += 256) {
         const int r = e / (p.bn / 4), c = (e - r * (p.bn / 4)) * 4;
         if (m0 + r >= p.M || n0 + c >= p.N) continue;
-        const float* in = p.part + ((long long)blockIdx.x * FF_BM + blockIdx.y * 8 + r) * p.bn + c;
+        const float* in = p.part + ((long long)blockIdx.x * rows + blockIdx.y * 8 + r) * p.bn + c;
         float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int s = 0; s < p.splits; s++) {
@@ -549,44 +595,60 @@ template <typename T> __global__ void __launch_bounds__(256) ffn_zero_kernel(T* 
 }
 
 // ---------------------------------------------------------------------------
-// The shape and cut of a product: M x N outputs over K, tiles of 128 x bn.
-FfnParams ffn_plan(int M, int N, int K, int bn) {
+// The shape and cut of a product: M x N outputs over K, tiles of 128 ctas x bn.
+FfnParams ffn_plan(int M, int N, int K, int bn, int ctas) {
     FfnParams p = {};
     p.bn = bn;
+    p.ctas = ctas;
     p.M = M;
     p.N = N;
     p.tiles_n = (int)cdiv(N, bn);
     p.chunks = (int)cdiv(K, FF_BK);
     p.per = p.chunks;
     p.splits = 1;
-    p.units = p.full = (int)cdiv(M, FF_BM) * p.tiles_n;
+    p.units = p.full = (int)cdiv(M, FF_BM * ctas) * p.tiles_n;
     return p;
 }
+// Microseconds of a k-chunk, measured: a pair reads half of B a CTA, which takes 16 KB instead
+// of 32 out of L2 a chunk and an MMA's operands twice as fast out of shared memory.
+double ffn_chunk_us(int bn, int ctas) { return ctas == 2 ? bn > 128 ? 0.3 : 0.2 : bn > 128 ? 0.4 : bn > 64 ? 0.27 : 0.2; }
 // The same for FF_MM.  What whole rounds over the SMs leave is cut in the way that takes the
-// least time, at 0.4 us a k-chunk (measured; 128 x 256) and 0.04 us to write and read a partial
-// tile: 176 tiles of 512 chunks (gw_in of 32768 rows, 1024 x 5632) run in 1.17 rounds, not 2.
+// least time, at 0.04 us to write and read a partial tile of 128 rows: 176 tiles of 512
+// chunks (gw_in of 32768 rows, 1024 x 5632; one CTA a tile) run in 1.17 rounds, not 2.
 FfnParams ffn_mm_plan(int M, int N, int K) {
-    FfnParams p = ffn_plan(M, N, K, N > 128 ? 256 : N > 64 ? 128 : 64);
-    const int sms = device_sm_count(), rest = p.full % sms;
-    double best = 1e30;
-    for (int s = 1; s <= 32 && rest > 0 && p.chunks > 0; s++) {
-        if (s > 1 && p.chunks / s < 4) break;
-        const int per = (p.chunks + s - 1) / s, n = (p.chunks + per - 1) / per;
-        const double t = 0.4 * per * ((rest * n + sms - 1) / sms) + (n > 1 ? 4.0 + 0.04 * rest * n : 0.0);
-        if (t < best) {
-            best = t;
-            p.per = per;
-            p.splits = n;
+    FfnParams best = {};
+    double least = 1e30;
+    for (int ctas = 1; ctas <= 2; ctas++) {
+        const int bn = N > 128 ? 256 : N > 64 || ctas == 2 ? 128 : 64, sms = device_sm_count() / ctas;
+        if (ctas == 2 && (N <= 64 || M <= FF_BM || sms < 1)) continue;
+        FfnParams p = ffn_plan(M, N, K, bn, ctas);
+        const int all = p.full, rest = all % sms;
+        const double chunk = ffn_chunk_us(bn, ctas), rounds = chunk * p.chunks * (all / sms);
+        for (int s = 1; s <= 32; s++) {
+            if (s > 1 && (rest == 0 || p.chunks / s < 4)) break;
+            const int per = (p.chunks + s - 1) / s, n = per > 0 ? (p.chunks + per - 1) / per : 1;
+            const double t = rounds + chunk * per * ((rest * n + sms - 1) / sms) + (n > 1 ? 4.0 + 0.04 * ctas * rest * n : 0.0);
+            if (t < least) {
+                least = t;
+                p.per = per;
+                p.splits = n;
+                p.rest = n > 1 ? rest : 0;
+                p.full = all - p.rest;
+                p.units = p.full + p.rest * n;
+                best = p;
+            }
         }
     }
-    if (p.splits > 1) {
-        p.rest = rest;
-        p.full -= rest;
-        p.units = p.full + p.rest * p.splits;
-    }
-    return p;
+    return best;
 }
-size_t part_bytes(const FfnParams& p) { return sizeof(float) * p.rest * p.splits * FF_BM * (size_t)p.bn; }
+// Whether pairs take the least time for whole tiles of 256 columns.
+bool ffn_pairs(int M, int tiles_n) {
+    const int sms = device_sm_count();
+    if (M <= FF_BM || sms < 2) return false;
+    const long long one = (long long)cdiv(M, FF_BM) * tiles_n, two = (long long)cdiv(M, 2 * FF_BM) * tiles_n;
+    return ffn_chunk_us(256, 2) * ((two + sms / 2 - 1) / (sms / 2)) <= ffn_chunk_us(256, 1) * ((one + sms - 1) / sms);
+}
+size_t part_bytes(const FfnParams& p) { return sizeof(float) * p.rest * p.splits * p.ctas * FF_BM * (size_t)p.bn; }
 size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Mat {
@@ -612,16 +674,32 @@ struct Maps {
     CUtensorMap a, b, a2, b2, o, o2;
 };
 
-template <typename T, int MODE, int ACT> hc_status ffn_launch(const Maps& m, const FfnParams& p, cudaStream_t st) {
+template <typename T, int MODE, int ACT, int CTAS>
+hc_status ffn_launch_ctas(const Maps& m, const FfnParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
-    once_per_device(done, [] {
-        return cudaFuncSetAttribute(ffn_kernel<T, MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, FF_SMEM) ==
-               cudaSuccess;
+    const auto kernel = ffn_kernel<T, MODE, ACT, CTAS>;
+    once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FF_SMEM) == cudaSuccess;
     });
-    const int sms = device_sm_count();
-    launch_next(ffn_kernel<T, MODE, ACT>, dim3(p.units < sms ? p.units : sms), dim3(FF_THREADS), FF_SMEM, st, m.a, m.b,
-                m.a2, m.b2, m.o, m.o2, p);
+    const int groups = device_sm_count() / CTAS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CTAS * (p.units < groups ? p.units : groups));
+    cfg.blockDim = dim3(FF_THREADS);
+    cfg.dynamicSmemBytes = FF_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CTAS;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CTAS == 2 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.a2, m.b2, m.o, m.o2, p);
     return launched(MODE == FF_IN ? "ffn_in_kernel" : MODE == FF_MID ? "ffn_mid_kernel" : "ffn_mm_kernel", st);
+}
+template <typename T, int MODE, int ACT> hc_status ffn_launch(const Maps& m, const FfnParams& p, cudaStream_t st) {
+    return p.ctas == 2 ? ffn_launch_ctas<T, MODE, ACT, 2>(m, p, st) : ffn_launch_ctas<T, MODE, ACT, 1>(m, p, st);
 }
 template <typename T, int MODE> hc_status ffn_act(int act, const Maps& m, const FfnParams& p, cudaStream_t st) {
     if (act == HC_PW_SILU) return ffn_launch<T, MODE, HC_PW_SILU>(m, p, st);
@@ -695,14 +773,14 @@ hc_status ffn_mm(const Mat& A, bool amn, const Mat& B, bool bmn, int M, int N, i
     }
     Maps m;
     hc_status e;
-    if ((e = in_map(&m.a, A, amn ? FF_BK : FF_BM)) || (e = in_map(&m.b, B, bmn ? FF_BK : p.bn)) ||
+    if ((e = in_map(&m.a, A, amn ? FF_BK : FF_BM)) || (e = in_map(&m.b, B, bmn ? FF_BK : p.bn / p.ctas)) ||
         (e = out_map(&m.o, out, row, N, 1, M)))
         return e;
     m.a2 = m.a;
     m.b2 = m.b;
     m.o2 = m.o;
     if ((e = ffn_launch<T, FF_MM, HC_PW_NONE>(m, p, st)) || p.rest == 0) return e;
-    launch_next(ffn_join_kernel<T>, dim3(p.rest, FF_BM / 8), dim3(256), 0, st, p, out, row);
+    launch_next(ffn_join_kernel<T>, dim3(p.rest, FF_BM * p.ctas / 8), dim3(256), 0, st, p, out, row);
     return launched("ffn_join_kernel", st);
 }
 
@@ -745,8 +823,9 @@ hc_status ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
     const int M = d->M, C = d->C, F = d->F;
     void* h = ws;
     // columns of a and u each a tile: 64 where 128 would leave SMs without one
-    const int hw = (long long)cdiv(M, FF_BM) * cdiv(F, 128) >= device_sm_count() ? 128 : 64;
-    FfnParams p = ffn_plan(M, F, C, hw);
+    const int ctas = ffn_pairs(M, cdiv(F, 128)) ? 2 : 1;
+    const int hw = ctas == 2 || (long long)cdiv(M, FF_BM) * cdiv(F, 128) >= device_sm_count() ? 128 : 64;
+    FfnParams p = ffn_plan(M, F, C, hw, ctas);
     p.bn = 2 * hw;
     p.F = F;
     const Mat xm = {x->p, row_of(x, d), C, M}, wi = {w_in, 2LL * F, 2 * F, C}, hm = {h, F, F, M}, wo = {w_out, C, C, F};
@@ -778,12 +857,12 @@ hc_status ffn_bwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
     const Mat xm = {x->p, row_of(x, d), C, M}, gym = {gy->p, row_of(gy, d), C, M};
     hc_status e = HC_OK;
     if (M > 0) {
-        FfnParams p = ffn_plan(M, F, C, 128);
+        FfnParams p = ffn_plan(M, F, C, 128, ffn_pairs(M, cdiv(F, 128)) ? 2 : 1);
         p.bn = 256;
         p.F = F;
         Maps m;
         if ((e = in_map(&m.a, xm, FF_BM)) || (e = in_map(&m.b, {w_in, 2LL * F, 2 * F, C}, FF_BK)) ||
-            (e = in_map(&m.a2, gym, FF_BM)) || (e = in_map(&m.b2, {w_out, C, C, F}, 128)) ||
+            (e = in_map(&m.a2, gym, FF_BM)) || (e = in_map(&m.b2, {w_out, C, C, F}, 128 / p.ctas)) ||
             (e = out_map(&m.o, h, F, F, 1, M)) || (e = out_map(&m.o2, pre, 2LL * F, F, 2, M)))
             return e;
         if ((e = ffn_act<T, FF_MID>(d->act, m, p, st))) return e;
