@@ -92,28 +92,58 @@ __device__ __forceinline__ bool ff_wait(uint64_t* b, unsigned parity, volatile i
     return mbar_wait(b, parity, abort_flag, &g_ffn_status);
 }
 
-// act(a) and act'(a)
-template <int ACT> __device__ __forceinline__ void act_both(float a, float& f, float& d) {
+// act(x) and act'(x) of pairs, as act_f and act_d of rows.cuh (the drain of a tile has as many
+// instructions to issue as its products take cycles at C = 512: 114688 rows, GELU, 377 us a value at
+// a time).
+template <int ACT, bool SLOPE> __device__ __forceinline__ void act_pair(f32x2 x, f32x2& f, f32x2& d) {
+    const f32x2 one = pk2(1.0f, 1.0f), minus = pk2(-1.0f, -1.0f);
+    const auto all = [](float v) { return pk2(v, v); };
+    float lo, hi;
     if constexpr (ACT == HC_PW_SILU) {
-        const float s = sigmoid_f(a);
-        f = a * s;
-        d = s * fmaf(a, 1.0f - s, 1.0f);
+        unpk2(mul2(x, all(-kLog2e)), lo, hi);
+        unpk2(add2(pk2(ex2f(lo), ex2f(hi)), one), lo, hi);
+        const f32x2 s = pk2(rcpf(lo), rcpf(hi));
+        f = mul2(x, s);
+        if constexpr (SLOPE) d = mul2(s, fma2(x, fma2(s, minus, one), one));
     } else if constexpr (ACT == HC_PW_GELU) {
-        float t, e;
-        const float r = normal_tail(a, t, e), g = e * fmaf(-0.39894228040143268f, t, r);
-        f = fmaf(-t, r * e, fmaxf(a, 0.0f));
-        d = a >= 0.0f ? 1.0f - g : g;
+        // normal_tail with n = -|x| and -s
+        float x0, x1;
+        unpk2(x, x0, x1);
+        const f32x2 n = pk2(fmaxf(-fabsf(x0), -14.0f), fmaxf(-fabsf(x1), -14.0f));
+        unpk2(fma2(n, all(-0.33f), one), lo, hi);
+        const f32x2 s = mul2(n, pk2(rcpf(lo), rcpf(hi)));
+        unpk2(mul2(mul2(x, all(-0.5f * kLog2e)), x), lo, hi);
+        const f32x2 e = pk2(ex2f(lo), ex2f(hi));
+        f32x2 p = fma2(s, all(1.96299188e-05f), all(0.000127479288f));
+        p = fma2(s, p, all(-0.000140480028f));
+        p = fma2(s, p, all(-0.0017548654f));
+        p = fma2(s, p, all(0.0114476355f));
+        p = fma2(s, p, all(0.118352972f));
+        p = fma2(s, p, all(0.3989425f));
+        const f32x2 r = fma2(s, p, all(0.5f));
+        f = fma2(n, mul2(r, e), pk2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
+        if constexpr (SLOPE) {
+            const f32x2 g = mul2(e, fma2(n, all(0.39894228040143268f), r));
+            float g0, g1;
+            unpk2(g, g0, g1);
+            unpk2(fma2(g, minus, one), lo, hi);
+            d = pk2(x0 >= 0.0f ? lo : g0, x1 >= 0.0f ? hi : g1);
+        }
     } else {
-        f = a;
-        d = 1.0f;
+        f = x;
+        if constexpr (SLOPE) d = one;
     }
 }
 
-template <typename T> __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
-    Pack<T, 2> p;
-    p.v[0] = from_f<T>(a);
-    p.v[1] = from_f<T>(b);
-    return *reinterpret_cast<const uint32_t*>(&p);
+template <typename T> __device__ __forceinline__ uint32_t pack_pair(f32x2 v) {
+    float a, b;
+    uint32_t r;
+    unpk2(v, a, b);
+    if constexpr (std::is_same<T, __half>::value)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
 
 // One warp's output box: 32 rows (a lane each) x 32 values, 64-byte swizzle.
@@ -137,11 +167,6 @@ __device__ __forceinline__ void box_store(const unsigned char* box, const CUtens
         bulk_commit();
     }
 }
-template <typename T> __device__ __forceinline__ void pack16(const float (&v)[16], uint32_t (&o)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) o[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
-}
-
 // amap, bmap: operands; a2map, b2map: gy and w_out of MID; omap: y, h or a gradient; o2map:
 // [ga | gu] of MID.
 template <typename T, int MODE, int ACT, int CTAS>
@@ -348,16 +373,14 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                     }
                     uint32_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        float f, d;
-                        act_both<ACT>(a[i], f, d);
-                        a[i] = g[i] * u[i] * d;
-                        u[i] *= f;
-                        g[i] *= f;
+                    for (int i = 0; i < 8; i++) {
+                        const f32x2 gg = pk2(g[2 * i], g[2 * i + 1]), uu = pk2(u[2 * i], u[2 * i + 1]);
+                        f32x2 f, d;
+                        act_pair<ACT, true>(pk2(a[2 * i], a[2 * i + 1]), f, d);
+                        h[i] = pack_pair<T>(mul2(f, uu));
+                        ga[cc][i] = pack_pair<T>(mul2(mul2(gg, uu), d));
+                        gu[cc][i] = pack_pair<T>(mul2(gg, f));
                     }
-                    pack16<T>(u, h);
-                    pack16<T>(a, ga[cc]);
-                    pack16<T>(g, gu[cc]);
                     box_put<T>(box, h, cc, lane);
                 }
                 const int col = un.n0 + 32 * part;
@@ -379,6 +402,7 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
 #pragma unroll
                 for (int cc = 0; cc < 2; cc++) {
                     float v[16];
+                    f32x2 o[8];
                     tc_ld16_async(base + 32 * bx + 16 * cc, v);
                     if (MODE == FF_IN) {
                         float u[16];
@@ -386,19 +410,26 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                         tc_wait_ld(v);
                         tc_wait_ld(u);
 #pragma unroll
-                        for (int i = 0; i < 16; i++) v[i] = act_f<ACT>(v[i]) * u[i];
+                        for (int i = 0; i < 8; i++) {
+                            f32x2 f, d;
+                            act_pair<ACT, false>(pk2(v[2 * i], v[2 * i + 1]), f, d);
+                            o[i] = mul2(f, pk2(u[2 * i], u[2 * i + 1]));
+                        }
                     } else {
                         tc_wait_ld(v);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) o[i] = pk2(v[2 * i], v[2 * i + 1]);
                     }
                     if (whole) {
-                        uint32_t o[8];
-                        pack16<T>(v, o);
-                        box_put<T>(box, o, cc, lane);
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) h[i] = pack_pair<T>(o[i]);
+                        box_put<T>(box, h, cc, lane);
                     } else {
-                        float* o = p.part + (un.slot * FF_BM + 32 * q + lane) * p.bn + 32 * bx + 16 * cc;
+                        float* to = p.part + (un.slot * FF_BM + 32 * q + lane) * p.bn + 32 * bx + 16 * cc;
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            *reinterpret_cast<float4*>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
                 if (whole) box_store(box, &omap, lane, col, 0, row, p.N, p.M);
