@@ -44,17 +44,52 @@ template <int R, int N> __device__ __forceinline__ void mul4(f32x2 (&acc)[R][N],
     }
 }
 
+// Rows of every type through one kernel: an element's type is a branch that all threads take
+// alike, a few instructions of a chunk (and a third of the kernels to compile).
+__device__ __forceinline__ const char* elem(const void* p, long long i, int dtype) {
+    return static_cast<const char*>(p) + (dtype == HC_DTYPE_F32 ? 4 : 2) * i;
+}
+// 16 bits of an element as fp32.
+__device__ __forceinline__ float half_of(unsigned v, int dtype) {
+    return dtype == HC_DTYPE_BF16 ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((unsigned short)v));
+}
 // Four elements of a row from channel c on, zeros past D.
-template <typename T> __device__ __forceinline__ void load4(const T* row, int c, int D, bool wide, float (&f)[4]) {
-    if (wide && c + 4 <= D) {
-        load_pack<T, 4>(row + c, f);
-    } else {
+__device__ __forceinline__ void load4(const char* row, int dtype, int c, int D, bool wide, float (&f)[4]) {
+    if (dtype == HC_DTYPE_F32) {
+        const float* p = reinterpret_cast<const float*>(row) + c;
+        if (wide && c + 4 <= D) {
+            load_pack<float, 4>(p, f);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) f[i] = c + i < D ? to_f(row[c + i]) : 0.0f;
+            for (int i = 0; i < 4; i++) f[i] = c + i < D ? p[i] : 0.0f;
+        }
+    } else {
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(row) + c;
+        unsigned v[4];
+        if (wide && c + 4 <= D) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            v[0] = w.x & 0xffffu;
+            v[1] = w.x >> 16;
+            v[2] = w.y & 0xffffu;
+            v[3] = w.y >> 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i] = c + i < D ? p[i] : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = half_of(v[i], dtype);
     }
 }
+__device__ __forceinline__ void store1(char* p, int dtype, float v) {
+    if (dtype == HC_DTYPE_F32)
+        *reinterpret_cast<float*>(p) = v;
+    else if (dtype == HC_DTYPE_BF16)
+        *reinterpret_cast<__nv_bfloat16*>(p) = from_f<__nv_bfloat16>(v);
+    else
+        *reinterpret_cast<__half*>(p) = from_f<__half>(v);
+}
 
-template <typename T, int PK, int PV, bool CARRY>
+template <int PK, int PV, bool CARRY>
 __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
     grid_begin();
     extern __shared__ __align__(16) unsigned char raw[];
@@ -70,12 +105,13 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
     const float l2 = attn_log2_decay(a.decay, h);
     const int Dk = p.Dk, Dv = p.Dv;
     const long long zsize = (long long)Dk * Dv;
-    const T* qb = static_cast<const T*>(p.q.p) + b * p.q.batch + (long long)h * Dk;
-    const T* kb = static_cast<const T*>(p.k.p) + b * p.k.batch + (long long)h * Dk;
-    const T* vb = static_cast<const T*>(p.v.p) + b * p.v.batch + (long long)h * Dv;
-    T* yb = static_cast<T*>(p.y.p) + b * p.y.batch + (long long)h * Dv;
+    const int dt = a.dtype, bytes = dt == HC_DTYPE_F32 ? 4 : 2;
+    const char* qb = elem(p.q.p, b * p.q.batch + (long long)h * Dk, dt);
+    const char* kb = elem(p.k.p, b * p.k.batch + (long long)h * Dk, dt);
+    const char* vb = elem(p.v.p, b * p.v.batch + (long long)h * Dv, dt);
+    char* yb = const_cast<char*>(elem(p.y.p, b * p.y.batch + (long long)h * Dv, dt));
     const auto wide4 = [&](const hc_rows& r, int D) {
-        return D % 4 == 0 && r.row % 4 == 0 && r.batch % 4 == 0 && ((uintptr_t)r.p & (4 * sizeof(T) - 1)) == 0;
+        return D % 4 == 0 && r.row % 4 == 0 && r.batch % 4 == 0 && ((uintptr_t)r.p & (4 * bytes - 1)) == 0;
     };
     const bool wq = wide4(p.q, Dk), wk = wide4(p.k, Dk), wv = wide4(p.v, Dv);
 
@@ -106,15 +142,15 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
             const bool in = t0 + i >= 0 && d < Dk;  // rows ahead of the sequence are zeros
 #pragma unroll
             for (int s = 0; s < 4; s++) qr[u][s] = kr[u][s] = 0.0f;
-            if (in && !CARRY) load4(qb + (long long)(t0 + i) * p.q.row, d, Dk, wq, qr[u]);
-            if (in) load4(kb + (long long)(t0 + i) * p.k.row, d, Dk, wk, kr[u]);
+            if (in && !CARRY) load4(qb + (long long)(t0 + i) * p.q.row * bytes, dt, d, Dk, wq, qr[u]);
+            if (in) load4(kb + (long long)(t0 + i) * p.k.row * bytes, dt, d, Dk, wk, kr[u]);
         }
 #pragma unroll
         for (int u = 0; u < NV; u++) {
             const int e = tid + FT * u, i = e / (PV / 4), d = (e - i * (PV / 4)) * 4;
 #pragma unroll
             for (int s = 0; s < 4; s++) vr[u][s] = 0.0f;
-            if (t0 + i >= 0 && d < Dv) load4(vb + (long long)(t0 + i) * p.v.row, d, Dv, wv, vr[u]);
+            if (t0 + i >= 0 && d < Dv) load4(vb + (long long)(t0 + i) * p.v.row * bytes, dt, d, Dv, wv, vr[u]);
         }
     };
     if (c0 < c1) fetch(first_row(c0));
@@ -187,14 +223,14 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
             for (int u = 0; u < 4; u++) {
                 const int i = 4 * ty + u;
                 if (i < lo) continue;
-                T* yr = yb + (long long)(t0 + i) * p.y.row;
+                char* yr = yb + (long long)(t0 + i) * p.y.row * bytes;
 #pragma unroll
                 for (int n = 0; n < N; n++) {
                     const int m = 2 * tx + 32 * n;
                     float f0, f1;
                     unpk2(o[u][n], f0, f1);
-                    if (m < Dv) yr[m] = from_f<T>(f0);
-                    if (m + 1 < Dv) yr[m + 1] = from_f<T>(f1);
+                    if (m < Dv) store1(yr + m * bytes, dt, f0);
+                    if (m + 1 < Dv) store1(yr + (m + 1) * bytes, dt, f1);
                 }
             }
         }
@@ -239,48 +275,47 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
             const int m = e / PV, n = e - m * PV;
             if (m < Dk && n < Dv) z1[(long long)m * p.zm + (long long)n * p.zn] = sm.z[m][n];
         }
-    if (!CARRY) attn_blank<T>(p, b, h, len, a.L, seg, a.segs);
+    if (!CARRY) {
+        if (dt == HC_DTYPE_F32)
+            attn_blank<float>(p, b, h, len, a.L, seg, a.segs);
+        else  // (a zero is the same two bytes in either type)
+            attn_blank<__half>(p, b, h, len, a.L, seg, a.segs);
+    }
 }
 
-template <typename T, int PK, int PV> hc_status launch_pads(const AttnArgs& a, bool carry, cudaStream_t st) {
+template <int PK, int PV> hc_status launch_pads(const AttnArgs& a, bool carry, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     constexpr int smem = (int)sizeof(AttnSmem<PK, PV>);
     once_per_device(done, [] {
-        return cudaFuncSetAttribute(attn_fp32_kernel<T, PK, PV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem) == cudaSuccess &&
-               cudaFuncSetAttribute(attn_fp32_kernel<T, PK, PV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem) == cudaSuccess;
+        return cudaFuncSetAttribute(attn_fp32_kernel<PK, PV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+                   cudaSuccess &&
+               cudaFuncSetAttribute(attn_fp32_kernel<PK, PV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+                   cudaSuccess;
     });
     const dim3 grid((unsigned)((long long)a.B * a.H * (carry ? a.cells() : a.segs)), a.passes);
     if (carry)
-        launch_next(attn_fp32_kernel<T, PK, PV, true>, grid, dim3(FT), smem, st, a);
+        launch_next(attn_fp32_kernel<PK, PV, true>, grid, dim3(FT), smem, st, a);
     else
-        launch_next(attn_fp32_kernel<T, PK, PV, false>, grid, dim3(FT), smem, st, a);
+        launch_next(attn_fp32_kernel<PK, PV, false>, grid, dim3(FT), smem, st, a);
     return launched(carry ? "attn_fp32_carry_kernel" : "attn_fp32_kernel", st);
 }
-
-template <typename T, int PK> hc_status launch_pk(const AttnArgs& a, bool carry, cudaStream_t st) {
+template <int PK> hc_status launch_pk(const AttnArgs& a, bool carry, cudaStream_t st) {
     const int pv = (a.p[0].Dv + 31) / 32;
-    return pv == 1   ? launch_pads<T, PK, 32>(a, carry, st)
-           : pv == 2 ? launch_pads<T, PK, 64>(a, carry, st)
-           : pv == 3 ? launch_pads<T, PK, 96>(a, carry, st)
-                     : launch_pads<T, PK, 128>(a, carry, st);
-}
-template <typename T> hc_status launch_type(const AttnArgs& a, bool carry, cudaStream_t st) {
-    const int pk = (a.p[0].Dk + 31) / 32;
-    return pk == 1   ? launch_pk<T, 32>(a, carry, st)
-           : pk == 2 ? launch_pk<T, 64>(a, carry, st)
-           : pk == 3 ? launch_pk<T, 96>(a, carry, st)
-                     : launch_pk<T, 128>(a, carry, st);
+    return pv == 1   ? launch_pads<PK, 32>(a, carry, st)
+           : pv == 2 ? launch_pads<PK, 64>(a, carry, st)
+           : pv == 3 ? launch_pads<PK, 96>(a, carry, st)
+                     : launch_pads<PK, 128>(a, carry, st);
 }
 
 }  // namespace
 
 hc_status launch_attn_fp32(const AttnArgs& all, bool carry, cudaStream_t st) {
     return attn_by_shape(all, carry, [&](const AttnArgs& a) {
-        return a.dtype == HC_DTYPE_F32    ? launch_type<float>(a, carry, st)
-               : a.dtype == HC_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, carry, st)
-                                          : launch_type<__half>(a, carry, st);
+        const int pk = (a.p[0].Dk + 31) / 32;
+        return pk == 1   ? launch_pk<32>(a, carry, st)
+               : pk == 2 ? launch_pk<64>(a, carry, st)
+               : pk == 3 ? launch_pk<96>(a, carry, st)
+                         : launch_pk<128>(a, carry, st);
     });
 }
 

@@ -400,10 +400,9 @@ template <typename T> struct LnFwd {
     bool flat;
     cudaStream_t st;
     template <int V, int TPR, int NV> void run() {
-        if (flat && s.C == TPR * NV * V)
-            go<V, TPR, NV, true>();
-        else
-            go<V, TPR, NV, false>();
+        if constexpr (sizeof(T) * V == 16)
+            if (flat && s.C == TPR * NV * V) return go<V, TPR, NV, true>();
+        go<V, TPR, NV, false>();
     }
     template <int V, int TPR, int NV, bool FLAT> void go() {
         constexpr int threads = ln_block(TPR), rows = threads / TPR;
@@ -422,10 +421,9 @@ template <typename T> struct LnBwd {
     bool flat;
     cudaStream_t st;
     template <int V, int TPR, int NV> void run() {
-        if (flat && s.C == TPR * NV * V)
-            go<V, TPR, NV, true>();
-        else
-            go<V, TPR, NV, false>();
+        if constexpr (sizeof(T) * V == 16)
+            if (flat && s.C == TPR * NV * V) return go<V, TPR, NV, true>();
+        go<V, TPR, NV, false>();
     }
     template <int V, int TPR, int NV, bool FLAT> void go() {
         constexpr int threads = ln_block(TPR);
@@ -435,7 +433,7 @@ template <typename T> struct LnBwd {
     }
 };
 
-// Accesses of V elements (16 bytes or 8): whole packs in a row, and every row on such a boundary.
+// Accesses of V elements (16 bytes, or two fp32): whole packs in a row, every row on such a boundary.
 template <int V> bool ln_wide(int C, const hc_rows* a, const hc_rows* b, const hc_rows* c) {
     return C % V == 0 && rows_vec(a, V) && rows_vec(b, V) && (!c || rows_vec(c, V));
 }
@@ -449,9 +447,10 @@ hc_status ln_fwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamm
     constexpr int W = 16 / sizeof(T);
     LnFwd<T> f{x, y, gamma, beta, mean, rstd, {d->L, d->C, d->B * d->L, d->eps, lens},
                !lens && ln_flat(d, x) && ln_flat(d, y), st};
-    if (!(ln_wide<W>(d->C, x, y, nullptr)       ? ln_dispatch<W, 32>(d->C, f)
-          : ln_wide<W / 2>(d->C, x, y, nullptr) ? ln_dispatch<W / 2, 16>(d->C, f)
-                                                : ln_dispatch<1, 16>(d->C, f))) {
+    constexpr int S = sizeof(T) == 4 ? 2 : 1;
+    if (!(ln_wide<W>(d->C, x, y, nullptr)   ? ln_dispatch<W, 32>(d->C, f)
+          : ln_wide<S>(d->C, x, y, nullptr) ? ln_dispatch<S, 16>(d->C, f)
+                                            : ln_dispatch<1, 16>(d->C, f))) {
         const long long most = 8LL * device_sm_count();
         launch_next(ln_fwd_long_kernel<T>, dim3((unsigned)(f.s.rows < most ? f.s.rows : most)), dim3(LN_THREADS), 0, st,
                     view<const T>(x), gamma, beta, view<T>(y), mean, rstd, f.s);
@@ -465,9 +464,10 @@ hc_status ln_bwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamm
     constexpr int W = 16 / sizeof(T);
     LnBwd<T> f{x, gy, gx, gamma, mean, rstd, part, {d->L, d->C, d->B * d->L, d->eps, lens}, ln_blocks(d),
                !lens && ln_flat(d, x) && ln_flat(d, gy) && ln_flat(d, gx), st};
-    if (!(ln_wide<W>(d->C, x, gy, gx)       ? ln_dispatch<W, 16>(d->C, f)
-          : ln_wide<W / 2>(d->C, x, gy, gx) ? ln_dispatch<W / 2, 16>(d->C, f)
-                                            : ln_dispatch<1, 16>(d->C, f)))
+    constexpr int S = sizeof(T) == 4 ? 2 : 1;
+    if (!(ln_wide<W>(d->C, x, gy, gx)   ? ln_dispatch<W, 16>(d->C, f)
+          : ln_wide<S>(d->C, x, gy, gx) ? ln_dispatch<S, 16>(d->C, f)
+                                        : ln_dispatch<1, 16>(d->C, f)))
         launch_next(ln_bwd_long_kernel<T>, dim3((unsigned)f.blocks), dim3(LN_THREADS), 0, st, view<const T>(x), gamma,
                     mean, rstd, view<const T>(gy), view<T>(gx), part, f.s);
     return launched("ln_bwd_kernel", st);
