@@ -57,14 +57,29 @@ struct FfnParams {
     int ctas;         // CTAs a tile: 128 rows each
     float* part;      // [split][rest][ctas][128][bn]
 };
+// Products that one launch runs one after another (FF_MM: up to three that do not read one
+// another's results; else one).
+constexpr int FF_GROUP = 3;
+struct FfnGroup {
+    FfnParams p[FF_GROUP];
+    int n, units;
+};
+struct Maps {
+    CUtensorMap a[FF_GROUP], b[FF_GROUP], o[FF_GROUP];  // operands and outputs; MID: x, gy; w_in, w_out; h, [ga | gu]
+};
 struct FfnUnit {
-    int m0, n0, c0, c1;
+    int i, m0, n0, c0, c1;
     long long slot;  // of `part`, or -1: a whole tile
 };
-template <int CTAS> __device__ __forceinline__ FfnUnit ffn_unit(const FfnParams& p, int u, int width) {
-    const int rank = CTAS == 2 ? blockIdx.x & 1 : 0;
+template <int CTAS, int MODE> __device__ __forceinline__ FfnUnit ffn_unit(const FfnGroup& g, int u) {
+    int i = 0;
+    if (MODE == FF_MM)
+        while (u >= g.p[i].units) u -= g.p[i++].units;
+    const FfnParams& p = g.p[i];
+    const int rank = CTAS == 2 ? blockIdx.x & 1 : 0, width = MODE == FF_MM ? p.bn : p.bn / 2;
     FfnUnit r;
     int tile = u;
+    r.i = i;
     r.c0 = 0;
     r.c1 = p.chunks;
     r.slot = -1;
@@ -167,13 +182,9 @@ __device__ __forceinline__ void box_store(const unsigned char* box, const CUtens
         bulk_commit();
     }
 }
-// amap, bmap: operands; a2map, b2map: gy and w_out of MID; omap: y, h or a gradient; o2map:
-// [ga | gu] of MID.
 template <typename T, int MODE, int ACT, int CTAS>
 __global__ void __launch_bounds__(FF_THREADS, 1)
-    ffn_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-               const __grid_constant__ CUtensorMap a2map, const __grid_constant__ CUtensorMap b2map,
-               const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap o2map, FfnParams p) {
+    ffn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FfnGroup group) {
     grid_begin();
     extern __shared__ __align__(1024) unsigned char dsmem[];
     unsigned char* ring = (unsigned char*)(((uintptr_t)dsmem + 1023) & ~(uintptr_t)1023);
@@ -209,14 +220,15 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
     if constexpr (CTAS == 2) cluster_sync();  // the other's barriers are there
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
-    const int hw = p.bn / 2;  // IN, MID: columns of each of a and u
+    const int hw = group.p[0].bn / 2;  // IN, MID: columns of each of a and u
 
     if (warp == 0 && elect_one()) {
         // ---------------- loads ----------------
         long long it = 0;
         bool ok = true;
-        for (int t = first; t < p.units && ok; t += step) {
-            const FfnUnit un = ffn_unit<CTAS>(p, t, MODE == FF_MM ? p.bn : hw);
+        for (int t = first; t < group.units && ok; t += step) {
+            const FfnUnit un = ffn_unit<CTAS, MODE>(group, t);
+            const FfnParams& p = group.p[un.i];
             const int m0 = un.m0, n0 = un.n0;
             for (int second = 0; second < (MODE == FF_MID ? 2 : 1) && ok; second++)
                 for (int c = un.c0; c < un.c1; c++, it++) {
@@ -239,25 +251,25 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                             tma_2d(dst, m, x, y, &sh.full[s]);
                     };
                     if (gh) {
-                        copy(sa, &a2map, k, m0);
-                        copy(sb, &b2map, k, n0 + rank * bn);
+                        copy(sa, &maps.a[1], k, m0);
+                        copy(sb, &maps.b[1], k, n0 + rank * bn);
                     } else if (MODE != FF_MM) {
-                        copy(sa, &amap, k, m0);
+                        copy(sa, &maps.a[un.i], k, m0);
                         for (int i = 0; i < bn / 64; i++) {
                             const int j = rank * (bn / 64) + i;  // 64-column block of a | u
-                            copy(sb + i * FF_MN_BLOCK, &bmap, j < hw / 64 ? n0 + 64 * j : p.F + n0 + 64 * (j - hw / 64), k);
+                            copy(sb + i * FF_MN_BLOCK, &maps.b[un.i], j < hw / 64 ? n0 + 64 * j : p.F + n0 + 64 * (j - hw / 64), k);
                         }
                     } else {
                         if (p.amn) {
-                            copy(sa, &amap, m0, k);
-                            copy(sa + FF_MN_BLOCK, &amap, m0 + 64, k);
+                            copy(sa, &maps.a[un.i], m0, k);
+                            copy(sa + FF_MN_BLOCK, &maps.a[un.i], m0 + 64, k);
                         } else {
-                            copy(sa, &amap, k, m0);
+                            copy(sa, &maps.a[un.i], k, m0);
                         }
                         if (p.bmn)
-                            for (int i = 0; i < bn / 64; i++) copy(sb + i * FF_MN_BLOCK, &bmap, n0 + rank * bn + 64 * i, k);
+                            for (int i = 0; i < bn / 64; i++) copy(sb + i * FF_MN_BLOCK, &maps.b[un.i], n0 + rank * bn + 64 * i, k);
                         else
-                            copy(sb, &bmap, k, n0 + rank * bn);
+                            copy(sb, &maps.b[un.i], k, n0 + rank * bn);
                     }
                 }
         }
@@ -310,8 +322,9 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
             }
             return true;
         };
-        for (int t = first; t < p.units && ok; t += step, tile++) {
-            const FfnUnit un = ffn_unit<CTAS>(p, t, MODE == FF_MM ? p.bn : hw);
+        for (int t = first; t < group.units && ok; t += step, tile++) {
+            const FfnUnit un = ffn_unit<CTAS, MODE>(group, t);
+            const FfnParams& p = group.p[un.i];
             const int b = tile & 1;
             if (MODE == FF_MID) {
                 // (the tile before last was drained before a | u of the last)
@@ -346,8 +359,9 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                 mbar_arrive(&sh.acc_empty[b]);
         };
         int tile = 0;
-        for (int t = first; t < p.units; t += step, tile++) {
-            const FfnUnit un = ffn_unit<CTAS>(p, t, MODE == FF_MM ? p.bn : hw);
+        for (int t = first; t < group.units; t += step, tile++) {
+            const FfnUnit un = ffn_unit<CTAS, MODE>(group, t);
+            const FfnParams& p = group.p[un.i];
             const int b = MODE == FF_MID ? 0 : tile & 1, row = un.m0 + 32 * q;
             if (!ff_wait(&sh.acc_full[b], (unsigned)((MODE == FF_MID ? tile : tile >> 1) & 1), abort_flag)) break;
             __syncwarp();
@@ -384,15 +398,15 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                     box_put<T>(box, h, cc, lane);
                 }
                 const int col = un.n0 + 32 * part;
-                box_store(box, &omap, lane, col, 0, row, p.F, p.M);
+                box_store(box, &maps.o[un.i], lane, col, 0, row, p.F, p.M);
                 box_free(lane);
                 box_put<T>(box, ga[0], 0, lane);
                 box_put<T>(box, ga[1], 1, lane);
-                box_store(box, &o2map, lane, col, 0, row, p.F, p.M);
+                box_store(box, &maps.o[1], lane, col, 0, row, p.F, p.M);
                 box_free(lane);
                 box_put<T>(box, gu[0], 0, lane);
                 box_put<T>(box, gu[1], 1, lane);
-                box_store(box, &o2map, lane, col, 1, row, p.F, p.M);
+                box_store(box, &maps.o[1], lane, col, 1, row, p.F, p.M);
                 continue;
             }
             for (int bx = part; bx < (MODE == FF_IN ? hw : p.bn) / 32; bx += 4) {
@@ -432,7 +446,7 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                             *reinterpret_cast<float4*>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-                if (whole) box_store(box, &omap, lane, col, 0, row, p.N, p.M);
+                if (whole) box_store(box, &maps.o[un.i], lane, col, 0, row, p.N, p.M);
             }
             tc_fence_before();
             __syncwarp();
@@ -597,17 +611,26 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
     cluster_sync();  // nobody's tile goes while it is read
 }
 
-// The tiles that were cut: out = sum over splits, in order.  Grid: (rest, groups of 8 rows of a
-// tile's ctas * 128).
+// The tiles that were cut: out = sum over splits, in order.  Grid: (cut tiles of all products,
+// groups of 8 rows of a tile's ctas * 128).
+struct FfnOut {
+    void* p[FF_GROUP];
+    long long row[FF_GROUP];
+};
 template <typename T>
-__global__ void __launch_bounds__(256) ffn_join_kernel(FfnParams p, T* out, long long row) {
+__global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ FfnGroup g, FfnOut out) {
     grid_begin();
-    const int tile = p.full + blockIdx.x, rows = FF_BM * p.ctas, m0 = tile / p.tiles_n * rows + blockIdx.y * 8, n0 = tile % p.tiles_n * p.bn;
+    int i = 0, cut = blockIdx.x;
+    while (cut >= g.p[i].rest) cut -= g.p[i++].rest;
+    const FfnParams& p = g.p[i];
+    const int tile = p.full + cut, rows = FF_BM * p.ctas, m0 = tile / p.tiles_n * rows + blockIdx.y * 8;
+    const int n0 = tile % p.tiles_n * p.bn;
     const long long stride = (long long)p.rest * rows * p.bn;
+    T* o = static_cast<T*>(out.p[i]);
     for (int e = threadIdx.x; e < 8 * p.bn / 4; e += 256) {
         const int r = e / (p.bn / 4), c = (e - r * (p.bn / 4)) * 4;
         if (m0 + r >= p.M || n0 + c >= p.N) continue;
-        const float* in = p.part + ((long long)blockIdx.x * rows + blockIdx.y * 8 + r) * p.bn + c;
+        const float* in = p.part + ((long long)cut * rows + blockIdx.y * 8 + r) * p.bn + c;
         float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int s = 0; s < p.splits; s++) {
@@ -617,7 +640,7 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(FfnParams p, T* out, long
             f[2] += v.z;
             f[3] += v.w;
         }
-        store_pack<T, 4>(out + (m0 + r) * row + n0 + c, f);
+        store_pack<T, 4>(o + (m0 + r) * out.row[i] + n0 + c, f);
     }
 }
 template <typename T> __global__ void __launch_bounds__(256) ffn_zero_kernel(T* out, long long n) {
@@ -682,6 +705,34 @@ bool ffn_pairs(int M, int tiles_n) {
 size_t part_bytes(const FfnParams& p) { return sizeof(float) * p.rest * p.splits * p.ctas * FF_BM * (size_t)p.bn; }
 size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
+// The three products of the backward pass (gx, gw_in, gw_out) in one launch, where each alone
+// would be a round or two of the GPU: tiles are cut so that a unit takes about half of what
+// the whole takes of an SM (7685 rows, 328 x 872: 19 + 23 + 19 us and two joins apart).  False:
+// longer than that, and they run one by one (whole tiles of unequal length would not fill it).
+bool ffn_group_plan(int M, int C, int F, FfnParams (&p)[3]) {
+    const int dims[3][3] = {{M, C, 2 * F}, {C, 2 * F, M}, {F, C, M}}, sms = device_sm_count();
+    double us[3], all = 0.0;
+    for (int i = 0; i < 3; i++) {
+        const int N = dims[i][1], bn = N > 128 ? 256 : N > 64 ? 128 : 64;
+        p[i] = ffn_plan(dims[i][0], N, dims[i][2], bn, 1);
+        us[i] = ffn_chunk_us(bn, 1);
+        all += us[i] * p[i].chunks * p[i].full / sms;
+    }
+    if (all > 48.0) return false;
+    for (int i = 0; i < 3; i++) {
+        const double s = us[i] * p[i].chunks / (all / 2 > 4.0 ? all / 2 : 4.0);
+        int n = s < 1.5 ? 1 : s > 32.0 ? 32 : (int)(s + 0.5);
+        if (n > p[i].chunks / 4) n = p[i].chunks / 4;
+        if (n <= 1) continue;
+        p[i].per = (p[i].chunks + n - 1) / n;
+        p[i].splits = (p[i].chunks + p[i].per - 1) / p[i].per;
+        p[i].rest = p[i].full;
+        p[i].full = 0;
+        p[i].units = p[i].rest * p[i].splits;
+    }
+    return true;
+}
+
 struct Mat {
     const void* p;
     long long row;  // elements
@@ -701,12 +752,8 @@ hc_status out_map(CUtensorMap* m, const void* p, long long row, int cols, int pa
     return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, st, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-struct Maps {
-    CUtensorMap a, b, a2, b2, o, o2;
-};
-
 template <typename T, int MODE, int ACT, int CTAS>
-hc_status ffn_launch_ctas(const Maps& m, const FfnParams& p, cudaStream_t st) {
+hc_status ffn_launch_ctas(const Maps& m, const FfnGroup& g, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     const auto kernel = ffn_kernel<T, MODE, ACT, CTAS>;
     once_per_device(done, [&] {
@@ -714,7 +761,7 @@ hc_status ffn_launch_ctas(const Maps& m, const FfnParams& p, cudaStream_t st) {
     });
     const int groups = device_sm_count() / CTAS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CTAS * (p.units < groups ? p.units : groups));
+    cfg.gridDim = dim3(CTAS * (g.units < groups ? g.units : groups));
     cfg.blockDim = dim3(FF_THREADS);
     cfg.dynamicSmemBytes = FF_SMEM;
     cfg.stream = st;
@@ -726,16 +773,68 @@ hc_status ffn_launch_ctas(const Maps& m, const FfnParams& p, cudaStream_t st) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = CTAS == 2 ? 2 : 1;
-    cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.a2, m.b2, m.o, m.o2, p);
+    cudaLaunchKernelEx(&cfg, kernel, m, g);
     return launched(MODE == FF_IN ? "ffn_in_kernel" : MODE == FF_MID ? "ffn_mid_kernel" : "ffn_mm_kernel", st);
 }
-template <typename T, int MODE, int ACT> hc_status ffn_launch(const Maps& m, const FfnParams& p, cudaStream_t st) {
-    return p.ctas == 2 ? ffn_launch_ctas<T, MODE, ACT, 2>(m, p, st) : ffn_launch_ctas<T, MODE, ACT, 1>(m, p, st);
+template <typename T, int MODE, int ACT> hc_status ffn_launch(const Maps& m, const FfnGroup& g, cudaStream_t st) {
+    return g.p[0].ctas == 2 ? ffn_launch_ctas<T, MODE, ACT, 2>(m, g, st) : ffn_launch_ctas<T, MODE, ACT, 1>(m, g, st);
 }
 template <typename T, int MODE> hc_status ffn_act(int act, const Maps& m, const FfnParams& p, cudaStream_t st) {
-    if (act == HC_PW_SILU) return ffn_launch<T, MODE, HC_PW_SILU>(m, p, st);
-    if (act == HC_PW_GELU) return ffn_launch<T, MODE, HC_PW_GELU>(m, p, st);
-    return ffn_launch<T, MODE, HC_PW_NONE>(m, p, st);
+    const FfnGroup g = {{p}, 1, p.units};
+    if (act == HC_PW_SILU) return ffn_launch<T, MODE, HC_PW_SILU>(m, g, st);
+    if (act == HC_PW_GELU) return ffn_launch<T, MODE, HC_PW_GELU>(m, g, st);
+    return ffn_launch<T, MODE, HC_PW_NONE>(m, g, st);
+}
+
+// out (M x N) = A B over K.  A: [M][K] rows, or with amn [K][M]; B: [N][K] rows, or with bmn [K][N].
+struct Product {
+    Mat A;
+    bool amn;
+    Mat B;
+    bool bmn;
+    int M, N, K;
+    void* out;  // NULL: not wanted
+    long long row;
+};
+// Runs products cut as `plan` says in one launch, and joins what was cut; `part` in turn.
+template <typename T>
+hc_status ffn_products(const Product* pr, const FfnParams* plan, int n, float* part, cudaStream_t st) {
+    FfnGroup g = {};
+    FfnOut out = {};
+    Maps m;
+    hc_status e;
+    int cut = 0;
+    for (int k = 0; k < n; k++) {
+        const Product& q = pr[k];
+        if (!q.out) continue;
+        FfnParams& p = g.p[g.n];
+        p = plan[k];
+        p.amn = q.amn;
+        p.bmn = q.bmn;
+        p.part = part;
+        part += part_bytes(p) / sizeof(float);
+        if ((e = in_map(&m.a[g.n], q.A, q.amn ? FF_BK : FF_BM)) || (e = in_map(&m.b[g.n], q.B, q.bmn ? FF_BK : p.bn / p.ctas)) ||
+            (e = out_map(&m.o[g.n], q.out, q.row, q.N, 1, q.M)))
+            return e;
+        out.p[g.n] = q.out;
+        out.row[g.n] = q.row;
+        g.units += p.units;
+        cut += p.rest;
+        g.n++;
+    }
+    if (g.n == 0) return HC_OK;
+    for (int k = g.n; k < FF_GROUP; k++) {
+        m.a[k] = m.a[0];
+        m.b[k] = m.b[0];
+        m.o[k] = m.o[0];
+    }
+    if ((e = ffn_launch<T, FF_MM, HC_PW_NONE>(m, g, st)) || cut == 0) return e;
+    launch_next(ffn_join_kernel<T>, dim3(cut, FF_BM * g.p[0].ctas / 8), dim3(256), 0, st, g, out);
+    return launched("ffn_join_kernel", st);
+}
+template <typename T> hc_status ffn_mm(const Product& p, float* part, cudaStream_t st) {
+    const FfnParams plan = ffn_mm_plan(p.M, p.N, p.K);
+    return ffn_products<T>(&p, &plan, 1, part, st);
 }
 
 // The cut of a product with few rows: columns a tile and CTAs a cluster, or splits = 0 where the
@@ -789,32 +888,6 @@ hc_status ffn_few_in(int act, const FewPlan& pl, const Mat& A, const Mat& B, int
     return ffn_few<T, FF_IN, HC_PW_NONE>(pl, A, B, M, F, F, out, F, st);
 }
 
-// out (M x N, T) = A B over K.  A: [M][K] rows, or with amn [K][M]; B: [N][K] rows, or with bmn [K][N].
-template <typename T>
-hc_status ffn_mm(const Mat& A, bool amn, const Mat& B, bool bmn, int M, int N, int K, T* out, long long row, float* part,
-                 cudaStream_t st) {
-    FfnParams p = ffn_mm_plan(M, N, K);
-    p.amn = amn;
-    p.bmn = bmn;
-    p.part = part;
-    if (K == 0) {  // no rows: the weights' gradients (contiguous) are zeros
-        const long long n = (long long)M * N, want = (n + 255) / 256, most = 16LL * device_sm_count();
-        launch_next(ffn_zero_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, out, n);
-        return launched("ffn_zero_kernel", st);
-    }
-    Maps m;
-    hc_status e;
-    if ((e = in_map(&m.a, A, amn ? FF_BK : FF_BM)) || (e = in_map(&m.b, B, bmn ? FF_BK : p.bn / p.ctas)) ||
-        (e = out_map(&m.o, out, row, N, 1, M)))
-        return e;
-    m.a2 = m.a;
-    m.b2 = m.b;
-    m.o2 = m.o;
-    if ((e = ffn_launch<T, FF_MM, HC_PW_NONE>(m, p, st)) || p.rest == 0) return e;
-    launch_next(ffn_join_kernel<T>, dim3(p.rest, FF_BM * p.ctas / 8), dim3(256), 0, st, p, out, row);
-    return launched("ffn_join_kernel", st);
-}
-
 bool ffn_desc_ok(const hc_gated_ffn_desc* d) {
     return d && d->M >= 0 && d->C >= 1 && d->F >= 1 && d->act >= HC_PW_NONE && d->act <= HC_PW_GELU && dtype_ok(d->dtype);
 }
@@ -839,8 +912,13 @@ Space ffn_space(const hc_gated_ffn_desc* d, int pass) {
     };
     if (pass == 0) {
         part(d->M, d->C, d->F);
+        return s;
+    }
+    s.pre = pad16(2 * m * d->F * 2);
+    FfnParams g[3];
+    if (d->M > 0 && ffn_group_plan(d->M, d->C, d->F, g)) {
+        s.part = part_bytes(g[0]) + part_bytes(g[1]) + part_bytes(g[2]);
     } else {
-        s.pre = pad16(2 * m * d->F * 2);
         part(d->M, d->C, 2 * d->F);
         part(d->C, 2 * d->F, d->M);
         part(d->F, d->C, d->M);
@@ -867,15 +945,17 @@ hc_status ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
         if ((e = ffn_few_in<T>(d->act, few, xm, wi, M, F, (T*)h, st))) return e;
         if (few_out.splits > 0)
             return ffn_few<T, FF_MM, HC_PW_NONE>(few_out, hm, wo, M, C, 0, (T*)y->p, row_of(y, d), st);
-        return ffn_mm<T>(hm, false, wo, true, M, C, F, (T*)y->p, row_of(y, d), (float*)(ws + ffn_space(d, 0).h), st);
+        return ffn_mm<T>({hm, false, wo, true, M, C, F, y->p, row_of(y, d)}, (float*)(ws + ffn_space(d, 0).h), st);
     }
-    if ((e = in_map(&m.a, xm, FF_BM)) || (e = in_map(&m.b, wi, FF_BK)) || (e = out_map(&m.o, h, F, F, 1, M))) return e;
-    m.a2 = m.a;
-    m.b2 = m.b;
-    m.o2 = m.o;
+    if ((e = in_map(&m.a[0], xm, FF_BM)) || (e = in_map(&m.b[0], wi, FF_BK)) || (e = out_map(&m.o[0], h, F, F, 1, M))) return e;
+    for (int k = 1; k < FF_GROUP; k++) {
+        m.a[k] = m.a[0];
+        m.b[k] = m.b[0];
+        m.o[k] = m.o[0];
+    }
     if ((e = ffn_act<T, FF_IN>(d->act, m, p, st))) return e;
     if (few_out.splits > 0) return ffn_few<T, FF_MM, HC_PW_NONE>(few_out, hm, wo, M, C, 0, (T*)y->p, row_of(y, d), st);
-    return ffn_mm<T>(hm, false, wo, true, M, C, F, (T*)y->p, row_of(y, d), (float*)(ws + ffn_space(d, 0).h), st);
+    return ffn_mm<T>({hm, false, wo, true, M, C, F, y->p, row_of(y, d)}, (float*)(ws + ffn_space(d, 0).h), st);
 }
 
 template <typename T>
@@ -885,25 +965,39 @@ hc_status ffn_bwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
     const Space sp = ffn_space(d, 1);
     void *h = ws, *pre = ws + sp.h;
     float* part = (float*)(ws + sp.h + sp.pre);
-    const Mat xm = {x->p, row_of(x, d), C, M}, gym = {gy->p, row_of(gy, d), C, M};
-    hc_status e = HC_OK;
-    if (M > 0) {
-        FfnParams p = ffn_plan(M, F, C, 128, ffn_pairs(M, cdiv(F, 128)) ? 2 : 1);
-        p.bn = 256;
-        p.F = F;
-        Maps m;
-        if ((e = in_map(&m.a, xm, FF_BM)) || (e = in_map(&m.b, {w_in, 2LL * F, 2 * F, C}, FF_BK)) ||
-            (e = in_map(&m.a2, gym, FF_BM)) || (e = in_map(&m.b2, {w_out, C, C, F}, 128 / p.ctas)) ||
-            (e = out_map(&m.o, h, F, F, 1, M)) || (e = out_map(&m.o2, pre, 2LL * F, F, 2, M)))
-            return e;
-        if ((e = ffn_act<T, FF_MID>(d->act, m, p, st))) return e;
-        if (gx && gx->p &&
-            (e = ffn_mm<T>({pre, 2LL * F, 2 * F, M}, false, {w_in, 2LL * F, 2 * F, C}, false, M, C, 2 * F, (T*)gx->p,
-                           row_of(gx, d), part, st)))
-            return e;
+    if (M == 0) {  // no rows: the weights' gradients are zeros
+        for (int k = 0; k < 2; k++) {
+            T* out = k ? gw_out : gw_in;
+            const long long n = (long long)C * F * (k ? 1 : 2), want = (n + 255) / 256, most = 16LL * device_sm_count();
+            if (!out) continue;
+            launch_next(ffn_zero_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, out, n);
+            const hc_status e = launched("ffn_zero_kernel", st);
+            if (e) return e;
+        }
+        return HC_OK;
     }
-    if (gw_in && (e = ffn_mm<T>(xm, true, {pre, 2LL * F, 2 * F, M}, true, C, 2 * F, M, gw_in, 2LL * F, part, st))) return e;
-    if (gw_out) return ffn_mm<T>({h, F, F, M}, true, gym, true, F, C, M, gw_out, C, part, st);
+    const Mat xm = {x->p, row_of(x, d), C, M}, gym = {gy->p, row_of(gy, d), C, M}, wi = {w_in, 2LL * F, 2 * F, C};
+    const Mat wo = {w_out, C, C, F}, hm = {h, F, F, M}, prem = {pre, 2LL * F, 2 * F, M};
+    FfnParams p = ffn_plan(M, F, C, 128, ffn_pairs(M, cdiv(F, 128)) ? 2 : 1);
+    p.bn = 256;
+    p.F = F;
+    Maps m;
+    hc_status e;
+    if ((e = in_map(&m.a[0], xm, FF_BM)) || (e = in_map(&m.b[0], wi, FF_BK)) || (e = in_map(&m.a[1], gym, FF_BM)) ||
+        (e = in_map(&m.b[1], wo, 128 / p.ctas)) || (e = out_map(&m.o[0], h, F, F, 1, M)) ||
+        (e = out_map(&m.o[1], pre, 2LL * F, F, 2, M)))
+        return e;
+    m.a[2] = m.a[0];
+    m.b[2] = m.b[0];
+    m.o[2] = m.o[0];
+    if ((e = ffn_act<T, FF_MID>(d->act, m, p, st))) return e;
+    const Product pr[3] = {{prem, false, wi, false, M, C, 2 * F, gx ? gx->p : nullptr, gx ? row_of(gx, d) : 0},
+                           {xm, true, prem, true, C, 2 * F, M, gw_in, 2LL * F},
+                           {hm, true, gym, true, F, C, M, gw_out, C}};
+    FfnParams g[3];
+    if (ffn_group_plan(M, C, F, g)) return ffn_products<T>(pr, g, 3, part, st);
+    for (int k = 0; k < 3; k++)
+        if (pr[k].out && (e = ffn_mm<T>(pr[k], part, st))) return e;
     return HC_OK;
 }
 
