@@ -7,8 +7,8 @@
 //   2  rows on the state: q Z                            [128 x DV x DK]
 //   3  (scores * powers of lambda) v                     [128 x DV x 128], scores in tensor memory
 //   4  the state's part, transposed: v^T (weights * k)   [DV x DK x 128], three times
-// The state stays in registers in fp32, transposed: a thread holds a column n of Z (half
-// of the DK values), adds product 4 to it and leaves a copy rounded to bf16 in shared memory for
+// The state stays in registers in fp32, transposed: a thread holds a column n of Z (a half
+// or a quarter of the DK values), adds product 4 to it and leaves a copy rounded to bf16 in shared memory for
 // product 2.
 // Roundings: scores and that copy once each to bf16 (y, whose terms have random
 // signs, is then off by 2.3e-3 instead of the 1.7e-3 of its own rounding).  k times its
@@ -25,8 +25,10 @@
 // another), which takes the columns of 1 and 2 once everything has been read from them.
 //   Wider heads: one block an SM, and product 4 runs while the scores are read and scaled
 // (its pieces only replace what products 1 and 2 have read), product 3 while the state is
-// added up, products 1 and 2 while the rows before are stored.
-// All 256 threads work on every step and one of warp 0 issues copies and products.
+// added up, products 1 and 2 while the rows before are stored.  (Product 1 of the next chunk
+// behind product 4, before the state is there, took 94 us where this takes 86 on 8 x 4096 x 8
+// heads: the thread that issues it is held up behind 4, few products wait in line.)
+// All threads work on every step and one of warp 0 issues copies and products.
 //
 // Chunks end at the sequence's end: rows past it are never read, and those ahead of its
 // first row are the copy engine's zero fill (negative row coordinates).  Every wait is
@@ -56,6 +58,8 @@ template <int DK, int DV> struct Shape {
     static constexpr uint32_t cols = pair ? 256 : 512;
     static constexpr uint32_t o1 = pair ? 192 : 128, o2 = pair ? 0 : 128 + DV, part = pair ? 0 : 384;
     static constexpr int per_sm = pair ? 2 : 1;
+    // 16 warps an SM either way: with 8, the steps between the products took twice as long
+    static constexpr int threads = pair ? 256 : 512, groups = threads / 128;  // warps of a lane quarter
 };
 
 struct TcMaps {
@@ -73,13 +77,13 @@ struct AttnSh {
     alignas(16) float col[32];
 };
 
-// The two warps of a lane quarter.
-__device__ __forceinline__ void pair_sync(int quarter) {
+// The warps of a lane quarter.
+template <int THREADS> __device__ __forceinline__ void quarter_sync(int quarter) {
     switch (quarter) {
-        case 0: asm volatile("bar.sync 1, 64;\n" ::: "memory"); break;
-        case 1: asm volatile("bar.sync 2, 64;\n" ::: "memory"); break;
-        case 2: asm volatile("bar.sync 3, 64;\n" ::: "memory"); break;
-        default: asm volatile("bar.sync 4, 64;\n" ::: "memory");
+        case 0: asm volatile("bar.sync 1, %0;\n" ::"n"(THREADS) : "memory"); break;
+        case 1: asm volatile("bar.sync 2, %0;\n" ::"n"(THREADS) : "memory"); break;
+        case 2: asm volatile("bar.sync 3, %0;\n" ::"n"(THREADS) : "memory"); break;
+        default: asm volatile("bar.sync 4, %0;\n" ::"n"(THREADS) : "memory");
     }
     __syncwarp();
 }
@@ -128,7 +132,7 @@ template <bool CARRY> __device__ __forceinline__ Unit unit_of(const AttnArgs& a,
 }
 
 template <int DK, int DV, bool CARRY>
-__global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
+__global__ void __launch_bounds__((Shape<DK, DV>::threads), (Shape<DK, DV>::per_sm))
     attn_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ AttnArgs a) {
     grid_begin();
     using S = Shape<DK, DV>;
@@ -137,7 +141,8 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
     volatile int* abort_flag = &sh.abort_flag;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: see elect_one
-    const int quarter = warp & 3, half = warp >> 2, row = 32 * quarter + lane;
+    constexpr int THREADS = S::threads, GROUPS = S::groups;
+    const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
 
     if (tid == 0) {
         mbar_init(&sh.full[0], 1);
@@ -217,9 +222,9 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         const auto first_row = [&](int it) { return len - (back ? u.c0 + it + 1 : u.chunks - u.c0 - it) * TT; };
 
         // ---- the state: column zn of Z, rows zm ..  With DV = 64 product 4 gives every column
-        // twice (lanes 0 .. 63 and 64 .. 127), and four threads share one.
-        constexpr int ZC = DK * DV / 256;
-        const int zn = row % DV, zm = (DV == 64 ? half + 2 * (quarter >> 1) : half) * ZC;
+        // twice (lanes 0 .. 63 and 64 .. 127), and twice as many threads share one.
+        constexpr int ZC = DK * DV / THREADS;
+        const int zn = row % DV, zm = (DV == 64 ? group + GROUPS * (quarter >> 1) : group) * ZC;
         f32x2 z[ZC / 2];
         {
             float z0[ZC] = {};
@@ -269,11 +274,12 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
         };
         const auto scale_scores = [&](uint32_t at) {
             // scores times powers of lambda, in bf16, back over themselves.  This warp takes column
-            // blocks half and half + 2 of its rows' four.
-            uint32_t pk[2][16];
+            // blocks group, group + GROUPS, .. of its rows' four.
+            constexpr int BLOCKS = 4 / GROUPS;
+            uint32_t pk[BLOCKS][16];
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-                const int cb = half + 2 * u;
+            for (int u = 0; u < BLOCKS; u++) {
+                const int cb = group + GROUPS * u;
                 if (cb == quarter) {
                     float s[32];
                     tc_ld32(at + 32 * cb, s);
@@ -298,12 +304,12 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                     for (int j = 0; j < 16; j++) pk[u][j] = 0;
                 }
             }
-            // the rows' other warp has read its scores too
+            // the rows' other warps have read their scores too
             tc_fence_before();
-            pair_sync(quarter);
+            quarter_sync<32 * GROUPS>(quarter);
             tc_fence_after();
-            tc_st16(at + 16 * half, pk[0]);
-            tc_st16(at + 16 * (half + 2), pk[1]);
+#pragma unroll
+            for (int u = 0; u < BLOCKS; u++) tc_st16(at + 16 * (group + GROUPS * u), pk[u]);
             tc_wait_st();
         };
         const auto issue_rows = [&](int s, uint32_t at) {  // product 3
@@ -317,31 +323,32 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
             __syncwarp();
         };
         // k times its weight in the state as three pieces, p0 over k, p1 over q, p2 over the
-        // state's copy: 16 bytes a time, all of one row; rows (tid >> 3) + 32 i of each 64-column block
-        constexpr int NB = DK / 64;
-        uint4 p0[4 * NB], p1[4 * NB], p2[4 * NB];
+        // state's copy: 16 bytes a time, all of one row; rows (tid >> 3) + THREADS / 8 * i of each
+        // 64-column block
+        constexpr int NP = TT * DK / 8 / THREADS, NW = TT * 8 / THREADS;
+        uint4 p0[NP], p1[NP], p2[NP];
         const auto split_k = [&](int s, int lo) {
-            f32x2 w[4];
+            f32x2 w[NW];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int j = (tid >> 3) + 32 * i;
+            for (int i = 0; i < NW; i++) {
+                const int j = (tid >> 3) + THREADS / 8 * i;
                 const float f = j < lo ? 0.0f : p.su * ex2f(l2 * (float)(back ? j - lo + 1 : TT - 1 - j));
                 w[i] = pk2(f, f);
             }
 #pragma unroll
-            for (int i = 0; i < 4 * NB; i++) p0[i] = *reinterpret_cast<const uint4*>(buf_k(s) + 16 * (tid + 256 * i));
+            for (int i = 0; i < NP; i++) p0[i] = *reinterpret_cast<const uint4*>(buf_k(s) + 16 * (tid + THREADS * i));
 #pragma unroll
-            for (int i = 0; i < 4 * NB; i++) {
-                split_pair(p0[i].x, w[i & 3], p0[i].x, p1[i].x, p2[i].x);
-                split_pair(p0[i].y, w[i & 3], p0[i].y, p1[i].y, p2[i].y);
-                split_pair(p0[i].z, w[i & 3], p0[i].z, p1[i].z, p2[i].z);
-                split_pair(p0[i].w, w[i & 3], p0[i].w, p1[i].w, p2[i].w);
+            for (int i = 0; i < NP; i++) {
+                split_pair(p0[i].x, w[i % NW], p0[i].x, p1[i].x, p2[i].x);
+                split_pair(p0[i].y, w[i % NW], p0[i].y, p1[i].y, p2[i].y);
+                split_pair(p0[i].z, w[i % NW], p0[i].z, p1[i].z, p2[i].z);
+                split_pair(p0[i].w, w[i % NW], p0[i].w, p1[i].w, p2[i].w);
             }
         };
         const auto put_pieces = [&](int s) {
 #pragma unroll
-            for (int i = 0; i < 4 * NB; i++) {
-                const uint32_t at = 16 * (tid + 256 * i);
+            for (int i = 0; i < NP; i++) {
+                const uint32_t at = 16 * (tid + THREADS * i);
                 *reinterpret_cast<uint4*>(buf_k(s) + at) = p0[i];
                 *reinterpret_cast<uint4*>(buf_q(s) + at) = p1[i];
                 *reinterpret_cast<uint4*>(sx + at) = p2[i];
@@ -391,18 +398,20 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                 }
             }
         };
-        constexpr int OC = DV / 2;  // output columns of a thread
+        constexpr int OC = DV / GROUPS;  // output columns of a thread
         uint32_t out[OC / 2];
         const auto read_rows = [&](int lo, uint32_t o2) {
             const float w = p.sx * ex2f(l2 * (float)(back ? TT - 1 - row : row >= lo ? row - lo + 1 : 0));
             const f32x2 ww = pk2(w, w);
 #pragma unroll
-            for (int cc = 0; cc < OC; cc += 32) {
-                float o[32], r[32];
-                tc_ld32(tmem + lanes + S::o1 + half * OC + cc, o);
-                tc_ld32(o2 + lanes + half * OC + cc, r);
+            for (int cc = 0; cc < OC; cc += 16) {
+                float o[16], r[16];
+                tc_ld16_async(tmem + lanes + S::o1 + group * OC + cc, o);
+                tc_ld16_async(o2 + lanes + group * OC + cc, r);
+                tc_wait_ld(o);
+                tc_wait_ld(r);
 #pragma unroll
-                for (int i = 0; i < 16; i++)
+                for (int i = 0; i < 8; i++)
                     out[cc / 2 + i] = narrow(fma2(ww, pk2(r[2 * i], r[2 * i + 1]), pk2(o[2 * i], o[2 * i + 1])));
             }
         };
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
             if (lo == 0) {
 #pragma unroll
                 for (int i = 0; i < OC; i += 8) {
-                    const int n = half * OC + i, ch = (n & 63) >> 3;
+                    const int n = group * OC + i, ch = (n & 63) >> 3;
                     *reinterpret_cast<uint4*>(buf_v(s) + (n >> 6) * TBLOCK + row * 128 + ((ch ^ (row & 7)) << 4)) =
                         make_uint4(out[i / 2], out[i / 2 + 1], out[i / 2 + 2], out[i / 2 + 3]);
                 }
@@ -423,8 +432,8 @@ __global__ void __launch_bounds__(256, (Shape<DK, DV>::per_sm))
                                    (long long)h * Dv;
 #pragma unroll
                 for (int i = 0; i < OC; i += 8)
-                    if (half * OC + i < Dv)
-                        *reinterpret_cast<uint4*>(y + half * OC + i) =
+                    if (group * OC + i < Dv)
+                        *reinterpret_cast<uint4*>(y + group * OC + i) =
                             make_uint4(out[i / 2], out[i / 2 + 1], out[i / 2 + 2], out[i / 2 + 3]);
             }
         };
@@ -582,9 +591,9 @@ template <int DK, int DV> hc_status launch_shape(const AttnArgs& a, bool carry, 
     const long long units = (long long)a.B * a.H * (carry ? a.cells() : a.segs) * a.passes, most = (long long)S::per_sm * device_sm_count();
     const dim3 grid((unsigned)(units < most ? units : most));
     if (carry)
-        launch_next(attn_tc_kernel<DK, DV, true>, grid, dim3(256), S::smem, st, m, a);
+        launch_next(attn_tc_kernel<DK, DV, true>, grid, dim3(S::threads), S::smem, st, m, a);
     else
-        launch_next(attn_tc_kernel<DK, DV, false>, grid, dim3(256), S::smem, st, m, a);
+        launch_next(attn_tc_kernel<DK, DV, false>, grid, dim3(S::threads), S::smem, st, m, a);
     return launched(carry ? "attn_tc_carry_kernel" : "attn_tc_kernel", st);
 }
 
