@@ -65,10 +65,12 @@ hc_status hc_layernorm_bwd(const hc_layernorm_desc* d, const hc_rows* x, const f
  * 1 <= Dk, Dv <= 128, L < 2^31 - 256, H * Dk and H * Dv <= 2^20, B * H < 2^31 /
  * 3 (HC_ERR_UNSUPPORTED beyond); sizes < 1 (L < 0) and a scale that is not
  * finite are HC_ERR_INVALID_ARG.
- * Arithmetic: fp32 rows are multiplied in fp32.  16-bit rows go through the
- * tensor cores where Dk and Dv are multiples of 8, addresses and strides
- * multiples of 16 bytes and sequences not short; scores and the state as it is
- * read are rounded once to bf16 (fp16) there, the state itself stays fp32. */
+ * Arithmetic: bf16 rows go through the tensor cores where Dk and Dv are multiples
+ * of 8, addresses and strides multiples of 16 bytes (strides not 0) and sequences
+ * not short (a few rows at most): scores, and the state as it is read, are rounded
+ * once to bf16 there; the state itself is fp32.  All others are multiplied in fp32.
+ * Rows are taken in chunks of up to 128: a value that is not finite may spoil its
+ * whole chunk, not only the rows behind it. */
 typedef struct {
     int B, L, H, Dk, Dv;
     float scale;

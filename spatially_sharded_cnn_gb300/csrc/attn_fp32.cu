@@ -155,6 +155,9 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
     };
     if (c0 < c1) fetch(first_row(c0));
 
+    float* z1 = CARRY ? p.carry + ((long long)pair * runs + run) * zsize
+                      : p.z1 && seg == a.segs - 1 ? p.z1 + pair * zsize
+                                            : nullptr;
     constexpr int N = PV / 32;  // pairs of columns 2 tx + 32 n, + 1
     const f32x2 none = pk2(0.0f, 0.0f);
     for (int idx = c0; idx < c1; idx++) {
@@ -206,8 +209,10 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
             for (int u = 0; u < 4; u++)
 #pragma unroll
                 for (int n = 0; n < N; n++) o[u][n] = none;
+            if (idx > 0 || p.z0) {  // else the state is zero
 #pragma unroll 2
-            for (int d = 0; d < Dk; d += 4) mul4<4, N>(o, &sm.q[4 * ty][d], PK + 4, &sm.z[d][2 * tx], PV);
+                for (int d = 0; d < Dk; d += 4) mul4<4, N>(o, &sm.q[4 * ty][d], PK + 4, &sm.z[d][2 * tx], PV);
+            }
 #pragma unroll
             for (int u = 0; u < 4; u++) {
                 const int i = 4 * ty + u;
@@ -234,6 +239,7 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
                 }
             }
         }
+        if (idx + 1 == c1 && !z1) break;
         // ---- the state behind the chunk: rows 4 ty .. + 32 r
         // (every row has read the state ahead of the barrier above)
         const float w = exp2f(l2 * (AT_T - lo));
@@ -267,9 +273,6 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
         __syncthreads();
     }
     if (c0 == c1) __syncthreads();  // the state as it was loaded
-    float* z1 = CARRY ? p.carry + ((long long)pair * runs + run) * zsize
-                      : p.z1 && seg == a.segs - 1 ? p.z1 + pair * zsize
-                                            : nullptr;
     if (z1)
         for (int e = tid; e < PK * PV; e += FT) {
             const int m = e / PV, n = e - m * PV;

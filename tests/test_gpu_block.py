@@ -97,6 +97,8 @@ AT = [(1, 1, 1, 1, 1, "f32", 0, False, True, True), (2, 5, 2, 3, 7, "f32", 0, Tr
       (1, 129, 1, 64, 64, "bf16", 0, False, False, False), (2, 300, 3, 40, 80, "bf16", 0, False, True, True),
       (2, 1000, 1, 128, 128, "bf16", 8, False, True, True), (5, 515, 2, 128, 64, "bf16", 0, True, True, True),
       (1, 2500, 1, 64, 128, "bf16", 0, False, True, True), (2, 400, 2, 96, 24, "bf16", 3, True, True, True),
+      (5, 9, 2, 64, 64, "bf16", 0, True, True, True), (2, 1, 1, 128, 128, "bf16", 0, False, True, True),
+      (5, 3, 2, 72, 16, "bf16", 8, True, True, True), (1, 10, 1, 64, 8, "bf16", 0, False, False, True),
       (5, 300, 2, 64, 64, "f16", 0, True, True, True), (2, 200, 1, 128, 120, "f16", 0, False, True, True),
       (1, 77, 3, 31, 9, "f16", 0, False, False, True)]
 
