@@ -119,7 +119,7 @@ bool attn_size_ok(const hc_linear_attn_desc* d) {
 // 10.3 : 14.0 of 64.
 bool attn_tc_sizes(const hc_linear_attn_desc* d) {
     const int D = d->Dk > d->Dv ? d->Dk : d->Dv;
-    return d->dtype == HC_DTYPE_BF16 && d->Dk % 8 == 0 && d->Dv % 8 == 0 && (D > 64 || d->L > (D > 32 ? 8 : 32));
+    return d->dtype == HC_DTYPE_BF16 && d->Dk % 8 == 0 && d->Dv % 8 == 0 && d->L > (D > 64 ? 0 : D > 32 ? 8 : 32);
 }
 // And its rows: the copy engine wants 16-byte boundaries and strides that are not 0.
 bool attn_tc_rows(const hc_linear_attn_desc* d, const hc_rows* r) {

@@ -112,6 +112,7 @@ def test_gated_ffn_refusals(hc):
     assert fwd(d, x=rows(hc, 0, row=16, dtype=1)) == INV and fwd(d, x=rows(hc, row=16, dtype=2)) == INV
     assert fwd(d, x=rows(hc, 4097, row=16, dtype=1)) == INV
     assert fwd(d, x=rows(hc, 4098, row=16, dtype=1)) == UNS and fwd(d, x=rows(hc, row=17, dtype=1)) == UNS
+    assert fwd(d, x=rows(hc, row=0, dtype=1)) == UNS          # one row for all
     assert fwd(d, y=rows(hc, 8200, row=16, dtype=1)) == UNS and fwd(d, y=rows(hc, 8192, row=20, dtype=1)) == UNS
     assert fwd(d, y=rows(hc, 8192, row=8, dtype=1)) == INV and fwd(d, y=x) == INV
     assert fwd(d, wi=0) == INV and fwd(d, wo=4104) == INV

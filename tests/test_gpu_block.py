@@ -168,6 +168,19 @@ def test_linear_attn_of_no_rows(hc):
     assert (hT.numpy() == 0).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_linear_attn_of_no_rows_bf16(hc, D):
+    """Sizes that tensor cores take when there are rows."""
+    d = hc.linear_attn_desc(2, 0, 1, D, D, torch.bfloat16)
+    q = torch.empty(2, 0, D, device="cuda", dtype=torch.bfloat16)
+    h0, gh = torch.randn(2, 1, D, D, device="cuda"), torch.randn(2, 1, D, D, device="cuda")
+    hT, g0 = Out((2, 1, D, D)), Out((2, 1, D, D))
+    e = lambda: torch.empty_like(q)
+    hc.check(hc.hc_linear_attn_fwd(d, q, q, q, e(), h0=h0, hT=hT.t))
+    hc.check(hc.hc_linear_attn_bwd(d, q, q, q, q, e(), e(), e(), h0=h0, ghT=gh, gh0=g0.t))
+    assert torch.equal(hT.t, h0) and torch.equal(g0.t, gh)
+
+
 @pytest.mark.parametrize("B,H,Dk,Dv,dt,wide", [(1, 1, 1, 1, "f32", 0), (3, 2, 41, 82, "f32", 3), (64, 4, 64, 64, "bf16", 8),
                                                (5, 3, 128, 128, "f16", 0), (2, 5, 16, 100, "bf16", 1)])
 def test_linear_attn_step(hc, B, H, Dk, Dv, dt, wide):
