@@ -5,7 +5,8 @@
 // shared memory, the state stays there, and 8 x 16 threads take each of the four products in
 // register tiles of 4 rows x pairs of columns, four steps of the sum at a time (one 16-byte read
 // a row serves all of a thread's columns).  Bound by the multiply-adds, two an instruction, and the
-// shared-memory reads that feed them.
+// shared-memory reads that feed them, with three blocks of four warps an SM to hide their latency:
+// 20 sequences of 512 rows x 4 heads of 41 / 82 take 70 us, 42 % of the issue slots.
 #include "attn.cuh"
 
 namespace hc {
@@ -25,7 +26,8 @@ template <int PK, int PV> struct AttnSmem {
 
 // acc[r][n] += a[r][0 .. 3] . b[0 .. 3][n]: rows of `a` in shared memory, `pitch` floats apart,
 // four rows of `b` (`step` floats apart) of which a thread takes the pairs 32 columns apart.
-template <int R, int N> __device__ __forceinline__ void mul4(f32x2 (&acc)[R][N], const float* a, int pitch, const float* b, int step) {
+template <int R, int N>
+__device__ __forceinline__ void mul4(f32x2 (&acc)[R][N], const float* a, int pitch, const float* b, int step) {
     float4 x[R];
 #pragma unroll
     for (int r = 0; r < R; r++) x[r] = *reinterpret_cast<const float4*>(a + r * pitch);

@@ -8,8 +8,8 @@
 //   3  (scores * powers of lambda) v                     [128 x DV x 128], scores in tensor memory
 //   4  the state's part, transposed: v^T (weights * k)   [DV x DK x 128], three times
 // The state stays in registers in fp32, transposed: a thread holds a column n of Z (a half
-// or a quarter of the DK values), adds product 4 to it and leaves a copy rounded to bf16 in shared memory for
-// product 2.
+// or a quarter of the DK values), adds product 4 to it and leaves a copy rounded to bf16 in
+// shared memory for product 2.
 // Roundings: scores and that copy once each to bf16 (y, whose terms have random
 // signs, is then off by 2.3e-3 instead of the 1.7e-3 of its own rounding).  k times its
 // weight goes into the state as three bf16 pieces (24 bits): states are fp32 outputs, which
@@ -584,11 +584,13 @@ template <int DK, int DV> hc_status launch_shape(const AttnArgs& a, bool carry, 
     TcMaps m;
     for (int i = 0; i < a.passes; i++) {
         hc_status e;
-        if ((e = rows_map(&m.y[i], a.p[i].y, a.p[i].Dv, a)) || (e = rows_map(&m.q[i], a.p[i].q, a.p[i].Dk, a)) || (e = rows_map(&m.k[i], a.p[i].k, a.p[i].Dk, a)) ||
+        if ((e = rows_map(&m.y[i], a.p[i].y, a.p[i].Dv, a)) || (e = rows_map(&m.q[i], a.p[i].q, a.p[i].Dk, a)) ||
+            (e = rows_map(&m.k[i], a.p[i].k, a.p[i].Dk, a)) ||
             (e = rows_map(&m.v[i], a.p[i].v, a.p[i].Dv, a)))
             return e;
     }
-    const long long units = (long long)a.B * a.H * (carry ? a.cells() : a.segs) * a.passes, most = (long long)S::per_sm * device_sm_count();
+    const long long units = (long long)a.B * a.H * (carry ? a.cells() : a.segs) * a.passes;
+    const long long most = (long long)S::per_sm * device_sm_count();
     const dim3 grid((unsigned)(units < most ? units : most));
     if (carry)
         launch_next(attn_tc_kernel<DK, DV, true>, grid, dim3(S::threads), S::smem, st, m, a);

@@ -17,8 +17,12 @@
 //
 // Operands come by TMA in 128-byte swizzled tiles, K-major or MN-major as the arrays lie,
 // so that nothing is transposed or copied; edges are the copy engine's zero fill.
-// Large products take pairs of CTAs (Shape 256 x 256, the two SMs of a cluster): each holds its 128
-// rows of A and accumulators, and half of B's columns.
+// Large products take pairs of CTAs (256 x 256 outputs a tile, the two SMs of a cluster): each holds
+// its 128 rows of A and accumulators, and half of B's columns (32768 rows, 1024 x 2816 SiLU, forward and
+// backward: 1377 us a CTA a tile, 1204 in pairs, where the products that are run would take 1097 at the
+// rate of the library's largest).  Bound by the tensor pipe: it is busy 76 to 86 % of the cycles of the
+// products, 68 % of MID's, whose gh is a product of half the width, and 61 % of IN's with GELU at C = 512,
+// which the drain's instructions hold up.
 // Warp roles (576 threads, one CTA an SM): warp 0 loads, warp 1 issues the MMAs, warps 2-17
 // drain finished accumulators (four per TMEM lane quarter, 32 columns at a time: with two
 // the activations' latency was longer than a tile's products at C = 512) and store through TMA.
@@ -108,8 +112,8 @@ __device__ __forceinline__ bool ff_wait(uint64_t* b, unsigned parity, volatile i
 }
 
 // act(x) and act'(x) of pairs, as act_f and act_d of rows.cuh (the drain of a tile has as many
-// instructions to issue as its products take cycles at C = 512: 114688 rows, GELU, 377 us a value at
-// a time).
+// instructions to issue as its products take cycles at C = 512: 114688 rows, 512 x 2048, GELU forward
+// 516 us a value at a time, 476 in pairs).
 template <int ACT, bool SLOPE> __device__ __forceinline__ void act_pair(f32x2 x, f32x2& f, f32x2& d) {
     const f32x2 one = pk2(1.0f, 1.0f), minus = pk2(-1.0f, -1.0f);
     const auto all = [](float v) { return pk2(v, v); };
@@ -167,7 +171,8 @@ __device__ __forceinline__ void box_free(int lane) {  // the store before has re
     __syncwarp();
 }
 // 16 values of the lane's row, columns 16 half ..
-template <typename T> __device__ __forceinline__ void box_put(unsigned char* box, const uint32_t (&v)[8], int half, int lane) {
+template <typename T>
+__device__ __forceinline__ void box_put(unsigned char* box, const uint32_t (&v)[8], int half, int lane) {
 #pragma unroll
     for (int j = 0; j < 2; j++)
         *reinterpret_cast<uint4*>(box + lane * 64 + (((2 * half + j) ^ ((lane >> 1) & 3)) << 4)) =
@@ -257,7 +262,8 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                         copy(sa, &maps.a[un.i], k, m0);
                         for (int i = 0; i < bn / 64; i++) {
                             const int j = rank * (bn / 64) + i;  // 64-column block of a | u
-                            copy(sb + i * FF_MN_BLOCK, &maps.b[un.i], j < hw / 64 ? n0 + 64 * j : p.F + n0 + 64 * (j - hw / 64), k);
+                            const int col = j < hw / 64 ? n0 + 64 * j : p.F + n0 + 64 * (j - hw / 64);
+                            copy(sb + i * FF_MN_BLOCK, &maps.b[un.i], col, k);
                         }
                     } else {
                         if (p.amn) {
@@ -267,7 +273,8 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                             copy(sa, &maps.a[un.i], k, m0);
                         }
                         if (p.bmn)
-                            for (int i = 0; i < bn / 64; i++) copy(sb + i * FF_MN_BLOCK, &maps.b[un.i], n0 + rank * bn + 64 * i, k);
+                            for (int i = 0; i < bn / 64; i++)
+                                copy(sb + i * FF_MN_BLOCK, &maps.b[un.i], n0 + rank * bn + 64 * i, k);
                         else
                             copy(sb, &maps.b[un.i], k, n0 + rank * bn);
                     }
@@ -299,8 +306,9 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
                 tc_commit(b);
         };
         const auto drained = [&](int b, unsigned parity) {  // by both CTAs
-            return mbar_wait_on([&] { return CTAS == 2 ? mbar_try_cluster(&sh.acc_empty[b], parity) : mbar_try(&sh.acc_empty[b], parity); },
-                                abort_flag, &g_ffn_status);
+            uint64_t* bar = &sh.acc_empty[b];
+            return mbar_wait_on([&] { return CTAS == 2 ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); }, abort_flag,
+                                &g_ffn_status);
         };
         const auto product = [&](uint32_t d, uint32_t id, int c0, int c1, int amn, int bmn) {
             for (int c = c0; c < c1; c++, it++) {
@@ -542,7 +550,8 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
             const int it = c - c0, s = it % FS_STAGES;
             if (!ff_wait(&full[s], (unsigned)((it / FS_STAGES) & 1), abort_flag)) break;
             tc_fence_after();
-            const uint64_t a0 = sdesc(ring + s * FS_STAGE, 16, 1024), b0 = sdesc(ring + s * FS_STAGE + FF_A_BYTES, FF_MN_BLOCK, 1024);
+            const uint64_t a0 = sdesc(ring + s * FS_STAGE, 16, 1024);
+            const uint64_t b0 = sdesc(ring + s * FS_STAGE + FF_A_BYTES, FF_MN_BLOCK, 1024);
 #pragma unroll
             for (int k = 0; k < FF_BK / 16; k++) tc_mma_bf16(tmem, a0 + 2 * k, b0 + 128 * k, id, it > 0 || k > 0);
             tc_commit(&empty[s]);
@@ -681,7 +690,8 @@ FfnParams ffn_mm_plan(int M, int N, int K) {
         for (int s = 1; s <= 32; s++) {
             if (s > 1 && (rest == 0 || p.chunks / s < 4)) break;
             const int per = (p.chunks + s - 1) / s, n = per > 0 ? (p.chunks + per - 1) / per : 1;
-            const double t = rounds + chunk * per * ((rest * n + sms - 1) / sms) + (n > 1 ? 4.0 + 0.04 * ctas * rest * n : 0.0);
+            const double join = n > 1 ? 4.0 + 0.04 * ctas * rest * n : 0.0;
+            const double t = rounds + chunk * per * ((rest * n + sms - 1) / sms) + join;
             if (t < least) {
                 least = t;
                 p.per = per;
@@ -813,7 +823,8 @@ hc_status ffn_products(const Product* pr, const FfnParams* plan, int n, float* p
         p.bmn = q.bmn;
         p.part = part;
         part += part_bytes(p) / sizeof(float);
-        if ((e = in_map(&m.a[g.n], q.A, q.amn ? FF_BK : FF_BM)) || (e = in_map(&m.b[g.n], q.B, q.bmn ? FF_BK : p.bn / p.ctas)) ||
+        if ((e = in_map(&m.a[g.n], q.A, q.amn ? FF_BK : FF_BM)) ||
+            (e = in_map(&m.b[g.n], q.B, q.bmn ? FF_BK : p.bn / p.ctas)) ||
             (e = out_map(&m.o[g.n], q.out, q.row, q.N, 1, q.M)))
             return e;
         out.p[g.n] = q.out;
@@ -855,7 +866,8 @@ FewPlan ffn_few_plan(int M, int N, int K, bool gated) {
     return p;
 }
 template <typename T, int MODE, int ACT>
-hc_status ffn_few(const FewPlan& pl, const Mat& A, const Mat& B, int M, int N, int F, T* out, long long row, cudaStream_t st) {
+hc_status ffn_few(const FewPlan& pl, const Mat& A, const Mat& B, int M, int N, int F, T* out, long long row,
+                  cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     once_per_device(done, [] {
         return cudaFuncSetAttribute(ffn_few_kernel<T, MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, FS_SMEM) ==
@@ -895,8 +907,10 @@ bool ffn_size_ok(const hc_gated_ffn_desc* d) {
     return d->dtype != HC_DTYPE_F32 && d->C % 8 == 0 && d->F % 8 == 0 && d->C <= 1 << 16 && d->F <= 1 << 16 &&
            d->M < 0x7fffffff - 256;
 }
-// Rows of the copy engine: every one on a 16-byte boundary.
-bool ffn_rows_ok(const hc_rows* r, int M) { return !r->p || (ptr_al(r->p, 16) && (M <= 1 || r->row % 8 == 0)); }
+// Rows of the copy engine: every one on a 16-byte boundary, and no stride of 0.
+bool ffn_rows_ok(const hc_rows* r, int M) {
+    return !r->p || (ptr_al(r->p, 16) && (M <= 1 || (r->row > 0 && r->row % 8 == 0)));
+}
 long long row_of(const hc_rows* r, const hc_gated_ffn_desc* d) { return d->M > 1 ? r->row : d->C; }
 
 struct Space {
@@ -947,7 +961,8 @@ hc_status ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in
             return ffn_few<T, FF_MM, HC_PW_NONE>(few_out, hm, wo, M, C, 0, (T*)y->p, row_of(y, d), st);
         return ffn_mm<T>({hm, false, wo, true, M, C, F, y->p, row_of(y, d)}, (float*)(ws + ffn_space(d, 0).h), st);
     }
-    if ((e = in_map(&m.a[0], xm, FF_BM)) || (e = in_map(&m.b[0], wi, FF_BK)) || (e = out_map(&m.o[0], h, F, F, 1, M))) return e;
+    if ((e = in_map(&m.a[0], xm, FF_BM)) || (e = in_map(&m.b[0], wi, FF_BK)) || (e = out_map(&m.o[0], h, F, F, 1, M)))
+        return e;
     for (int k = 1; k < FF_GROUP; k++) {
         m.a[k] = m.a[0];
         m.b[k] = m.b[0];
