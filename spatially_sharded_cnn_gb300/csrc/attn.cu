@@ -132,15 +132,19 @@ struct Cut {
 };
 // Segments of a sequence: as many as give the GPU enough blocks to fill it in launches of
 // `passes` passes, two chunks each at least; then cells, so that the carry pass, which the last
-// segments are no part of, fills it too.
-Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd) {
-    const int T = tc ? AT_TC : AT_T, per_sm = tc ? d->Dk > 64 || d->Dv > 64 ? 1 : 2 : d->Dk > 96 && d->Dv > 64 ? 2 : 3;
-    const int pad = tc ? 64 : 32;
-    // (passes of another shape are another launch)
-    const int passes = bwd && cdiv(d->Dk, pad) == cdiv(d->Dv, pad) ? 3 : 1, kept = passes == 3 ? 2 : 1;
+// segments are no part of, fills it too.  In fp32 a batch with lengths is cut for twice the blocks,
+// as those behind a sequence's end have nothing to do (once : twice, us; lengths evenly between 0
+// and L; training of 5 x 1537 x 4 heads of 41 / 82 220 : 182, 8 x 1024 x 4 heads of 64 183 : 150, 5 x
+// 1537 x 4 heads of 96 300 : 308; on the tensor cores 20 x 1500 x 4 heads of 64 110 : 139).
+Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd, bool ragged) {
+    const int most = d->Dk > d->Dv ? d->Dk : d->Dv, least = d->Dk > d->Dv ? d->Dv : d->Dk;
+    const int T = tc ? AT_TC : AT_T, per_sm = tc ? most > 64 ? 1 : 2 : most > 96 && least > 64 ? 2 : 3;
+    // (on the tensor cores passes of another shape are another launch)
+    const int passes = bwd && (!tc || (most > 64) == (least > 64)) ? 3 : 1, kept = passes == 3 ? 2 : 1;
     const long long pairs = (long long)d->B * d->H, want = (long long)per_sm * device_sm_count();
     const int chunks = (int)(((long long)d->L + T - 1) / T);
-    long long segs = pairs * passes < want ? want / (pairs * passes) : 1;
+    const long long blocks = ragged && !tc ? 2 * want : want;
+    long long segs = pairs * passes < blocks ? blocks / (pairs * passes) : 1;
     if (segs > chunks / 2) segs = chunks / 2;
     if (segs < 1) segs = 1;
     const int per = (int)((chunks + segs - 1) / segs);
@@ -204,8 +208,10 @@ hc_status hc_linear_attn_workspace_size(const hc_linear_attn_desc* d, int pass, 
     if (!attn_desc_ok(d) || pass < 0 || pass > 1 || !bytes) return HC_ERR_INVALID_ARG;
     if (!attn_size_ok(d)) return HC_ERR_UNSUPPORTED;
     size_t n = 0;
-    for (int tc = 0; tc <= (int)attn_tc_sizes(d); tc++) {
-        const size_t f = carry_floats(d, attn_cut(d, tc, false)), b = pass ? 2 * carry_floats(d, attn_cut(d, tc, true)) : 0;
+    for (int way = 0; way < (attn_tc_sizes(d) ? 4 : 2); way++) {
+        const bool tc = way > 1, ragged = way & 1;
+        const size_t f = carry_floats(d, attn_cut(d, tc, false, ragged));
+        const size_t b = pass ? 2 * carry_floats(d, attn_cut(d, tc, true, ragged)) : 0;
         n = n > f ? n : f;
         n = n > b ? n : b;
     }
@@ -229,7 +235,7 @@ hc_status hc_linear_attn_fwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     traced_begin(st);
     bool tc = attn_tc_sizes(d);
     for (const hc_rows* r : {q, k, v, y}) tc = tc && attn_tc_rows(d, r);
-    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, false));
+    AttnArgs a = attn_args(d, log_decay, lens, attn_cut(d, tc, false, lens));
     a.passes = 1;
     a.p[0] = {*q, *k, *v, *y, d->Dk, d->Dv, d->scale, d->scale, 1.0f, 0, h0, hT, d->Dv, 1,
               a.segs > 1 ? (float*)ws : nullptr, 1};
@@ -259,7 +265,7 @@ hc_status hc_linear_attn_bwd(const hc_linear_attn_desc* d, const hc_rows* q, con
     traced_begin(st);
     bool tc = attn_tc_sizes(d);
     for (const hc_rows* r : {q, k, v, gy, gq, gk, gv}) tc = tc && attn_tc_rows(d, r);
-    const Cut cut = attn_cut(d, tc, true);
+    const Cut cut = attn_cut(d, tc, true, lens);
     AttnArgs a = attn_args(d, log_decay, lens, cut);
     float *cs = nullptr, *cg = nullptr;
     if (a.segs > 1) {

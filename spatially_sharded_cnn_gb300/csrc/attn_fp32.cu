@@ -92,12 +92,8 @@ __device__ __forceinline__ void store1(char* p, int dtype, float v) {
 }
 
 template <int PK, int PV, bool CARRY>
-__global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
-    grid_begin();
-    extern __shared__ __align__(16) unsigned char raw[];
-    AttnSmem<PK, PV>& sm = *reinterpret_cast<AttnSmem<PK, PV>*>(raw);
+__device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass& p, AttnSmem<PK, PV>& sm) {
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const AttnPass& p = a.p[blockIdx.y];
     const int runs = CARRY ? a.cells() : a.segs, run = blockIdx.x % runs, pair = blockIdx.x / runs;  // a cell or a segment
     const int seg = CARRY ? run / a.split : run;
     const int b = pair / a.H, h = pair - b * a.H;
@@ -250,6 +246,7 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
         for (int r = 0; r < PK / 32; r++) {
             f32x2 z[4][N];
             const int m = 4 * ty + 32 * r;
+            if (m >= Dk) break;
 #pragma unroll
             for (int u = 0; u < 4; u++)
 #pragma unroll
@@ -288,9 +285,21 @@ __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
     }
 }
 
+// Passes of Dk up to PK and Dv up to PV, or the other way round: those of one gradient call are one
+// launch.
+template <int PK, int PV, bool CARRY> __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
+    grid_begin();
+    extern __shared__ __align__(16) unsigned char raw[];
+    const AttnPass& p = a.p[blockIdx.y];
+    if (PK == PV || (p.Dk > PV && p.Dk <= PK))
+        attn_fp32_pass<PK, PV, CARRY>(a, p, *reinterpret_cast<AttnSmem<PK, PV>*>(raw));
+    else
+        attn_fp32_pass<PV, PK, CARRY>(a, p, *reinterpret_cast<AttnSmem<PV, PK>*>(raw));
+}
+
 template <int PK, int PV> hc_status launch_pads(const AttnArgs& a, bool carry, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
-    constexpr int smem = (int)sizeof(AttnSmem<PK, PV>);
+    constexpr int one = (int)sizeof(AttnSmem<PK, PV>), two = (int)sizeof(AttnSmem<PV, PK>), smem = one > two ? one : two;
     once_per_device(done, [] {
         return cudaFuncSetAttribute(attn_fp32_kernel<PK, PV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
                    cudaSuccess &&
@@ -304,24 +313,29 @@ template <int PK, int PV> hc_status launch_pads(const AttnArgs& a, bool carry, c
         launch_next(attn_fp32_kernel<PK, PV, false>, grid, dim3(FT), smem, st, a);
     return launched(carry ? "attn_fp32_carry_kernel" : "attn_fp32_kernel", st);
 }
-template <int PK> hc_status launch_pk(const AttnArgs& a, bool carry, cudaStream_t st) {
-    const int pv = (a.p[0].Dv + 31) / 32;
-    return pv == 1   ? launch_pads<PK, 32>(a, carry, st)
-           : pv == 2 ? launch_pads<PK, 64>(a, carry, st)
-           : pv == 3 ? launch_pads<PK, 96>(a, carry, st)
-                     : launch_pads<PK, 128>(a, carry, st);
-}
 
 }  // namespace
 
 hc_status launch_attn_fp32(const AttnArgs& all, bool carry, cudaStream_t st) {
-    return attn_by_shape(all, carry, [&](const AttnArgs& a) {
-        const int pk = (a.p[0].Dk + 31) / 32;
-        return pk == 1   ? launch_pk<32>(a, carry, st)
-               : pk == 2 ? launch_pk<64>(a, carry, st)
-               : pk == 3 ? launch_pk<96>(a, carry, st)
-                         : launch_pk<128>(a, carry, st);
-    });
+    AttnArgs a = all;
+    if (carry) {  // the passes that fill one
+        a.passes = 0;
+        for (int i = 0; i < all.passes; i++)
+            if (all.p[i].keep) a.p[a.passes++] = all.p[i];
+    }
+    const int k = cdiv(a.p[0].Dk, 32), v = cdiv(a.p[0].Dv, 32), most = k > v ? k : v, least = k > v ? v : k;
+    switch (most * 4 + least) {
+        case 5: return launch_pads<32, 32>(a, carry, st);
+        case 9: return launch_pads<64, 32>(a, carry, st);
+        case 10: return launch_pads<64, 64>(a, carry, st);
+        case 13: return launch_pads<96, 32>(a, carry, st);
+        case 14: return launch_pads<96, 64>(a, carry, st);
+        case 15: return launch_pads<96, 96>(a, carry, st);
+        case 17: return launch_pads<128, 32>(a, carry, st);
+        case 18: return launch_pads<128, 64>(a, carry, st);
+        case 19: return launch_pads<128, 96>(a, carry, st);
+        default: return launch_pads<128, 128>(a, carry, st);
+    }
 }
 
 }  // namespace hc
