@@ -175,13 +175,13 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
         __syncthreads();
         if (idx + 1 < c1) fetch(first_row(idx + 1));
         if (!CARRY) {
-            // ---- scores of rows 4 ty .. on rows 2 tx, + 1
+            // ---- scores of rows 4 ty .. on rows tx, tx + 16 (eight lanes' reads of k then meet every bank)
             float s[4][2] = {};
 #pragma unroll 4
             for (int d = 0; d < Dk; d += 4) {
                 float4 k2[2];
 #pragma unroll
-                for (int w = 0; w < 2; w++) k2[w] = *reinterpret_cast<const float4*>(&sm.k[2 * tx + w][d]);
+                for (int w = 0; w < 2; w++) k2[w] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * w][d]);
 #pragma unroll
                 for (int u = 0; u < 4; u++) {
                     const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[4 * ty + u][d]);
@@ -192,14 +192,12 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
             }
 #pragma unroll
             for (int u = 0; u < 4; u++) {
-                const int i = 4 * ty + u, j = 2 * tx;
-                float f[2];
+                const int i = 4 * ty + u;
 #pragma unroll
                 for (int w = 0; w < 2; w++) {
-                    const int n = p.back ? j + w - i : i - j - w;
-                    f[w] = n >= 0 ? s[u][w] * (p.si * exp2f(l2 * n)) : 0.0f;
+                    const int j = tx + 16 * w, n = p.back ? j - i : i - j;
+                    sm.p[i][j] = n >= 0 ? s[u][w] * (p.si * exp2f(l2 * n)) : 0.0f;
                 }
-                *reinterpret_cast<float2*>(&sm.p[i][j]) = make_float2(f[0], f[1]);
             }
             // ---- rows on the state
             f32x2 o[4][N];
