@@ -138,7 +138,8 @@ struct Cut {
 // 1537 x 4 heads of 96 300 : 308; on the tensor cores 20 x 1500 x 4 heads of 64 110 : 139).
 Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd, bool ragged) {
     const int most = d->Dk > d->Dv ? d->Dk : d->Dv, least = d->Dk > d->Dv ? d->Dv : d->Dk;
-    const int T = tc ? AT_TC : AT_T, per_sm = tc ? most > 64 ? 1 : 2 : most > 96 && least > 64 ? 2 : 3;
+    // (what registers and shared memory let an SM hold)
+    const int per_sm = tc ? most > 64 ? 1 : 2 : least > (most > 96 ? 32 : 64) ? 2 : 3, T = tc ? AT_TC : AT_T;
     // (on the tensor cores passes of another shape are another launch)
     const int passes = bwd && (!tc || (most > 64) == (least > 64)) ? 3 : 1, kept = passes == 3 ? 2 : 1;
     const long long pairs = (long long)d->B * d->H, want = (long long)per_sm * device_sm_count();

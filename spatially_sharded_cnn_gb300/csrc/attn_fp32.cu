@@ -238,7 +238,8 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
         if (idx + 1 == c1 && !z1) break;
         // ---- the state behind the chunk: rows 4 ty .. + 32 r
         // (every row has read the state ahead of the barrier above)
-        const float w = exp2f(l2 * (AT_T - lo));
+        // (z + (w - 1) z: a rounded w near 1 would be the same factor off in every chunk, 1e-6 over 50)
+        const float w = expm1f(l2 * (0.693147181f * (AT_T - lo)));
         const f32x2 ww = pk2(w, w);
 #pragma unroll
         for (int r = 0; r < PK / 32; r++) {
@@ -248,7 +249,10 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
 #pragma unroll
             for (int u = 0; u < 4; u++)
 #pragma unroll
-                for (int n = 0; n < N; n++) z[u][n] = mul2(ww, *reinterpret_cast<const f32x2*>(&sm.z[m + u][2 * tx + 32 * n]));
+                for (int n = 0; n < N; n++) {
+                    const f32x2 was = *reinterpret_cast<const f32x2*>(&sm.z[m + u][2 * tx + 32 * n]);
+                    z[u][n] = fma2(was, ww, was);
+                }
 #pragma unroll 4
             for (int j = 0; j < AT_T; j++) {
                 const float f = sm.wj[j];
