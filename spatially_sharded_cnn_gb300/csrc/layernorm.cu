@@ -5,7 +5,7 @@
 // the squared deviations from it are summed from registers (two passes over values
 // that do not move, so no cancellation), and the row is written.  Bound by memory:
 // x in and y out, and for the backward pass x and gy in and gx out: 224 x 1024 x 512 bf16 take
-// 81 us forward, 149 backward (69 and 104 at the rate of a copy).
+// 82 us forward, 135 backward (69 and 104 at the rate of a copy).
 #include "rows.cuh"
 
 namespace hc {
@@ -57,11 +57,37 @@ template <int TPR> __device__ __forceinline__ float ln_sum(float v, float* red) 
     return v;
 }
 
+// Two at a time.
+template <int TPR> __device__ __forceinline__ void ln_sums(float& a, float& b, float* red) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (TPR > 32) {
+        const int w = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) {
+            red[2 * w] = a;
+            red[2 * w + 1] = b;
+        }
+        __syncthreads();
+        a = b = 0.0f;
+#pragma unroll
+        for (int k = 0; k < TPR / 32; k++) {
+            a += red[2 * k];
+            b += red[2 * k + 1];
+        }
+    }
+}
+
 __device__ __forceinline__ bool ln_live(const LnShape& s, int b, int l) { return !s.lens || l < s.lens[b]; }
 
-// FLAT: one run of rows at one stride, all of them there, and threads that all have NV whole
-// packs of channels.  The rows' loads are then no branches, and those of two rows go out together
-// (224 x 1024 x 512 bf16 forward: 123 us with the branches, 73 without).
+// FLAT: one run of rows at one stride, all of them there.  FULL: threads that all have NV whole
+// packs of channels.  Else a thread without channels reads the row's first pack and does not use
+// it: no load of a flat row is behind a branch, and those of two rows go out together (224 x 1024 x
+// 512 bf16 forward: 123 us with branches, 73 without; 768 channels 191 and 125).  Rows of ragged
+// batches stay behind one (5 x 1537 x 330 fp32, training: 19.2 us, 21.2 where they read another's).
 struct LnRow {
     long long r;
     int b, l;
@@ -88,7 +114,7 @@ template <bool FLAT, typename T> __device__ __forceinline__ T* ln_ptr(const View
 
 // NV packs of V values a thread: channels (i * TPR + lane) * V of pack i.  Blocks
 // walk over the rows, ROWS at a time.
-template <typename T, int V, int TPR, int NV, bool FLAT>
+template <typename T, int V, int TPR, int NV, bool FLAT, bool FULL>
 __global__ void __launch_bounds__(ln_block(TPR))
     ln_fwd_kernel(View<const T> x, const float* gamma, const float* beta, View<T> y, float* mean, float* rstd,
                   LnShape s) {
@@ -111,7 +137,7 @@ __global__ void __launch_bounds__(ln_block(TPR))
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int c = (i * TPR + lane) * V;
-                if (FLAT || (w[u].live && c < s.C)) q[u][i] = load_raw<T, V>(xr + c);
+                if (FLAT || w[u].live) q[u][i] = load_raw<T, V>(FULL || c < s.C ? xr + c : xr);
             }
         }
         float v[U][NV][V], m[U], rs[U];
@@ -120,14 +146,10 @@ __global__ void __launch_bounds__(ln_block(TPR))
             m[u] = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                if (FLAT || (w[u].live && (i * TPR + lane) * V < s.C)) {
-                    unpack(q[u][i], v[u][i]);
-                } else {
+                unpack(q[u][i], v[u][i]);
+                const bool on = FULL || (i * TPR + lane) * V < s.C;
 #pragma unroll
-                    for (int k = 0; k < V; k++) v[u][i][k] = 0.0f;
-                }
-#pragma unroll
-                for (int k = 0; k < V; k++) m[u] += v[u][i][k];
+                for (int k = 0; k < V; k++) m[u] += on ? v[u][i][k] : 0.0f;
             }
         }
 #pragma unroll
@@ -137,12 +159,11 @@ __global__ void __launch_bounds__(ln_block(TPR))
             rs[u] = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                if (FLAT || (i * TPR + lane) * V < s.C) {
+                const bool on = FULL || (i * TPR + lane) * V < s.C;
 #pragma unroll
-                    for (int k = 0; k < V; k++) {
-                        v[u][i][k] -= m[u];
-                        rs[u] = fmaf(v[u][i][k], v[u][i][k], rs[u]);
-                    }
+                for (int k = 0; k < V; k++) {
+                    v[u][i][k] = on ? v[u][i][k] - m[u] : 0.0f;
+                    rs[u] = fmaf(v[u][i][k], v[u][i][k], rs[u]);
                 }
             }
         }
@@ -159,7 +180,7 @@ __global__ void __launch_bounds__(ln_block(TPR))
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * TPR + lane) * V;
-            if (!FLAT && c >= s.C) continue;
+            if (!FULL && c >= s.C) continue;
             float g[V], bt[V];
             ln_param<V>(gamma + c, g);
             ln_param<V>(beta + c, bt);
@@ -209,13 +230,13 @@ __global__ void __launch_bounds__(LN_THREADS) ln_fwd_long_kernel(View<const T> x
 // that its block walks; the block's row groups are then added in order into
 // part[block][ggamma C | gbeta C].  gy * gamma is rounded before its mean is taken
 // from it, as it was in that mean: where a row's gradient cancels to zero, it is zero.
-template <typename T, int V, int TPR, int NV, bool FLAT>
+template <typename T, int V, int TPR, int NV, bool FLAT, bool FULL>
 __global__ void __launch_bounds__(ln_block(TPR))
     ln_bwd_kernel(View<const T> x, const float* gamma, const float* mean, const float* rstd, View<const T> gy,
                   View<T> gx, float* part, LnShape s) {
     grid_begin();
     constexpr int ROWS = ln_block(TPR) / TPR;
-    __shared__ float red[32];
+    __shared__ float red[32];  // two for each of 16 warps
     extern __shared__ float own[];  // [ROWS][2][C], rows of several groups
     const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const float inv = 1.0f / s.C;
@@ -225,21 +246,41 @@ __global__ void __launch_bounds__(ln_block(TPR))
     for (int i = 0; i < NV; i++)
 #pragma unroll
         for (int k = 0; k < W; k++) gg[i][k] = gb[i][k] = pk2(0.0f, 0.0f);
-    for (long long r0 = (long long)blockIdx.x * ROWS; r0 < s.rows; r0 += (long long)gridDim.x * ROWS) {
-        const LnRow w = ln_row<FLAT>(s, r0 + sub);
-        const bool live = FLAT ? w.in : w.live;
+    // AHEAD: the next row is under way while this one is taken, where the registers for it cost no
+    // block (224 x 1024 x 512 bf16: 151 us without, 134 with; x 256, a pack a thread: 73 and 94)
+    constexpr bool AHEAD = sizeof(T) == 2 && V == 8 && NV == 2;
+    struct Row {
+        Pack<T, V> x[NV], g[NV];
+        float rs, m;
+    };
+    const auto fetch = [&](const LnRow& w, Row& o) {
         const T *xr = ln_ptr<FLAT>(x, w), *gr = ln_ptr<FLAT>(gy, w);
-        Pack<T, V> xq[NV], gq[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * TPR + lane) * V;
-            if (FLAT || (live && c < s.C)) {
-                xq[i] = load_raw<T, V>(xr + c);
-                gq[i] = load_raw<T, V>(gr + c);
-            }
+            if (!FLAT && !w.live) continue;
+            o.x[i] = load_raw<T, V>(FULL || c < s.C ? xr + c : xr);
+            o.g[i] = load_raw<T, V>(FULL || c < s.C ? gr + c : gr);
         }
-        const float rs = live ? rstd[w.r] : 0.0f, m = live ? -mean[w.r] : 0.0f;
-        const f32x2 rs2 = pk2(rs, rs), mm = pk2(m, m);
+        o.rs = FLAT || w.live ? rstd[w.r] : 0.0f;
+        o.m = FLAT || w.live ? -mean[w.r] : 0.0f;
+    };
+    const long long step = (long long)gridDim.x * ROWS;
+    Row ahead;
+    if constexpr (AHEAD) fetch(ln_row<FLAT>(s, blockIdx.x * (long long)ROWS + sub), ahead);
+    for (long long r0 = (long long)blockIdx.x * ROWS; r0 < s.rows; r0 += step) {
+        const LnRow w = ln_row<FLAT>(s, r0 + sub);
+        const bool live = FLAT ? w.in : w.live;
+        Row row;
+        if constexpr (AHEAD) {
+            row = ahead;
+            fetch(ln_row<FLAT>(s, r0 + step + sub), ahead);
+        } else {
+            fetch(w, row);
+        }
+        Pack<T, V>(&xq)[NV] = row.x;
+        Pack<T, V>(&gq)[NV] = row.g;
+        const f32x2 rs2 = pk2(row.rs, row.rs), mm = pk2(row.m, row.m);
         // xhat and gamma * gy of pair k of pack i
         const auto pair = [&](int i, int k, const float(&ga)[V], f32x2& xh, f32x2& g, f32x2& q) {
             float xv[V], gv[V];
@@ -255,7 +296,7 @@ __global__ void __launch_bounds__(ln_block(TPR))
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * TPR + lane) * V;
-            if (!live || (!FLAT && c >= s.C)) continue;
+            if (!live || (!FULL && c >= s.C)) continue;
             float ga[V];
             ln_param<V>(gamma + c, ga);
 #pragma unroll
@@ -273,15 +314,16 @@ __global__ void __launch_bounds__(ln_block(TPR))
         s1 += t;
         unpk2(a2, s2, t);
         s2 += t;
-        s1 = -__fmul_rn(ln_sum<TPR>(s1, red), inv);
-        s2 = -__fmul_rn(ln_sum<TPR>(s2, red), inv);
+        ln_sums<TPR>(s1, s2, red);
+        s1 = -__fmul_rn(s1, inv);
+        s2 = -__fmul_rn(s2, inv);
         if (!w.in) continue;
         const f32x2 m1 = pk2(s1, s1), m2 = pk2(s2, s2);
         T* out = ln_ptr<FLAT>(gx, w);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * TPR + lane) * V;
-            if (!FLAT && c >= s.C) continue;
+            if (!FULL && c >= s.C) continue;
             float o[V];
             if (live) {
                 float ga[V];
@@ -365,10 +407,12 @@ __global__ void __launch_bounds__(LN_THREADS)
     }
 }
 
-// The threads of a row and the packs a thread, MOST values or fewer: the first that
-// hold C channels.  False: none does.
+// The threads of a row and the packs a thread, MOST values or fewer: the first that hold C
+// channels (a variant that holds no more than one with fewer threads is left out).  False: none does.
 template <int V, int MOST, int TPR, int NV, typename F> bool ln_try(int C, F& f) {
-    if constexpr (NV * V <= MOST)
+    constexpr int packs = MOST / V < 8 ? MOST / V : 8, warp = 32 * packs, two = warp > 128 ? warp : 128;
+    constexpr int less = TPR == 64 ? warp : TPR == 128 ? two : TPR == 512 ? 128 * packs : 0;
+    if constexpr (NV * V <= MOST && TPR * NV > less)
         if (C <= TPR * NV * V) {
             f.template run<V, TPR, NV>();
             return true;
@@ -377,14 +421,17 @@ template <int V, int MOST, int TPR, int NV, typename F> bool ln_try(int C, F& f)
 }
 template <int V, int MOST, typename F> bool ln_dispatch(int C, F& f) {
     return ln_try<V, MOST, 8, 1>(C, f) || ln_try<V, MOST, 8, 2>(C, f) || ln_try<V, MOST, 32, 1>(C, f) ||
-           ln_try<V, MOST, 32, 2>(C, f) || ln_try<V, MOST, 32, 4>(C, f) || ln_try<V, MOST, 32, 8>(C, f) ||
-           ln_try<V, MOST, 128, 4>(C, f) || ln_try<V, MOST, 128, 8>(C, f) || ln_try<V, MOST, 512, 2>(C, f) ||
-           ln_try<V, MOST, 512, 4>(C, f) || ln_try<V, MOST, 512, 8>(C, f) || ln_try<V, MOST, 512, 16>(C, f);
+           ln_try<V, MOST, 32, 2>(C, f) || ln_try<V, MOST, 32, 3>(C, f) || ln_try<V, MOST, 32, 4>(C, f) ||
+           ln_try<V, MOST, 32, 8>(C, f) || ln_try<V, MOST, 64, 2>(C, f) || ln_try<V, MOST, 128, 2>(C, f) ||
+           ln_try<V, MOST, 128, 4>(C, f) || ln_try<V, MOST, 128, 8>(C, f) || ln_try<V, MOST, 512, 1>(C, f) ||
+           ln_try<V, MOST, 512, 2>(C, f) || ln_try<V, MOST, 512, 4>(C, f) || ln_try<V, MOST, 512, 8>(C, f) ||
+           ln_try<V, MOST, 512, 16>(C, f);
 }
 
 // Blocks of the backward pass: each leaves a row of sums.
 long long ln_blocks(const hc_layernorm_desc* d) {
-    const long long rows = (long long)d->B * d->L, most = 4LL * device_sm_count();
+    // (rows of 513 to 2048 channels take blocks of 64 or 128 threads)
+    const long long rows = (long long)d->B * d->L, most = (d->C > 512 && d->C <= 2048 ? 8LL : 4LL) * device_sm_count();
     return rows < most ? rows : most;
 }
 
@@ -402,13 +449,13 @@ template <typename T> struct LnFwd {
     cudaStream_t st;
     template <int V, int TPR, int NV> void run() {
         if constexpr (sizeof(T) * V == 16)
-            if (flat && s.C == TPR * NV * V) return go<V, TPR, NV, true>();
-        go<V, TPR, NV, false>();
+            if (flat) return s.C == TPR * NV * V ? go<V, TPR, NV, true, true>() : go<V, TPR, NV, true, false>();
+        go<V, TPR, NV, false, false>();
     }
-    template <int V, int TPR, int NV, bool FLAT> void go() {
+    template <int V, int TPR, int NV, bool FLAT, bool FULL> void go() {
         constexpr int threads = ln_block(TPR), rows = threads / TPR;
         const long long want = cdiv(s.rows, rows * (NV * V <= 16 ? 2 : 1)), most = 32LL * device_sm_count();
-        launch_next(ln_fwd_kernel<T, V, TPR, NV, FLAT>, dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, st,
+        launch_next(ln_fwd_kernel<T, V, TPR, NV, FLAT, FULL>, dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, st,
                     view<const T>(x), gamma, beta, view<T>(y), mean, rstd, s);
     }
 };
@@ -423,13 +470,13 @@ template <typename T> struct LnBwd {
     cudaStream_t st;
     template <int V, int TPR, int NV> void run() {
         if constexpr (sizeof(T) * V == 16)
-            if (flat && s.C == TPR * NV * V) return go<V, TPR, NV, true>();
-        go<V, TPR, NV, false>();
+            if (flat) return s.C == TPR * NV * V ? go<V, TPR, NV, true, true>() : go<V, TPR, NV, true, false>();
+        go<V, TPR, NV, false, false>();
     }
-    template <int V, int TPR, int NV, bool FLAT> void go() {
+    template <int V, int TPR, int NV, bool FLAT, bool FULL> void go() {
         constexpr int threads = ln_block(TPR);
         const size_t smem = threads > TPR ? (size_t)(threads / TPR) * 2 * s.C * sizeof(float) : 0;
-        launch_next(ln_bwd_kernel<T, V, TPR, NV, FLAT>, dim3((unsigned)blocks), dim3(threads), smem, st, view<const T>(x),
+        launch_next(ln_bwd_kernel<T, V, TPR, NV, FLAT, FULL>, dim3((unsigned)blocks), dim3(threads), smem, st, view<const T>(x),
                     gamma, mean, rstd, view<const T>(gy), view<T>(gx), part, s);
     }
 };
