@@ -73,25 +73,37 @@ __device__ __forceinline__ float attn_cell_decay(float l2, const AttnArgs& a, in
     const bool first = c1 > c0 && (back ? c1 == chunks : c0 == 0);
     return exp2f(l2 * (float)((c1 - c0) * T - (first ? part : 0)));
 }
+// Whether four rows m of a column are one 16-byte piece of the array (transposed states).
+__device__ __forceinline__ bool attn_quads(const AttnPass& p) { return p.zm == 1 && p.zn % 4 == 0; }
+
 // The state ahead of segment seg, N elements of it a thread: `at` gives element i's place in
-// the array (below 0: none).  The loads of all elements are under way at once: none is
-// behind a branch (that took 40 us of 80 on 8 x 4096 x 8 heads of 128).
+// the array (below 0: none); four elements are rows m of a column.  The loads of all elements are
+// under way at once: none is behind a branch (that took 40 us of 80 on 8 x 4096 x 8 heads of 128).
 template <int N, typename F>
 __device__ __forceinline__ void attn_state_ahead(const AttnPass& p, const AttnArgs& a, long long pair, int seg, float l2,
                                                  int chunks, int T, int part, F&& at, float (&z)[N]) {
     const long long size = (long long)p.Dk * p.Dv;
     const bool joined = seg > 0 && a.cells() > kFewCells;
     const float* from = joined ? p.carry + (pair * a.cells() + seg - 1) * size : p.z0 ? p.z0 + pair * size : nullptr;
-    int place[N];
+    const bool quads = attn_quads(p);
+    const auto load = [&](const float* s, float(&v)[N]) {
+        if (quads) {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        place[i] = max(at(i), 0);
-        z[i] = 0.0f;
-    }
-    if (from) {
+            for (int i = 0; i < N; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(s + max(at(i), 0));
+                v[i] = f.x;
+                v[i + 1] = f.y;
+                v[i + 2] = f.z;
+                v[i + 3] = f.w;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; i++) z[i] = from[place[i]];
-    }
+            for (int i = 0; i < N; i++) v[i] = s[max(at(i), 0)];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < N; i++) z[i] = 0.0f;
+    if (from) load(from, z);
     if (joined) {
 #pragma unroll
         for (int i = 0; i < N; i++) z[i] = at(i) >= 0 ? z[i] : 0.0f;
@@ -101,8 +113,7 @@ __device__ __forceinline__ void attn_state_ahead(const AttnPass& p, const AttnAr
         const float w = attn_cell_decay(l2, a, c, chunks, T, part, p.back);
         const float* own = p.carry + (pair * a.cells() + c) * size;
         float v[N];
-#pragma unroll
-        for (int i = 0; i < N; i++) v[i] = own[place[i]];
+        load(own, v);
 #pragma unroll
         for (int i = 0; i < N; i++) z[i] = fmaf(z[i], w, v[i]);
     }

@@ -113,18 +113,18 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
     };
     const bool wq = wide4(p.q, Dk), wk = wide4(p.k, Dk), wv = wide4(p.v, Dv);
 
-    // the state ahead of the segment
-    for (int e0 = 0; e0 < PK * PV; e0 += FT * 16) {
+    // the state ahead of the segment: four rows of a column at a time
+    for (int e0 = tid; e0 < PK / 4 * PV; e0 += FT * 4) {
         float z[16] = {};
         const auto place = [&](int i) {
-            const int e = e0 + tid + FT * i, m = e / PV, n = e - m * PV;
-            return e < PK * PV && m < Dk && n < Dv ? m * p.zm + n * p.zn : -1;
+            const int e = e0 + FT * (i >> 2), m = e / PV * 4 + (i & 3), n = e % PV;
+            return e < PK / 4 * PV && m < Dk && n < Dv ? m * p.zm + n * p.zn : -1;
         };
         if (!CARRY) attn_state_ahead<16>(p, a, pair, seg, l2, chunks, AT_T, chunks * AT_T - len, place, z);
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-            const int e = e0 + tid + FT * i;
-            if (e < PK * PV) sm.z[e / PV][e % PV] = z[i];
+            const int e = e0 + FT * (i >> 2);
+            if (e < PK / 4 * PV) sm.z[e / PV * 4 + (i & 3)][e % PV] = z[i];
         }
     }
 
@@ -274,11 +274,19 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
         __syncthreads();
     }
     if (c0 == c1) __syncthreads();  // the state as it was loaded
-    if (z1)
-        for (int e = tid; e < PK * PV; e += FT) {
-            const int m = e / PV, n = e - m * PV;
-            if (m < Dk && n < Dv) z1[(long long)m * p.zm + (long long)n * p.zn] = sm.z[m][n];
+    if (z1) {
+        const bool quads = attn_quads(p);
+        for (int e = tid; e < PK / 4 * PV; e += FT) {
+            const int m = e / PV * 4, n = e % PV;
+            if (m >= Dk || n >= Dv) continue;
+            float* to = z1 + m * p.zm + n * p.zn;
+            if (quads) {
+                *reinterpret_cast<float4*>(to) = make_float4(sm.z[m][n], sm.z[m + 1][n], sm.z[m + 2][n], sm.z[m + 3][n]);
+            } else {
+                for (int i = 0; i < 4 && m + i < Dk; i++) to[i * p.zm] = sm.z[m + i][n];
+            }
         }
+    }
     if (!CARRY) {
         if (dt == HC_DTYPE_F32)
             attn_blank<float>(p, b, h, len, a.L, seg, a.segs);

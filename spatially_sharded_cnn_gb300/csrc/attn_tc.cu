@@ -537,11 +537,21 @@ __global__ void __launch_bounds__((Shape<DK, DV>::threads), (Shape<DK, DV>::per_
                           : p.z1 && seg == a.segs - 1 ? p.z1 + pair * zsize
                                                 : nullptr;
         if (z1 && zn < Dv) {
+            const bool quads = attn_quads(p);
 #pragma unroll
-            for (int i = 0; i < ZC; i += 2) {
+            for (int i = 0; i < ZC; i += 4) {
                 const int m = zm + i;
-                float* zp = z1 + (long long)m * p.zm + (long long)zn * p.zn;
-                if (m < Dk) unpk2(z[i / 2], zp[0], zp[p.zm]);
+                float* zp = z1 + m * p.zm + zn * p.zn;
+                float f[4];
+                unpk2(z[i / 2], f[0], f[1]);
+                unpk2(z[i / 2 + 1], f[2], f[3]);
+                if (m >= Dk) continue;
+                if (quads) {
+                    *reinterpret_cast<float4*>(zp) = make_float4(f[0], f[1], f[2], f[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) zp[k * p.zm] = f[k];
+                }
             }
         }
         if constexpr (!CARRY) attn_blank<__nv_bfloat16>(p, b, h, len, a.L, seg, a.segs);
