@@ -134,8 +134,8 @@ struct Cut {
 // `passes` passes, two chunks each at least; then cells, so that the carry pass, which the last
 // segments are no part of, fills it too.  In fp32 a batch with lengths is cut for twice the blocks,
 // as those behind a sequence's end have nothing to do (once : twice, us; lengths evenly between 0
-// and L; training of 5 x 1537 x 4 heads of 41 / 82 220 : 182, 8 x 1024 x 4 heads of 64 183 : 150, 5 x
-// 1537 x 4 heads of 96 300 : 308; on the tensor cores 20 x 1500 x 4 heads of 64 110 : 139).
+// and L; training of 5 x 1537 x 4 heads of 41 / 82 211 : 174, 8 x 1024 x 4 heads of 64 170 : 136, 5 x
+// 1537 x 4 heads of 96 310 : 265; on the tensor cores 20 x 1500 x 4 heads of 64 109 : 135).
 Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd, bool ragged) {
     const int most = d->Dk > d->Dv ? d->Dk : d->Dv, least = d->Dk > d->Dv ? d->Dv : d->Dk;
     // (what registers and shared memory let an SM hold)
