@@ -18,6 +18,7 @@ struct LnShape {
     int rows;    // B * L
     float eps;
     const int* lens;
+    bool flat;   // rows at one stride throughout, all of them there
 };
 
 // Threads of a block: rows of up to a warp share one, a longer row has its own.
@@ -100,7 +101,10 @@ template <bool FLAT> __device__ __forceinline__ LnRow ln_row(const LnShape& s, l
         return {r, 0, (int)r, in, true};
     } else {
         LnRow w{r, 0, 0, r < s.rows, false};
-        if (w.in) {
+        if (s.flat) {  // (of accesses that are no whole 16 bytes)
+            w.l = (int)r;
+            w.live = w.in;
+        } else if (w.in) {
             w.b = (int)r / s.L;
             w.l = (int)r - w.b * s.L;
             w.live = ln_live(s, w.b, w.l);
@@ -408,9 +412,10 @@ __global__ void __launch_bounds__(LN_THREADS)
 }
 
 // The threads of a row and the packs a thread, MOST values or fewer: the first that hold C
-// channels (a variant that holds no more than one with fewer threads is left out).  False: none does.
+// channels (a variant that holds no more than one with fewer threads is left out: 224 x 1024 x 333 bf16
+// forward takes 180 us with 128 threads a row of four values each, 135 with a warp).  False: none does.
 template <int V, int MOST, int TPR, int NV, typename F> bool ln_try(int C, F& f) {
-    constexpr int packs = MOST / V < 8 ? MOST / V : 8, warp = 32 * packs, two = warp > 128 ? warp : 128;
+    constexpr int packs = MOST / V < 16 ? MOST / V : 16, warp = 32 * packs, two = warp > 128 ? warp : 128;
     constexpr int less = TPR == 64 ? warp : TPR == 128 ? two : TPR == 512 ? 128 * packs : 0;
     if constexpr (NV * V <= MOST && TPR * NV > less)
         if (C <= TPR * NV * V) {
@@ -422,10 +427,10 @@ template <int V, int MOST, int TPR, int NV, typename F> bool ln_try(int C, F& f)
 template <int V, int MOST, typename F> bool ln_dispatch(int C, F& f) {
     return ln_try<V, MOST, 8, 1>(C, f) || ln_try<V, MOST, 8, 2>(C, f) || ln_try<V, MOST, 32, 1>(C, f) ||
            ln_try<V, MOST, 32, 2>(C, f) || ln_try<V, MOST, 32, 3>(C, f) || ln_try<V, MOST, 32, 4>(C, f) ||
-           ln_try<V, MOST, 32, 8>(C, f) || ln_try<V, MOST, 64, 2>(C, f) || ln_try<V, MOST, 128, 2>(C, f) ||
-           ln_try<V, MOST, 128, 4>(C, f) || ln_try<V, MOST, 128, 8>(C, f) || ln_try<V, MOST, 512, 1>(C, f) ||
-           ln_try<V, MOST, 512, 2>(C, f) || ln_try<V, MOST, 512, 4>(C, f) || ln_try<V, MOST, 512, 8>(C, f) ||
-           ln_try<V, MOST, 512, 16>(C, f);
+           ln_try<V, MOST, 32, 8>(C, f) || ln_try<V, MOST, 32, 16>(C, f) || ln_try<V, MOST, 64, 2>(C, f) ||
+           ln_try<V, MOST, 128, 2>(C, f) || ln_try<V, MOST, 128, 4>(C, f) || ln_try<V, MOST, 128, 8>(C, f) ||
+           ln_try<V, MOST, 128, 16>(C, f) || ln_try<V, MOST, 512, 1>(C, f) || ln_try<V, MOST, 512, 2>(C, f) ||
+           ln_try<V, MOST, 512, 4>(C, f) || ln_try<V, MOST, 512, 8>(C, f) || ln_try<V, MOST, 512, 16>(C, f);
 }
 
 // Blocks of the backward pass: each leaves a row of sums.
@@ -445,11 +450,10 @@ template <typename T> struct LnFwd {
     const float *gamma, *beta;
     float *mean, *rstd;
     LnShape s;
-    bool flat;
     cudaStream_t st;
     template <int V, int TPR, int NV> void run() {
         if constexpr (sizeof(T) * V == 16)
-            if (flat) return s.C == TPR * NV * V ? go<V, TPR, NV, true, true>() : go<V, TPR, NV, true, false>();
+            if (s.flat) return s.C == TPR * NV * V ? go<V, TPR, NV, true, true>() : go<V, TPR, NV, true, false>();
         go<V, TPR, NV, false, false>();
     }
     template <int V, int TPR, int NV, bool FLAT, bool FULL> void go() {
@@ -466,11 +470,10 @@ template <typename T> struct LnBwd {
     float* part;
     LnShape s;
     long long blocks;
-    bool flat;
     cudaStream_t st;
     template <int V, int TPR, int NV> void run() {
         if constexpr (sizeof(T) * V == 16)
-            if (flat) return s.C == TPR * NV * V ? go<V, TPR, NV, true, true>() : go<V, TPR, NV, true, false>();
+            if (s.flat) return s.C == TPR * NV * V ? go<V, TPR, NV, true, true>() : go<V, TPR, NV, true, false>();
         go<V, TPR, NV, false, false>();
     }
     template <int V, int TPR, int NV, bool FLAT, bool FULL> void go() {
@@ -481,7 +484,8 @@ template <typename T> struct LnBwd {
     }
 };
 
-// Accesses of V elements (16 bytes, or two fp32): whole packs in a row, every row on such a boundary.
+// Accesses of V elements (16 bytes, or two): whole packs in a row, every row on such a boundary
+// (224 x 1024 x 330 bf16, training: 321 us in twos, 668 one by one).
 template <int V> bool ln_wide(int C, const hc_rows* a, const hc_rows* b, const hc_rows* c) {
     return C % V == 0 && rows_vec(a, V) && rows_vec(b, V) && (!c || rows_vec(c, V));
 }
@@ -493,11 +497,10 @@ template <typename T>
 hc_status ln_fwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamma, const float* beta, const hc_rows* y,
                  float* mean, float* rstd, const int* lens, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
-    LnFwd<T> f{x, y, gamma, beta, mean, rstd, {d->L, d->C, d->B * d->L, d->eps, lens},
-               !lens && ln_flat(d, x) && ln_flat(d, y), st};
-    constexpr int S = sizeof(T) == 4 ? 2 : 1;
+    LnFwd<T> f{x, y, gamma, beta, mean, rstd, 
+               {d->L, d->C, d->B * d->L, d->eps, lens, !lens && ln_flat(d, x) && ln_flat(d, y)}, st};
     if (!(ln_wide<W>(d->C, x, y, nullptr)   ? ln_dispatch<W, 32>(d->C, f)
-          : ln_wide<S>(d->C, x, y, nullptr) ? ln_dispatch<S, 16>(d->C, f)
+          : ln_wide<2>(d->C, x, y, nullptr) ? ln_dispatch<2, 16>(d->C, f)
                                             : ln_dispatch<1, 16>(d->C, f))) {
         const long long most = 8LL * device_sm_count();
         launch_next(ln_fwd_long_kernel<T>, dim3((unsigned)(f.s.rows < most ? f.s.rows : most)), dim3(LN_THREADS), 0, st,
@@ -510,11 +513,11 @@ template <typename T>
 hc_status ln_bwd(const hc_layernorm_desc* d, const hc_rows* x, const float* gamma, const float* mean, const float* rstd,
                  const hc_rows* gy, const hc_rows* gx, float* part, const int* lens, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
-    LnBwd<T> f{x, gy, gx, gamma, mean, rstd, part, {d->L, d->C, d->B * d->L, d->eps, lens}, ln_blocks(d),
-               !lens && ln_flat(d, x) && ln_flat(d, gy) && ln_flat(d, gx), st};
-    constexpr int S = sizeof(T) == 4 ? 2 : 1;
+    LnBwd<T> f{x, gy, gx, gamma, mean, rstd, part,
+               {d->L, d->C, d->B * d->L, d->eps, lens, !lens && ln_flat(d, x) && ln_flat(d, gy) && ln_flat(d, gx)},
+               ln_blocks(d), st};
     if (!(ln_wide<W>(d->C, x, gy, gx)   ? ln_dispatch<W, 16>(d->C, f)
-          : ln_wide<S>(d->C, x, gy, gx) ? ln_dispatch<S, 16>(d->C, f)
+          : ln_wide<2>(d->C, x, gy, gx) ? ln_dispatch<2, 16>(d->C, f)
                                         : ln_dispatch<1, 16>(d->C, f)))
         launch_next(ln_bwd_long_kernel<T>, dim3((unsigned)f.blocks), dim3(LN_THREADS), 0, st, view<const T>(x), gamma,
                     mean, rstd, view<const T>(gy), view<T>(gx), part, f.s);
