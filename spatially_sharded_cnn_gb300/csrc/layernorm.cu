@@ -459,7 +459,8 @@ template <typename T> struct LnFwd {
     template <int V, int TPR, int NV, bool FLAT, bool FULL> void go() {
         constexpr int threads = ln_block(TPR), rows = threads / TPR;
         const long long want = cdiv(s.rows, rows * (NV * V <= 16 ? 2 : 1)), most = 32LL * device_sm_count();
-        launch_next(ln_fwd_kernel<T, V, TPR, NV, FLAT, FULL>, dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, st,
+        const dim3 grid((unsigned)(want < most ? want : most));
+        launch_next(ln_fwd_kernel<T, V, TPR, NV, FLAT, FULL>, grid, dim3(threads), 0, st,
                     view<const T>(x), gamma, beta, view<T>(y), mean, rstd, s);
     }
 };
@@ -479,8 +480,8 @@ template <typename T> struct LnBwd {
     template <int V, int TPR, int NV, bool FLAT, bool FULL> void go() {
         constexpr int threads = ln_block(TPR);
         const size_t smem = threads > TPR ? (size_t)(threads / TPR) * 2 * s.C * sizeof(float) : 0;
-        launch_next(ln_bwd_kernel<T, V, TPR, NV, FLAT, FULL>, dim3((unsigned)blocks), dim3(threads), smem, st, view<const T>(x),
-                    gamma, mean, rstd, view<const T>(gy), view<T>(gx), part, s);
+        launch_next(ln_bwd_kernel<T, V, TPR, NV, FLAT, FULL>, dim3((unsigned)blocks), dim3(threads), smem, st,
+                    view<const T>(x), gamma, mean, rstd, view<const T>(gy), view<T>(gx), part, s);
     }
 };
 

@@ -36,7 +36,10 @@ LN = [(1, 1, 1, "f32", 0, False), (2, 3, 8, "f32", 0, False), (3, 7, 33, "bf16",
       (5, 19, 100, "f16", 4, True), (2, 31, 128, "f32", 0, False), (4, 9, 250, "f16", 0, False), (1, 300, 256, "bf16", 8, False),
       (5, 40, 330, "f32", 2, True), (3, 21, 512, "bf16", 0, True), (2, 11, 1000, "f32", 0, False), (1, 17, 1025, "bf16", 7, False),
       (2, 5, 2048, "f16", 0, True), (1, 9, 4100, "f32", 0, False), (1, 6, 9000, "bf16", 0, False), (1, 3, 20001, "f32", 0, False),
-      (1, 4, 40000, "f16", 0, False), (700, 5, 48, "bf16", 0, True)]
+      (1, 4, 40000, "f16", 0, False), (700, 5, 48, "bf16", 0, True),
+      (40, 60, 96, "bf16", 0, False), (4, 50, 768, "bf16", 0, False), (3, 40, 1024, "f16", 0, False),
+      (2, 700, 1536, "bf16", 0, False), (2, 9, 3000, "bf16", 0, True), (6, 33, 330, "bf16", 0, False),
+      (2, 20, 333, "f16", 1, False), (900, 3, 20, "f16", 0, False), (2, 11, 1389, "bf16", 0, False)]
 
 
 @pytest.mark.parametrize("B,L,C,dt,wide,ragged", LN)
@@ -100,7 +103,9 @@ AT = [(1, 1, 1, 1, 1, "f32", 0, False, True, True), (2, 5, 2, 3, 7, "f32", 0, Tr
       (5, 9, 2, 64, 64, "bf16", 0, True, True, True), (2, 1, 1, 128, 128, "bf16", 0, False, True, True),
       (5, 3, 2, 72, 16, "bf16", 8, True, True, True), (1, 10, 1, 64, 8, "bf16", 0, False, False, True),
       (5, 300, 2, 64, 64, "f16", 0, True, True, True), (2, 200, 1, 128, 120, "f16", 0, False, True, True),
-      (1, 77, 3, 31, 9, "f16", 0, False, False, True)]
+      (1, 77, 3, 31, 9, "f16", 0, False, False, True),
+      (5, 400, 2, 41, 82, "f32", 0, True, True, True), (1, 900, 1, 128, 40, "f16", 0, False, True, True),
+      (2, 610, 1, 30, 100, "f32", 0, True, True, True)]
 
 
 def attn_inputs(seed, t, B, L, H, Dk, Dv, wide, lens, state, decays):
