@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) attn_step_kernel(View<const T> q, View<co
     const int pair = blockIdx.x, b = pair / H, h = pair - b * H;
     const int cols = (Dv + V - 1) / V, R = 256 / cols;
     const int r = threadIdx.x / cols, c = (threadIdx.x - r * cols) * V;
-    const float w = exp2f(attn_log2_decay(decay, h));
+    const AttnFade w = attn_fade(attn_log_decay(decay, h));
     const T* qr = q.p + b * q.batch + (long long)h * Dk;
     const T* kr = k.p + b * k.batch + (long long)h * Dk;
     const T* vr = v.p + b * v.batch + (long long)h * Dv;
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256) attn_step_kernel(View<const T> q, View<co
             load_pack<float, V>(z + (long long)d * Dv, s);
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                s[i] = fmaf(s[i], w, kf * vf[i]);
+                s[i] = attn_faded(w, s[i], kf * vf[i]);
                 acc[i] = fmaf(qf, s[i], acc[i]);
             }
             store_pack<float, V>(z + (long long)d * Dv, s);

@@ -58,10 +58,27 @@ __host__ __device__ inline int attn_len(const int* lens, int b, int L) {
     const int n = lens[b];
     return n < 0 ? 0 : n > L ? L : n;
 }
-__device__ __forceinline__ float attn_log2_decay(const float* decay, int h) {
+__device__ __forceinline__ float attn_log_decay(const float* decay, int h) {
     if (!decay) return 0.0f;
     const float a = decay[h];
-    return (a < kLowDecay ? kLowDecay : a) * kLog2e;
+    return a < kLowDecay ? kLowDecay : a;
+}
+__device__ __forceinline__ float attn_log2_decay(const float* decay, int h) { return attn_log_decay(decay, h) * kLog2e; }
+
+// A state z over rows whose log decays add up to x, with what they add to it, t: lambda z + t, for a
+// lambda near 1 as z + ((lambda - 1) z + t).  A rounded lambda would be the same factor off each time
+// (8192 tokens at a decay of -7e-5 ended 8e-5 off), and so would (lambda - 1) z added by itself,
+// whose rounding repeats while z hardly moves.  Small lambdas are exact to a few 2^-24 themselves.
+struct AttnFade {
+    float m;    // lambda - 1, or lambda
+    bool keep;
+};
+__device__ __forceinline__ AttnFade attn_fade(float x) {
+    const bool keep = x > -0.5f;
+    return {keep ? expm1f(x) : expf(x), keep};
+}
+__device__ __forceinline__ float attn_faded(const AttnFade& f, float z, float t) {
+    return (f.keep ? z : 0.0f) + fmaf(z, f.m, t);
 }
 
 // What a state loses over cell c of a sequence of `chunks` chunks of T rows: lambda^rows.

@@ -1,0 +1,80 @@
+"""Linear attention over long and idle streams, head by head: states that are carried over many rows with a slow decay,
+states that fade while nothing is added, heads of every memory beside one another.
+
+A factor lambda that is rounded once near 1 is the same amount off at every row (or chunk, or cell of a sequence), so
+that the state of n of them is up to n half steps (2^-24) off; what does not build up are roundings of the sums, which
+have random signs: sqrt(n) of them.  Outputs are compared with the largest value of their own head: a head that
+remembers thousands of rows holds values tens of times those of one that remembers three.
+
+Tolerances are those of test_gpu_block.py (1e-5 for states) unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_mixer import DT, Data, Out, near
+
+pytestmark = pytest.mark.gpu
+SLOW = (-2.4e-4, -1.3e-4, -7e-5, -3e-5, -1e-5, -1e-6, 0.0)
+
+
+@pytest.fixture(scope="module")
+def hc():
+    assert torch.cuda.is_available()
+    from spatially_sharded_cnn_gb300 import build
+    build.build()
+    from spatially_sharded_cnn_gb300 import hc as mod
+    return mod
+
+
+def near_heads(name, out, ref, H, bar):
+    """near() for each head: states (B, H, Dk, Dv), rows (B, L, H * D)."""
+    got = torch.from_numpy(out.numpy()).to(out.t.dtype) if isinstance(out, Out) else out
+    for h in range(H):
+        one = lambda t: t[:, h] if t.ndim == 4 else t.reshape(*t.shape[:2], H, -1)[:, :, h]
+        near(f"{name}, head {h}", one(got), one(ref), bar)
+
+
+def summed(k, v, a, z0, first=0):
+    """z0 lambda^n + sum over rows j of lambda^(n - 1 - j + first) k_j v_j^T, in 64 bits: k (n, H, Dk), v (n, H, Dv)."""
+    n = k.shape[0]
+    a = a.double()
+    w = torch.exp(a * torch.arange(n - 1 + first, first - 1, -1, device="cuda", dtype=torch.float64)[:, None])  # (n, H)
+    z = torch.einsum("nhd,nhe->hde", k.double() * w[..., None], v.double())
+    return z + torch.exp(a * n)[:, None, None] * z0.double()
+
+
+# ---------------------------------------------------------------- one token after another
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_step_slow_decays(hc, dt):
+    """8192 single tokens end in the state that the sequence ends in.  Each is rounded twice at most, by up to 2^-24 of
+    the state, with random signs: sqrt(2 * 8192) * 2^-24 / sqrt(3) = 4.4e-6 of it."""
+    t, n, H, D = DT[dt], 8192, len(SLOW), 16
+    s = Data(11, t)
+    q, k, v = (s.rows(n, 1, H * D)[0][:, 0] for _ in range(3))
+    decay, _ = s.param(H, value=np.array(SLOW))
+    h0, _ = s.param(1, H, D, D)
+    d = hc.linear_attn_desc(1, 1, H, D, D, t)
+    state, y = h0.clone(), Out((1, H * D), t)
+    for i in range(n):
+        hc.check(hc.hc_linear_attn_step(d, q[i:i + 1], k[i:i + 1], v[i:i + 1], state, y.t, decay))
+    ref = summed(k.view(n, H, D), v.view(n, H, D), decay, h0[0])
+    near_heads("state", state, ref[None].cpu().numpy(), H, 1e-5)
+    last = D ** -0.5 * torch.einsum("hd,hde->he", q[-1].view(H, D).double(), ref)
+    near_heads("y", y.t[None], last.reshape(1, 1, H * D).cpu().numpy(), H, 1e-5)
+
+
+def test_step_idle(hc):
+    """Tokens whose k is zero: the state is lambda^n of what it was, whatever lambda is."""
+    values = (-0.2, -0.7, -3.0, -9.0, -16.0, -40.0)
+    H, D, n = len(values), 8, 2
+    s = Data(12, torch.float32)
+    q, v = (s.rows(1, 1, H * D)[0][:, 0] for _ in range(2))
+    decay, a = s.param(H, value=np.array(values))
+    h0, hr = s.param(1, H, D, D)
+    d = hc.linear_attn_desc(1, 1, H, D, D, torch.float32)
+    state, y = h0.clone(), Out((1, H * D))
+    for _ in range(n):
+        hc.check(hc.hc_linear_attn_step(d, q, torch.zeros_like(q), v, state, y.t, decay))
+    # (a * log2(e) is rounded by up to 2^-24 of it: 40 * 6e-8 = 2.4e-6 of lambda)
+    near_heads("state", state, hr * np.exp(n * a)[None, :, None, None], H, 1e-5)
