@@ -11,7 +11,9 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_mixer import DT, Data, Out, near
+import block_ref as R
+from test_gpu_block import attn_inputs, run_attn
+from test_gpu_mixer import DT, ROUND, Data, Out, near
 
 pytestmark = pytest.mark.gpu
 SLOW = (-2.4e-4, -1.3e-4, -7e-5, -3e-5, -1e-5, -1e-6, 0.0)
@@ -78,3 +80,42 @@ def test_step_idle(hc):
         hc.check(hc.hc_linear_attn_step(d, q, torch.zeros_like(q), v, state, y.t, decay))
     # (a * log2(e) is rounded by up to 2^-24 of it: 40 * 6e-8 = 2.4e-6 of lambda)
     near_heads("state", state, hr * np.exp(n * a)[None, :, None, None], H, 1e-5)
+
+
+# ---------------------------------------------------------------- sequences
+
+@pytest.mark.parametrize("dt,Dk,Dv,sms", [("bf16", 64, 64, 1), ("bf16", 64, 64, 0), ("bf16", 128, 128, 1),
+                                          ("bf16", 128, 72, 0), ("bf16", 40, 128, 1)])
+def test_sequence_slow_decays(hc, dt, Dk, Dv, sms):
+    """98341 rows, as one segment (one SM) and cut into segments: states, their gradients, and the rows at the far end."""
+    t, L, H, tail = DT[dt], 98341, len(SLOW) + 1, 40
+    a = attn_inputs(13, t, 1, 1, H, Dk, Dv, 0, None, True, False)  # (its rows are not used)
+    s = Data(14, t)
+    rows = lambda D: torch.randn(1, L, H * D, generator=torch.Generator("cuda").manual_seed(int(s.r.integers(1 << 30))),
+                                 device="cuda").to(t)
+    q, k, v, gy = rows(Dk), rows(Dk), rows(Dv), rows(Dv)
+    a.update(q=(q,), k=(k,), v=(v,), gy=(gy,), decay=s.param(H, value=np.array(SLOW + (-0.3,))))
+    decay, ar = a["decay"]
+    d = hc.linear_attn_desc(1, L, H, Dk, Dv, t)
+    hc.check(hc.hc_set_sm_count(sms))
+    try:
+        o = run_attn(hc, d, a, 1, L, H, Dk, Dv, t, 0, None)
+    finally:
+        hc.check(hc.hc_set_sm_count(0))
+    assert hc.hc_sync_check(None) == hc.HC_OK
+    heads = lambda x: x[0].view(x.shape[1], H, -1)
+    # the state ahead of the last rows, the state's gradient behind the first (lambda G of row `tail`)
+    ahead = summed(heads(k)[:-tail], heads(v)[:-tail], decay, a["h0"][0][0])
+    back = lambda x: heads(x).flip(0)
+    behind = summed(d.scale * back(q)[:-tail].double(), back(gy)[:-tail], decay, a["ghT"][0][0], first=1)
+    n = lambda x: x.double().cpu().numpy()
+    lo, hi = slice(0, tail), slice(L - tail, L)
+    end = R.linear_attn(*(n(x[:, hi]) for x in (q, k, v)), H, d.scale, ar, n(ahead[None]), None, n(gy[:, hi]))
+    top = R.linear_attn(*(n(x[:, lo]) for x in (q, k, v)), H, d.scale, ar, a["h0"][1], None, n(gy[:, lo]), n(behind[None]))
+    bar = 1e-5 + ROUND[t]
+    near_heads("state", o["state"], end["state"], H, 1e-5)
+    near_heads("gstate", o["gstate"], top["gstate"], H, 1e-5)
+    near_heads("y", o["y"].t[:, hi], end["y"], H, bar)
+    near_heads("gq", o["gq"].t[:, hi], end["gq"], H, bar)
+    near_heads("gk", o["gk"].t[:, lo], top["gk"], H, bar)
+    near_heads("gv", o["gv"].t[:, lo], top["gv"], H, bar)
