@@ -139,7 +139,7 @@ struct Cut {
 Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd, bool ragged) {
     const int most = d->Dk > d->Dv ? d->Dk : d->Dv, least = d->Dk > d->Dv ? d->Dv : d->Dk;
     // (what registers and shared memory let an SM hold)
-    const int per_sm = tc ? most > 64 ? 1 : 2 : least > (most > 96 ? 32 : 64) ? 2 : 3, T = tc ? AT_TC : AT_T;
+    const int per_sm = tc ? most > 64 ? 1 : 2 : attn_fp32_per_sm(most, least), T = tc ? AT_TC : AT_T;
     // (on the tensor cores passes of another shape are another launch)
     const int passes = bwd && (!tc || (most > 64) == (least > 64)) ? 3 : 1, kept = passes == 3 ? 2 : 1;
     const long long pairs = (long long)d->B * d->H, want = (long long)per_sm * device_sm_count();

@@ -170,6 +170,8 @@ template <typename F> hc_status attn_by_shape(const AttnArgs& all, bool carry, F
 
 // The kernels in fp32 (any type of row): 32-row chunks.  On the tensor cores (bf16): 128.
 constexpr int AT_T = 32, AT_TC = 128;
+// Blocks of the fp32 kernels that an SM holds, for pads (or head sizes) `most` >= `least`.
+__host__ __device__ constexpr int attn_fp32_per_sm(int most, int least) { return least > (most > 96 ? 32 : 64) ? 2 : 3; }
 hc_status launch_attn_fp32(const AttnArgs& a, bool carry, cudaStream_t st);
 hc_status launch_attn_tc(const AttnArgs& a, bool carry, cudaStream_t st);
 // Cells joined in order, in place: carry[s - 1] becomes the state ahead of segment s.

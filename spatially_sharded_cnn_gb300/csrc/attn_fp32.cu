@@ -100,7 +100,7 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
     const int len = attn_len(a.lens, b, a.L), chunks = (len + AT_T - 1) / AT_T;
     const int c0 = min(chunks, seg * a.per + (CARRY ? run - seg * a.split : 0) * a.cell_per);
     const int c1 = min(chunks, min(CARRY ? c0 + a.cell_per : 0x7fffffff, (seg + 1) * a.per));
-    const float l2 = attn_log2_decay(a.decay, h);
+    const float ld = attn_log_decay(a.decay, h), l2 = ld * kLog2e;
     const int Dk = p.Dk, Dv = p.Dv;
     const long long zsize = (long long)Dk * Dv;
     const int dt = a.dtype, bytes = dt == HC_DTYPE_F32 ? 4 : 2;
@@ -238,9 +238,8 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
         if (idx + 1 == c1 && !z1) break;
         // ---- the state behind the chunk: rows 4 ty .. + 32 r
         // (every row has read the state ahead of the barrier above)
-        // (z + (w - 1) z: a rounded w near 1 would be the same factor off in every chunk, 1e-6 over 50)
-        const float w = expm1f(l2 * (0.693147181f * (AT_T - lo)));
-        const f32x2 ww = pk2(w, w);
+        const AttnFade f = attn_fade(ld * (float)(AT_T - lo));
+        const f32x2 mm = pk2(f.m, f.m), keep = f.keep ? pk2(1.0f, 1.0f) : none;
 #pragma unroll
         for (int r = 0; r < PK / 32; r++) {
             f32x2 z[4][N];
@@ -249,15 +248,13 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
 #pragma unroll
             for (int u = 0; u < 4; u++)
 #pragma unroll
-                for (int n = 0; n < N; n++) {
-                    const f32x2 was = *reinterpret_cast<const f32x2*>(&sm.z[m + u][2 * tx + 32 * n]);
-                    z[u][n] = fma2(was, ww, was);
-                }
+                for (int n = 0; n < N; n++)
+                    z[u][n] = mul2(*reinterpret_cast<const f32x2*>(&sm.z[m + u][2 * tx + 32 * n]), mm);
 #pragma unroll 4
             for (int j = 0; j < AT_T; j++) {
-                const float f = sm.wj[j];
+                const float wj = sm.wj[j];
                 const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[j][m]);
-                const float kw[4] = {k4.x * f, k4.y * f, k4.z * f, k4.w * f};
+                const float kw[4] = {k4.x * wj, k4.y * wj, k4.z * wj, k4.w * wj};
                 f32x2 v2[N];
 #pragma unroll
                 for (int n = 0; n < N; n++) v2[n] = *reinterpret_cast<const f32x2*>(&sm.v[j][2 * tx + 32 * n]);
@@ -269,7 +266,10 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
 #pragma unroll
             for (int u = 0; u < 4; u++)
 #pragma unroll
-                for (int n = 0; n < N; n++) *reinterpret_cast<f32x2*>(&sm.z[m + u][2 * tx + 32 * n]) = z[u][n];
+                for (int n = 0; n < N; n++) {  // attn_faded
+                    f32x2& to = *reinterpret_cast<f32x2*>(&sm.z[m + u][2 * tx + 32 * n]);
+                    to = fma2(to, keep, z[u][n]);
+                }
         }
         __syncthreads();
     }
@@ -297,7 +297,8 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
 
 // Passes of Dk up to PK and Dv up to PV, or the other way round: those of one gradient call are one
 // launch.
-template <int PK, int PV, bool CARRY> __global__ void __launch_bounds__(FT) attn_fp32_kernel(AttnArgs a) {
+template <int PK, int PV, bool CARRY>
+__global__ void __launch_bounds__(FT, (attn_fp32_per_sm(PK, PV))) attn_fp32_kernel(AttnArgs a) {
     grid_begin();
     extern __shared__ __align__(16) unsigned char raw[];
     const AttnPass& p = a.p[blockIdx.y];

@@ -85,7 +85,8 @@ def test_step_idle(hc):
 # ---------------------------------------------------------------- sequences
 
 @pytest.mark.parametrize("dt,Dk,Dv,sms", [("bf16", 64, 64, 1), ("bf16", 64, 64, 0), ("bf16", 128, 128, 1),
-                                          ("bf16", 128, 72, 0), ("bf16", 40, 128, 1)])
+                                          ("bf16", 128, 72, 0), ("bf16", 40, 128, 1), ("f32", 32, 32, 1),
+                                          ("f32", 32, 41, 0), ("f16", 32, 32, 0)])
 def test_sequence_slow_decays(hc, dt, Dk, Dv, sms):
     """98341 rows, as one segment (one SM) and cut into segments: states, their gradients, and the rows at the far end."""
     t, L, H, tail = DT[dt], 98341, len(SLOW) + 1, 40
@@ -119,3 +120,24 @@ def test_sequence_slow_decays(hc, dt, Dk, Dv, sms):
     near_heads("gq", o["gq"].t[:, hi], end["gq"], H, bar)
     near_heads("gk", o["gk"].t[:, lo], top["gk"], H, bar)
     near_heads("gv", o["gv"].t[:, lo], top["gv"], H, bar)
+
+
+@pytest.mark.parametrize("dt,D,rows,values", [("f32", 24, 32, (-0.01, -0.1, -0.3, -0.6)), ("f16", 40, 32, (-0.02, -0.2, -0.6)),
+                                              ("bf16", 64, 128, (-0.003, -0.02, -0.1, -0.15)),
+                                              ("bf16", 128, 128, (-0.003, -0.02, -0.1, -0.15)),
+                                              ("bf16", 8, 600, (-0.003, -0.02, -0.04)), ("f32", 8, 600, (-0.003, -0.02, -0.04))])
+def test_sequence_fades(hc, dt, D, rows, values):
+    """After `rows` rows nothing is added for twice as long (k is zero): the state is lambda^n of what it was, down to
+    e^-50, relative to itself (exponents are rounded by 2^-24 of 50: 3e-6)."""
+    t, L, H = DT[dt], 3 * rows, len(values)
+    a = attn_inputs(16, t, 1, L, H, D, D, 0, None, True, False)
+    a["k"][0][:, rows:] = 0
+    a["k"][1][:, rows:] = 0
+    a["q"][0][:, :2 * rows] = 0  # and backwards: the state's gradient from the last third
+    a["q"][1][:, :2 * rows] = 0
+    a["decay"] = Data(17, t).param(H, value=np.array(values))
+    d = hc.linear_attn_desc(1, L, H, D, D, t)
+    o = run_attn(hc, d, a, 1, L, H, D, D, t, 0, None)
+    ref = R.linear_attn(a["q"][1], a["k"][1], a["v"][1], H, d.scale, a["decay"][1], a["h0"][1], None, a["gy"][1], a["ghT"][1])
+    near_heads("state", o["state"], ref["state"], H, 1e-5)
+    near_heads("gstate", o["gstate"], ref["gstate"], H, 1e-5)
