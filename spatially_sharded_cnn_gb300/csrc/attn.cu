@@ -14,12 +14,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int T) {
     grid_begin();
     const AttnPass& p = a.p[blockIdx.z];
     if (!p.keep) return;
-    __shared__ float w[32];
+    __shared__ AttnFade w[32];
     const int e = blockIdx.y * 256 + threadIdx.x, pair = blockIdx.x, size = p.Dk * p.Dv, cells = a.cells();
     const bool in = e < size;
     const int b = pair / a.H, h = pair - b * a.H;
     const int len = attn_len(a.lens, b, a.L), chunks = (len + T - 1) / T, part = chunks * T - len;
-    const float l2 = attn_log2_decay(a.decay, h);
+    const float ld = attn_log_decay(a.decay, h);
     float z = in && p.z0 ? p.z0[(long long)pair * size + e] : 0.0f;
     float* c = p.carry + (long long)pair * cells * size + e;
     int cell = 0, seg = 0;
@@ -29,13 +29,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int T) {
         for (int i = 0; i < 32; i++) own[i] = in && s0 + i < cells ? c[(long long)(s0 + i) * size] : 0.0f;
         __syncthreads();
         if (threadIdx.x < 32 && s0 + (int)threadIdx.x < cells)
-            w[threadIdx.x] = attn_cell_decay(l2, a, s0 + threadIdx.x, chunks, T, part, p.back);
+            w[threadIdx.x] = attn_cell_fade(ld, a, s0 + threadIdx.x, chunks, T, part, p.back);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 32; i++) {
             const int s = s0 + i;
             if (s >= cells) break;
-            z = fmaf(z, w[i], own[i]);
+            z = attn_faded(w[i], z, own[i]);
             if (++cell == a.split) {  // a segment ends
                 cell = 0;
                 if (in) c[(long long)seg++ * size] = z;

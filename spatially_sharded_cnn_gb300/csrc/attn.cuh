@@ -63,7 +63,6 @@ __device__ __forceinline__ float attn_log_decay(const float* decay, int h) {
     const float a = decay[h];
     return a < kLowDecay ? kLowDecay : a;
 }
-__device__ __forceinline__ float attn_log2_decay(const float* decay, int h) { return attn_log_decay(decay, h) * kLog2e; }
 
 // A state z over rows whose log decays add up to x, with what they add to it, t: lambda z + t, for a
 // lambda near 1 as z + ((lambda - 1) z + t).  A rounded lambda would be the same factor off each time
@@ -81,14 +80,14 @@ __device__ __forceinline__ float attn_faded(const AttnFade& f, float z, float t)
     return (f.keep ? z : 0.0f) + fmaf(z, f.m, t);
 }
 
-// What a state loses over cell c of a sequence of `chunks` chunks of T rows: lambda^rows.
+// What a state loses over cell c of a sequence of `chunks` chunks of T rows, at log decay ld a row.
 // `part`: rows that the chunk with the first row lacks.
-__device__ __forceinline__ float attn_cell_decay(float l2, const AttnArgs& a, int c, int chunks, int T, int part,
-                                                 int back) {
+__device__ __forceinline__ AttnFade attn_cell_fade(float ld, const AttnArgs& a, int c, int chunks, int T, int part,
+                                                   int back) {
     const int seg = c / a.split, c0 = min(chunks, seg * a.per + (c - seg * a.split) * a.cell_per);
     const int c1 = min(chunks, min(c0 + a.cell_per, (seg + 1) * a.per));
     const bool first = c1 > c0 && (back ? c1 == chunks : c0 == 0);
-    return exp2f(l2 * (float)((c1 - c0) * T - (first ? part : 0)));
+    return attn_fade(ld * (float)((c1 - c0) * T - (first ? part : 0)));
 }
 // Whether four rows m of a column are one 16-byte piece of the array (transposed states).
 __device__ __forceinline__ bool attn_quads(const AttnPass& p) { return p.zm == 1 && p.zn % 4 == 0; }
@@ -97,7 +96,7 @@ __device__ __forceinline__ bool attn_quads(const AttnPass& p) { return p.zm == 1
 // the array (below 0: none); four elements are rows m of a column.  The loads of all elements are
 // under way at once: none is behind a branch (that took 40 us of 80 on 8 x 4096 x 8 heads of 128).
 template <int N, typename F>
-__device__ __forceinline__ void attn_state_ahead(const AttnPass& p, const AttnArgs& a, long long pair, int seg, float l2,
+__device__ __forceinline__ void attn_state_ahead(const AttnPass& p, const AttnArgs& a, long long pair, int seg, float ld,
                                                  int chunks, int T, int part, F&& at, float (&z)[N]) {
     const long long size = (long long)p.Dk * p.Dv;
     const bool joined = seg > 0 && a.cells() > kFewCells;
@@ -127,12 +126,12 @@ __device__ __forceinline__ void attn_state_ahead(const AttnPass& p, const AttnAr
         return;
     }
     for (int c = 0; c < seg * a.split; c++) {
-        const float w = attn_cell_decay(l2, a, c, chunks, T, part, p.back);
+        const AttnFade w = attn_cell_fade(ld, a, c, chunks, T, part, p.back);
         const float* own = p.carry + (pair * a.cells() + c) * size;
         float v[N];
         load(own, v);
 #pragma unroll
-        for (int i = 0; i < N; i++) z[i] = fmaf(z[i], w, v[i]);
+        for (int i = 0; i < N; i++) z[i] = attn_faded(w, z[i], v[i]);
     }
 #pragma unroll
     for (int i = 0; i < N; i++) z[i] = at(i) >= 0 ? z[i] : 0.0f;

@@ -120,7 +120,7 @@ __device__ __forceinline__ void attn_fp32_pass(const AttnArgs& a, const AttnPass
             const int e = e0 + FT * (i >> 2), m = e / PV * 4 + (i & 3), n = e % PV;
             return e < PK / 4 * PV && m < Dk && n < Dv ? m * p.zm + n * p.zn : -1;
         };
-        if (!CARRY) attn_state_ahead<16>(p, a, pair, seg, l2, chunks, AT_T, chunks * AT_T - len, place, z);
+        if (!CARRY) attn_state_ahead<16>(p, a, pair, seg, ld, chunks, AT_T, chunks * AT_T - len, place, z);
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             const int e = e0 + FT * (i >> 2);

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__((Shape<DK, DV>::threads), (Shape<DK, DV>::per_
             float z0[ZC] = {};
             const auto place = [&](int i) { return zm + i < Dk && zn < Dv ? (zm + i) * p.zm + zn * p.zn : -1; };
             if (!CARRY)
-                attn_state_ahead<ZC>(p, a, pair, seg, l2, u.chunks, TT, u.chunks * TT - len, place, z0);
+                attn_state_ahead<ZC>(p, a, pair, seg, ld, u.chunks, TT, u.chunks * TT - len, place, z0);
 #pragma unroll
             for (int i = 0; i < ZC; i += 2) z[i / 2] = pk2(z0[i], z0[i + 1]);
         }

@@ -13,7 +13,7 @@ import torch
 
 import block_ref as R
 from test_gpu_block import attn_inputs, run_attn
-from test_gpu_mixer import DT, ROUND, Data, Out, near
+from test_gpu_mixer import DT, ROUND, Data, Out, near, space
 
 pytestmark = pytest.mark.gpu
 SLOW = (-2.4e-4, -1.3e-4, -7e-5, -3e-5, -1e-5, -1e-6, 0.0)
@@ -120,6 +120,24 @@ def test_sequence_slow_decays(hc, dt, Dk, Dv, sms):
     near_heads("gq", o["gq"].t[:, hi], end["gq"], H, bar)
     near_heads("gk", o["gk"].t[:, lo], top["gk"], H, bar)
     near_heads("gv", o["gv"].t[:, lo], top["gv"], H, bar)
+
+
+@pytest.mark.parametrize("decay", [-1.7e-5, -9e-6, -5.3e-6, -3.1e-6, -1.1e-6, -4e-7])
+def test_cells_slow_decays(hc, decay):
+    """One head of fp32 rows alone, cut into some 400 cells: what a state loses over a cell is not rounded to a factor
+    near 1, either.  Sums inside cells are rounded at every row, by up to 2^-24 of the cell's sum (state / sqrt(400)):
+    224 rows of 400 cells leave sqrt(224) * 2^-24 / sqrt(3) = 5e-7 of the state, the joins sqrt(400) * 2^-24 / sqrt(3) =
+    7e-7; held to 3e-6."""
+    t, L, D = torch.float32, 98304, 32
+    s = Data(15, t)
+    q, k, v = (torch.randn(1, L, D, generator=torch.Generator("cuda").manual_seed(i), device="cuda") for i in range(3))
+    a, _ = s.param(1, value=np.array([decay]))
+    h0, _ = s.param(1, 1, D, D)
+    d = hc.linear_attn_desc(1, L, 1, D, D, t)
+    y, hT = torch.empty_like(q), Out((1, 1, D, D))
+    hc.check(hc.hc_linear_attn_fwd(d, q, k, v, y, a, h0, hT.t, None, *space(hc, hc.hc_linear_attn_workspace_size(d, 0))))
+    ref = summed(k[0][:, None], v[0][:, None], a, h0[0])
+    near("state", hT, ref[None].cpu().numpy(), 3e-6)
 
 
 @pytest.mark.parametrize("dt,D,rows,values", [("f32", 24, 32, (-0.01, -0.1, -0.3, -0.6)), ("f16", 40, 32, (-0.02, -0.2, -0.6)),
