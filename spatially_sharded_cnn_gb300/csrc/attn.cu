@@ -139,9 +139,9 @@ struct Cut {
 Cut attn_cut(const hc_linear_attn_desc* d, bool tc, bool bwd, bool ragged) {
     const int most = d->Dk > d->Dv ? d->Dk : d->Dv, least = d->Dk > d->Dv ? d->Dv : d->Dk;
     // (what registers and shared memory let an SM hold)
-    const int per_sm = tc ? most > 64 ? 1 : 2 : attn_fp32_per_sm(most, least), T = tc ? AT_TC : AT_T;
-    // (on the tensor cores passes of another shape are another launch)
-    const int passes = bwd && (!tc || (most > 64) == (least > 64)) ? 3 : 1, kept = passes == 3 ? 2 : 1;
+    const int per_sm = tc ? attn_wide(most) ? 1 : 2 : attn_fp32_per_sm(most, least), T = tc ? AT_TC : AT_T;
+    // (on the tensor cores passes of another kernel are another launch)
+    const int passes = bwd && (!tc || attn_wide(most) == attn_wide(least)) ? 3 : 1, kept = passes == 3 ? 2 : 1;
     const long long pairs = (long long)d->B * d->H, want = (long long)per_sm * device_sm_count();
     const int chunks = (int)(((long long)d->L + T - 1) / T);
     const long long blocks = ragged && !tc ? 2 * want : want;

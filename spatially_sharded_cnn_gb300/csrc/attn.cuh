@@ -148,16 +148,19 @@ __device__ __forceinline__ void attn_blank(const AttnPass& p, int b, int h, int 
     }
 }
 
-// Runs f on the passes of each shape (Dk, Dv) together; of a carry pass on those that
-// fill one.
-template <typename F> hc_status attn_by_shape(const AttnArgs& all, bool carry, F&& f) {
+// The tensor cores' kernels: head sizes up to 64, or up to 128.
+__host__ __device__ constexpr bool attn_wide(int D) { return D > 64; }
+// Runs f on the passes of each kernel together (gq's and gk's sizes are gv's the other way round); of a
+// carry pass on those that fill one.
+template <typename F> hc_status attn_by_kernel(const AttnArgs& all, bool carry, F&& f) {
     bool done[3] = {};
     for (int i = 0; i < all.passes; i++) {
         if (done[i] || (carry && !all.p[i].keep)) continue;
         AttnArgs a = all;
         a.passes = 0;
         for (int j = i; j < all.passes; j++)
-            if (!done[j] && (!carry || all.p[j].keep) && all.p[j].Dk == all.p[i].Dk && all.p[j].Dv == all.p[i].Dv) {
+            if (!done[j] && (!carry || all.p[j].keep) && attn_wide(all.p[j].Dk) == attn_wide(all.p[i].Dk) &&
+                attn_wide(all.p[j].Dv) == attn_wide(all.p[i].Dv)) {
                 a.p[a.passes++] = all.p[j];
                 done[j] = true;
             }

@@ -617,8 +617,8 @@ template <int DK, int DV> hc_status launch_shape(const AttnArgs& a, bool carry, 
 }  // namespace
 
 hc_status launch_attn_tc(const AttnArgs& all, bool carry, cudaStream_t st) {
-    return attn_by_shape(all, carry, [&](const AttnArgs& a) {
-        const bool k = a.p[0].Dk > 64, v = a.p[0].Dv > 64;
+    return attn_by_kernel(all, carry, [&](const AttnArgs& a) {
+        const bool k = attn_wide(a.p[0].Dk), v = attn_wide(a.p[0].Dv);
         return k ? v ? launch_shape<128, 128>(a, carry, st) : launch_shape<128, 64>(a, carry, st)
                  : v ? launch_shape<64, 128>(a, carry, st) : launch_shape<64, 64>(a, carry, st);
     });
