@@ -124,7 +124,8 @@ hc_status hc_gated_ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const v
  * gh = gy w_out^T, ga = gh * u * act'(a), gu = gh * act(a) (each rounded once):
  *   gx = ga w_in[:, :F]^T + gu w_in[:, F:]^T,
  *   gw_in = x^T [ga | gu] ([C][2 F]),  gw_out = h^T gy ([F][C]),
- * both contiguous and of the desc's type; each of the three may be NULL. */
+ * both contiguous and of the desc's type; each of the three may be NULL.  No gradient overlaps another or an
+ * input, the weights among them (HC_ERR_INVALID_ARG), nor does y in the forward pass. */
 hc_status hc_gated_ffn_bwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in, const void* w_out,
                            const hc_rows* gy, const hc_rows* gx, void* gw_in, void* gw_out, void* ws, size_t ws_bytes,
                            void* stream);

@@ -911,6 +911,17 @@ bool ffn_size_ok(const hc_gated_ffn_desc* d) {
 bool ffn_rows_ok(const hc_rows* r, int M) {
     return !r->p || (ptr_al(r->p, 16) && (M <= 1 || (r->row > 0 && r->row % 8 == 0)));
 }
+// Whether [p, p + n) shares an element with another such run, or with the M rows of r (elements of two bytes).
+bool runs_meet(const void* p, long long n, const void* q, long long m) {
+    const char *a = (const char*)p, *b = (const char*)q;
+    return a && b && a < b + 2 * m && b < a + 2 * n;
+}
+bool run_meets_rows(const void* p, long long n, const hc_rows* r, const hc_gated_ffn_desc* d) {
+    if (!p || !r || !r->p || d->M == 0) return false;
+    const long long row = d->M > 1 ? r->row : d->C, from = ((const char*)p - (const char*)r->p) / 2;  // (both on 16 bytes)
+    const long long first = from < d->C ? 0 : (from - d->C) / row + 1;  // that ends behind the run's start
+    return first < d->M && first * row < from + n;
+}
 long long row_of(const hc_rows* r, const hc_gated_ffn_desc* d) { return d->M > 1 ? r->row : d->C; }
 
 struct Space {
@@ -1059,6 +1070,8 @@ hc_status hc_gated_ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const v
         !f32_ok(w_out))
         return HC_ERR_INVALID_ARG;
     if (!ffn_rows_ok(x, d->M) || !ffn_rows_ok(y, d->M)) return HC_ERR_UNSUPPORTED;
+    const long long n_in = 2LL * d->C * d->F, n_out = n_in / 2;
+    if (run_meets_rows(w_in, n_in, y, d) || run_meets_rows(w_out, n_out, y, d)) return HC_ERR_INVALID_ARG;
     if (need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
     if (d->M == 0) return HC_OK;
     const cudaStream_t st = (cudaStream_t)stream;
@@ -1078,6 +1091,14 @@ hc_status hc_gated_ffn_bwd(const hc_gated_ffn_desc* d, const hc_rows* x, const v
         !f32_ok(w_in) || !f32_ok(w_out) || !f32_opt_ok(gw_in) || !f32_opt_ok(gw_out))
         return HC_ERR_INVALID_ARG;
     if (!ffn_rows_ok(x, d->M) || !ffn_rows_ok(gy, d->M) || (gx && !ffn_rows_ok(gx, d->M))) return HC_ERR_UNSUPPORTED;
+    // the launch that writes one gradient reads what the others are taken from
+    const long long n_in = 2LL * d->C * d->F, n_out = n_in / 2;
+    if (runs_meet(gw_in, n_in, w_in, n_in) || runs_meet(gw_in, n_in, w_out, n_out) || runs_meet(gw_out, n_out, w_in, n_in) ||
+        runs_meet(gw_out, n_out, w_out, n_out) || runs_meet(gw_in, n_in, gw_out, n_out) || run_meets_rows(w_in, n_in, gx, d) ||
+        run_meets_rows(w_out, n_out, gx, d))
+        return HC_ERR_INVALID_ARG;
+    for (const hc_rows* r : {x, gy, gx})
+        if (run_meets_rows(gw_in, n_in, r, d) || run_meets_rows(gw_out, n_out, r, d)) return HC_ERR_INVALID_ARG;
     if (need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;
     const cudaStream_t st = (cudaStream_t)stream;
     traced_begin(st);
