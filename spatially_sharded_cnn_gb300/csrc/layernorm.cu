@@ -537,7 +537,7 @@ hc_status hc_layernorm_fwd(const hc_layernorm_desc* d, const hc_rows* x, const f
     if (!ln_desc_ok(d)) return HC_ERR_INVALID_ARG;
     if (!ln_size_ok(d)) return HC_ERR_UNSUPPORTED;
     if (!rows_in_ok(x, d->dtype, d->L) || !rows_out_ok(y, d->dtype, d->B, d->L, d->C) || rows_same(x, y) ||
-        !f32_ok(gamma) || !f32_ok(beta) || !f32_opt_ok(mean) || !f32_opt_ok(rstd) || !ptr_al(lens, 4))
+        !f32_ok(gamma) || !f32_ok(beta) || !f32_opt_ok(mean) || !f32_opt_ok(rstd) || (mean && mean == rstd) || !ptr_al(lens, 4))
         return HC_ERR_INVALID_ARG;
     if (d->L == 0) return HC_OK;
     const cudaStream_t st = (cudaStream_t)stream;
@@ -563,7 +563,8 @@ hc_status hc_layernorm_bwd(const hc_layernorm_desc* d, const hc_rows* x, const f
     if (e) return e;
     if (!rows_in_ok(x, d->dtype, d->L) || !rows_in_ok(gy, d->dtype, d->L) ||
         !rows_out_ok(gx, d->dtype, d->B, d->L, d->C) || rows_same(gx, x) || rows_same(gx, gy) || !f32_ok(gamma) ||
-        (d->L > 0 && (!f32_ok(mean) || !f32_ok(rstd))) || !f32_opt_ok(ggamma) || !f32_opt_ok(gbeta) || !ptr_al(lens, 4))
+        (d->L > 0 && (!f32_ok(mean) || !f32_ok(rstd))) || !f32_opt_ok(ggamma) || !f32_opt_ok(gbeta) ||
+        (ggamma && ggamma == gbeta) || !ptr_al(lens, 4))
         return HC_ERR_INVALID_ARG;
     const bool sums = ggamma || gbeta;
     if (sums && need && (!f32_ok(ws) || ws_bytes < need)) return HC_ERR_WORKSPACE;

@@ -72,3 +72,13 @@ def test_gated_ffn_rows_over_weights(hc):
         assert fwd(y) == hc.HC_ERR_INVALID_ARG
     for y in (WI + IN, WO - ROWS, GX):
         assert fwd(y) == hc.HC_ERR_WORKSPACE
+
+
+def test_layernorm_two_outputs_in_one_place(hc):
+    INV = hc.HC_ERR_INVALID_ARG
+    d = hc.layernorm_desc(2, 8, 8, hc.HC_DTYPE_F32)
+    assert hc._lib.hc_layernorm_fwd(C.byref(d), rows(hc), 4096, 4096, rows(hc, 8192), 1 << 20, 1 << 20, 0, None) == INV
+    bwd = lambda gg, gb: hc._lib.hc_layernorm_bwd(C.byref(d), rows(hc), 4096, 4096, 4096, rows(hc, 16384), rows(hc, 8192), gg, gb,
+                                                 0, 0, 0, None)
+    assert bwd(1 << 20, 1 << 20) == INV
+    assert bwd(1 << 20, 2 << 20) == hc.HC_ERR_WORKSPACE and bwd(1 << 20, 0) == hc.HC_ERR_WORKSPACE
