@@ -106,8 +106,9 @@ hc_status hc_linear_attn_step(const hc_linear_attn_desc* d, const hc_rows* q, co
  *   a = x w_in[:, :F],  u = x w_in[:, F:],  h = act(a) * u,  y = h w_out,
  * act an hc_pw_act.  Products are summed in fp32; h is rounded once to the
  * desc's type, y once.  C and F are multiples of 8 up to 2^16, rows start on
- * 16-byte boundaries (address, row stride, which is not 0), M < 2^31 - 256:
- * HC_ERR_UNSUPPORTED otherwise, and for fp32.  M = 0 is a valid call. */
+ * 16-byte boundaries (address, row stride, which is not 0), M < 2^31 - 256, M * C
+ * and M * F at most 2^38: HC_ERR_UNSUPPORTED otherwise, and for fp32.  M = 0 is a
+ * valid call. */
 typedef struct {
     int M, C, F;
     int act;   /* hc_pw_act */

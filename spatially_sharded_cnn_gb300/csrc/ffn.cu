@@ -905,7 +905,7 @@ bool ffn_desc_ok(const hc_gated_ffn_desc* d) {
 }
 bool ffn_size_ok(const hc_gated_ffn_desc* d) {
     return d->dtype != HC_DTYPE_F32 && d->C % 8 == 0 && d->F % 8 == 0 && d->C <= 1 << 16 && d->F <= 1 << 16 &&
-           d->M < 0x7fffffff - 256;
+           d->M < 0x7fffffff - 256 && (long long)d->M * (d->C > d->F ? d->C : d->F) <= 1LL << 38;  // (tiles fit an int)
 }
 // Rows of the copy engine: every one on a 16-byte boundary, and no stride of 0.
 bool ffn_rows_ok(const hc_rows* r, int M) {
