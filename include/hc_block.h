@@ -66,9 +66,10 @@ hc_status hc_layernorm_bwd(const hc_layernorm_desc* d, const hc_rows* x, const f
  * 3 (HC_ERR_UNSUPPORTED beyond); sizes < 1 (L < 0) and a scale that is not
  * finite are HC_ERR_INVALID_ARG.
  * Arithmetic: bf16 rows go through the tensor cores where Dk and Dv are multiples
- * of 8, addresses and strides multiples of 16 bytes (strides not 0) and sequences
- * not short (a few rows at most): scores, and the state as it is read, are rounded
- * once to bf16 there; the state itself is fp32.  All others are multiplied in fp32.
+ * of 8, addresses and strides multiples of 16 bytes (strides not 0) and L is more
+ * than 32 (8 where Dk or Dv is above 32, 0 where one is above 64): scores, and the
+ * state as it is read, are rounded once to bf16 there; the state itself is fp32.
+ * All others are multiplied in fp32.
  * Rows are taken in chunks of up to 128: a value that is not finite may spoil its
  * whole chunk, not only the rows behind it. */
 typedef struct {
@@ -105,7 +106,9 @@ hc_status hc_linear_attn_step(const hc_linear_attn_desc* d, const hc_rows* q, co
  * aligned, all of the desc's type, HC_DTYPE_BF16 or HC_DTYPE_F16:
  *   a = x w_in[:, :F],  u = x w_in[:, F:],  h = act(a) * u,  y = h w_out,
  * act an hc_pw_act.  Products are summed in fp32; h is rounded once to the
- * desc's type, y once.  C and F are multiples of 8 up to 2^16, rows start on
+ * desc's type, y once.  In fp16 a value of h, or of ga and gu below, beyond 65504
+ * is infinite, and its row of y or gx and the gradients of the weights that it
+ * enters are infinite or NaN; one below 2^-25 is zero (bf16 has fp32's range).  C and F are multiples of 8 up to 2^16, rows start on
  * 16-byte boundaries (address, row stride, which is not 0), M < 2^31 - 256, M * C
  * and M * F at most 2^38: HC_ERR_UNSUPPORTED otherwise, and for fp32.  M = 0 is a
  * valid call. */
