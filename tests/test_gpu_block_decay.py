@@ -13,7 +13,7 @@ import torch
 
 import block_ref as R
 from test_gpu_block import attn_inputs, run_attn
-from test_gpu_mixer import DT, ROUND, Data, Out, near, space
+from test_gpu_mixer import DT, ROUND, Data, Out, lens_of, near, space
 
 pytestmark = pytest.mark.gpu
 SLOW = (-2.4e-4, -1.3e-4, -7e-5, -3e-5, -1e-5, -1e-6, 0.0)
@@ -88,7 +88,7 @@ def test_step_idle(hc):
                                           ("bf16", 128, 72, 0), ("bf16", 40, 128, 1), ("f32", 32, 32, 1),
                                           ("f32", 32, 41, 0), ("f16", 32, 32, 0)])
 def test_sequence_slow_decays(hc, dt, Dk, Dv, sms):
-    """98341 rows, as one segment (one SM) and cut into segments: states, their gradients, and the rows at the far end."""
+    """98341 rows, as one segment (one SM) and cut into segments: states, their gradients, the rows at the far end."""
     t, L, H, tail = DT[dt], 98341, len(SLOW) + 1, 40
     a = attn_inputs(13, t, 1, 1, H, Dk, Dv, 0, None, True, False)  # (its rows are not used)
     s = Data(14, t)
@@ -159,3 +159,22 @@ def test_sequence_fades(hc, dt, D, rows, values):
     ref = R.linear_attn(a["q"][1], a["k"][1], a["v"][1], H, d.scale, a["decay"][1], a["h0"][1], None, a["gy"][1], a["ghT"][1])
     near_heads("state", o["state"], ref["state"], H, 1e-5)
     near_heads("gstate", o["gstate"], ref["gstate"], H, 1e-5)
+
+
+HEADS = (-0.01, -0.3, -0.0004, -40.0, -np.inf, 0.0)
+
+
+@pytest.mark.parametrize("dt,B,L,Dk,Dv,ragged", [("bf16", 2, 300, 64, 64, False), ("bf16", 1, 900, 128, 128, False),
+                                                 ("bf16", 5, 200, 40, 128, True), ("bf16", 5, 515, 64, 64, True),
+                                                 ("f32", 5, 150, 41, 24, True), ("f16", 1, 400, 64, 32, False)])
+def test_heads(hc, dt, B, L, Dk, Dv, ragged):
+    """Heads that remember 100 rows, 3, thousands, nothing to speak of, nothing at all and everything, each against itself."""
+    t, H = DT[dt], len(HEADS)
+    lens, lens_t = lens_of(ragged, B, L)
+    a = attn_inputs(18, t, B, L, H, Dk, Dv, 0, lens, True, False)
+    a["decay"] = Data(19, t).param(H, value=np.array(HEADS))
+    d = hc.linear_attn_desc(B, L, H, Dk, Dv, t)
+    o = run_attn(hc, d, a, B, L, H, Dk, Dv, t, 0, lens_t)
+    ref = R.linear_attn(a["q"][1], a["k"][1], a["v"][1], H, d.scale, a["decay"][1], a["h0"][1], lens, a["gy"][1], a["ghT"][1])
+    for name, out in o.items():
+        near_heads(name, out, ref[name], H, 1e-5 + (ROUND[t] if out.t.dtype == t and t != torch.float32 else 0.0))
