@@ -19,8 +19,9 @@
 // so that nothing is transposed or copied; edges are the copy engine's zero fill.
 // Large products take pairs of CTAs (256 x 256 outputs a tile, the two SMs of a cluster): each holds
 // its 128 rows of A and accumulators, and half of B's columns (32768 rows, 1024 x 2816 SiLU, forward and
-// backward: 1377 us a CTA a tile, 1204 in pairs, where the products that are run would take 1097 at the
-// rate of the library's largest).  Bound by the tensor pipe: it is busy 76 to 86 % of the cycles of the
+// backward, from rest : after seconds of load, which hold the clock near 1.5 GHz: 1361 : 1504 us a CTA a
+// tile, 1215 : 1395 in pairs; the products that are run would take 1097 : 1216 at the rates of the
+// library's largest).  Bound by the tensor pipe: it is busy 76 to 86 % of the cycles of the
 // products, 68 % of MID's, whose gh is a product of half the width, and 61 % of IN's with GELU at C = 512,
 // which the drain's instructions hold up.
 // Warp roles (576 threads, one CTA an SM): warp 0 loads, warp 1 issues the MMAs, warps 2-17
@@ -113,7 +114,7 @@ __device__ __forceinline__ bool ff_wait(uint64_t* b, unsigned parity, volatile i
 
 // act(x) and act'(x) of pairs, as act_f and act_d of rows.cuh (the drain of a tile has as many
 // instructions to issue as its products take cycles at C = 512: 114688 rows, 512 x 2048, GELU forward
-// 516 us a value at a time, 476 in pairs).
+// from rest : under load 521 : 561 us a value at a time, 480 : 541 in pairs).
 template <int ACT, bool SLOPE> __device__ __forceinline__ void act_pair(f32x2 x, f32x2& f, f32x2& d) {
     const f32x2 one = pk2(1.0f, 1.0f), minus = pk2(-1.0f, -1.0f);
     const auto all = [](float v) { return pk2(v, v); };
@@ -479,7 +480,11 @@ __global__ void __launch_bounds__(FF_THREADS, 1)
 // and then takes a share of the rows from everyone's, summed in the order of the ranks.  MODE
 // FF_IN (out: h) or FF_MM (out: y).  Warps: 0 loads, 1 multiplies, all eight add up.
 constexpr int FS_THREADS = 256;
-constexpr int FS_SPLITS = 6;  // CTAs of a cluster at most: of eight, the sixteen clusters of 16 tiles ran in two rounds
+// CTAs of a cluster at most.  Of eight, the sixteen clusters of 16 tiles ran in two rounds; at most 4 : 6 : 8, us
+// of 64 rows, forward: 4096 x 64 (1 and 64 tiles) 14.8 : 13.5 : 12.9, 4096 x 256 (4 and 64) 14.8 : 13.5 : 13.0,
+// 4096 x 1024 (16 and 64) 16.1 : 15.0 : 20.9, 1024 x 2816 (44 and 16) 14.2 : 13.5 : 18.5, 2560 x 2560 (40 and 40)
+// 17.4 : 17.3 : 17.5.
+constexpr int FS_SPLITS = 6;
 constexpr int FS_STAGES = 6;
 constexpr uint32_t FS_STAGE = FF_A_BYTES + 128 * FF_BK * 2;  // 128 accumulator columns at most
 constexpr int FS_SMEM = FS_STAGES * FS_STAGE;                // and the tile in fp32 (64 KB) over it
@@ -717,8 +722,12 @@ size_t pad16(size_t n) { return (n + 15) / 16 * 16; }
 
 // The three products of the backward pass (gx, gw_in, gw_out) in one launch, where each alone
 // would be a round or two of the GPU: tiles are cut so that a unit takes about half of what
-// the whole takes of an SM (7685 rows, 328 x 872: 19 + 23 + 19 us and two joins apart).  False:
-// longer than that, and they run one by one (whole tiles of unequal length would not fill it).
+// the whole takes of an SM.  False: longer than that, and they run one by one (whole tiles of unequal
+// length would not fill it).  One by one : in one launch, us of the backward pass, rows, C x F: 1000, 128 x
+// 512 37 : 22; 2000, 256 x 704 49 : 25; 7685, 328 x 872 92 : 75; 16384, 256 x 704 87 : 73; 4096, 512 x 1024
+// 70 : 61; 2048, 1024 x 1024 59 : 60; 32768, 128 x 512 89 : 73.  Beyond the limit 8192, 512 x 2048 134 : 138, but
+// 16384, 512 x 1024 136 : 126 and 4096, 1024 x 2816 149 : 130.  A quarter : half : all of the whole a unit:
+// 7685, 328 x 872 98 : 75 : 93; 16384, 256 x 704 100 : 73 : 70; 4096, 512 x 1024 68 : 61 : 51.
 bool ffn_group_plan(int M, int C, int F, FfnParams (&p)[3]) {
     const int dims[3][3] = {{M, C, 2 * F}, {C, 2 * F, M}, {F, C, M}}, sms = device_sm_count();
     double us[3], all = 0.0;
