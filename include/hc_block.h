@@ -108,10 +108,10 @@ hc_status hc_linear_attn_step(const hc_linear_attn_desc* d, const hc_rows* q, co
  * act an hc_pw_act.  Products are summed in fp32; h is rounded once to the
  * desc's type, y once.  In fp16 a value of h, or of ga and gu below, beyond 65504
  * is infinite, and its row of y or gx and the gradients of the weights that it
- * enters are infinite or NaN; one below 2^-25 is zero (bf16 has fp32's range).  C and F are multiples of 8 up to 2^16, rows start on
- * 16-byte boundaries (address, row stride, which is not 0), M < 2^31 - 256, M * C
- * and M * F at most 2^38: HC_ERR_UNSUPPORTED otherwise, and for fp32.  M = 0 is a
- * valid call. */
+ * enters are infinite or NaN; one below 2^-25 is zero (bf16 has fp32's range).
+ * C and F are multiples of 8 up to 2^16, rows start on 16-byte boundaries
+ * (address, row stride, which is not 0), M < 2^31 - 256, M * C and M * F at most
+ * 2^38: HC_ERR_UNSUPPORTED otherwise, and for fp32.  M = 0 is a valid call. */
 typedef struct {
     int M, C, F;
     int act;   /* hc_pw_act */
@@ -128,8 +128,9 @@ hc_status hc_gated_ffn_fwd(const hc_gated_ffn_desc* d, const hc_rows* x, const v
  * gh = gy w_out^T, ga = gh * u * act'(a), gu = gh * act(a) (each rounded once):
  *   gx = ga w_in[:, :F]^T + gu w_in[:, F:]^T,
  *   gw_in = x^T [ga | gu] ([C][2 F]),  gw_out = h^T gy ([F][C]),
- * both contiguous and of the desc's type; each of the three may be NULL.  No gradient overlaps another or an
- * input, the weights among them (HC_ERR_INVALID_ARG), nor does y in the forward pass. */
+ * both contiguous and of the desc's type; each of the three may be NULL.  No
+ * gradient of the weights overlaps another gradient or an input, and neither gx
+ * nor, in the forward pass, y the weights (HC_ERR_INVALID_ARG). */
 hc_status hc_gated_ffn_bwd(const hc_gated_ffn_desc* d, const hc_rows* x, const void* w_in, const void* w_out,
                            const hc_rows* gy, const hc_rows* gx, void* gw_in, void* gw_out, void* ws, size_t ws_bytes,
                            void* stream);

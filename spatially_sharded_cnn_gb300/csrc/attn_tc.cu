@@ -27,7 +27,8 @@
 // (its pieces only replace what products 1 and 2 have read), product 3 while the state is
 // added up, products 1 and 2 while the rows before are stored.  (Product 1 of the next chunk
 // behind product 4, before the state is there: 94 us for 86 of this kernel alone, 8 x 4096 x 8
-// heads, whose call with its carry pass takes 105: the thread that issues it is held up behind 4, few products wait in line.)
+// heads, whose call with its carry pass takes 105: the thread that issues it is held up behind 4, few
+// products wait in line.)
 // All threads work on every step and one of warp 0 issues copies and products.
 //
 // Chunks end at the sequence's end: rows past it are never read, and those ahead of its
